@@ -12,7 +12,10 @@
  * (kv_cache_write).  Past that path: the building blocks on their own
  * (llama_linear, llama_gate_up_silu, llama_fused_add_rmsnorm,
  * llama_paged_attention), sampling with temperature, top-k and top-p
- * (llama_sample), the Qwen3-MoE sparse block and decoder layer
+ * (llama_sample), a KV cache held in 4 bits with the attention over it
+ * (kv_cache_write_q4, kv_cache_read_q4, llama_paged_attention_q4) and the norm
+ * and rotation of query and key heads before it (llama_qk_norm_rope), the
+ * Qwen3-MoE sparse block and decoder layer
  * (llama_moe_forward, llama_moe_layer_forward), norm weights folded into the
  * projections (llama_fold_norm_weights) and a self-test of the device-side
  * failure path (llama_selftest_wait_timeout).
@@ -285,6 +288,115 @@ int llama_paged_attention(const LlamaLayerConfig* cfg, const LlamaBatch* batch, 
 int llama_paged_attention_noalloc(const LlamaLayerConfig* cfg, const LlamaBatch* batch, const void* q,
                                   const void* k_cache, const void* v_cache, void* out, llama_stream_t stream);
 size_t llama_paged_attention_noalloc_limit(void);
+
+/* A KV cache held in 4 bits.
+ * k_cache and v_cache are [num_blocks, n_kv_heads, tile] bytes with tile =
+ * llama_kv_cache_q4_tile_bytes(head_dim) = 9 * head_dim: a tile holds the 16
+ * tokens of a block for one KV head, 4.5 bits an element, head_dim 64 or 128,
+ * block_size 16.  Blocks, slots and block tables are those of the bf16 cache.
+ * An element is stored as a 4-bit e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a
+ * sign), every 16 neighbouring elements of a token's head row with one e4m3
+ * scale, and k_scale / v_scale are powers of two (2^-32 .. 2^32) for a whole
+ * array:
+ *   scale = e4m3(max |x| / (6 g)),  code = e2m1(x / (scale g)),
+ *   value = code scale g,           g = k_scale or v_scale,
+ * each to nearest, ties to even, saturating.  scale reaches from 2^-9 to 448,
+ * so g is chosen to bring the largest |x| well below 2688 g and the typical
+ * ones above 0.1 g (1 suits normed keys; a calibrated factor is rounded to a
+ * power of two, which loses nothing but range).  A NaN is stored as zero and
+ * an infinity saturates, so a cache never holds one.  A tile never written
+ * may hold any bytes.  The same k_scale and v_scale go to every call on a
+ * cache.  The order of the bytes in a tile:
+ *   code of K element e of token k:  byte k * d/2 + e/2
+ *   code of V element e of token k:  byte (k/8) * 4d + (e/w * 4 + k%8/2) * w
+ *                                    + k%2 * w/2 + e%w / 2,  w = d/8
+ *   (even elements in the low half of their byte)
+ *   scale of K group s (elements 16s ..) of token k:
+ *                 byte 8d + (k%8 * 4 + s/p) * 2p + k/8 * p + s%p,  p = d/64
+ *   scale of V group s of token k:  byte 8d + (s * 4 + k%8/2) * 4 + k/8 * 2 + k%2
+ * The pages have no counterpart: they keep the cache in the model's type. */
+size_t llama_kv_cache_q4_tile_bytes(int head_dim);  /* 0 for an unsupported head_dim */
+
+/* k, v [num_tokens, n_kv_heads, head_dim] bf16, k_stride / v_stride elements
+ * from one token to the next (multiples of 8, at least n_kv_heads*head_dim: the
+ * rows of a merged projection can be written from where they are), quantised
+ * into the cache at each token's slot (block = slot/16, token = slot%16).
+ * Negative slots are skipped; slots >= num_blocks*16 are reported as a device
+ * guard and skipped.  The slots of one call are distinct (which of two tokens
+ * with one slot is kept, element by element, is not defined). */
+int kv_cache_write_q4(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slot_mapping,
+                      int num_tokens, int n_kv_heads, int head_dim, int block_size, int num_blocks, float k_scale,
+                      float v_scale, void* k_cache, void* v_cache, llama_stream_t stream);
+
+/* The rows at slot_mapping [num_tokens] of a 4-bit cache as bf16, to k, v
+ * [num_tokens, n_kv_heads, head_dim] with the given strides.  A slot may occur
+ * more than once.  Rows of negative slots are left as they were, those of slots
+ * >= num_blocks*16 too, and the latter are reported as a device guard.  Exact:
+ * a stored value is a bf16 number. */
+int kv_cache_read_q4(const void* k_cache, const void* v_cache, const int32_t* slot_mapping, int num_tokens,
+                     int n_kv_heads, int head_dim, int block_size, int num_blocks, float k_scale, float v_scale,
+                     void* k, int64_t k_stride, void* v, int64_t v_stride, llama_stream_t stream);
+
+/* llama_paged_attention over a 4-bit cache: the same batch, arguments and
+ * results, K and V being the values the cache stands for.  Of cfg only n_heads,
+ * n_kv_heads, head_dim and block_size matter (it is checked as a whole).  Rows
+ * of out behind the last sequence are left as they were; a token whose position
+ * is negative or not below its seq_lens is reported as a device guard and its
+ * row left.
+ * Sequences with one new token, or with so few that new * n_heads / n_kv_heads
+ * <= 16 (draft tokens to verify), read the 4-bit cache directly.  For longer
+ * ones the workspace takes a 16-bit copy of the sequence's K and V, of
+ * prefill_blocks blocks at least for all of them: the sum over those sequences
+ * of ceil(seq_lens/16).  A sequence that does not fit any more is reported as a
+ * device guard and its rows left.  prefill_blocks 0 suits batches without them. */
+int llama_paged_attention_q4(const LlamaLayerConfig* cfg, const LlamaBatch* batch, const void* q, const void* k_cache,
+                             const void* v_cache, float k_scale, float v_scale, int prefill_blocks, void* out,
+                             void* workspace, size_t workspace_bytes, llama_stream_t stream);
+size_t llama_paged_attention_q4_workspace_size(const LlamaLayerConfig* cfg, int max_tokens, int max_seqs,
+                                               int max_seq_len, int prefill_blocks);
+
+/* The norm of every query and key head (the Qwen3 layers' q_norm and k_norm)
+ * and the rotary position embedding, in one pass, from and to bf16 rows:
+ *   y = x / sqrt(mean(x^2) + rms_eps) * w       per head (w NULL: y = x)
+ *   (y_a, y_b) = f (y_a cos - y_b sin, y_b cos + y_a sin), angle position *
+ *   inv_freq_i, for pair i of the first rotary_dim elements:
+ *   (i, i + rotary_dim/2), or (2i, 2i+1) with interleaved = 1.
+ * inv_freq_i = theta^(-2i/rotary_dim), then by rope_scaling:
+ *   LLAMA_ROPE_LINEAR  divided by rs_factor;
+ *   LLAMA_ROPE_LLAMA3  the rule of LlamaLayerConfig.rope_scaling 1;
+ *   LLAMA_ROPE_YARN    divided by rs_factor for pairs that turn less than
+ *                      rs_low_freq_factor (beta_slow, 1) times in
+ *                      rs_original_max_pos positions, kept for those that turn
+ *                      more than rs_high_freq_factor (beta_fast, 32) times, a
+ *                      linear ramp over the pairs between; f =
+ *                      rs_attention_factor (0.1 ln(rs_factor) + 1 as published).
+ * f is 1 but for yarn.  head_dim 64 or 128; rotary_dim a multiple of 16 up to
+ * head_dim, 0 for the norm alone (positions may then be NULL).  q [num_tokens,
+ * n_heads, head_dim] and k [num_tokens, n_kv_heads, head_dim] have q_stride and
+ * k_stride elements from one token to the next (multiples of 8), so they can be
+ * the columns of a merged projection; the outputs have strides of their own and
+ * may be the inputs themselves (same pointer and stride).  Computed in fp32,
+ * rounded once. */
+enum { LLAMA_ROPE_PLAIN = 0, LLAMA_ROPE_LLAMA3 = 1, LLAMA_ROPE_LINEAR = 2, LLAMA_ROPE_YARN = 3 };
+typedef struct {
+  int n_heads;
+  int n_kv_heads;
+  int head_dim;
+  int rotary_dim;
+  int interleaved;
+  float rms_eps;
+  float rope_theta;
+  int rope_scaling;
+  float rs_factor;
+  float rs_low_freq_factor;
+  float rs_high_freq_factor;
+  int rs_original_max_pos;
+  float rs_attention_factor;
+} LlamaQkNormRopeConfig;
+int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, const void* k_norm_w,
+                       const int32_t* positions, int num_tokens, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                       llama_stream_t stream);
 
 /* Sampling beyond greedy ([LLAMA-70B] Sampler, sample(): temperature scaling,
  * the top-k / top-p sampler, greedy rows below a temperature threshold, the

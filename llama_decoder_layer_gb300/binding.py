@@ -9,6 +9,7 @@ module raises instead of computing anything itself.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -65,8 +66,17 @@ class LlamaBatch(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("slot_mapping", ctypes.c_void_p)]
 
 
+class LlamaQkNormRopeConfig(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("rms_eps", ctypes.c_float),
+                ("rope_theta", ctypes.c_float), ("rope_scaling", ctypes.c_int), ("rs_factor", ctypes.c_float),
+                ("rs_low_freq_factor", ctypes.c_float), ("rs_high_freq_factor", ctypes.c_float),
+                ("rs_original_max_pos", ctypes.c_int), ("rs_attention_factor", ctypes.c_float)]
+
+
 # every entry point of include/llama_layer.h with its C signature
 _VP, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_I64 = ctypes.c_int64
 _P_CFG, _P_W, _P_B = ctypes.POINTER(LlamaLayerConfig), ctypes.POINTER(LlamaLayerWeights), ctypes.POINTER(LlamaBatch)
 SIGNATURES = {
     "llama_workspace_size": (_SZ, [_P_CFG, _I, _I, _I, _I]),
@@ -81,6 +91,13 @@ SIGNATURES = {
     "llama_paged_attention": (_I, [_P_CFG, _P_B, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "llama_paged_attention_noalloc": (_I, [_P_CFG, _P_B, _VP, _VP, _VP, _VP, _VP]),
     "llama_paged_attention_noalloc_limit": (_SZ, []),
+    "llama_kv_cache_q4_tile_bytes": (_SZ, [_I]),
+    "kv_cache_write_q4": (_I, [_VP, _I64, _VP, _I64, _VP, _I, _I, _I, _I, _I, _F, _F, _VP, _VP, _VP]),
+    "kv_cache_read_q4": (_I, [_VP, _VP, _VP, _I, _I, _I, _I, _I, _F, _F, _VP, _I64, _VP, _I64, _VP]),
+    "llama_paged_attention_q4": (_I, [_P_CFG, _P_B, _VP, _VP, _VP, _F, _F, _I, _VP, _VP, _SZ, _VP]),
+    "llama_paged_attention_q4_workspace_size": (_SZ, [_P_CFG, _I, _I, _I, _I]),
+    "llama_qk_norm_rope": (_I, [ctypes.POINTER(LlamaQkNormRopeConfig), _VP, _VP, _VP, _I, _VP, _I64, _VP, _I64, _VP,
+                                _I64, _VP, _I64, _VP]),
     "llama_get_device_error": (_I, [_VP, ctypes.POINTER(ctypes.c_int)]),
     "llama_status_string": (ctypes.c_char_p, [_I]),
     "llama_num_sms": (_I, []),
@@ -294,6 +311,167 @@ def paged_attention_noalloc(cfg: LayerConfig, batch: Batch, q, k_cache, v_cache,
     st = lib().llama_paged_attention_noalloc(ctypes.byref(c), ctypes.byref(b), _ptr(q), _ptr(k_cache),
                                              _ptr(v_cache), _ptr(out), _stream(stream))
     _check(st, "llama_paged_attention_noalloc")
+
+
+def _token_rows(t: torch.Tensor, where: str) -> int:
+    """Elements from one token to the next of t [tokens, heads, head_dim], whose
+    heads lie side by side."""
+    if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.stride(2) != 1 or
+            (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def kv_cache_q4_tile_bytes(head_dim: int) -> int:
+    """Bytes of one (block, KV head) tile of a 4-bit cache array: the last
+    dimension of a cache [num_blocks, n_kv_heads, tile] uint8."""
+    n = int(lib().llama_kv_cache_q4_tile_bytes(int(head_dim)))
+    if n == 0:
+        raise LlamaError(LLAMA_ERR_UNSUPPORTED, "llama_kv_cache_q4_tile_bytes")
+    return n
+
+
+def _check_cache_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, n_kv: int, head_dim: int, where: str) -> None:
+    for c in (k_cache, v_cache):
+        if (c.dtype != torch.uint8 or c.dim() != 3 or c.shape[1] != n_kv or c.shape[2] != 9 * head_dim
+                or not c.is_contiguous()):
+            raise LlamaError(LLAMA_ERR_ARG, where)
+    if k_cache.shape[0] != v_cache.shape[0]:
+        raise LlamaError(LLAMA_ERR_ARG, where)
+
+
+def _check_slots(slots: torch.Tensor, tokens: int, where: str) -> None:
+    if slots.dtype != torch.int32 or slots.numel() != tokens or not slots.is_contiguous():
+        raise LlamaError(LLAMA_ERR_ARG, where)
+
+
+def kv_cache_write_q4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0, block_size: int = 16,
+                      stream=None) -> None:
+    """k, v [T, n_kv, head_dim] (any stride between tokens) quantised into 4-bit
+    caches [num_blocks, n_kv, tile]; see kv_cache_write_q4 in the header."""
+    ks, vs = _token_rows(k, "kv_cache_write_q4"), _token_rows(v, "kv_cache_write_q4")
+    T, nkv, d = k.shape
+    if v.shape != k.shape:
+        raise LlamaError(LLAMA_ERR_ARG, "kv_cache_write_q4")
+    _check_slots(slot_mapping, T, "kv_cache_write_q4")
+    _check_cache_q4(k_cache, v_cache, nkv, d, "kv_cache_write_q4")
+    st = lib().kv_cache_write_q4(_ptr(k), ks, _ptr(v), vs, _ptr(slot_mapping), T, nkv, d, block_size,
+                                 k_cache.shape[0], k_scale, v_scale, _ptr(k_cache), _ptr(v_cache), _stream(stream))
+    _check(st, "kv_cache_write_q4")
+
+
+def kv_cache_read_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, k: torch.Tensor,
+                     v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0, block_size: int = 16,
+                     stream=None) -> None:
+    """The rows at slot_mapping of 4-bit caches as bf16, into k, v [T, n_kv,
+    head_dim]; see kv_cache_read_q4 in the header."""
+    ks, vs = _token_rows(k, "kv_cache_read_q4"), _token_rows(v, "kv_cache_read_q4")
+    T, nkv, d = k.shape
+    if v.shape != k.shape:
+        raise LlamaError(LLAMA_ERR_ARG, "kv_cache_read_q4")
+    _check_slots(slot_mapping, T, "kv_cache_read_q4")
+    _check_cache_q4(k_cache, v_cache, nkv, d, "kv_cache_read_q4")
+    st = lib().kv_cache_read_q4(_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, nkv, d, block_size,
+                                k_cache.shape[0], k_scale, v_scale, _ptr(k), ks, _ptr(v), vs, _stream(stream))
+    _check(st, "kv_cache_read_q4")
+
+
+def prefill_blocks(q_lens: Sequence[int], seq_lens: Sequence[int], group: int) -> int:
+    """The prefill_blocks of a batch for paged_attention_q4: the cache blocks of
+    the sequences with more than one new token and q_len * group > 16 (group =
+    n_heads / n_kv_heads)."""
+    return sum((s + 15) // 16 for q, s in zip(q_lens, seq_lens) if q > 1 and q * group > 16)
+
+
+def paged_attention_q4_workspace_size(cfg: LayerConfig, max_tokens: int, max_seqs: int, max_seq_len: int,
+                                      prefill_blocks: int = 0) -> int:
+    c = cfg.c()
+    n = lib().llama_paged_attention_q4_workspace_size(ctypes.byref(c), max_tokens, max_seqs, max_seq_len,
+                                                      prefill_blocks)
+    if n == 0:
+        raise LlamaError(LLAMA_ERR_ARG, "llama_paged_attention_q4_workspace_size")
+    return int(n)
+
+
+def paged_attention_q4(cfg: LayerConfig, batch: Batch, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       out: torch.Tensor, workspace: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
+                       prefill_blocks: int = 0, stream=None) -> None:
+    """Paged attention over 4-bit caches; see llama_paged_attention_q4 in the header."""
+    _check_cache_q4(k_cache, v_cache, cfg.n_kv_heads, cfg.head_dim, "llama_paged_attention_q4")
+    if k_cache.shape[0] != batch.num_blocks:
+        raise LlamaError(LLAMA_ERR_ARG, "llama_paged_attention_q4")
+    for t in (q, out):
+        if (t.dtype != torch.bfloat16 or not t.is_contiguous() or
+                t.numel() != batch.positions.numel() * cfg.n_heads * cfg.head_dim):
+            raise LlamaError(LLAMA_ERR_ARG, "llama_paged_attention_q4")
+    c, b = cfg.c(), batch.c()
+    st = lib().llama_paged_attention_q4(ctypes.byref(c), ctypes.byref(b), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                        k_scale, v_scale, prefill_blocks, _ptr(out), _ptr(workspace),
+                                        workspace.numel(), _stream(stream))
+    _check(st, "llama_paged_attention_q4")
+
+
+_ROPE_TYPES = {"default": 0, "llama3": 1, "linear": 2, "yarn": 3}
+
+
+@dataclass
+class QkNormRopeConfig:
+    """Heads, norm and rotary embedding of qk_norm_rope.  rotary_dim None: the
+    whole head.  rope_scaling: None, or a config.json block with rope_type (or
+    type) linear, llama3 or yarn and that type's parameters."""
+
+    n_heads: int
+    n_kv_heads: int
+    head_dim: int
+    rotary_dim: Optional[int] = None
+    interleaved: bool = False
+    rms_eps: float = 1e-6
+    rope_theta: float = 10000.0
+    rope_scaling: Optional[dict] = None
+
+    def c(self) -> LlamaQkNormRopeConfig:
+        s = self.rope_scaling or {}
+        kind = s.get("rope_type", s.get("type", "default"))
+        if kind not in _ROPE_TYPES:
+            raise LlamaError(LLAMA_ERR_ARG, f"rope_type {kind!r}")
+        factor = float(s.get("factor", 1.0))
+        low, high = s.get("low_freq_factor", 1.0), s.get("high_freq_factor", 4.0)
+        attn = 1.0
+        if kind == "yarn":
+            low, high = s.get("beta_slow", 1.0), s.get("beta_fast", 32.0)
+            attn = s.get("attention_factor")
+            if attn is None:
+                attn = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+        return LlamaQkNormRopeConfig(
+            self.n_heads, self.n_kv_heads, self.head_dim,
+            self.head_dim if self.rotary_dim is None else self.rotary_dim, 1 if self.interleaved else 0, self.rms_eps,
+            self.rope_theta, _ROPE_TYPES[kind], factor, float(low), float(high),
+            int(s.get("original_max_position_embeddings", 0)), float(attn))
+
+
+def qk_norm_rope(cfg: QkNormRopeConfig, q_norm: Optional[torch.Tensor], k_norm: Optional[torch.Tensor],
+                 positions: Optional[torch.Tensor], q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor,
+                 k_out: torch.Tensor, stream=None) -> None:
+    """Per-head norm (q_norm, k_norm [head_dim] or None) and rotation of q [T,
+    n_heads, head_dim] and k [T, n_kv_heads, head_dim], any stride between
+    tokens; q_out / k_out may be q / k; see llama_qk_norm_rope in the header."""
+    where = "llama_qk_norm_rope"
+    strides = [_token_rows(t, where) for t in (q, k, q_out, k_out)]
+    T = q.shape[0]
+    if (q.shape != q_out.shape or k.shape != k_out.shape or k.shape[0] != T or
+            tuple(q.shape[1:]) != (cfg.n_heads, cfg.head_dim) or tuple(k.shape[1:]) != (cfg.n_kv_heads, cfg.head_dim)):
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    if positions is not None:
+        _check_slots(positions, T, where)
+    for w in (q_norm, k_norm):
+        if w is not None and (w.dtype != torch.bfloat16 or w.numel() != cfg.head_dim or not w.is_contiguous()):
+            raise LlamaError(LLAMA_ERR_ARG, where)
+    c = cfg.c()
+    st = lib().llama_qk_norm_rope(ctypes.byref(c), _ptr(q_norm), _ptr(k_norm), _ptr(positions), T, _ptr(q), strides[0],
+                                  _ptr(k), strides[1], _ptr(q_out), strides[2], _ptr(k_out), strides[3],
+                                  _stream(stream))
+    _check(st, where)
 
 
 def set_gemm_schedule(schedule: int) -> None:

@@ -14,6 +14,7 @@
 // to the post-attention norm, then the sparse MoE block in place of gate_up
 // and down.  With folded norms (null norm weights) the norm kernels write each
 // row's rsqrt and the qkv and gate_up GEMMs scale their rows by it.
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -24,6 +25,7 @@
 #include "kernels.h"
 #include "launch.cuh"
 #include "llama_layer.h"
+#include "q4.cuh"
 
 namespace llama {
 
@@ -488,6 +490,43 @@ int standalone_gemm(GemmArgs& g, void* workspace, cudaStream_t s) {
   return gemm_launch(g, s);
 }
 
+// A scale of a 4-bit cache array: a power of two (so that dividing and
+// multiplying by it is exact), within 2^-32 .. 2^32 (so that every stored value
+// is a normal bf16).
+bool q4_scale_ok(float g) {
+  int e = 0;
+  return g > 0.f && g < INFINITY && frexpf(g, &e) == 0.5f && e > -32 && e <= 33;
+}
+
+// The checks that writing and reading a 4-bit cache share; fills what they have in common.
+int cache_q4_args(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slots, int T,
+                  int n_kv, int head_dim, int block_size, int num_blocks, float k_scale, float v_scale,
+                  const void* k_cache, const void* v_cache, CacheQ4Args* a) {
+  if (T < 0 || n_kv < 1 || head_dim < 1 || block_size < 1 || num_blocks < 1) return LLAMA_ERR_ARG;
+  if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale)) return LLAMA_ERR_ARG;
+  if ((head_dim != 64 && head_dim != 128) || block_size != kQ4Block) return LLAMA_ERR_UNSUPPORTED;
+  if (T == 0) return LLAMA_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache) return LLAMA_ERR_ARG;
+  if (static_cast<long long>(num_blocks) * block_size > 0x7fffffffLL) return LLAMA_ERR_ARG;
+  const int64_t width = static_cast<int64_t>(n_kv) * head_dim;
+  if (k_stride < width || v_stride < width) return LLAMA_ERR_ARG;
+  if (k_stride % 8 || v_stride % 8) return LLAMA_ERR_UNSUPPORTED;
+  if (!a16(k) || !a16(v) || !a16(k_cache) || !a16(v_cache)) return LLAMA_ERR_UNSUPPORTED;
+  a->k_stride = k_stride;
+  a->v_stride = v_stride;
+  a->slots = slots;
+  a->T = T;
+  a->n_kv = n_kv;
+  a->head_dim = head_dim;
+  a->num_blocks = num_blocks;
+  a->k_scale = k_scale;
+  a->v_scale = v_scale;
+  a->inv_k_scale = 1.f / k_scale;
+  a->inv_v_scale = 1.f / v_scale;
+  a->err = device_error_word();
+  return LLAMA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -563,6 +602,118 @@ int llama_paged_attention(const LlamaLayerConfig* cfg, const LlamaBatch* batch, 
   AttnArgs a = attn_args(*cfg, *batch, q, k_cache, v_cache, out, reinterpret_cast<float*>(ws_base(workspace)), part,
                          device_error_word(), false);
   return cuda_status(attention_launch(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t llama_kv_cache_q4_tile_bytes(int head_dim) {
+  return head_dim == 64 || head_dim == 128 ? static_cast<size_t>(q4_tile_bytes(head_dim)) : 0;
+}
+
+int kv_cache_write_q4(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int32_t* slot_mapping,
+                      int num_tokens, int n_kv_heads, int head_dim, int block_size, int num_blocks, float k_scale,
+                      float v_scale, void* k_cache, void* v_cache, llama_stream_t stream) {
+  CacheQ4Args a{};
+  const int st = cache_q4_args(k, k_stride, v, v_stride, slot_mapping, num_tokens, n_kv_heads, head_dim, block_size,
+                               num_blocks, k_scale, v_scale, k_cache, v_cache, &a);
+  if (st || num_tokens == 0) return st;
+  a.k = k;
+  a.v = v;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  return cuda_status(kv_write_q4_launch(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kv_cache_read_q4(const void* k_cache, const void* v_cache, const int32_t* slot_mapping, int num_tokens,
+                     int n_kv_heads, int head_dim, int block_size, int num_blocks, float k_scale, float v_scale,
+                     void* k, int64_t k_stride, void* v, int64_t v_stride, llama_stream_t stream) {
+  CacheQ4Args a{};
+  const int st = cache_q4_args(k, k_stride, v, v_stride, slot_mapping, num_tokens, n_kv_heads, head_dim, block_size,
+                               num_blocks, k_scale, v_scale, k_cache, v_cache, &a);
+  if (st || num_tokens == 0) return st;
+  a.k_out = k;
+  a.v_out = v;
+  a.k_cache = const_cast<void*>(k_cache);
+  a.v_cache = const_cast<void*>(v_cache);
+  return cuda_status(kv_read_q4_launch(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t llama_paged_attention_q4_workspace_size(const LlamaLayerConfig* cfg, int max_tokens, int max_seqs,
+                                               int max_seq_len, int prefill_blocks) {
+  if (check_cfg(cfg) != LLAMA_OK || max_tokens < 0 || max_seqs < 0 || max_seq_len < 0 || prefill_blocks < 0) return 0;
+  return attn_q4_workspace_bytes(max_tokens, max_seqs, max_seq_len, prefill_blocks, cfg->n_heads, cfg->n_kv_heads,
+                                 cfg->head_dim) + 256;
+}
+
+int llama_paged_attention_q4(const LlamaLayerConfig* cfg, const LlamaBatch* batch, const void* q, const void* k_cache,
+                             const void* v_cache, float k_scale, float v_scale, int prefill_blocks, void* out,
+                             void* workspace, size_t workspace_bytes, llama_stream_t stream) {
+  int st = check_cfg(cfg);
+  if (st) return st;
+  if ((st = check_batch(batch, cfg))) return st;
+  if (!q4_scale_ok(k_scale) || !q4_scale_ok(v_scale) || prefill_blocks < 0) return LLAMA_ERR_ARG;
+  if (batch->num_tokens == 0) return LLAMA_OK;
+  if (!q || !k_cache || !v_cache || !out) return LLAMA_ERR_ARG;
+  if (!a16(q) || !a16(k_cache) || !a16(v_cache) || !a16(out)) return LLAMA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(prefill_blocks) * cfg->n_kv_heads * cfg->block_size > 0x7fffffffLL) return LLAMA_ERR_ARG;
+  const size_t need = attn_q4_workspace_bytes(batch->num_tokens, batch->num_seqs, batch->max_seq_len, prefill_blocks,
+                                              cfg->n_heads, cfg->n_kv_heads, cfg->head_dim);
+  if (workspace == nullptr || workspace_bytes < need + 256) return LLAMA_ERR_WORKSPACE;
+  AttnQ4Args a{};
+  a.a = attn_args(*cfg, *batch, q, k_cache, v_cache, out, nullptr, 0, device_error_word(), false);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.prefill_blocks = prefill_blocks;
+  a.ws = ws_base(workspace);
+  return cuda_status(attention_q4_launch(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, const void* k_norm_w,
+                       const int32_t* positions, int num_tokens, const void* q, int64_t q_stride, const void* k,
+                       int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                       llama_stream_t stream) {
+  if (cfg == nullptr || num_tokens < 0) return LLAMA_ERR_ARG;
+  if (cfg->n_heads < 1 || cfg->n_kv_heads < 1 || cfg->head_dim < 1 || cfg->rotary_dim < 0 ||
+      cfg->rotary_dim > cfg->head_dim || !(cfg->rms_eps >= 0.f) || (cfg->interleaved != 0 && cfg->interleaved != 1))
+    return LLAMA_ERR_ARG;
+  if (cfg->rotary_dim > 0) {
+    const float th = cfg->rope_theta;
+    if (!(th > 0.f && th < INFINITY) || cfg->rope_scaling < LLAMA_ROPE_PLAIN || cfg->rope_scaling > LLAMA_ROPE_YARN)
+      return LLAMA_ERR_ARG;
+    if (cfg->rope_scaling != LLAMA_ROPE_PLAIN && !(cfg->rs_factor > 0.f && cfg->rs_factor < INFINITY))
+      return LLAMA_ERR_ARG;
+    if ((cfg->rope_scaling == LLAMA_ROPE_LLAMA3 || cfg->rope_scaling == LLAMA_ROPE_YARN) &&
+        (!(cfg->rs_low_freq_factor > 0.f) || !(cfg->rs_high_freq_factor > cfg->rs_low_freq_factor) ||
+         !(cfg->rs_high_freq_factor < INFINITY) || cfg->rs_original_max_pos <= 0))
+      return LLAMA_ERR_ARG;
+    if (cfg->rope_scaling == LLAMA_ROPE_YARN &&
+        (!(th > 1.f) || !(cfg->rs_attention_factor > 0.f && cfg->rs_attention_factor < INFINITY)))
+      return LLAMA_ERR_ARG;
+  }
+  if (cfg->head_dim != 64 && cfg->head_dim != 128) return LLAMA_ERR_UNSUPPORTED;
+  if (cfg->rotary_dim % 16 || cfg->n_heads > 65535 || cfg->n_kv_heads > 65535) return LLAMA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return LLAMA_OK;
+  if (!q || !k || !q_out || !k_out || (cfg->rotary_dim > 0 && !positions)) return LLAMA_ERR_ARG;
+  const int64_t qw = static_cast<int64_t>(cfg->n_heads) * cfg->head_dim;
+  const int64_t kw = static_cast<int64_t>(cfg->n_kv_heads) * cfg->head_dim;
+  if (q_stride < qw || q_out_stride < qw || k_stride < kw || k_out_stride < kw) return LLAMA_ERR_ARG;
+  if (q_stride % 8 || q_out_stride % 8 || k_stride % 8 || k_out_stride % 8) return LLAMA_ERR_UNSUPPORTED;
+  const void* ps[6] = {q, k, q_out, k_out, q_norm_w, k_norm_w};
+  for (const void* p : ps)
+    if (p != nullptr && !a16(p)) return LLAMA_ERR_UNSUPPORTED;
+  QkNormRopeArgs a{};
+  a.cfg = cfg;
+  a.q_norm_w = q_norm_w;
+  a.k_norm_w = k_norm_w;
+  a.positions = positions;
+  a.T = num_tokens;
+  a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  return cuda_status(qk_norm_rope_launch(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int llama_sample(const float* logits, int rows, int vocab, const float* temperature, const int32_t* top_k,

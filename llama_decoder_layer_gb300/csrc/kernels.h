@@ -97,6 +97,33 @@ int fold_norm_launch(const void* gamma, const void* w, int rows, int cols, void*
 int kv_write_launch(const void* k, const void* v, const int32_t* slots, int T, int n_kv, int head_dim,
                     int block_size, int num_blocks, void* k_cache, void* v_cache, int* err, cudaStream_t s);
 
+// 4-bit cache rows (cache_q4.cu): write k, v at slots, or read them back into
+// k_out, v_out.  Strides in elements between tokens; the scales are powers of two.
+struct CacheQ4Args {
+  const void *k, *v;      // [T, n_kv, head_dim] bf16 (write)
+  void *k_out, *v_out;    // the same, read back (read)
+  long long k_stride, v_stride;
+  const int32_t* slots;   // [T], < 0 = skip
+  int T, n_kv, head_dim, num_blocks;
+  float k_scale, v_scale, inv_k_scale, inv_v_scale;
+  void *k_cache, *v_cache;  // [num_blocks, n_kv, 9 * head_dim] bytes
+  int* err;
+};
+int kv_write_q4_launch(const CacheQ4Args& a, cudaStream_t s);
+int kv_read_q4_launch(const CacheQ4Args& a, cudaStream_t s);
+
+// norm and rotation of q and k heads (qk_rope.cu); strides in elements between tokens
+struct QkNormRopeArgs {
+  const LlamaQkNormRopeConfig* cfg;
+  const void *q_norm_w, *k_norm_w;  // [head_dim] or null: not normed
+  const int32_t* positions;
+  int T;
+  const void *q, *k;
+  void *q_out, *k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+};
+int qk_norm_rope_launch(const QkNormRopeArgs& a, cudaStream_t s);
+
 int embed_launch(const void* table, const int32_t* ids, int T, int H, int vocab, void* out, int* err, bool pdl,
                  cudaStream_t s);
 
@@ -132,6 +159,16 @@ size_t attn_partials_bytes(int B, int T, int max_seq_len, int nq, int head_dim);
 // *joined (if given) is set when the caller's stream waited on the side
 // stream: the next kernel then has a full dependency, not a programmatic one.
 int attention_launch(const AttnArgs& a, cudaStream_t s, bool* joined = nullptr);
+
+// attention over the 4-bit cache (attention_q4.cu)
+struct AttnQ4Args {
+  AttnArgs a;  // k_cache, v_cache: 4-bit; partials unused
+  float k_scale, v_scale;
+  int prefill_blocks;  // bound on the blocks of the sequences that take the prefill path
+  uint8_t* ws;         // 256-aligned, attn_q4_workspace_bytes(...)
+};
+size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int nq, int nkv, int head_dim);
+int attention_q4_launch(const AttnQ4Args& a, cudaStream_t s);
 
 // Sparse MoE block: workspace layout (byte offsets from a 256-aligned base)
 // and the launch sequence.

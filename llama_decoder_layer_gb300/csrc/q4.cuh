@@ -1,0 +1,113 @@
+// The 4-bit KV-cache format: where a (token, element) of a tile lies, and the
+// conversions between bf16 / fp32 values and the stored bits.
+//
+// A tile holds 16 tokens of one KV head: 8 D bytes of e2m1 codes, then D bytes
+// of e4m3 scales, one per 16 neighbouring elements of a token.  The value of an
+// element is code * scale * g, g a power of two for the whole array.  code *
+// scale has at most 2 + 4 significant bits and lies on a grid of 2^-10 below
+// 2688, so it is exact in bf16 and in fp16, and dividing or multiplying by g
+// is exact in fp32.
+//
+// The order of the bytes is the one in which the decode attention's lanes take
+// them (lane = 4 g + t holds rows g, g + 8 and columns 2t, 2t + 1, 2t + 8,
+// 2t + 9 of an m16n8k16 operand): a lane reads its share of the codes with one
+// 16-byte load per 8 keys (8 bytes at D = 64) and its scales with one load, at
+// consecutive addresses over the warp, with no exchange between lanes.
+//   K codes:  token row k at k * D/2, element e at byte e / 2 (low half first):
+//             lane t of row k contracts over elements t * D/4 ..
+//   V codes:  token k, element e at (k / 8) * 4 D + (e / W * 4 + (k % 8) / 2) * W
+//             + (k % 2) * W/2 + (e % W) / 2, W = D / 8: lane (g, t) holds elements
+//             g * W .. of the token pair (2t, 2t + 1) of each half
+//   K scales: 8 D + ((k % 8) * 4 + s / P) * 2 P + (k / 8) * P + s % P for group s,
+//             P = D / 64
+//   V scales: 8 D + (s * 4 + (k % 8) / 2) * 4 + (k / 8) * 2 + k % 2
+// Every token's codes and scales lie in bytes of their own, so tokens are
+// written independently of one another.
+#pragma once
+
+#include "common.cuh"
+
+namespace llama {
+
+constexpr int kQ4Block = 16;  // tokens a tile
+constexpr int kQ4Group = 16;  // elements a scale
+
+__host__ __device__ constexpr int q4_tile_bytes(int D) { return 9 * D; }
+
+template <int D>
+__host__ __device__ __forceinline__ int q4_k_scale_at(int k, int s) {
+  constexpr int P = D / 64;
+  return 8 * D + ((k & 7) * 4 + s / P) * 2 * P + (k >> 3) * P + s % P;
+}
+
+template <int D>
+__host__ __device__ __forceinline__ int q4_v_scale_at(int k, int s) {
+  return 8 * D + (s * 4 + ((k & 7) >> 1)) * 4 + (k >> 3) * 2 + (k & 1);
+}
+
+// byte of the code of V element e of token k
+template <int D>
+__host__ __device__ __forceinline__ int q4_v_code_at(int k, int e) {
+  constexpr int W = D / 8;
+  return (k >> 3) * 4 * D + ((e / W) * 4 + ((k & 7) >> 1)) * W + (k & 1) * (W / 2) + (e % W) / 2;
+}
+
+// four bytes of e2m1 pairs -> four fp16 pairs (the low half of a byte in the low half)
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// two e4m3 bytes -> an fp16 pair (exact)
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t v) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(static_cast<uint16_t>(v)));
+  return d;
+}
+
+// nearest e4m3 of x >= 0, at most 448, in the low byte
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(0.f), "f"(x));
+  return d & 0xFFu;
+}
+
+// nearest e2m1 of eight values (ties to the even code, at most 6 in size), x[0] in the lowest four bits
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&x)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return w;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ float f16_lo(uint32_t v) {
+  float f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(v));
+  return f;
+}
+
+__device__ __forceinline__ float f16_hi(uint32_t v) {
+  float f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "r"(v));
+  return f;
+}
+
+}  // namespace llama
