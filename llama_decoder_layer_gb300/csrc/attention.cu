@@ -66,7 +66,7 @@ struct AttnParams {
   int* err;
 };
 
-constexpr uint32_t kNoItem = 0xFFFFFFFFu;
+constexpr uint32_t kNoItem = kNoPrefillItem;
 
 // number of prefill work items the host sizes the list for: at most
 // ceil(q_len / tile) per sequence, tile >= 8 tokens, so at most T / 8 + B
@@ -1318,8 +1318,7 @@ bool fork_join_events(cudaEvent_t* fork, cudaEvent_t* join) {
 }
 
 template <int D>
-int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, AttnParams& p, cudaStream_t s,
-             bool* joined) {
+cudaError_t set_attributes() {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
@@ -1329,11 +1328,21 @@ int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, At
       attr = cudaFuncSetAttribute(k_attn_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   static_cast<int>(prefill_smem<D>()));
   });
+  return attr;
+}
+
+// the tensor-memory prefill kernel serves this shape
+bool prefill_on_tc(int head_dim, int group) { return head_dim == 128 && 128 % group == 0; }
+
+template <int D>
+int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, AttnParams& p, cudaStream_t s,
+             bool* joined) {
+  const cudaError_t attr = set_attributes<D>();
   if (attr != cudaSuccess) return attr;
   const int max_blk = (a.max_seq_len + kBS - 1) / kBS;
   p.max_chunks = num_chunks(max_blk);
   if (p.max_chunks < 1) p.max_chunks = 1;
-  const bool tc = a.max_query_len >= 2 && D == 128 && 128 % p.group == 0;
+  const bool tc = a.max_query_len >= 2 && prefill_on_tc(D, p.group);
   const int tile_tokens = tc ? 128 / p.group : 16;  // tensor-core prefill: 128 rows = tokens x group heads
   const int items = (a.T + tile_tokens - 1) / tile_tokens + a.B;
   // With prefill sequences in the batch, the decode kernels (HBM-bound) run on
@@ -1403,6 +1412,25 @@ int launch_prefill_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap
                        pdl, tk, tv, p);
 }
 
+// what every attention kernel takes from the arguments
+AttnParams base_params(const AttnArgs& a) {
+  AttnParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.qsl = a.qsl;
+  p.seq_lens = a.seq_lens;
+  p.positions = a.positions;
+  p.block_table = a.block_table;
+  p.max_blocks = a.max_blocks;
+  p.num_blocks = a.num_blocks;
+  p.nq = a.nq;
+  p.nkv = a.nkv;
+  p.group = a.nq / a.nkv;
+  p.scale_log2 = kLog2e / sqrtf(static_cast<float>(a.head_dim));
+  p.err = a.err;
+  return p;
+}
+
 }  // namespace
 
 size_t attn_partials_bytes(int B, int T, int max_seq_len, int nq, int head_dim) {
@@ -1419,20 +1447,7 @@ int attention_launch(const AttnArgs& a, cudaStream_t s, bool* joined) {
   CUtensorMap tk, tv;
   if (!make_cache_tmap(&tk, a.k_cache, rows, a.head_dim)) return cudaErrorInvalidValue;
   if (!make_cache_tmap(&tv, a.v_cache, rows, a.head_dim)) return cudaErrorInvalidValue;
-  AttnParams p{};
-  p.q = static_cast<const __nv_bfloat16*>(a.q);
-  p.out = static_cast<__nv_bfloat16*>(a.out);
-  p.qsl = a.qsl;
-  p.seq_lens = a.seq_lens;
-  p.positions = a.positions;
-  p.block_table = a.block_table;
-  p.max_blocks = a.max_blocks;
-  p.num_blocks = a.num_blocks;
-  p.nq = a.nq;
-  p.nkv = a.nkv;
-  p.group = a.nq / a.nkv;
-  p.scale_log2 = kLog2e / sqrtf(static_cast<float>(a.head_dim));
-  p.err = a.err;
+  AttnParams p = base_params(a);
   const int max_blk = (a.max_seq_len + kBS - 1) / kBS;
   const size_t n = static_cast<size_t>(a.B) * (num_chunks(max_blk) < 1 ? 1 : num_chunks(max_blk)) * a.nq;
   if (attn_partials_bytes(a.B, a.T, a.max_seq_len, a.nq, a.head_dim) > a.partials_bytes) return cudaErrorInvalidValue;
@@ -1443,6 +1458,27 @@ int attention_launch(const AttnArgs& a, cudaStream_t s, bool* joined) {
   if (a.head_dim == 128) return launch_d<128>(a, tk, tv, p, s, joined);
   if (a.head_dim == 64) return launch_d<64>(a, tk, tv, p, s, joined);
   return cudaErrorInvalidValue;
+}
+
+int prefill_tile_tokens(const AttnArgs& a) {
+  const int group = a.nq / a.nkv;
+  return prefill_on_tc(a.head_dim, group) ? 128 / group : 16;
+}
+
+int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int n_items, bool pdl, cudaStream_t s) {
+  if (n_items > 65535) return cudaErrorInvalidValue;  // grid y
+  const long long rows = static_cast<long long>(a.num_blocks) * a.nkv * kBS;
+  CUtensorMap tk, tv;
+  if (!make_cache_tmap(&tk, a.k_cache, rows, a.head_dim)) return cudaErrorInvalidValue;
+  if (!make_cache_tmap(&tv, a.v_cache, rows, a.head_dim)) return cudaErrorInvalidValue;
+  AttnParams p = base_params(a);
+  p.pre_items = const_cast<uint32_t*>(items);
+  const bool tc = prefill_on_tc(a.head_dim, p.group);
+  const int tile = prefill_tile_tokens(a);
+  const cudaError_t attr = a.head_dim == 128 ? set_attributes<128>() : set_attributes<64>();
+  if (attr != cudaSuccess) return attr;
+  if (a.head_dim == 128) return launch_prefill_d<128>(a, tk, tv, p, tc, tile, n_items, pdl, s);
+  return launch_prefill_d<64>(a, tk, tv, p, tc, tile, n_items, pdl, s);
 }
 
 }  // namespace llama

@@ -3,10 +3,35 @@
 //   o[t, h] = sum_j softmax_j(q[t, h] . K[b, h / g, j] / sqrt(d)) V[b, h / g, j],
 //   j = 0 .. position(t), K and V the values of the 4-bit tiles (q4.cuh)
 //
-// One CTA per (token, KV head): its four warps take the keys in turn, a lane
-// D / 32 neighbouring elements, with an online softmax per warp and query head;
-// the warps' states are merged in shared memory.
+// * Sequences of one new token, or of so few that new * g <= 16 rows share a
+//   pass over the keys: k_attn_q4_decode, bound by the cache's bytes.
+//   - Work is the list of (sequence, KV head, block), cut into one equal range
+//     per CTA (four CTAs an SM), whatever the lengths; every CTA finds its range
+//     from the sequence lengths itself.  A (sequence, KV head) cut by a border
+//     leaves partial sums (unnormalised o, maximum, sum) that k_attn_q4_combine
+//     joins in order; the others are finished where they are.
+//   - A CTA's four warps take the blocks of its range in turn, each through a
+//     ring of its own filled by bulk copies (a tile of K and one of V, 9 D bytes
+//     each, contiguous), across the borders of sequences.
+//   - S^T = K Q^T and O^T = V^T P^T with m16n8k16 in fp16, fp32 sums: keys and
+//     head elements on the 16-row side, the query rows on the 8-column side, so
+//     a group of 8 heads wastes nothing.  The tile's byte order makes every
+//     lane's operands its own: codes -> fp16 by the conversion instruction
+//     (2 values each), times the scale, exact (6 significant bits).  The
+//     conversions are the widest use of a pipe: 64 of 2 a clock per 2304 bytes.
+//     (A tcgen05.mma would want the operands back in shared memory or TMEM, and
+//     its 128 rows filled by 8.)
+//   - q is brought to fp16 with a power of two per row that puts its largest
+//     element at 2^14 (exact but for elements 2^-29 of that).  Weights are fp16
+//     (relative error 2^-11), relative to a maximum that is only moved when a
+//     score passes it by 2^8, times 2^6: normal fp16 down to 2^-20 of it.
+// * Longer sequences: their blocks are expanded once into a 16-bit copy
+//   (k_q4_expand) over which the prefill kernels of the bf16 cache run: every
+//   tile is read by all query tiles, so decoding it there would repeat the work
+//   and load the softmax's pipes.
 #include <math.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -19,119 +44,801 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 4;
-constexpr int kHeads = 4;  // query heads at a time
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxRows = 16;        // query rows (new tokens x group) of the decode path
+constexpr int kCtasPerSm = 4;
+constexpr int kMinShare = 8;        // blocks a CTA takes at least: two a warp
+constexpr float kMaxStep = 8.f;     // log2 by which a score may pass the running maximum
+constexpr float kWeightBias = 6.f;  // weights are stored times 2^6
+constexpr float kMinusInf = -INFINITY;
+
+template <int D>
+constexpr int stages() { return D == 128 ? 4 : 6; }
 
 struct Q4Params {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
   const uint8_t *k_cache, *v_cache;
   const int32_t *qsl, *seq_lens, *positions, *block_table;
-  int T, B, max_blocks, num_blocks, nq, nkv, group, max_seq_len;
+  int T, B, max_blocks, num_blocks, nq, nkv, group, max_query_len, max_seq_len;
   float scale_log2, v_scale;
+  float* part_o;   // [CTA][2][kMaxRows][D]
+  float2* part_ml; // [CTA][2][kMaxRows]: maximum, sum
+  int4* cut;       // [CTA]: sequence (or -1), KV head, last CTA of the piece that begins here
   int* err;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_q4(const Q4Params p) {
-  constexpr int E = D / 32;
-  __shared__ float sm[kWarps][kHeads], sl[kWarps][kHeads], so[kWarps][kHeads][D];
-  const int t = blockIdx.x, kvh = blockIdx.y;
-  if (t >= p.qsl[p.B]) return;
-  int lo = 0, hi = p.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.qsl[mid] <= t) lo = mid; else hi = mid - 1;
+// Blocks of a sequence on the decode path; 0 if it has no new tokens, takes the
+// prefill path, or is out of bounds (*bad).
+__device__ __forceinline__ int decode_blocks(const Q4Params& p, int b, int& t0, int& rows, int& len, bool& bad) {
+  t0 = p.qsl[b];
+  const int n = p.qsl[b + 1] - t0;
+  len = p.seq_lens[b];
+  rows = n * p.group;
+  bad = n > p.max_query_len || t0 < 0 || t0 > p.T - n;  // n rows of q and out from t0 on, as the launch was sized for
+  if (bad || n < 1 || (n > 1 && (n > kMaxRows || rows > kMaxRows))) return 0;
+  const int nblk = (len + kQ4Block - 1) / kQ4Block;
+  bad = len < 1 || len > p.max_seq_len || nblk > p.max_blocks;
+  return bad ? 0 : nblk;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
+  static_assert(N == 2 || N == 4, "8 or 16 bytes");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+
+// NT: 8-row tiles of query rows (the rows of a sequence: new token r / group, head r % group)
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_decode(const Q4Params p) {
+  constexpr int TB = q4_tile_bytes(D);
+  constexpr int S = stages<D>();
+  constexpr int KW = D / 32;   // words of K codes a lane and 8 keys; of V codes too
+  constexpr int MT = D / 16;   // 16-element tiles of the head
+  constexpr int W = D / 8;     // head elements a lane holds of O
+  constexpr int ROWS = 8 * NT;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* obuf = reinterpret_cast<float*>(smem + kWarps * S * 2 * TB);        // [warp][ROWS][D]
+  float2* mlbuf = reinterpret_cast<float2*>(obuf + kWarps * ROWS * D);       // [warp][ROWS]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(mlbuf + kWarps * ROWS);       // [warp][S]
+  long long* plan = reinterpret_cast<long long*>(bars + kWarps * S);         // [8]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * S; ++i) mbar_init(smem_u32(bars + i), 1);
+    fence_mbar_init();
   }
-  const int b = lo, n_keys = p.positions[t] + 1;
-  if (n_keys < 1 || n_keys > p.seq_lens[b] || n_keys > p.max_seq_len || (n_keys + 15) / 16 > p.max_blocks) {
-    if (kvh == 0 && threadIdx.x == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the CTA's range of blocks: exclusive sums of the sequences' blocks, a
+  // run of sequences per thread
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int bfirst = min(p.B, static_cast<int>(threadIdx.x) * per), blast = min(p.B, bfirst + per);
+  long long mine = 0;
+  for (int b = bfirst; b < blast; ++b) {
+    int t0, rows, len;
+    bool bad;
+    mine += decode_blocks(p, b, t0, rows, len, bad);
+    if (bad && blockIdx.x == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) plan[warp] = incl;
+  __syncthreads();
+  long long excl = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) excl += plan[w];
+    total += plan[w];
+  }
+  total *= p.nkv;
+  excl *= p.nkv;
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < kMinShare) share = kMinShare;
+  const long long begin = share * blockIdx.x, end = min(total, begin + share);
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (begin >= end) return;
+  if (begin >= excl && begin < excl + mine * p.nkv) {
+    long long at = begin - excl;
+    for (int b = bfirst; b < blast; ++b) {
+      int t0, rows, len;
+      bool bad;
+      const long long n = static_cast<long long>(decode_blocks(p, b, t0, rows, len, bad)) * p.nkv;
+      if (at < n) {
+        plan[4] = b;
+        plan[5] = at;
+        break;
+      }
+      at -= n;
+    }
+  }
+  __syncthreads();
+  const int count = static_cast<int>(end - begin);  // a CTA's share of fewer than 2^31 x nkv / grid blocks
+
+  // ---- the warp's producer (lane 0): blocks warp, warp + 4, ... of the range
+  const uint32_t ring = smem_u32(smem) + warp * S * 2 * TB;
+  const uint32_t bar0 = smem_u32(bars + warp * S);
+  int pb = static_cast<int>(plan[4]), pn = 0, ph, pj;
+  {
+    int t0, rows, len;
+    bool bad;
+    pn = decode_blocks(p, pb, t0, rows, len, bad);
+    ph = static_cast<int>(plan[5] / pn);
+    pj = static_cast<int>(plan[5] % pn);
+  }
+  int cb = pb, ch = ph, cj = pj;  // the consumers' place: sequence, KV head, block
+  const uint64_t pol = policy_evict_first();
+  int issued = 0;
+  const int mine_n = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
+  pj += warp;
+  auto issue = [&]() {  // lane 0: the next block of this warp into its stage
+    while (pj >= pn) {
+      pj -= pn;
+      if (++ph == p.nkv) {
+        ph = 0;
+        int t0, rows, len;
+        bool bad;
+        do pn = decode_blocks(p, ++pb, t0, rows, len, bad);
+        while (pn == 0);
+      }
+    }
+    int blk = p.block_table[static_cast<size_t>(pb) * p.max_blocks + pj];
+    if (blk < 0 || blk >= p.num_blocks) {
+      report_error(p.err, kErrGuard, kWhereBlockTable);
+      blk = 0;
+    }
+    const size_t at = (static_cast<size_t>(blk) * p.nkv + ph) * TB;
+    const int st = issued % S;
+    const uint32_t dst = ring + st * 2 * TB, bar = bar0 + 8 * st;
+    mbar_arrive_expect_tx(bar, 2 * TB);
+    bulk_load(dst, p.k_cache + at, TB, bar, pol);
+    bulk_load(dst + TB, p.v_cache + at, TB, bar, pol);
+    ++issued;
+    pj += kWarps;
+  };
+  if (lane == 0)
+    while (issued < S && issued < mine_n) issue();
+  __syncwarp();
+
+  bool ok = true;
+  int used = 0;  // blocks this warp has taken
+  int left = count;
+  int first = 0;  // index in the range of the piece's first block
+  while (left > 0) {
+    // ---- a piece: blocks cj .. of (cb, ch)
+    int t0, rows, len;
+    bool bad;
+    const int nblk = decode_blocks(p, cb, t0, rows, len, bad);
+    const int n = min(left, nblk - cj);
+    // q as the 8-column operand: lane (g, t) holds row g, elements t * D/4 ..
+    uint32_t bq[NT][D / 8];
+    float sc[NT][2];
+    int lim[NT][2];
+    int lim_lo = 0x7fffffff;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      uint4 u[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) u[i] = make_uint4(0, 0, 0, 0);
+      int pos = len - 1;
+      if (r < rows) {
+        const int tok = t0 + r / p.group;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (static_cast<size_t>(tok) * p.nq + ch * p.group + r % p.group) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) u[i] = src[i];
+        pos = p.positions[tok];
+        if (pos < 0 || pos >= len) pos = len - 1;  // such a row is not stored
+      }
+      float amax = 0.f;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -112);
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) bq[nt][i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // this lane's score columns are rows 2t and 2t + 1
+        sc[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
+        lim[nt][c] = __shfl_sync(0xffffffffu, pos, 4 * (2 * t + c));
+        lim_lo = min(lim_lo, lim[nt][c]);
+      }
+    }
+    lim_lo = min(lim_lo, __shfl_xor_sync(0xffffffffu, lim_lo, 1));
+    lim_lo = min(lim_lo, __shfl_xor_sync(0xffffffffu, lim_lo, 2));
+
+    float o[NT][MT][4], m[NT][2], base[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      m[nt][0] = m[nt][1] = kMinusInf;
+      base[nt][0] = base[nt][1] = 0.f;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    // the warp's blocks of the piece: range indices congruent to warp
+    const int skip = (warp - first) & (kWarps - 1);
+    for (int i = skip; ok && i < n; i += kWarps) {
+      const int st = used % S;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, (used / S) & 1, nullptr))) {
+        ok = false;
+        break;
+      }
+      ++used;
+      const uint32_t kt = ring + st * 2 * TB, vt = kt + TB;
+      const int key0 = (cj + i) * kQ4Block;
+      // ---- S^T = K Q^T
+      float s[NT][2][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[nt][0][c] = s[nt][1][c] = 0.f;
+      {
+        uint32_t wa[KW], wb[KW];
+        lds_words(wa, kt + lane * (4 * KW));
+        lds_words(wb, kt + 4 * D + lane * (4 * KW));
+        uint32_t sa[2], sb[2];  // scales of rows g and g + 8, doubled, for the lane's first and second 16 elements
+        if constexpr (D == 128) {
+          const uint32_t sw = lds_u32(kt + 8 * D + lane * 4);
+          const uint32_t a = e4m3x2_to_f16(sw), b = e4m3x2_to_f16(sw >> 16);
+          sa[0] = __byte_perm(a, 0, 0x1010);
+          sa[1] = __byte_perm(a, 0, 0x3232);
+          sb[0] = __byte_perm(b, 0, 0x1010);
+          sb[1] = __byte_perm(b, 0, 0x3232);
+        } else {
+          const uint32_t a = e4m3x2_to_f16(lds_u16(kt + 8 * D + lane * 2));
+          sa[0] = sa[1] = __byte_perm(a, 0, 0x1010);
+          sb[0] = sb[1] = __byte_perm(a, 0, 0x3232);
+        }
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t a[4], b[4];
+          e2m1x8_to_f16(wa[w], a);
+          e2m1x8_to_f16(wb[w], b);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            a[x] = hmul2(a[x], sa[w / 2]);
+            b[x] = hmul2(b[x], sb[w / 2]);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {  // contraction step 2w + x
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16_16816(s[nt][x], a[2 * x], b[2 * x], a[2 * x + 1], b[2 * x + 1], bq[nt][4 * w + 2 * x],
+                            bq[nt][4 * w + 2 * x + 1]);
+          }
+        }
+      }
+      // ---- weights
+      uint32_t pw[NT][2];
+      bool above = false;
+      const bool edge = key0 + kQ4Block - 1 > lim_lo;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // column c & 1 (row 2t + (c & 1)), key g + 8 (c >> 1)
+          float v = (s[nt][0][c] + s[nt][1][c]) * sc[nt][c & 1];
+          if (edge && key0 + g + 8 * (c >> 1) > lim[nt][c & 1]) v = kMinusInf;
+          s[nt][0][c] = v;
+          above |= v > m[nt][c & 1] + kMaxStep;
+        }
+      }
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float mx = fmaxf(s[nt][0][c], s[nt][0][c + 2]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float mn = fmaxf(m[nt][c], mx);
+            const float nb = mn == kMinusInf ? 0.f : mn;
+            const float a = fast_exp2(m[nt][c] - nb);
+            m[nt][c] = mn;
+            base[nt][c] = nb - kWeightBias;
+            l[nt][c] *= a;
+#pragma unroll
+            for (int i2 = 0; i2 < MT; ++i2) {
+              o[nt][i2][c] *= a;
+              o[nt][i2][c + 2] *= a;
+            }
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          e[c] = fast_exp2(s[nt][0][c] - base[nt][c & 1]);
+          l[nt][c & 1] += e[c];
+        }
+        pw[nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+        pw[nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
+      }
+      // ---- O^T += V^T P^T
+      {
+        uint32_t v0[KW], v1[KW];
+        lds_words(v0, vt + lane * (4 * KW));
+        lds_words(v1, vt + 4 * D + lane * (4 * KW));
+        const uint32_t sw = lds_u32(vt + 8 * D + ((D == 128 ? g : g >> 1) * 4 + t) * 4);
+        uint32_t s0 = e4m3x2_to_f16(sw), s1 = e4m3x2_to_f16(sw >> 16);
+        if (key0 + kQ4Block > len) {  // tokens past the sequence: their bytes may be anything
+          const int k0 = key0 + 2 * t;
+          s0 = (k0 < len ? s0 & 0xFFFFu : 0u) | (k0 + 1 < len ? s0 & 0xFFFF0000u : 0u);
+          s1 = (k0 + 8 < len ? s1 & 0xFFFFu : 0u) | (k0 + 9 < len ? s1 & 0xFFFF0000u : 0u);
+        }
+#pragma unroll
+        for (int w = 0; w < KW / 2; ++w) {
+          // bytes of two tokens' codes of one element: even elements, odd elements
+          uint32_t e0[4], d0[4], e1[4], d1[4];
+          e2m1x8_to_f16((v0[w] & 0x0F0F0F0Fu) | ((v0[w + KW / 2] << 4) & 0xF0F0F0F0u), e0);
+          e2m1x8_to_f16(((v0[w] >> 4) & 0x0F0F0F0Fu) | (v0[w + KW / 2] & 0xF0F0F0F0u), d0);
+          e2m1x8_to_f16((v1[w] & 0x0F0F0F0Fu) | ((v1[w + KW / 2] << 4) & 0xF0F0F0F0u), e1);
+          e2m1x8_to_f16(((v1[w] >> 4) & 0x0F0F0F0Fu) | (v1[w + KW / 2] & 0xF0F0F0F0u), d1);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t a0 = hmul2(e0[x], s0), a1 = hmul2(d0[x], s0), a2 = hmul2(e1[x], s1), a3 = hmul2(d1[x], s1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + x], a0, a1, a2, a3, pw[nt][0], pw[nt][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && issued < mine_n) {
+        fence_proxy_async_smem();
+        issue();
+      }
+      __syncwarp();
+    }
+
+    // ---- the warps' states of the piece, joined in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v = l[nt][c];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        const int r = nt * 8 + 2 * t + c;
+        if (g == 0) mlbuf[warp * ROWS + r] = make_float2(m[nt][c], v);
+        float* dst = obuf + (warp * ROWS + r) * D + g * W;
+#pragma unroll
+        for (int i = 0; i < MT; i += 2)
+          *reinterpret_cast<float4*>(dst + 2 * i) =
+              make_float4(o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+      }
+    }
+    __syncthreads();
+    const bool whole = cj == 0 && n == nblk;
+    const int slot = cj == 0 ? 1 : 0;  // a piece that begins here, or one continued from the CTA before
+    for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
+      const int r = idx / (D / 4), c4 = (idx % (D / 4)) * 4;
+      float M = kMinusInf;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mlbuf[w * ROWS + r].x);
+      const float mb = M == kMinusInf ? 0.f : M;
+      float L = 0.f;
+      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = mlbuf[w * ROWS + r];
+        const float f = fast_exp2(ml.x - mb);
+        const float4 x = *reinterpret_cast<const float4*>(obuf + (w * ROWS + r) * D + c4);
+        L += ml.y * f;
+        O.x += x.x * f;
+        O.y += x.y * f;
+        O.z += x.z * f;
+        O.w += x.w * f;
+      }
+      if (whole) {
+        const int tok = t0 + r / p.group;
+        const int pos = p.positions[tok];
+        if (pos < 0 || pos >= len) {
+          if (ch == 0 && c4 == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
+          continue;
+        }
+        const float inv = p.v_scale / L;
+        uint2 u;
+        u.x = pack_bf16x2(O.x * inv, O.y * inv);
+        u.y = pack_bf16x2(O.z * inv, O.w * inv);
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.nq + ch * p.group + r % p.group) * D + c4) = u;
+      } else {
+        const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + slot) * kMaxRows + r;
+        *reinterpret_cast<float4*>(p.part_o + at * D + c4) = O;
+        if (c4 == 0) p.part_ml[at] = make_float2(M, L);
+      }
+    }
+    if (threadIdx.x == 0 && cj == 0 && n < nblk)
+      p.cut[blockIdx.x] = make_int4(cb, ch, static_cast<int>((begin + first + nblk - 1) / share), 0);
+    __syncthreads();
+    left -= n;
+    first += n;
+    cj = 0;
+    if (left > 0 && ++ch == p.nkv) {
+      ch = 0;
+      int t1, r1, l1;
+      bool b1;
+      do ++cb;
+      while (decode_blocks(p, cb, t1, r1, l1, b1) == 0);
+    }
+  }
+  if (!ok) {
+    if (lane == 0) report_error(p.err, kErrTimeout, kWhereAttnDecode);
+    // let the copies still in flight land before the shared memory is given up
+    issued = __shfl_sync(0xffffffffu, issued, 0);
+    for (int i = used; i < issued; ++i) mbar_wait(bar0 + 8 * (i % S), (i / S) & 1, nullptr);
+  }
+}
+
+// Joins the pieces of every (sequence, KV head) that spans CTAs: the CTA of the
+// decode grid in which it begins, one warp per row (two when 8 rows), parts in order.
+constexpr int kCombineThreads = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) k_attn_q4_combine(const Q4Params p) {
+  pdl_wait();
+  const int4 cut = p.cut[blockIdx.x];
+  if (cut.x < 0) return;
+  const int first = blockIdx.x, parts = cut.z - first + 1;
+  int t0, rows, len;
+  bool bad;
+  decode_blocks(p, cut.x, t0, rows, len, bad);
+  const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (r >= rows) return;
+  const int tok = t0 + r / p.group;
+  const int pos = p.positions[tok];
+  if (pos < 0 || pos >= len) {
+    if (cut.y == 0 && lane == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e0 = lane * E;
-  for (int h0 = 0; h0 < p.group; h0 += kHeads) {
-    float q[kHeads][E], o[kHeads][E], m[kHeads], l[kHeads];
+  auto at = [&](int i) { return (static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kMaxRows + r; };
+  float M = kMinusInf;
+  for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[at(i)].x);
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  const float mb = M == kMinusInf ? 0.f : M;
+  constexpr int E = D / 32;
+  float L = 0.f, O[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        o[i][e] = 0.f;
-        q[i][e] = h0 + i < p.group ? __bfloat162float(p.q[(static_cast<size_t>(t) * p.nq + kvh * p.group + h0 + i) * D +
-                                                          e0 + e])
-                                   : 0.f;
-      }
+  for (int e = 0; e < E; ++e) O[e] = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < parts; ++i) {
+    const float2 ml = p.part_ml[at(i)];
+    const float* src = p.part_o + at(i) * D + lane * E;
+    float x[E];
+    if constexpr (E == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      x[0] = v.x, x[1] = v.y;
     }
-    for (int j = warp; j < n_keys; j += kWarps) {
-      int blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + j / 16];
-      if (blk < 0 || blk >= p.num_blocks) {
-        if (lane == 0) report_error(p.err, kErrGuard, kWhereBlockTable);
-        blk = 0;
-      }
-      const size_t at = (static_cast<size_t>(blk) * p.nkv + kvh) * q4_tile_bytes(D);
-      const uint8_t *kt = p.k_cache + at, *vt = p.v_cache + at;
-      const int k = j % 16;
-      float kv[E], vv[E];
-      const float ks = f16_lo(e4m3x2_to_f16(kt[q4_k_scale_at<D>(k, e0 / 16)]));
-      const float vs = f16_lo(e4m3x2_to_f16(vt[q4_v_scale_at<D>(k, e0 / 16)]));
+    const float f = fast_exp2(ml.x - mb);
+    L += ml.y * f;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        uint32_t h[4];
-        e2m1x8_to_f16(kt[k * (D / 2) + (e0 + e) / 2] | (vt[q4_v_code_at<D>(k, e0 + e)] << 8), h);
-        kv[e] = f16_lo(h[0]) * ks;
-        kv[e + 1] = f16_hi(h[0]) * ks;
-        vv[e] = f16_lo(h[1]) * vs;
-        vv[e + 1] = f16_hi(h[1]) * vs;
-      }
+    for (int e = 0; e < E; ++e) O[e] += x[e] * f;
+  }
+  const float inv = p.v_scale / L;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(
+      p.out + (static_cast<size_t>(tok) * p.nq + cut.y * p.group + r % p.group) * D + lane * E);
 #pragma unroll
-      for (int i = 0; i < kHeads; ++i) {
-        float s = 0.f;
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(O[e] * inv, O[e + 1] * inv);
+}
+
+// ---------------------------------------------------------------------------
+// longer sequences
+// ---------------------------------------------------------------------------
+struct PrefillQ4 {
+  const int32_t *qsl, *seq_lens, *block_table;
+  int T, B, max_blocks, num_blocks, nkv, group, max_query_len, max_seq_len, prefill_blocks;
+  int tile_tokens, max_items, stride;
+  int32_t* base;    // [B + 1] blocks of the copy before each sequence
+  uint32_t* items;  // the prefill kernels' work list
+  int32_t* table;   // [B, stride] block table of the copy
+  const uint8_t *k_cache, *v_cache;
+  __nv_bfloat16 *k_copy, *v_copy;  // [prefill_blocks, nkv, 16, D]
+  float k_scale, v_scale;
+  int* err;
+};
+
+// One CTA: where each prefill sequence's blocks go in the copy, and its query
+// tiles (longest causal range first within a sequence).  A sequence that is out
+// of bounds or does not fit the copy is reported and left out.
+__global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
+  __shared__ long long tot[32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto scan = [&](long long v, long long& all) {  // inclusive sum over the CTA, and the whole sum
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(q[i][e], kv[e], s);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.scale_log2;
-        const float n = fmaxf(m[i], s), a = exp2f(m[i] - n), w = exp2f(s - n);
-        m[i] = n;
-        l[i] = l[i] * a + w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[i][e] = o[i][e] * a + w * vv[e];
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      if (lane == 0) {
-        sm[warp][i] = m[i];
-        sl[warp][i] = l[i];
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) so[warp][i][e0 + e] = o[i][e];
-    }
+    if (lane == 31) tot[warp] = v;
     __syncthreads();
-    for (int x = threadIdx.x; x < kHeads * D; x += kWarps * 32) {
-      const int i = x / D, e = x % D;
-      if (h0 + i >= p.group) continue;
-      float M = -INFINITY, L = 0.f, O = 0.f;
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w][i]);
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(sm[w][i] - M);
-        L += sl[w][i] * f;
-        O += so[w][i][e] * f;
+    long long before = 0;
+    all = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += tot[w];
+      all += tot[w];
+    }
+    return before + v;
+  };
+  long long blocks_before = 0, items_before = 0, all;
+  for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
+    const int b = b0 + threadIdx.x;
+    int n = 0;
+    long long blocks = 0;
+    if (b < p.B) {
+      const int t0 = p.qsl[b];
+      n = p.qsl[b + 1] - t0;
+      if (n > 1 && (n > kMaxRows || n * p.group > kMaxRows)) {
+        const int len = p.seq_lens[b];
+        blocks = (static_cast<long long>(len) + kQ4Block - 1) / kQ4Block;
+        if (n > p.max_query_len || t0 < 0 || t0 > p.T - n || len < 1 || len > p.max_seq_len ||
+            blocks > p.max_blocks) {
+          // n > max_query_len and t0 are reported by the decode kernel, which looks at every sequence
+          if (n <= p.max_query_len) report_error(p.err, kErrGuard, kWhereQueryLen);
+          blocks = 0;
+        }
       }
-      p.out[(static_cast<size_t>(t) * p.nq + kvh * p.group + h0 + i) * D + e] = __float2bfloat16_rn(O / L * p.v_scale);
+    }
+    const long long base = blocks_before + scan(blocks, all) - blocks;
+    blocks_before += all;
+    int tiles = 0;
+    if (blocks > 0) {
+      if (base + blocks > p.prefill_blocks)
+        report_error(p.err, kErrGuard, kWhereQueryLen);
+      else
+        tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
+    }
+    if (b < p.B) p.base[b] = static_cast<int32_t>(base < p.prefill_blocks ? base : p.prefill_blocks);
+    const long long item = items_before + scan(tiles, all) - tiles;
+    items_before += all;
+    for (int j = 0; j < tiles; ++j)
+      if (item + j < p.max_items)
+        p.items[item + j] = (static_cast<uint32_t>(b) << 16) | static_cast<uint32_t>(tiles - 1 - j);
+  }
+  if (threadIdx.x == 0)
+    p.base[p.B] = static_cast<int32_t>(blocks_before < p.prefill_blocks ? blocks_before : p.prefill_blocks);
+  for (long long i = items_before + threadIdx.x; i < p.max_items; i += blockDim.x) p.items[i] = kNoPrefillItem;
+}
+
+// One CTA per block of the copy: K and V of all KV heads in bf16 (exact), zero
+// past the sequence's end, and its entry of the copy's block table.
+template <int D>
+__global__ void __launch_bounds__(256) k_q4_expand(const PrefillQ4 p) {
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x;
+  if (s >= p.base[p.B]) return;
+  int lo = 0, hi = p.B - 1;  // the last sequence with base <= s
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.base[mid] <= s) lo = mid; else hi = mid - 1;
+  }
+  const int b = lo, j = s - p.base[b], len = p.seq_lens[b];
+  if (j >= p.stride || j * kQ4Block >= len) return;
+  if (threadIdx.x == 0) p.table[static_cast<size_t>(b) * p.stride + j] = s;
+  int blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + j];
+  if (blk < 0 || blk >= p.num_blocks) {
+    if (threadIdx.x == 0) report_error(p.err, kErrGuard, kWhereBlockTable);
+    blk = 0;
+  }
+  constexpr int GR = D / kQ4Group;
+  const int half = p.nkv * kQ4Block * GR;
+  for (int i = threadIdx.x; i < 2 * half; i += blockDim.x) {
+    const bool is_v = i >= half;
+    const int x = is_v ? i - half : i;
+    const int grp = x % GR, k = (x / GR) % kQ4Block, h = x / (GR * kQ4Block);
+    const uint8_t* tile = (is_v ? p.v_cache : p.k_cache) + (static_cast<size_t>(blk) * p.nkv + h) * q4_tile_bytes(D);
+    uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (j * kQ4Block + k < len) {
+      uint32_t code[2], s8;
+      if (!is_v) {
+        const uint2 c = *reinterpret_cast<const uint2*>(tile + k * (D / 2) + grp * 8);
+        code[0] = c.x;
+        code[1] = c.y;
+        s8 = tile[q4_k_scale_at<D>(k, grp)];
+      } else {
+        code[0] = *reinterpret_cast<const uint32_t*>(tile + q4_v_code_at<D>(k, grp * 16));
+        code[1] = *reinterpret_cast<const uint32_t*>(tile + q4_v_code_at<D>(k, grp * 16 + 8));
+        s8 = tile[q4_v_scale_at<D>(k, grp)];
+      }
+      const float m = f16_lo(e4m3x2_to_f16(s8)) * (is_v ? p.v_scale : p.k_scale);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[4];
+        e2m1x8_to_f16(code[c], v);
+        u[c].x = pack_bf16x2(f16_lo(v[0]) * m, f16_hi(v[0]) * m);
+        u[c].y = pack_bf16x2(f16_lo(v[1]) * m, f16_hi(v[1]) * m);
+        u[c].z = pack_bf16x2(f16_lo(v[2]) * m, f16_hi(v[2]) * m);
+        u[c].w = pack_bf16x2(f16_lo(v[3]) * m, f16_hi(v[3]) * m);
+      }
+    }
+    __nv_bfloat16* dst = is_v ? p.v_copy : p.k_copy;
+    uint4* d4 = reinterpret_cast<uint4*>(dst + ((static_cast<size_t>(s) * p.nkv + h) * kQ4Block + k) * D + grp * 16);
+    d4[0] = u[0];
+    d4[1] = u[1];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <int D, int NT>
+size_t decode_smem() {
+  constexpr int S = stages<D>(), ROWS = 8 * NT;
+  return static_cast<size_t>(kWarps) * S * 2 * q4_tile_bytes(D) + kWarps * ROWS * D * 4 + kWarps * ROWS * 8 +
+         kWarps * S * 8 + 8 * 8;
+}
+
+struct Layout {
+  size_t part_o, part_ml, cut, base, items, table, k_copy, v_copy, total;
+  int grid, max_items, stride;
+};
+
+Layout layout(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int head_dim) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  Layout L{};
+  L.grid = num_sms() * kCtasPerSm;
+  L.max_items = (T + 7) / 8 + B;
+  L.stride = (max_seq_len + kQ4Block - 1) / kQ4Block;
+  const size_t rows = static_cast<size_t>(L.grid) * 2 * kMaxRows;
+  size_t off = 0;
+  L.part_o = off;
+  off += up(rows * head_dim * sizeof(float));
+  L.part_ml = off;
+  off += up(rows * sizeof(float2));
+  L.cut = off;
+  off += up(static_cast<size_t>(L.grid) * sizeof(int4));
+  if (prefill_blocks > 0) {
+    const size_t copy = up(static_cast<size_t>(prefill_blocks) * nkv * kQ4Block * head_dim * 2);
+    L.table = off;
+    off += up(static_cast<size_t>(B) * L.stride * 4);
+    L.k_copy = off;
+    off += copy;
+    L.v_copy = off;
+    off += copy;
+  }
+  L.base = off;
+  off += up((static_cast<size_t>(B) + 1) * 4);
+  L.items = off;
+  off += up(static_cast<size_t>(L.max_items) * 4);
+  L.total = off;
+  return L;
+}
+
+template <int D, int NT>
+int launch_decode(const Q4Params& p, int grid, bool pdl, cudaStream_t s) {
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(k_attn_q4_decode<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(decode_smem<D, NT>()));
+  });
+  if (attr != cudaSuccess) return attr;
+  cudaError_t e = launch_kernel(k_attn_q4_decode<D, NT>, dim3(grid), dim3(kThreads), decode_smem<D, NT>(), s, pdl, p);
+  if (e == cudaSuccess) e = launch_kernel(k_attn_q4_combine<D>, dim3(grid), dim3(kCombineThreads), 0, s, true, p);
+  return e;
+}
+
+template <int D>
+int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStream_t s) {
+  const AttnArgs& a = q4.a;
+  const int mq = a.max_query_len;
+  const bool long_seqs = mq > 1 && (mq > kMaxRows || mq * p.group > kMaxRows);
+  int e = 0;
+  bool pdl = false;
+  if (long_seqs) {
+    PrefillQ4 f{};
+    f.qsl = a.qsl;
+    f.seq_lens = a.seq_lens;
+    f.block_table = a.block_table;
+    f.T = a.T;
+    f.B = a.B;
+    f.max_query_len = mq;
+    f.max_blocks = a.max_blocks;
+    f.num_blocks = a.num_blocks;
+    f.nkv = a.nkv;
+    f.group = p.group;
+    f.max_seq_len = a.max_seq_len;
+    f.prefill_blocks = q4.prefill_blocks;
+    f.tile_tokens = prefill_tile_tokens(a);
+    f.max_items = (a.T + f.tile_tokens - 1) / f.tile_tokens + a.B;
+    f.stride = L.stride;
+    f.base = reinterpret_cast<int32_t*>(q4.ws + L.base);
+    f.items = reinterpret_cast<uint32_t*>(q4.ws + L.items);
+    f.table = reinterpret_cast<int32_t*>(q4.ws + L.table);
+    f.k_cache = p.k_cache;
+    f.v_cache = p.v_cache;
+    f.k_copy = reinterpret_cast<__nv_bfloat16*>(q4.ws + L.k_copy);
+    f.v_copy = reinterpret_cast<__nv_bfloat16*>(q4.ws + L.v_copy);
+    f.k_scale = q4.k_scale;
+    f.v_scale = q4.v_scale;
+    f.err = a.err;
+    if ((e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(1024), 0, s, pdl, f))) return e;
+    pdl = true;
+    if (q4.prefill_blocks > 0) {
+      if ((e = launch_kernel(k_q4_expand<D>, dim3(q4.prefill_blocks), dim3(256), 0, s, true, f))) return e;
+      AttnArgs c = a;
+      c.k_cache = f.k_copy;
+      c.v_cache = f.v_copy;
+      c.block_table = f.table;
+      c.max_blocks = L.stride;
+      c.num_blocks = q4.prefill_blocks;
+      if ((e = prefill_items_launch(c, f.items, f.max_items, true, s))) return e;
     }
   }
+  // rows a sequence of the decode path may have
+  const int toks = mq > 1 ? min(mq, kMaxRows / p.group > 1 ? kMaxRows / p.group : 1) : 1;
+  const long long bound = static_cast<long long>(a.B) * a.nkv * L.stride;
+  const long long want = (bound + kMinShare - 1) / kMinShare;
+  if (toks * p.group <= 8) {
+    const int full = num_sms() * kCtasPerSm;
+    return launch_decode<D, 1>(p, want < full ? static_cast<int>(want) : full, pdl, s);
+  }
+  const int full = num_sms() * 3;
+  return launch_decode<D, 2>(p, want < full ? static_cast<int>(want) : full, pdl, s);
 }
 
 }  // namespace
 
-size_t attn_q4_workspace_bytes(int, int, int, int, int, int, int) { return 256; }
+size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int, int nkv, int head_dim) {
+  return layout(T, B, max_seq_len, prefill_blocks, nkv, head_dim).total;
+}
 
 int attention_q4_launch(const AttnQ4Args& q4, cudaStream_t s) {
   const AttnArgs& a = q4.a;
   if (a.T <= 0 || a.B <= 0) return 0;
+  const Layout L = layout(a.T, a.B, a.max_seq_len, q4.prefill_blocks, a.nkv, a.head_dim);
   Q4Params p{};
   p.q = static_cast<const __nv_bfloat16*>(a.q);
   p.out = static_cast<__nv_bfloat16*>(a.out);
@@ -143,6 +850,7 @@ int attention_q4_launch(const AttnQ4Args& q4, cudaStream_t s) {
   p.block_table = a.block_table;
   p.T = a.T;
   p.B = a.B;
+  p.max_query_len = a.max_query_len;
   p.max_blocks = a.max_blocks;
   p.num_blocks = a.num_blocks;
   p.nq = a.nq;
@@ -151,10 +859,11 @@ int attention_q4_launch(const AttnQ4Args& q4, cudaStream_t s) {
   p.max_seq_len = a.max_seq_len;
   p.scale_log2 = kLog2e / sqrtf(static_cast<float>(a.head_dim)) * q4.k_scale;
   p.v_scale = q4.v_scale;
+  p.part_o = reinterpret_cast<float*>(q4.ws + L.part_o);
+  p.part_ml = reinterpret_cast<float2*>(q4.ws + L.part_ml);
+  p.cut = reinterpret_cast<int4*>(q4.ws + L.cut);
   p.err = a.err;
-  const dim3 grid(a.T, a.nkv);
-  if (a.head_dim == 128) return launch_kernel(k_attn_q4<128>, grid, dim3(kWarps * 32), 0, s, false, p);
-  return launch_kernel(k_attn_q4<64>, grid, dim3(kWarps * 32), 0, s, false, p);
+  return a.head_dim == 128 ? launch_d<128>(q4, p, L, s) : launch_d<64>(q4, p, L, s);
 }
 
 }  // namespace llama

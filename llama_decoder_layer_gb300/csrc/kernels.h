@@ -170,6 +170,13 @@ struct AttnQ4Args {
 size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int nq, int nkv, int head_dim);
 int attention_q4_launch(const AttnQ4Args& a, cudaStream_t s);
 
+// The prefill kernels alone, over a work list of (sequence << 16 | query tile)
+// entries on the device, kNoPrefillItem past the end, tiles of
+// prefill_tile_tokens(a) tokens.
+constexpr uint32_t kNoPrefillItem = 0xFFFFFFFFu;
+int prefill_tile_tokens(const AttnArgs& a);
+int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int n_items, bool pdl, cudaStream_t s);
+
 // Sparse MoE block: workspace layout (byte offsets from a 256-aligned base)
 // and the launch sequence.
 struct MoeLayout {

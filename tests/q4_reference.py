@@ -87,10 +87,10 @@ def cache_rows(tiles, slots, d, is_v, g):
 
 
 def attention(q, positions, qsl, block_table, k_tiles, v_tiles, kg, vg):
-    """q [T, nq, d] fp64 -> (out [T, nq, d], sum p |v| [T, nq, d])."""
+    """q [T, nq, d] fp64 -> (out, sum p |v|, sum |v| over the keys seen), [T, nq, d] each."""
     T, nq, d = q.shape
     nkv = k_tiles.shape[1]
-    out, spread = np.zeros(q.shape), np.zeros(q.shape)
+    out, spread, flat = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
     for b in range(len(qsl) - 1):
         if qsl[b + 1] == qsl[b]:
             continue
@@ -104,7 +104,8 @@ def attention(q, positions, qsl, block_table, k_tiles, v_tiles, kg, vg):
         p = torch.softmax(torch.where(seen[:, None], s, -math.inf), -1)
         out[qsl[b]:qsl[b + 1]] = torch.einsum("thj,jhd->thd", p, v).numpy()
         spread[qsl[b]:qsl[b + 1]] = torch.einsum("thj,jhd->thd", p, v.abs()).numpy()
-    return out, spread
+        flat[qsl[b]:qsl[b + 1]] = torch.einsum("tj,jhd->thd", seen.double(), v.abs()).numpy()
+    return out, spread, flat
 
 
 def frequencies(rot, theta, scaling):

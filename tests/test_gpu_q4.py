@@ -10,6 +10,11 @@ Tolerances.  A bf16 result is rounded once: 2^-8 of its size (half a step).
   stored as fp16, 2^-8 as bf16 (a prompt's path), and the scores' fp32 error, at
   most 2^-12 for |score| < 2^9 with sums of 128 products, so the result is off
   by at most 2^-8 |o| + 2 (eps_p + 2^-12) sum p |v| (numerator and denominator).
+  fp16 weights are stored as 2^(s - m + 6), m a maximum that is never above the
+  largest score s_max: the largest weight is at least 2^6, and one below fp16's
+  normal range is off by up to half its smallest number, 2^-25, which is 2^-31 of
+  the largest.  The largest, normalised, is at most 1, so this adds at most 2^-31
+  sum |v| over the keys seen.
 """
 
 import numpy as np
@@ -265,12 +270,12 @@ class Case:
     def check(self, out=None):
         T = int(self.qsl[-1])
         got = f64(self.out if out is None else out).reshape(-1, self.nq, self.d)
-        want, spread = R.attention(f64(self.q)[:T], self.pos, self.qsl, self.table, self.tiles[0], self.tiles[1],
+        want, spread, flat = R.attention(f64(self.q)[:T], self.pos, self.qsl, self.table, self.tiles[0], self.tiles[1],
                                    self.kg, self.vg)
         new = np.concatenate([np.full(n, n) for n, _ in self.seqs])
         eps_p = np.where((new > 1) & (new * (self.nq // self.nkv) > 16), 2.0 ** -8, 2.0 ** -11)[:, None, None]
         err = np.abs(got[:T] - want)
-        tol = 2.0 ** -8 * np.abs(want) + 2 * (eps_p + 2.0 ** -12) * spread
+        tol = 2.0 ** -8 * np.abs(want) + 2 * (eps_p + 2.0 ** -12) * spread + 2.0 ** -31 * flat
         bad = ~(err <= tol)
         assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3].tolist(), float(np.nanmax(err)))
         assert np.all(got[T:] == 5.0)  # rows behind the last sequence
@@ -370,6 +375,16 @@ def test_bad_positions_lengths_and_blocks_are_reported():
                 f64(c.q), c.pos, c.qsl, c.table, c.tiles[0], c.tiles[1], 1.0, 1.0)[0]
             rest = np.r_[0:c.qsl[1], c.qsl[2]:c.qsl[3]]
             assert np.abs(got[rest] - want[rest]).max() < 0.05 * np.abs(want).max(), (new, what)
+
+
+def test_too_few_prefill_blocks_are_reported():
+    c = Case([(1, 40), (50, 60), (20, 100)], 8, 2, 128, seed=12)
+    c.run(pre=4)  # room for the first prompt (4 blocks), not for the second (7)
+    guard()
+    got = f64(c.out).reshape(-1, 8, 128)
+    want, spread, _ = R.attention(f64(c.q), c.pos, c.qsl, c.table, c.tiles[0], c.tiles[1], 1.0, 1.0)
+    assert np.all(np.abs(got - want)[:51] <= 2.0 ** -8 * np.abs(want[:51]) + 2.0 ** -6 * spread[:51])
+    assert np.all(got[51:] == 5.0)
 
 
 def test_same_result_on_every_run_and_on_another_stream():
@@ -472,6 +487,6 @@ def test_prompt_then_tokens_through_all_of_them(nq, nkv, d):
         R.pack_rows(tiles[0], slots.tolist(), *R.quantise(f64(k), kg), d, False)
         R.pack_rows(tiles[1], slots.tolist(), *R.quantise(f64(v), vg), d, True)
         assert np.array_equal(kc.cpu().numpy(), tiles[0]) and np.array_equal(vc.cpu().numpy(), tiles[1])
-        want, spread = R.attention(f64(qd), pos.tolist(), qsl.tolist(), table.tolist(), tiles[0], tiles[1], kg, vg)
+        want, spread, flat = R.attention(f64(qd), pos.tolist(), qsl.tolist(), table.tolist(), tiles[0], tiles[1], kg, vg)
         err = np.abs(f64(out).reshape(T, nq, d) - want)
-        assert np.all(err <= 2.0 ** -8 * np.abs(want) + 2 * (2.0 ** -8 + 2.0 ** -12) * spread)
+        assert np.all(err <= 2.0 ** -8 * np.abs(want) + 2 * (2.0 ** -8 + 2.0 ** -12) * spread + 2.0 ** -31 * flat)
