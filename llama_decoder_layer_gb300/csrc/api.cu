@@ -654,6 +654,9 @@ int llama_paged_attention_q4(const LlamaLayerConfig* cfg, const LlamaBatch* batc
   if (!q || !k_cache || !v_cache || !out) return LLAMA_ERR_ARG;
   if (!a16(q) || !a16(k_cache) || !a16(v_cache) || !a16(out)) return LLAMA_ERR_UNSUPPORTED;
   if (static_cast<long long>(prefill_blocks) * cfg->n_kv_heads * cfg->block_size > 0x7fffffffLL) return LLAMA_ERR_ARG;
+  // a sequence's (KV head, block) pairs are counted in 32 bits on the device
+  if ((static_cast<long long>(batch->max_seq_len) / cfg->block_size + 16) * cfg->n_kv_heads > 0x7fffffffLL)
+    return LLAMA_ERR_UNSUPPORTED;
   const size_t need = attn_q4_workspace_bytes(batch->num_tokens, batch->num_seqs, batch->max_seq_len, prefill_blocks,
                                               cfg->n_heads, cfg->n_kv_heads, cfg->head_dim);
   if (workspace == nullptr || workspace_bytes < need + 256) return LLAMA_ERR_WORKSPACE;

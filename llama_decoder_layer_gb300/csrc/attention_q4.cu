@@ -32,6 +32,7 @@
 #include <math.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -48,12 +49,13 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 16;        // query rows (new tokens x group) of the decode path
 constexpr int kCtasPerSm = 4;
 constexpr int kMinShare = 8;        // blocks a CTA takes at least: two a warp
+constexpr int kPieceCost = 4;       // what a (sequence, KV head) costs a CTA beside its blocks, in blocks
 constexpr float kMaxStep = 8.f;     // log2 by which a score may pass the running maximum
 constexpr float kWeightBias = 6.f;  // weights are stored times 2^6
 constexpr float kMinusInf = -INFINITY;
 
 template <int D>
-constexpr int stages() { return D == 128 ? 4 : 6; }
+constexpr int stages() { return D == 128 ? 4 : 8; }  // a power of two
 
 struct Q4Params {
   const __nv_bfloat16* q;
@@ -82,6 +84,12 @@ __device__ __forceinline__ int decode_blocks(const Q4Params& p, int b, int& t0, 
   return bad ? 0 : nblk;
 }
 
+__device__ __forceinline__ int plan_blocks(const Q4Params& p, int b) {
+  int t0, rows, len;
+  bool bad;
+  return decode_blocks(p, b, t0, rows, len, bad);
+}
+
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -102,6 +110,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+// bits of a where mask has ones, of b where it has zeros
+template <uint32_t kMask>
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(d) : "r"(a), "r"(b), "n"(kMask));
+  return d;
+}
+
+// a value that is the same in every lane, in a form the compiler can keep once per warp
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
   static_assert(N == 2 || N == 4, "8 or 16 bytes");
@@ -117,11 +136,30 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-  return v;
+// A lane's asynchronous copy of N bytes (4, 8 or 16) into its own shared memory.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// all but the newest N groups of this lane have landed
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where a CTA's range begins or ends.
+struct Place {
+  long long blocks;  // blocks before it
+  long long unit;    // first unit of its piece
+  int b, h, j;       // sequence, KV head, block
+  int nblk;          // blocks of the sequence
+};
 
 // NT: 8-row tiles of query rows (the rows of a sequence: new token r / group, head r % group)
 template <int D, int NT>
@@ -132,29 +170,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
   constexpr int MT = D / 16;   // 16-element tiles of the head
   constexpr int W = D / 8;     // head elements a lane holds of O
   constexpr int ROWS = 8 * NT;
+  // a stage of a warp's ring: K codes of keys 0-7, 8-15, V codes of the same,
+  // K scales, V scales, each a run of the lanes' own bytes
+  constexpr int CB = 32 * 4 * KW, STB = 4 * CB + 2 * 128;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* obuf = reinterpret_cast<float*>(smem + kWarps * S * 2 * TB);        // [warp][ROWS][D]
-  float2* mlbuf = reinterpret_cast<float2*>(obuf + kWarps * ROWS * D);       // [warp][ROWS]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(mlbuf + kWarps * ROWS);       // [warp][S]
-  long long* plan = reinterpret_cast<long long*>(bars + kWarps * S);         // [8]
+  float* obuf = reinterpret_cast<float*>(smem + kWarps * S * STB);      // [warp][ROWS][D]
+  float2* mlbuf = reinterpret_cast<float2*>(obuf + kWarps * ROWS * D);  // [warp][ROWS]
+  __shared__ long long sums[kWarps];
+  __shared__ Place range[2];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kWarps * S; ++i) mbar_init(smem_u32(bars + i), 1);
-    fence_mbar_init();
-  }
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_trigger();
 
-  // ---- the CTA's range of blocks: exclusive sums of the sequences' blocks, a
-  // run of sequences per thread
+  // ---- the CTA's range: exclusive sums of the sequences' blocks (and their
+  // number, in the low 17 bits: at most 65535), a run of sequences per thread.  A
+  // piece (sequence, KV head) counts kPieceCost units before those of its blocks.
   const int per = (p.B + kThreads - 1) / kThreads;
   const int bfirst = min(p.B, static_cast<int>(threadIdx.x) * per), blast = min(p.B, bfirst + per);
   long long mine = 0;
   for (int b = bfirst; b < blast; ++b) {
     int t0, rows, len;
     bool bad;
-    mine += decode_blocks(p, b, t0, rows, len, bad);
+    const int n = decode_blocks(p, b, t0, rows, len, bad);
+    if (n > 0) mine += (static_cast<long long>(n) << 17) + 1;
     if (bad && blockIdx.x == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
   }
   long long incl = mine;
@@ -163,175 +202,200 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     const long long v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) plan[warp] = incl;
+  if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  long long excl = incl - mine, total = 0;
+  long long excl = incl - mine, all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) excl += plan[w];
-    total += plan[w];
+    if (w < warp) excl += sums[w];
+    all += sums[w];
   }
-  total *= p.nkv;
-  excl *= p.nkv;
-  long long share = (total + gridDim.x - 1) / gridDim.x;
+  auto units_of = [&](long long v) { return ((v >> 17) + kPieceCost * (v & 0x1FFFF)) * p.nkv; };
+  const long long total = units_of(all);
+  long long share = total < 0x7fffffffLL ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x
+                                         : (total + gridDim.x - 1) / gridDim.x;
   if (share < kMinShare) share = kMinShare;
   const long long begin = share * blockIdx.x, end = min(total, begin + share);
   if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (begin >= end) return;
-  if (begin >= excl && begin < excl + mine * p.nkv) {
-    long long at = begin - excl;
-    for (int b = bfirst; b < blast; ++b) {
-      int t0, rows, len;
-      bool bad;
-      const long long n = static_cast<long long>(decode_blocks(p, b, t0, rows, len, bad)) * p.nkv;
-      if (at < n) {
-        plan[4] = b;
-        plan[5] = at;
-        break;
+  {
+    const long long first_unit = units_of(excl), last_unit = first_unit + units_of(mine);
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const long long at = which == 0 ? begin : end - 1;  // the end by its last unit
+      if (at < first_unit || at >= last_unit) continue;
+      long long unit = first_unit, blocks = (excl >> 17) * p.nkv;
+      for (int b = bfirst; b < blast; ++b) {
+        const int n = per == 1 ? static_cast<int>(mine >> 17) : plan_blocks(p, b);
+        if (n == 0) continue;
+        const long long units = static_cast<long long>(n + kPieceCost) * p.nkv;
+        if (at < unit + units) {
+          Place x;
+          x.b = b;
+          x.nblk = n;
+          x.h = static_cast<int>(static_cast<uint32_t>(at - unit) / static_cast<uint32_t>(n + kPieceCost));
+          x.unit = unit + static_cast<long long>(x.h) * (n + kPieceCost);
+          // blocks before unit `at` (for the end: before the unit after it)
+          x.j = max(0, static_cast<int>(at - x.unit) + which - kPieceCost);
+          x.blocks = blocks + static_cast<long long>(x.h) * n + x.j;
+          range[which] = x;
+          break;
+        }
+        unit += units;
+        blocks += static_cast<long long>(n) * p.nkv;
       }
-      at -= n;
     }
   }
   __syncthreads();
-  const int count = static_cast<int>(end - begin);  // a CTA's share of fewer than 2^31 x nkv / grid blocks
+  const int count = uniform(static_cast<int>(range[1].blocks - range[0].blocks));
+  if (count <= 0) return;
 
-  // ---- the warp's producer (lane 0): blocks warp, warp + 4, ... of the range
-  const uint32_t ring = smem_u32(smem) + warp * S * 2 * TB;
-  const uint32_t bar0 = smem_u32(bars + warp * S);
-  int pb = static_cast<int>(plan[4]), pn = 0, ph, pj;
-  {
-    int t0, rows, len;
-    bool bad;
-    pn = decode_blocks(p, pb, t0, rows, len, bad);
-    ph = static_cast<int>(plan[5] / pn);
-    pj = static_cast<int>(plan[5] % pn);
-  }
-  int cb = pb, ch = ph, cj = pj;  // the consumers' place: sequence, KV head, block
-  const uint64_t pol = policy_evict_first();
-  int issued = 0;
+  // ---- the warp's blocks: warp, warp + 4, ... of the range.  Lane i looks up
+  // the tiles of blocks i, 32 + i, ... of those, 32 at once.
+  int cb = uniform(range[0].b), ch = uniform(range[0].h), cj = uniform(range[0].j);
+  long long unit = range[0].unit;
+  const uint32_t ring = smem_u32(smem) + warp * S * STB;
   const int mine_n = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
-  pj += warp;
-  auto issue = [&]() {  // lane 0: the next block of this warp into its stage
-    while (pj >= pn) {
-      pj -= pn;
-      if (++ph == p.nkv) {
-        ph = 0;
-        int t0, rows, len;
-        bool bad;
-        do pn = decode_blocks(p, ++pb, t0, rows, len, bad);
+  int issued = 0;
+  int pb = cb, pn = range[0].nblk, tile = 0;
+  uint32_t px = static_cast<uint32_t>(ch) * pn + cj + warp + kWarps * lane;  // block within sequence pb, over its heads
+  auto look_up = [&]() {
+    if (issued + lane < mine_n) {
+      while (px >= static_cast<uint32_t>(pn) * p.nkv) {
+        px -= static_cast<uint32_t>(pn) * p.nkv;
+        do pn = plan_blocks(p, ++pb);
         while (pn == 0);
       }
+      const uint32_t h = px / pn, jb = px - h * pn;
+      int blk = p.block_table[static_cast<size_t>(pb) * p.max_blocks + jb];
+      if (blk < 0 || blk >= p.num_blocks) {
+        report_error(p.err, kErrGuard, kWhereBlockTable);
+        blk = 0;
+      }
+      tile = blk * p.nkv + h;
+      px += kWarps * 32;
     }
-    int blk = p.block_table[static_cast<size_t>(pb) * p.max_blocks + pj];
-    if (blk < 0 || blk >= p.num_blocks) {
-      report_error(p.err, kErrGuard, kWhereBlockTable);
-      blk = 0;
-    }
-    const size_t at = (static_cast<size_t>(blk) * p.nkv + ph) * TB;
-    const int st = issued % S;
-    const uint32_t dst = ring + st * 2 * TB, bar = bar0 + 8 * st;
-    mbar_arrive_expect_tx(bar, 2 * TB);
-    bulk_load(dst, p.k_cache + at, TB, bar, pol);
-    bulk_load(dst + TB, p.v_cache + at, TB, bar, pol);
-    ++issued;
-    pj += kWarps;
+    __syncwarp();
   };
-  if (lane == 0)
-    while (issued < S && issued < mine_n) issue();
-  __syncwarp();
+  // the next block's copies: every lane fetches the bytes it will use
+  const uint8_t* const k_lane = p.k_cache + lane * (4 * KW);
+  const uint8_t* const v_lane = p.v_cache + lane * (4 * KW);
+  const uint8_t* const ks_lane = p.k_cache + 8 * D + (D == 128 ? lane * 4 : (lane >> 1) * 4);
+  const uint8_t* const vs_lane = p.v_cache + 8 * D + ((D == 128 ? g : g >> 1) * 4 + t) * 4;
+  const uint32_t ring_c = ring + lane * (4 * KW), ring_s = ring + 4 * CB + lane * 4;
+  auto issue = [&]() {
+    if (issued < mine_n) {
+      if (issued % 32 == 0) look_up();
+      const size_t at = static_cast<size_t>(__shfl_sync(0xffffffffu, tile, issued % 32)) * TB;
+      const uint32_t st = (issued % S) * STB;
+      copy_async<4 * KW>(ring_c + st, k_lane + at);
+      copy_async<4 * KW>(ring_c + st + CB, k_lane + at + 4 * D);
+      copy_async<4>(ring_s + st, ks_lane + at);
+      copy_async<4 * KW>(ring_c + st + 2 * CB, v_lane + at);
+      copy_async<4 * KW>(ring_c + st + 3 * CB, v_lane + at + 4 * D);
+      copy_async<4>(ring_s + st + 128, vs_lane + at);
+    }
+    ++issued;
+    copy_commit();
+  };
 
-  bool ok = true;
-  int used = 0;  // blocks this warp has taken
-  int left = count;
-  int first = 0;  // index in the range of the piece's first block
-  while (left > 0) {
-    // ---- a piece: blocks cj .. of (cb, ch)
-    int t0, rows, len;
+  // ---- pieces: blocks cj .. of (cb, ch)
+  int t0, rows, len, nblk;
+  uint4 qu[NT][D / 32];  // row nt * 8 + g, elements t * D/4 ..
+  int qpos[NT];
+  auto load_q = [&]() {
     bool bad;
-    const int nblk = decode_blocks(p, cb, t0, rows, len, bad);
-    const int n = min(left, nblk - cj);
-    // q as the 8-column operand: lane (g, t) holds row g, elements t * D/4 ..
-    uint32_t bq[NT][D / 8];
-    float sc[NT][2];
-    int lim[NT][2];
-    int lim_lo = 0x7fffffff;
+    nblk = uniform(decode_blocks(p, cb, t0, rows, len, bad));
+    len = uniform(len);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g;
-      uint4 u[D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) u[i] = make_uint4(0, 0, 0, 0);
-      int pos = len - 1;
+      for (int i = 0; i < D / 32; ++i) qu[nt][i] = make_uint4(0, 0, 0, 0);
+      qpos[nt] = len - 1;
       if (r < rows) {
         const int tok = t0 + r / p.group;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (static_cast<size_t>(tok) * p.nq + ch * p.group + r % p.group) * D + t * (D / 4));
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) u[i] = src[i];
-        pos = p.positions[tok];
-        if (pos < 0 || pos >= len) pos = len - 1;  // such a row is not stored
+        for (int i = 0; i < D / 32; ++i) qu[nt][i] = src[i];
+        qpos[nt] = p.positions[tok];
       }
+    }
+  };
+  if (NT == 1) load_q();  // before the ring is filled: behind those copies it would wait for all of them
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) issue();
+  int used = 0;  // blocks this warp has taken
+  int left = count;
+  int first = 0;  // index in the range of the piece's first block
+  while (left > 0) {
+    if (NT > 1) load_q();
+    const int n = min(left, nblk - cj);
+    // q as the 8-column operand
+    uint32_t bq[NT][D / 8];
+    float sc[NT][2];
+    int lim_lo = 0x7fffffff;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (qpos[nt] < 0 || qpos[nt] >= len) qpos[nt] = len - 1;  // such a row is not stored
+      lim_lo = min(lim_lo, qpos[nt]);
       float amax = 0.f;
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(qu[nt]);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
       const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -112);
       const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2;
+      // (at least 2^-124: smaller ones give scores below 2^-60 either way)
+      const float down =
+          fmaxf(__uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2, 4.70197740e-38f);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) bq[nt][i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {  // this lane's score columns are rows 2t and 2t + 1
         sc[nt][c] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
-        lim[nt][c] = __shfl_sync(0xffffffffu, pos, 4 * (2 * t + c));
-        lim_lo = min(lim_lo, lim[nt][c]);
       }
     }
-    lim_lo = min(lim_lo, __shfl_xor_sync(0xffffffffu, lim_lo, 1));
-    lim_lo = min(lim_lo, __shfl_xor_sync(0xffffffffu, lim_lo, 2));
+    lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
 
-    float o[NT][MT][4], m[NT][2], base[NT][2], l[NT][2];
+    // thr: the unscaled score that moves the maximum, base: what is subtracted
+    // from the scaled ones (the maximum less the weights' 2^6)
+    float o[NT][MT][4], thr[NT][2], base[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-      m[nt][0] = m[nt][1] = kMinusInf;
+      thr[nt][0] = thr[nt][1] = kMinusInf;
       base[nt][0] = base[nt][1] = 0.f;
       l[nt][0] = l[nt][1] = 0.f;
     }
-    // the warp's blocks of the piece: range indices congruent to warp
-    const int skip = (warp - first) & (kWarps - 1);
-    for (int i = skip; ok && i < n; i += kWarps) {
-      const int st = used % S;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar0 + 8 * st, (used / S) & 1, nullptr))) {
-        ok = false;
-        break;
-      }
-      ++used;
-      const uint32_t kt = ring + st * 2 * TB, vt = kt + TB;
-      const int key0 = (cj + i) * kQ4Block;
+
+    // N blocks of the piece, from its block i on (i, i + 4, ..)
+    auto step = [&](int i, auto blocks) {
+      constexpr int N = decltype(blocks)::value;
+      float s[N][NT][4];
+      copy_wait<S - N>();
       // ---- S^T = K Q^T
-      float s[NT][2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < N; ++x) {
+        const uint32_t st = ((used + x) % S) * STB;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[nt][0][c] = s[nt][1][c] = 0.f;
-      {
+        for (int nt = 0; nt < NT; ++nt) s[x][nt][0] = s[x][nt][1] = s[x][nt][2] = s[x][nt][3] = 0.f;
         uint32_t wa[KW], wb[KW];
-        lds_words(wa, kt + lane * (4 * KW));
-        lds_words(wb, kt + 4 * D + lane * (4 * KW));
+        lds_words(wa, ring_c + st);
+        lds_words(wb, ring_c + st + CB);
+        const uint32_t sw = lds_u32(ring_s + st);
         uint32_t sa[2], sb[2];  // scales of rows g and g + 8, doubled, for the lane's first and second 16 elements
         if constexpr (D == 128) {
-          const uint32_t sw = lds_u32(kt + 8 * D + lane * 4);
           const uint32_t a = e4m3x2_to_f16(sw), b = e4m3x2_to_f16(sw >> 16);
           sa[0] = __byte_perm(a, 0, 0x1010);
           sa[1] = __byte_perm(a, 0, 0x3232);
           sb[0] = __byte_perm(b, 0, 0x1010);
           sb[1] = __byte_perm(b, 0, 0x3232);
         } else {
-          const uint32_t a = e4m3x2_to_f16(lds_u16(kt + 8 * D + lane * 2));
+          const uint32_t a = e4m3x2_to_f16(sw >> (16 * (lane & 1)));
           sa[0] = sa[1] = __byte_perm(a, 0, 0x1010);
           sb[0] = sb[1] = __byte_perm(a, 0, 0x3232);
         }
@@ -341,100 +405,120 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
           e2m1x8_to_f16(wa[w], a);
           e2m1x8_to_f16(wb[w], b);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            a[x] = hmul2(a[x], sa[w / 2]);
-            b[x] = hmul2(b[x], sb[w / 2]);
+          for (int y = 0; y < 4; ++y) {
+            a[y] = hmul2(a[y], sa[w / 2]);
+            b[y] = hmul2(b[y], sb[w / 2]);
           }
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {  // contraction step 2w + x
+          for (int y = 0; y < 2; ++y)  // contraction step 2w + y
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(s[nt][x], a[2 * x], b[2 * x], a[2 * x + 1], b[2 * x + 1], bq[nt][4 * w + 2 * x],
-                            bq[nt][4 * w + 2 * x + 1]);
-          }
+              mma_f16_16816(s[x][nt], a[2 * y], b[2 * y], a[2 * y + 1], b[2 * y + 1], bq[nt][4 * w + 2 * y],
+                            bq[nt][4 * w + 2 * y + 1]);
         }
       }
-      // ---- weights
-      uint32_t pw[NT][2];
+      // ---- weights: score c of a tile is column c & 1 (row 2t + (c & 1)), key g + 8 (c >> 1)
+      const int key0 = (cj + i) * kQ4Block;
+      if (key0 + (N - 1) * kWarps * kQ4Block + kQ4Block - 1 > lim_lo) {
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int lim = __shfl_sync(0xffffffffu, qpos[nt], 4 * (2 * t + (c & 1)));
+              if (key0 + x * kWarps * kQ4Block + g + 8 * (c >> 1) > lim) s[x][nt][c] = kMinusInf;
+            }
+      }
+      float mx[NT][2];
       bool above = false;
-      const bool edge = key0 + kQ4Block - 1 > lim_lo;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // column c & 1 (row 2t + (c & 1)), key g + 8 (c >> 1)
-          float v = (s[nt][0][c] + s[nt][1][c]) * sc[nt][c & 1];
-          if (edge && key0 + g + 8 * (c >> 1) > lim[nt][c & 1]) v = kMinusInf;
-          s[nt][0][c] = v;
-          above |= v > m[nt][c & 1] + kMaxStep;
+        for (int c = 0; c < 2; ++c) {
+          mx[nt][c] = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+#pragma unroll
+          for (int x = 1; x < N; ++x) mx[nt][c] = fmax3(mx[nt][c], s[x][nt][c], s[x][nt][c + 2]);
+          above |= mx[nt][c] > thr[nt][c];
         }
-      }
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float mx = fmaxf(s[nt][0][c], s[nt][0][c + 2]);
+            float v = mx[nt][c];
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-            const float mn = fmaxf(m[nt][c], mx);
-            const float nb = mn == kMinusInf ? 0.f : mn;
-            const float a = fast_exp2(m[nt][c] - nb);
-            m[nt][c] = mn;
-            base[nt][c] = nb - kWeightBias;
+            for (int y = 4; y < 32; y <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, y));
+            // (v, thr and base are the same in every lane of the column)
+            const float step_up = __fdividef(kMaxStep, sc[nt][c]);
+            if (!(v > thr[nt][c] - step_up) && v == v) continue;  // not above the maximum (or nothing of this row yet)
+            const float nb = v * sc[nt][c] - kWeightBias;
+            const float a = thr[nt][c] == kMinusInf ? 0.f : fast_exp2(base[nt][c] - nb);
+            thr[nt][c] = v + step_up;
+            base[nt][c] = nb;
             l[nt][c] *= a;
 #pragma unroll
-            for (int i2 = 0; i2 < MT; ++i2) {
-              o[nt][i2][c] *= a;
-              o[nt][i2][c + 2] *= a;
+            for (int y = 0; y < MT; ++y) {
+              o[nt][y][c] *= a;
+              o[nt][y][c + 2] *= a;
             }
           }
+        __syncwarp();
       }
+      uint32_t pw[N][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float e[4];
+      for (int x = 0; x < N; ++x)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          e[c] = fast_exp2(s[nt][0][c] - base[nt][c & 1]);
-          l[nt][c & 1] += e[c];
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            e[c] = fast_exp2(fmaf(s[x][nt][c], sc[nt][c & 1], -base[nt][c & 1]));
+            l[nt][c & 1] += e[c];
+          }
+          pw[x][nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+          pw[x][nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
         }
-        pw[nt][0] = transpose8x8(pack_f16x2(e[0], e[1]));
-        pw[nt][1] = transpose8x8(pack_f16x2(e[2], e[3]));
-      }
       // ---- O^T += V^T P^T
-      {
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        const uint32_t st = ((used + x) % S) * STB;
         uint32_t v0[KW], v1[KW];
-        lds_words(v0, vt + lane * (4 * KW));
-        lds_words(v1, vt + 4 * D + lane * (4 * KW));
-        const uint32_t sw = lds_u32(vt + 8 * D + ((D == 128 ? g : g >> 1) * 4 + t) * 4);
+        lds_words(v0, ring_c + st + 2 * CB);
+        lds_words(v1, ring_c + st + 3 * CB);
+        const uint32_t sw = lds_u32(ring_s + st + 128);
         uint32_t s0 = e4m3x2_to_f16(sw), s1 = e4m3x2_to_f16(sw >> 16);
-        if (key0 + kQ4Block > len) {  // tokens past the sequence: their bytes may be anything
-          const int k0 = key0 + 2 * t;
-          s0 = (k0 < len ? s0 & 0xFFFFu : 0u) | (k0 + 1 < len ? s0 & 0xFFFF0000u : 0u);
-          s1 = (k0 + 8 < len ? s1 & 0xFFFFu : 0u) | (k0 + 9 < len ? s1 & 0xFFFF0000u : 0u);
+        const int k0 = key0 + x * kWarps * kQ4Block;
+        if (k0 + kQ4Block > len) {  // tokens past the sequence: their bytes may be anything
+          const int k = k0 + 2 * t;
+          s0 = (k < len ? s0 & 0xFFFFu : 0u) | (k + 1 < len ? s0 & 0xFFFF0000u : 0u);
+          s1 = (k + 8 < len ? s1 & 0xFFFFu : 0u) | (k + 9 < len ? s1 & 0xFFFF0000u : 0u);
         }
 #pragma unroll
         for (int w = 0; w < KW / 2; ++w) {
           // bytes of two tokens' codes of one element: even elements, odd elements
           uint32_t e0[4], d0[4], e1[4], d1[4];
-          e2m1x8_to_f16((v0[w] & 0x0F0F0F0Fu) | ((v0[w + KW / 2] << 4) & 0xF0F0F0F0u), e0);
-          e2m1x8_to_f16(((v0[w] >> 4) & 0x0F0F0F0Fu) | (v0[w + KW / 2] & 0xF0F0F0F0u), d0);
-          e2m1x8_to_f16((v1[w] & 0x0F0F0F0Fu) | ((v1[w + KW / 2] << 4) & 0xF0F0F0F0u), e1);
-          e2m1x8_to_f16(((v1[w] >> 4) & 0x0F0F0F0Fu) | (v1[w + KW / 2] & 0xF0F0F0F0u), d1);
+          e2m1x8_to_f16(select_bits<0x0F0F0F0Fu>(v0[w], v0[w + KW / 2] << 4), e0);
+          e2m1x8_to_f16(select_bits<0x0F0F0F0Fu>(v0[w] >> 4, v0[w + KW / 2]), d0);
+          e2m1x8_to_f16(select_bits<0x0F0F0F0Fu>(v1[w], v1[w + KW / 2] << 4), e1);
+          e2m1x8_to_f16(select_bits<0x0F0F0F0Fu>(v1[w] >> 4, v1[w + KW / 2]), d1);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t a0 = hmul2(e0[x], s0), a1 = hmul2(d0[x], s0), a2 = hmul2(e1[x], s1), a3 = hmul2(d1[x], s1);
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t a0 = hmul2(e0[y], s0), a1 = hmul2(d0[y], s0), a2 = hmul2(e1[y], s1), a3 = hmul2(d1[y], s1);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + x], a0, a1, a2, a3, pw[nt][0], pw[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + y], a0, a1, a2, a3, pw[x][nt][0], pw[x][nt][1]);
           }
         }
       }
-      __syncwarp();
-      if (lane == 0 && issued < mine_n) {
-        fence_proxy_async_smem();
-        issue();
-      }
-      __syncwarp();
-    }
+      used += N;
+#pragma unroll
+      for (int x = 0; x < N; ++x) issue();  // the stages just read take the next blocks
+    };
+    // the warp's blocks of the piece: range indices congruent to warp
+    constexpr int kStep = NT == 1 ? 2 : 1;
+    int i = (warp - first) & (kWarps - 1);
+    for (; i + (kStep - 1) * kWarps < n; i += kStep * kWarps) step(i, std::integral_constant<int, kStep>{});
+    if (kStep > 1 && i < n) step(i, std::integral_constant<int, 1>{});
 
     // ---- the warps' states of the piece, joined in shared memory
 #pragma unroll
@@ -445,18 +529,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
         const int r = nt * 8 + 2 * t + c;
-        if (g == 0) mlbuf[warp * ROWS + r] = make_float2(m[nt][c], v);
+        if (g == 0) mlbuf[warp * ROWS + r] = make_float2(thr[nt][c] == kMinusInf ? kMinusInf : base[nt][c] + kWeightBias, v);
         float* dst = obuf + (warp * ROWS + r) * D + g * W;
 #pragma unroll
-        for (int i = 0; i < MT; i += 2)
-          *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(o[nt][i][c], o[nt][i][c + 2], o[nt][i + 1][c], o[nt][i + 1][c + 2]);
+        for (int y = 0; y < MT; y += 2)
+          *reinterpret_cast<float4*>(dst + 2 * y) =
+              make_float4(o[nt][y][c], o[nt][y][c + 2], o[nt][y + 1][c], o[nt][y + 1][c + 2]);
       }
     }
-    __syncthreads();
     const bool whole = cj == 0 && n == nblk;
     const int slot = cj == 0 ? 1 : 0;  // a piece that begins here, or one continued from the CTA before
-    for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kThreads) {
+    if (threadIdx.x == 0 && cj == 0 && n < nblk)
+      p.cut[blockIdx.x] = make_int4(cb, ch, static_cast<int>((unit + kPieceCost + nblk - 1) / share), 0);
+    const int out_t0 = t0, out_rows = rows, out_len = len, out_h = ch;
+    left -= n;
+    first += n;
+    unit += nblk + kPieceCost;
+    cj = 0;
+    if (left > 0) {  // (8 rows: the next piece's are on their way while this one is stored; 16 take too many registers)
+      if (++ch == p.nkv) {
+        ch = 0;
+        do ++cb;
+        while (plan_blocks(p, cb) == 0);
+      }
+      if (NT == 1) load_q();
+    }
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < out_rows * (D / 4); idx += kThreads) {
       const int r = idx / (D / 4), c4 = (idx % (D / 4)) * 4;
       float M = kMinusInf;
 #pragma unroll
@@ -476,43 +575,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
         O.w += x.w * f;
       }
       if (whole) {
-        const int tok = t0 + r / p.group;
+        const int tok = out_t0 + r / p.group;
         const int pos = p.positions[tok];
-        if (pos < 0 || pos >= len) {
-          if (ch == 0 && c4 == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
+        if (pos < 0 || pos >= out_len) {
+          if (out_h == 0 && c4 == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
           continue;
         }
         const float inv = p.v_scale / L;
         uint2 u;
         u.x = pack_bf16x2(O.x * inv, O.y * inv);
         u.y = pack_bf16x2(O.z * inv, O.w * inv);
-        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.nq + ch * p.group + r % p.group) * D + c4) = u;
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.nq + out_h * p.group + r % p.group) * D + c4) =
+            u;
       } else {
         const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + slot) * kMaxRows + r;
         *reinterpret_cast<float4*>(p.part_o + at * D + c4) = O;
         if (c4 == 0) p.part_ml[at] = make_float2(M, L);
       }
     }
-    if (threadIdx.x == 0 && cj == 0 && n < nblk)
-      p.cut[blockIdx.x] = make_int4(cb, ch, static_cast<int>((begin + first + nblk - 1) / share), 0);
     __syncthreads();
-    left -= n;
-    first += n;
-    cj = 0;
-    if (left > 0 && ++ch == p.nkv) {
-      ch = 0;
-      int t1, r1, l1;
-      bool b1;
-      do ++cb;
-      while (decode_blocks(p, cb, t1, r1, l1, b1) == 0);
-    }
   }
-  if (!ok) {
-    if (lane == 0) report_error(p.err, kErrTimeout, kWhereAttnDecode);
-    // let the copies still in flight land before the shared memory is given up
-    issued = __shfl_sync(0xffffffffu, issued, 0);
-    for (int i = used; i < issued; ++i) mbar_wait(bar0 + 8 * (i % S), (i / S) & 1, nullptr);
-  }
+  copy_wait<0>();
 }
 
 // Joins the pieces of every (sequence, KV head) that spans CTAs: the CTA of the
@@ -716,8 +799,7 @@ __global__ void __launch_bounds__(256) k_q4_expand(const PrefillQ4 p) {
 template <int D, int NT>
 size_t decode_smem() {
   constexpr int S = stages<D>(), ROWS = 8 * NT;
-  return static_cast<size_t>(kWarps) * S * 2 * q4_tile_bytes(D) + kWarps * ROWS * D * 4 + kWarps * ROWS * 8 +
-         kWarps * S * 8 + 8 * 8;
+  return static_cast<size_t>(kWarps) * S * (4 * (32 * D / 8) + 2 * 128) + kWarps * ROWS * D * 4 + kWarps * ROWS * 8;
 }
 
 struct Layout {
