@@ -158,8 +158,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without making a Stream object (3 us of a 5 us launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -313,13 +313,16 @@ def paged_attention_noalloc(cfg: LayerConfig, batch: Batch, q, k_cache, v_cache,
     _check(st, "llama_paged_attention_noalloc")
 
 
-def _token_rows(t: torch.Tensor, where: str) -> int:
-    """Elements from one token to the next of t [tokens, heads, head_dim], whose
-    heads lie side by side."""
-    if (t.dim() != 3 or t.dtype != torch.bfloat16 or t.stride(2) != 1 or
-            (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
-        raise LlamaError(LLAMA_ERR_ARG, where)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _token_rows(t: torch.Tensor, where: str):
+    """(shape, elements from one token to the next) of t [tokens, heads,
+    head_dim] bf16, whose heads lie side by side."""
+    shape = t.shape
+    if len(shape) == 3 and t.dtype is torch.bfloat16:
+        tokens, heads, d = shape
+        token_stride, head_stride, stride = t.stride()
+        if stride == 1 and (head_stride == d or heads == 1):
+            return shape, token_stride if tokens > 1 else heads * d
+    raise LlamaError(LLAMA_ERR_ARG, where)
 
 
 def kv_cache_q4_tile_bytes(head_dim: int) -> int:
@@ -331,17 +334,18 @@ def kv_cache_q4_tile_bytes(head_dim: int) -> int:
     return n
 
 
-def _check_cache_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, n_kv: int, head_dim: int, where: str) -> None:
-    for c in (k_cache, v_cache):
-        if (c.dtype != torch.uint8 or c.dim() != 3 or c.shape[1] != n_kv or c.shape[2] != 9 * head_dim
-                or not c.is_contiguous()):
-            raise LlamaError(LLAMA_ERR_ARG, where)
-    if k_cache.shape[0] != v_cache.shape[0]:
+def _check_cache_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, n_kv: int, head_dim: int, where: str) -> int:
+    """Blocks of two 4-bit cache arrays of these heads."""
+    shape = k_cache.shape
+    if (len(shape) != 3 or shape[1] != n_kv or shape[2] != 9 * head_dim or v_cache.shape != shape or
+            k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8 or
+            not k_cache.is_contiguous() or not v_cache.is_contiguous()):
         raise LlamaError(LLAMA_ERR_ARG, where)
+    return shape[0]
 
 
 def _check_slots(slots: torch.Tensor, tokens: int, where: str) -> None:
-    if slots.dtype != torch.int32 or slots.numel() != tokens or not slots.is_contiguous():
+    if slots.dtype is not torch.int32 or slots.numel() != tokens or not slots.is_contiguous():
         raise LlamaError(LLAMA_ERR_ARG, where)
 
 
@@ -350,15 +354,18 @@ def kv_cache_write_q4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tens
                       stream=None) -> None:
     """k, v [T, n_kv, head_dim] (any stride between tokens) quantised into 4-bit
     caches [num_blocks, n_kv, tile]; see kv_cache_write_q4 in the header."""
-    ks, vs = _token_rows(k, "kv_cache_write_q4"), _token_rows(v, "kv_cache_write_q4")
-    T, nkv, d = k.shape
-    if v.shape != k.shape:
-        raise LlamaError(LLAMA_ERR_ARG, "kv_cache_write_q4")
-    _check_slots(slot_mapping, T, "kv_cache_write_q4")
-    _check_cache_q4(k_cache, v_cache, nkv, d, "kv_cache_write_q4")
-    st = lib().kv_cache_write_q4(_ptr(k), ks, _ptr(v), vs, _ptr(slot_mapping), T, nkv, d, block_size,
-                                 k_cache.shape[0], k_scale, v_scale, _ptr(k_cache), _ptr(v_cache), _stream(stream))
-    _check(st, "kv_cache_write_q4")
+    where = "kv_cache_write_q4"
+    shape, ks = _token_rows(k, where)
+    v_shape, vs = _token_rows(v, where)
+    if v_shape != shape:
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    T, nkv, d = shape
+    _check_slots(slot_mapping, T, where)
+    blocks = _check_cache_q4(k_cache, v_cache, nkv, d, where)
+    st = lib().kv_cache_write_q4(k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, nkv, d, block_size,
+                                 blocks, k_scale, v_scale, k_cache.data_ptr(), v_cache.data_ptr(), _stream(stream))
+    if st:
+        raise LlamaError(st, where)
 
 
 def kv_cache_read_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor, k: torch.Tensor,
@@ -366,15 +373,18 @@ def kv_cache_read_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping:
                      stream=None) -> None:
     """The rows at slot_mapping of 4-bit caches as bf16, into k, v [T, n_kv,
     head_dim]; see kv_cache_read_q4 in the header."""
-    ks, vs = _token_rows(k, "kv_cache_read_q4"), _token_rows(v, "kv_cache_read_q4")
-    T, nkv, d = k.shape
-    if v.shape != k.shape:
-        raise LlamaError(LLAMA_ERR_ARG, "kv_cache_read_q4")
-    _check_slots(slot_mapping, T, "kv_cache_read_q4")
-    _check_cache_q4(k_cache, v_cache, nkv, d, "kv_cache_read_q4")
-    st = lib().kv_cache_read_q4(_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, nkv, d, block_size,
-                                k_cache.shape[0], k_scale, v_scale, _ptr(k), ks, _ptr(v), vs, _stream(stream))
-    _check(st, "kv_cache_read_q4")
+    where = "kv_cache_read_q4"
+    shape, ks = _token_rows(k, where)
+    v_shape, vs = _token_rows(v, where)
+    if v_shape != shape:
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    T, nkv, d = shape
+    _check_slots(slot_mapping, T, where)
+    blocks = _check_cache_q4(k_cache, v_cache, nkv, d, where)
+    st = lib().kv_cache_read_q4(k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, nkv, d, block_size,
+                                blocks, k_scale, v_scale, k.data_ptr(), ks, v.data_ptr(), vs, _stream(stream))
+    if st:
+        raise LlamaError(st, where)
 
 
 def prefill_blocks(q_lens: Sequence[int], seq_lens: Sequence[int], group: int) -> int:
@@ -398,18 +408,18 @@ def paged_attention_q4(cfg: LayerConfig, batch: Batch, q: torch.Tensor, k_cache:
                        out: torch.Tensor, workspace: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
                        prefill_blocks: int = 0, stream=None) -> None:
     """Paged attention over 4-bit caches; see llama_paged_attention_q4 in the header."""
-    _check_cache_q4(k_cache, v_cache, cfg.n_kv_heads, cfg.head_dim, "llama_paged_attention_q4")
-    if k_cache.shape[0] != batch.num_blocks:
-        raise LlamaError(LLAMA_ERR_ARG, "llama_paged_attention_q4")
-    for t in (q, out):
-        if (t.dtype != torch.bfloat16 or not t.is_contiguous() or
-                t.numel() != batch.positions.numel() * cfg.n_heads * cfg.head_dim):
-            raise LlamaError(LLAMA_ERR_ARG, "llama_paged_attention_q4")
-    c, b = cfg.c(), batch.c()
-    st = lib().llama_paged_attention_q4(ctypes.byref(c), ctypes.byref(b), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                        k_scale, v_scale, prefill_blocks, _ptr(out), _ptr(workspace),
+    where = "llama_paged_attention_q4"
+    b = batch.c()
+    n = b.num_tokens * cfg.n_heads * cfg.head_dim
+    if (_check_cache_q4(k_cache, v_cache, cfg.n_kv_heads, cfg.head_dim, where) != b.num_blocks or
+            q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or q.numel() != n or out.numel() != n or
+            not q.is_contiguous() or not out.is_contiguous()):
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    st = lib().llama_paged_attention_q4(cfg.c(), b, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale,
+                                        v_scale, prefill_blocks, out.data_ptr(), workspace.data_ptr(),
                                         workspace.numel(), _stream(stream))
-    _check(st, "llama_paged_attention_q4")
+    if st:
+        raise LlamaError(st, where)
 
 
 _ROPE_TYPES = {"default": 0, "llama3": 1, "linear": 2, "yarn": 3}
@@ -457,21 +467,21 @@ def qk_norm_rope(cfg: QkNormRopeConfig, q_norm: Optional[torch.Tensor], k_norm: 
     n_heads, head_dim] and k [T, n_kv_heads, head_dim], any stride between
     tokens; q_out / k_out may be q / k; see llama_qk_norm_rope in the header."""
     where = "llama_qk_norm_rope"
-    strides = [_token_rows(t, where) for t in (q, k, q_out, k_out)]
-    T = q.shape[0]
-    if (q.shape != q_out.shape or k.shape != k_out.shape or k.shape[0] != T or
-            tuple(q.shape[1:]) != (cfg.n_heads, cfg.head_dim) or tuple(k.shape[1:]) != (cfg.n_kv_heads, cfg.head_dim)):
+    (q_shape, qs), (k_shape, ks) = _token_rows(q, where), _token_rows(k, where)
+    (q_out_shape, qos), (k_out_shape, kos) = _token_rows(q_out, where), _token_rows(k_out, where)
+    T, n_heads, d = q_shape
+    if (q_out_shape != q_shape or k_out_shape != k_shape or k_shape != (T, cfg.n_kv_heads, d) or
+            n_heads != cfg.n_heads or d != cfg.head_dim):
         raise LlamaError(LLAMA_ERR_ARG, where)
     if positions is not None:
         _check_slots(positions, T, where)
     for w in (q_norm, k_norm):
-        if w is not None and (w.dtype != torch.bfloat16 or w.numel() != cfg.head_dim or not w.is_contiguous()):
+        if w is not None and (w.dtype is not torch.bfloat16 or w.numel() != d or not w.is_contiguous()):
             raise LlamaError(LLAMA_ERR_ARG, where)
-    c = cfg.c()
-    st = lib().llama_qk_norm_rope(ctypes.byref(c), _ptr(q_norm), _ptr(k_norm), _ptr(positions), T, _ptr(q), strides[0],
-                                  _ptr(k), strides[1], _ptr(q_out), strides[2], _ptr(k_out), strides[3],
-                                  _stream(stream))
-    _check(st, where)
+    st = lib().llama_qk_norm_rope(cfg.c(), _ptr(q_norm), _ptr(k_norm), _ptr(positions), T, q.data_ptr(), qs,
+                                  k.data_ptr(), ks, q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream(stream))
+    if st:
+        raise LlamaError(st, where)
 
 
 def set_gemm_schedule(schedule: int) -> None:
