@@ -66,7 +66,8 @@ struct Q4Params {
   float scale_log2, v_scale;
   float* part_o;   // [CTA][2][kMaxRows][D]
   float2* part_ml; // [CTA][2][kMaxRows]: maximum, sum
-  int4* cut;       // [CTA]: sequence (or -1), KV head, last CTA of the piece that begins here
+  int4* cut;       // sequence (or -1: nothing to join), KV head, last CTA, first CTA of a piece
+  int cut_by_piece;  // cut is indexed by sequence * nkv + KV head (else by the piece's first CTA)
   int* err;
 };
 
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
                                          : (total + gridDim.x - 1) / gridDim.x;
   if (share < kMinShare) share = kMinShare;
   const long long begin = share * blockIdx.x, end = min(total, begin + share);
-  if (threadIdx.x == 0) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !p.cut_by_piece) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (begin >= end) return;
   {
     const long long first_unit = units_of(excl), last_unit = first_unit + units_of(mine);
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
       for (int x = 0; x < N; ++x) issue();  // the stages just read take the next blocks
     };
     // the warp's blocks of the piece: range indices congruent to warp
-    constexpr int kStep = NT == 1 ? 2 : 1;
+    constexpr int kStep = 2;
     int i = (warp - first) & (kWarps - 1);
     for (; i + (kStep - 1) * kWarps < n; i += kStep * kWarps) step(i, std::integral_constant<int, kStep>{});
     if (kStep > 1 && i < n) step(i, std::integral_constant<int, 1>{});
@@ -539,8 +540,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     }
     const bool whole = cj == 0 && n == nblk;
     const int slot = cj == 0 ? 1 : 0;  // a piece that begins here, or one continued from the CTA before
-    if (threadIdx.x == 0 && cj == 0 && n < nblk)
-      p.cut[blockIdx.x] = make_int4(cb, ch, static_cast<int>((unit + kPieceCost + nblk - 1) / share), 0);
+    if (threadIdx.x == 0 && cj == 0 && (n < nblk || p.cut_by_piece))
+      p.cut[p.cut_by_piece ? cb * p.nkv + ch : blockIdx.x] = make_int4(
+          n < nblk ? cb : -1, ch, static_cast<int>((unit + kPieceCost + nblk - 1) / share), blockIdx.x);
     const int out_t0 = t0, out_rows = rows, out_len = len, out_h = ch;
     left -= n;
     first += n;
@@ -598,53 +600,77 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
   copy_wait<0>();
 }
 
-// Joins the pieces of every (sequence, KV head) that spans CTAs: the CTA of the
-// decode grid in which it begins, one warp per row (two when 8 rows), parts in order.
-constexpr int kCombineThreads = 512;
+// Joins the parts of every piece that spans CTAs, in order.  Up to as many pieces
+// as decode CTAs: one entry of `cut` per piece and grid.y CTAs share its rows,
+// so that a few long pieces have many warps; beyond that one entry per decode CTA
+// (the piece that begins in it and ends in a later one).
+constexpr int kCombineWarps = 16;
 
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) k_attn_q4_combine(const Q4Params p) {
+__global__ void __launch_bounds__(kCombineWarps * 32) k_attn_q4_combine(const Q4Params p) {
+  __shared__ float so[kCombineWarps][D];
+  __shared__ float sl[kCombineWarps];
   pdl_wait();
-  const int4 cut = p.cut[blockIdx.x];
-  if (cut.x < 0) return;
-  const int first = blockIdx.x, parts = cut.z - first + 1;
   int t0, rows, len;
   bool bad;
+  if (p.cut_by_piece && decode_blocks(p, blockIdx.x / p.nkv, t0, rows, len, bad) == 0) return;
+  const int4 cut = p.cut[blockIdx.x];
+  if (cut.x < 0) return;
   decode_blocks(p, cut.x, t0, rows, len, bad);
-  const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int first = cut.w, parts = cut.z - first + 1;
+  const int gy = gridDim.y, y = blockIdx.y;
+  const int mine = y < rows ? (rows - y + gy - 1) / gy : 0;  // rows y, y + gy, ...
+  if (mine == 0) return;
+  const int wpr = mine <= 1 ? 16 : mine <= 2 ? 8 : mine <= 4 ? 4 : mine <= 8 ? 2 : 1;  // warps a row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = y + (warp / wpr) * gy, sub = warp % wpr;
+  auto at = [&](int i) { return (static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kMaxRows + r; };
+  constexpr int E = D / 32;
+  float L = 0.f, O[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) O[e] = 0.f;
+  if (r < rows) {
+    float M = kMinusInf;
+    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[at(i)].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    const float mb = M == kMinusInf ? 0.f : M;
+#pragma unroll 8
+    for (int i = sub; i < parts; i += wpr) {
+      const float2 ml = p.part_ml[at(i)];
+      const float* src = p.part_o + at(i) * D + lane * E;
+      float x[E];
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        x[0] = v.x, x[1] = v.y;
+      }
+      const float f = fast_exp2(ml.x - mb);
+      L += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) O[e] += x[e] * f;
+    }
+  }
+  if (wpr > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = O[e];
+    if (lane == 0) sl[warp] = L;
+    __syncthreads();
+    if (sub != 0) return;
+    for (int w = 1; w < wpr; ++w) {
+      L += sl[warp + w];
+#pragma unroll
+      for (int e = 0; e < E; ++e) O[e] += so[warp + w][lane * E + e];
+    }
+  }
   if (r >= rows) return;
   const int tok = t0 + r / p.group;
   const int pos = p.positions[tok];
   if (pos < 0 || pos >= len) {
     if (cut.y == 0 && lane == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
     return;
-  }
-  auto at = [&](int i) { return (static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kMaxRows + r; };
-  float M = kMinusInf;
-  for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[at(i)].x);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  const float mb = M == kMinusInf ? 0.f : M;
-  constexpr int E = D / 32;
-  float L = 0.f, O[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) O[e] = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < parts; ++i) {
-    const float2 ml = p.part_ml[at(i)];
-    const float* src = p.part_o + at(i) * D + lane * E;
-    float x[E];
-    if constexpr (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      x[0] = v.x, x[1] = v.y;
-    }
-    const float f = fast_exp2(ml.x - mb);
-    L += ml.y * f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) O[e] += x[e] * f;
   }
   const float inv = p.v_scale / L;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
@@ -755,41 +781,32 @@ __global__ void __launch_bounds__(256) k_q4_expand(const PrefillQ4 p) {
     if (threadIdx.x == 0) report_error(p.err, kErrGuard, kWhereBlockTable);
     blk = 0;
   }
-  constexpr int GR = D / kQ4Group;
-  const int half = p.nkv * kQ4Block * GR;
-  for (int i = threadIdx.x; i < 2 * half; i += blockDim.x) {
-    const bool is_v = i >= half;
-    const int x = is_v ? i - half : i;
-    const int grp = x % GR, k = (x / GR) % kQ4Block, h = x / (GR * kQ4Block);
-    const uint8_t* tile = (is_v ? p.v_cache : p.k_cache) + (static_cast<size_t>(blk) * p.nkv + h) * q4_tile_bytes(D);
-    uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (j * kQ4Block + k < len) {
-      uint32_t code[2], s8;
-      if (!is_v) {
-        const uint2 c = *reinterpret_cast<const uint2*>(tile + k * (D / 2) + grp * 8);
-        code[0] = c.x;
-        code[1] = c.y;
-        s8 = tile[q4_k_scale_at<D>(k, grp)];
-      } else {
-        code[0] = *reinterpret_cast<const uint32_t*>(tile + q4_v_code_at<D>(k, grp * 16));
-        code[1] = *reinterpret_cast<const uint32_t*>(tile + q4_v_code_at<D>(k, grp * 16 + 8));
-        s8 = tile[q4_v_scale_at<D>(k, grp)];
-      }
-      const float m = f16_lo(e4m3x2_to_f16(s8)) * (is_v ? p.v_scale : p.k_scale);
+  // chunks of 8 elements, K then V: (head, token, chunk); all of a thread's loads in flight at once
+  constexpr int C = D / 8, kUnroll = 4;
+  const int half = p.nkv * kQ4Block * C;
+  for (int i0 = threadIdx.x; i0 < 2 * half; i0 += blockDim.x * kUnroll) {
+    uint32_t code[kUnroll], s8[kUnroll];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[4];
-        e2m1x8_to_f16(code[c], v);
-        u[c].x = pack_bf16x2(f16_lo(v[0]) * m, f16_hi(v[0]) * m);
-        u[c].y = pack_bf16x2(f16_lo(v[1]) * m, f16_hi(v[1]) * m);
-        u[c].z = pack_bf16x2(f16_lo(v[2]) * m, f16_hi(v[2]) * m);
-        u[c].w = pack_bf16x2(f16_lo(v[3]) * m, f16_hi(v[3]) * m);
+    for (int n = 0; n < kUnroll; ++n) {
+      const int i = i0 + n * blockDim.x;
+      const bool is_v = i >= half;
+      const int x = is_v ? i - half : i, c = x % C, k = (x / C) % kQ4Block, h = x / (C * kQ4Block);
+      code[n] = s8[n] = 0;
+      if (i < 2 * half && j * kQ4Block + k < len) {
+        const uint8_t* tile =
+            (is_v ? p.v_cache : p.k_cache) + (static_cast<size_t>(blk) * p.nkv + h) * q4_tile_bytes(D);
+        code[n] = *reinterpret_cast<const uint32_t*>(tile + q4_code_at<D>(is_v, k, c));
+        s8[n] = tile[q4_scale_at<D>(is_v, k, c >> 1)];
       }
     }
-    __nv_bfloat16* dst = is_v ? p.v_copy : p.k_copy;
-    uint4* d4 = reinterpret_cast<uint4*>(dst + ((static_cast<size_t>(s) * p.nkv + h) * kQ4Block + k) * D + grp * 16);
-    d4[0] = u[0];
-    d4[1] = u[1];
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n) {
+      const int i = i0 + n * blockDim.x;
+      if (i >= 2 * half) break;
+      const bool is_v = i >= half;
+      __nv_bfloat16* dst = (is_v ? p.v_copy : p.k_copy) + static_cast<size_t>(s) * p.nkv * kQ4Block * D;
+      reinterpret_cast<uint4*>(dst)[is_v ? i - half : i] = q4_to_bf16(code[n], s8[n], is_v ? p.v_scale : p.k_scale);
+    }
   }
 }
 
@@ -839,7 +856,7 @@ Layout layout(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int he
 }
 
 template <int D, int NT>
-int launch_decode(const Q4Params& p, int grid, bool pdl, cudaStream_t s) {
+int launch_decode(Q4Params p, int grid, bool pdl, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
@@ -847,9 +864,17 @@ int launch_decode(const Q4Params& p, int grid, bool pdl, cudaStream_t s) {
                                 static_cast<int>(decode_smem<D, NT>()));
   });
   if (attr != cudaSuccess) return attr;
-  cudaError_t e = launch_kernel(k_attn_q4_decode<D, NT>, dim3(grid), dim3(kThreads), decode_smem<D, NT>(), s, pdl, p);
-  if (e == cudaSuccess) e = launch_kernel(k_attn_q4_combine<D>, dim3(grid), dim3(kCombineThreads), 0, s, true, p);
-  return e;
+  const long long pieces = static_cast<long long>(p.B) * p.nkv;
+  p.cut_by_piece = pieces <= grid;
+  const cudaError_t e =
+      launch_kernel(k_attn_q4_decode<D, NT>, dim3(grid), dim3(kThreads), decode_smem<D, NT>(), s, pdl, p);
+  if (e != cudaSuccess) return e;
+  dim3 join(grid);
+  if (p.cut_by_piece) {
+    const int per_piece = static_cast<int>(num_sms() / pieces);
+    join = dim3(static_cast<unsigned>(pieces), per_piece < 1 ? 1 : per_piece > 8 * NT ? 8 * NT : per_piece);
+  }
+  return launch_kernel(k_attn_q4_combine<D>, join, dim3(kCombineWarps * 32), 0, s, true, p);
 }
 
 template <int D>

@@ -7,14 +7,20 @@
 // infinity as a value beyond every scale, so the cache holds finite values
 // only and a bad token cannot reach rows that do not attend to it.  s = 0
 // (every |x| below 6 g 2^-10) stores zeros.
-//   The rounding is that of the exact quotients: x has 8 significant bits, 6 m
-// and s t (t a border between two codes) at most 8, so a quotient that is not a
-// border itself is at least 2^-9 away from it, and one that is comes out of the
-// fp32 division exactly.
-// Reading: bf16(code * s * g), exact while it is a normal bf16.
+//   The rounding is that of the exact quotients: x has 8 significant bits, a
+// border t of the codes times s at most 7, so x / s either is t or is at least
+// 2^-8 t >= 2^-10 away from it.  x times 1 / s in fp32 is off by less than 2^-19
+// below 8; rounded to a multiple of 2^-13 it is t where the quotient is, and stays
+// on its side where it is not.  (max / 6 is an fp32 division: the borders of e4m3
+// times 6 have at most 7 bits, and a quotient that is one comes out exactly.)
+// Reading: bf16(code * s * g), exact.
 //
-// Both move 2 + 9/16 bytes an element and are bound by HBM: a thread takes one
-// group of 16 (32 bytes of bf16 against 8 + 1 bytes).
+// Both move 2 + 9/16 bytes an element and are bound by HBM.  A thread takes
+// chunks of 8 elements (16 bytes of bf16, 4 of codes), kUnroll of them kThreads
+// apart with all their loads in flight, so that a warp's bf16 accesses are
+// contiguous; two lanes share a scale.  (16 elements a thread, with 64-bit index
+// arithmetic and an fp32 division per element, took 104 us for 32768 tokens x 8 x
+// 128 written and read back.)
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -25,135 +31,167 @@ namespace llama {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
 
+// n / d for n < 2^31 by one multiplication
+struct FastDiv {
+  uint32_t mul, shift, d;
+  explicit FastDiv(uint32_t div) : mul(0), shift(0), d(div) {
+    while ((1ull << shift) < div) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(__umulhi(n, mul)) + n) >> shift);
+  }
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Where chunk i of the launch's tokens x heads x D / 8 chunks lies.
 template <int D>
-__global__ void __launch_bounds__(kThreads) k_kv_write_q4(const CacheQ4Args a) {
-  constexpr int GR = D / kQ4Group;
-  const long long half = static_cast<long long>(a.T) * a.n_kv * GR;
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < 2 * half;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const bool is_v = i >= half;
-    const long long j = is_v ? i - half : i;
-    const int s = static_cast<int>(j % GR);
-    const int h = static_cast<int>((j / GR) % a.n_kv);
-    const int t = static_cast<int>(j / (static_cast<long long>(GR) * a.n_kv));
-    const int slot = a.slots[t];
-    if (slot < 0) continue;
-    if (slot >= a.num_blocks * kQ4Block) {
-      if (s == 0 && h == 0 && !is_v) report_error(a.err, kErrGuard, kWhereSlot);
-      continue;
-    }
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) +
-                               t * (is_v ? a.v_stride : a.k_stride) + h * D + s * kQ4Group;
-    const float inv_g = is_v ? a.inv_v_scale : a.inv_k_scale;
-    float x[16];
+struct Chunk {
+  long long t;  // token
+  int h, c, slot;
+  bool ok;
+};
+
+// chunk of a token `i` from token t0 on; the slot is loaded, out-of-range ones reported
+template <int D>
+__device__ __forceinline__ Chunk<D> chunk_of(const CacheQ4Args& a, const FastDiv& per_token, long long t0, uint32_t i,
+                                             bool is_v) {
+  constexpr int C = D / 8;
+  Chunk<D> x;
+  const uint32_t t = per_token(i), r = i - t * per_token.d;
+  x.t = t0 + t;
+  x.h = r / C;
+  x.c = r % C;
+  x.ok = x.t < a.T;
+  x.slot = x.ok ? a.slots[x.t] : -1;
+  if (x.slot >= a.num_blocks * kQ4Block) {
+    if (r == 0 && !is_v) report_error(a.err, kErrGuard, kWhereSlot);
+    x.ok = false;
+  }
+  x.ok = x.ok && x.slot >= 0;
+  return x;
+}
+
+// CTA (x, y): kThreads * kUnroll chunks of K (y = 0) or V, of the tokens of one
+// span (so that the index arithmetic stays in 32 bits).
+template <int D>
+__global__ void __launch_bounds__(kThreads) k_kv_write_q4(const CacheQ4Args a, const FastDiv per_token, int span,
+                                                          int ctas_per_span) {
+  const bool is_v = blockIdx.y != 0;
+  const long long t0 = static_cast<long long>(blockIdx.x / ctas_per_span) * span;
+  const uint32_t i0 = (blockIdx.x % ctas_per_span) * (kThreads * kUnroll) + threadIdx.x;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k);
+  const long long stride = is_v ? a.v_stride : a.k_stride;
+  const float inv_g = is_v ? a.inv_v_scale : a.inv_k_scale;
+  uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache);
+  Chunk<D> x[kUnroll];
+  uint4 u[kUnroll];
+#pragma unroll
+  for (int n = 0; n < kUnroll; ++n) {
+    x[n] = chunk_of<D>(a, per_token, t0, i0 + n * kThreads, is_v);
+    if (i0 + n * kThreads >= static_cast<uint32_t>(span) * per_token.d) x[n].ok = false;
+    u[n] = make_uint4(0, 0, 0, 0);
+    if (x[n].ok) u[n] = *reinterpret_cast<const uint4*>(src + x[n].t * stride + x[n].h * D + x[n].c * 8);
+  }
+#pragma unroll
+  for (int n = 0; n < kUnroll; ++n) {
+    float v[8] = {bf16_lo(u[n].x), bf16_hi(u[n].x), bf16_lo(u[n].y), bf16_hi(u[n].y),
+                  bf16_lo(u[n].z), bf16_hi(u[n].z), bf16_lo(u[n].w), bf16_hi(u[n].w)};
     float amax = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint4 u = reinterpret_cast<const uint4*>(src)[c];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(v[e]));
+    if (amax != amax) {  // rare: NaN counts as zero
+      amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[8 * c + 2 * e] = bf16_lo(w[e]) * inv_g;
-        x[8 * c + 2 * e + 1] = bf16_hi(w[e]) * inv_g;
+      for (int e = 0; e < 8; ++e) {
+        v[e] = v[e] != v[e] ? 0.f : v[e];
+        amax = fmaxf(amax, fabsf(v[e]));
       }
     }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      x[e] = x[e] != x[e] ? 0.f : x[e];
-      amax = fmaxf(amax, fabsf(x[e]));
-    }
-    const uint32_t s8 = f32_to_e4m3(__fdiv_rn(amax, 6.f));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // the group's other half is in the next lane
+    const uint32_t s8 = f32_to_e4m3(__fdiv_rn(amax * inv_g, 6.f));
     const float sc = f16_lo(e4m3x2_to_f16(s8));
-    uint32_t code[2];
+    const float inv = s8 == 0 ? 0.f : __frcp_rn(sc) * inv_g;
+    constexpr float kSnap = 1.5f * 1024.f;  // sums with it are multiples of 2^-13 below 2^10
+    float y[8];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = s8 == 0 ? 0.f : __fdiv_rn(x[8 * c + e], sc);
-      code[c] = f32x8_to_e2m1(y);
-    }
-    const int k = slot % kQ4Block;
-    uint8_t* tile = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
-                    (static_cast<size_t>(slot / kQ4Block) * a.n_kv + h) * q4_tile_bytes(D);
-    if (!is_v) {
-      *reinterpret_cast<uint2*>(tile + k * (D / 2) + s * 8) = make_uint2(code[0], code[1]);
-      tile[q4_k_scale_at<D>(k, s)] = static_cast<uint8_t>(s8);
-    } else {
-      *reinterpret_cast<uint32_t*>(tile + q4_v_code_at<D>(k, s * 16)) = code[0];
-      *reinterpret_cast<uint32_t*>(tile + q4_v_code_at<D>(k, s * 16 + 8)) = code[1];
-      tile[q4_v_scale_at<D>(k, s)] = static_cast<uint8_t>(s8);
+    for (int e = 0; e < 8; ++e) y[e] = copysignf(__fadd_rn(__fmaf_rn(fabsf(v[e]), inv, kSnap), -kSnap), v[e]);
+    const uint32_t code = s8 == 0 ? 0u : f32x8_to_e2m1(y);
+    const int k = x[n].slot & 15, s = x[n].c >> 1;
+    const uint32_t next = __shfl_down_sync(0xffffffffu, s8, 2);  // the next group's scale (K stores two at D = 128)
+    if (x[n].ok) {
+      uint8_t* tile = cache + (static_cast<size_t>(x[n].slot >> 4) * a.n_kv + x[n].h) * q4_tile_bytes(D);
+      *reinterpret_cast<uint32_t*>(tile + q4_code_at<D>(is_v, k, x[n].c)) = code;
+      if (D == 128 && !is_v) {
+        if ((x[n].c & 3) == 0)
+          *reinterpret_cast<uint16_t*>(tile + q4_k_scale_at<D>(k, s)) = static_cast<uint16_t>(s8 | (next << 8));
+      } else if ((x[n].c & 1) == 0) {
+        tile[q4_scale_at<D>(is_v, k, s)] = static_cast<uint8_t>(s8);
+      }
     }
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) k_kv_read_q4(const CacheQ4Args a) {
-  constexpr int GR = D / kQ4Group;
-  const long long half = static_cast<long long>(a.T) * a.n_kv * GR;
-  for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x; i < 2 * half;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const bool is_v = i >= half;
-    const long long j = is_v ? i - half : i;
-    const int s = static_cast<int>(j % GR);
-    const int h = static_cast<int>((j / GR) % a.n_kv);
-    const int t = static_cast<int>(j / (static_cast<long long>(GR) * a.n_kv));
-    const int slot = a.slots[t];
-    if (slot < 0) continue;
-    if (slot >= a.num_blocks * kQ4Block) {
-      if (s == 0 && h == 0 && !is_v) report_error(a.err, kErrGuard, kWhereSlot);
-      continue;
-    }
-    const int k = slot % kQ4Block;
-    const uint8_t* tile = static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache) +
-                          (static_cast<size_t>(slot / kQ4Block) * a.n_kv + h) * q4_tile_bytes(D);
-    uint32_t code[2];
-    uint32_t s8;
-    if (!is_v) {
-      const uint2 c = *reinterpret_cast<const uint2*>(tile + k * (D / 2) + s * 8);
-      code[0] = c.x;
-      code[1] = c.y;
-      s8 = tile[q4_k_scale_at<D>(k, s)];
-    } else {
-      code[0] = *reinterpret_cast<const uint32_t*>(tile + q4_v_code_at<D>(k, s * 16));
-      code[1] = *reinterpret_cast<const uint32_t*>(tile + q4_v_code_at<D>(k, s * 16 + 8));
-      s8 = tile[q4_v_scale_at<D>(k, s)];
-    }
-    const float m = f16_lo(e4m3x2_to_f16(s8)) * (is_v ? a.v_scale : a.k_scale);
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? a.v_out : a.k_out) + t * (is_v ? a.v_stride : a.k_stride) +
-                         h * D + s * kQ4Group;
+__global__ void __launch_bounds__(kThreads) k_kv_read_q4(const CacheQ4Args a, const FastDiv per_token, int span,
+                                                         int ctas_per_span) {
+  const bool is_v = blockIdx.y != 0;
+  const long long t0 = static_cast<long long>(blockIdx.x / ctas_per_span) * span;
+  const uint32_t i0 = (blockIdx.x % ctas_per_span) * (kThreads * kUnroll) + threadIdx.x;
+  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache);
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? a.v_out : a.k_out);
+  const long long stride = is_v ? a.v_stride : a.k_stride;
+  const float g = is_v ? a.v_scale : a.k_scale;
+  Chunk<D> x[kUnroll];
+  uint32_t code[kUnroll], s8[kUnroll];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t p[4];
-      e2m1x8_to_f16(code[c], p);
-      uint4 u;
-      u.x = pack_bf16x2(f16_lo(p[0]) * m, f16_hi(p[0]) * m);
-      u.y = pack_bf16x2(f16_lo(p[1]) * m, f16_hi(p[1]) * m);
-      u.z = pack_bf16x2(f16_lo(p[2]) * m, f16_hi(p[2]) * m);
-      u.w = pack_bf16x2(f16_lo(p[3]) * m, f16_hi(p[3]) * m);
-      reinterpret_cast<uint4*>(dst)[c] = u;
-    }
+  for (int n = 0; n < kUnroll; ++n) {
+    x[n] = chunk_of<D>(a, per_token, t0, i0 + n * kThreads, is_v);
+    if (i0 + n * kThreads >= static_cast<uint32_t>(span) * per_token.d) x[n].ok = false;
   }
+#pragma unroll
+  for (int n = 0; n < kUnroll; ++n) {
+    if (!x[n].ok) continue;
+    const int k = x[n].slot & 15;
+    const uint8_t* tile = cache + (static_cast<size_t>(x[n].slot >> 4) * a.n_kv + x[n].h) * q4_tile_bytes(D);
+    code[n] = *reinterpret_cast<const uint32_t*>(tile + q4_code_at<D>(is_v, k, x[n].c));
+    s8[n] = tile[q4_scale_at<D>(is_v, k, x[n].c >> 1)];
+  }
+#pragma unroll
+  for (int n = 0; n < kUnroll; ++n)
+    if (x[n].ok)
+      *reinterpret_cast<uint4*>(dst + x[n].t * stride + x[n].h * D + x[n].c * 8) = q4_to_bf16(code[n], s8[n], g);
 }
 
-int grid_of(const CacheQ4Args& a) {
-  const long long work = 2LL * a.T * a.n_kv * (a.head_dim / kQ4Group);
-  const long long g = (work + kThreads - 1) / kThreads, cap = static_cast<long long>(num_sms()) * 16;
-  return static_cast<int>(g > cap ? cap : g);
+// tokens a span: chunk indices within one stay below 2^30
+template <typename Kernel>
+int launch(Kernel kernel, const CacheQ4Args& a, cudaStream_t s) {
+  const uint32_t per_token = static_cast<uint32_t>(a.n_kv) * (a.head_dim / 8);
+  const long long most = (1 << 30) / static_cast<long long>(per_token);
+  const int span = static_cast<int>(a.T < most ? a.T : most);
+  const long long ctas = (static_cast<long long>(span) * per_token + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+  const long long spans = (static_cast<long long>(a.T) + span - 1) / span;
+  return launch_kernel(kernel, dim3(static_cast<unsigned>(spans * ctas), 2), dim3(kThreads), 0, s, false, a,
+                       FastDiv(per_token), span, static_cast<int>(ctas));
 }
 
 }  // namespace
 
 int kv_write_q4_launch(const CacheQ4Args& a, cudaStream_t s) {
   if (a.T <= 0) return 0;
-  if (a.head_dim == 128) return launch_kernel(k_kv_write_q4<128>, dim3(grid_of(a)), dim3(kThreads), 0, s, false, a);
-  return launch_kernel(k_kv_write_q4<64>, dim3(grid_of(a)), dim3(kThreads), 0, s, false, a);
+  return a.head_dim == 128 ? launch(k_kv_write_q4<128>, a, s) : launch(k_kv_write_q4<64>, a, s);
 }
 
 int kv_read_q4_launch(const CacheQ4Args& a, cudaStream_t s) {
   if (a.T <= 0) return 0;
-  if (a.head_dim == 128) return launch_kernel(k_kv_read_q4<128>, dim3(grid_of(a)), dim3(kThreads), 0, s, false, a);
-  return launch_kernel(k_kv_read_q4<64>, dim3(grid_of(a)), dim3(kThreads), 0, s, false, a);
+  return a.head_dim == 128 ? launch(k_kv_read_q4<128>, a, s) : launch(k_kv_read_q4<64>, a, s);
 }
 
 }  // namespace llama

@@ -92,6 +92,17 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&x)[8]) {
   return w;
 }
 
+// byte of the codes of elements 8 c .. 8 c + 7 of token k (K or V), and of their scale
+template <int D>
+__host__ __device__ __forceinline__ int q4_code_at(bool is_v, int k, int c) {
+  return is_v ? q4_v_code_at<D>(k, c * 8) : k * (D / 2) + c * 4;
+}
+
+template <int D>
+__host__ __device__ __forceinline__ int q4_scale_at(bool is_v, int k, int s) {
+  return is_v ? q4_v_scale_at<D>(k, s) : q4_k_scale_at<D>(k, s);
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -108,6 +119,15 @@ __device__ __forceinline__ float f16_hi(uint32_t v) {
   float f;
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(f) : "r"(v));
   return f;
+}
+
+// eight codes, their scale's bits and g -> eight bf16 values (exact)
+__device__ __forceinline__ uint4 q4_to_bf16(uint32_t code, uint32_t s8, float g) {
+  const float m = f16_lo(e4m3x2_to_f16(s8)) * g;
+  uint32_t p[4];
+  e2m1x8_to_f16(code, p);
+  return make_uint4(pack_bf16x2(f16_lo(p[0]) * m, f16_hi(p[0]) * m), pack_bf16x2(f16_lo(p[1]) * m, f16_hi(p[1]) * m),
+                    pack_bf16x2(f16_lo(p[2]) * m, f16_hi(p[2]) * m), pack_bf16x2(f16_lo(p[3]) * m, f16_hi(p[3]) * m));
 }
 
 }  // namespace llama
