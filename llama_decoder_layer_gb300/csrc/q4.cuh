@@ -71,10 +71,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t v) {
   return d;
 }
 
-// nearest e4m3 of x >= 0, at most 448, in the low byte
-__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+// nearest e4m3 (at most 448, in the low byte) of the fp16 number nearest to x >= 0
+__device__ __forceinline__ uint32_t f32_to_e4m3_by_f16(float x) {
+  uint32_t h;
   uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(0.f), "f"(x));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(0.f), "f"(x));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(h));
   return d & 0xFFu;
 }
 
@@ -124,10 +126,16 @@ __device__ __forceinline__ float f16_hi(uint32_t v) {
 // eight codes, their scale's bits and g -> eight bf16 values (exact)
 __device__ __forceinline__ uint4 q4_to_bf16(uint32_t code, uint32_t s8, float g) {
   const float m = f16_lo(e4m3x2_to_f16(s8)) * g;
-  uint32_t p[4];
+  const uint64_t m2 = f2_pack(m, m);
+  uint32_t p[4], w[4];
   e2m1x8_to_f16(code, p);
-  return make_uint4(pack_bf16x2(f16_lo(p[0]) * m, f16_hi(p[0]) * m), pack_bf16x2(f16_lo(p[1]) * m, f16_hi(p[1]) * m),
-                    pack_bf16x2(f16_lo(p[2]) * m, f16_hi(p[2]) * m), pack_bf16x2(f16_lo(p[3]) * m, f16_hi(p[3]) * m));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f2_unpack(f2_mul(f2_pack(f16_lo(p[i]), f16_hi(p[i])), m2), lo, hi);
+    w[i] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace llama

@@ -10,15 +10,17 @@
 // and the one rounding of the output.
 //
 // Bound by HBM (2 bytes read and 2 written an element).  A row sits in D / 8
-// lanes, 16 bytes each, so the sum of squares is log2(D / 8) shuffles and the
-// half layout's partner is R / 16 lanes away: the lanes exchange the raw bf16
-// words (4 shuffles).  A CTA serves one token (or some rounds of its rows, when
-// tokens are few): all its rows are requested first, kRows a thread; meanwhile
-// R / 2 threads compute the token's cosines and sines, and every lane folds them
-// with the norm weights into two factors per element, so that a row costs
-//   y = inv * (x * (w cos) + x' * (w' sin))
-// with inv = rsqrt(mean(x^2) + eps).  (Rows one after the other, each waiting for
-// its load: 371 us for 32768 tokens x 72 heads x 128.)
+// lanes; a lane holds four rotated pairs whole (elements 4c .. and R/2 + 4c .. of
+// the half layout, 8c .. of the interleaved one; eight neighbours past R), so
+// that nothing but the sum of squares crosses lanes and the arithmetic runs on
+// two elements an instruction.  A warp takes one token (a part of its rows, when
+// tokens are few): two or four lanes' worth of cosines and sines a lane, exchanged
+// through shared memory and folded with the norm weights into two factors per
+// element, then its rows, kRounds of them in flight while as many are worked on:
+//   y = inv * (x * (w cos) + x' * (w' sin)),  inv = rsqrt(mean(x^2) + eps)
+// (A CTA of 256 threads a token, with 16-byte chunks whose partners came by
+// shuffles, spent 189 instructions a chunk and took 297 us for 32768 tokens x 72
+// heads x 128.)
 //
 // Angles: inv_freq / 2 pi is computed on the host in double and passed as two
 // floats; position * (hi + lo) is reduced to a fraction of a revolution with the
@@ -35,7 +37,10 @@ namespace llama {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRounds = 4;  // rounds of rows (32 / (D / 8) each) loaded at once
+constexpr int kCtasPerSm = 5;
 constexpr int kMaxPairs = 64;
 
 struct RopeTable {
@@ -43,174 +48,192 @@ struct RopeTable {
 };
 
 struct QkParams {
-  const uint4 *q, *k, *qw, *kw;
-  uint4 *q_out, *k_out;
+  const uint2 *q, *k, *qw, *kw;
+  uint2 *q_out, *k_out;
   const int32_t* positions;
-  long long q_stride, k_stride, q_out_stride, k_out_stride;  // 16-byte chunks a token
-  int nq, nkv, rot, inter;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // 8-byte chunks a token
+  int T, nq, nkv, rot;
+  int parts;  // warps a token
   float eps, factor;
 };
 
-__device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
-  v[0] = bf16_lo(u.x);
-  v[1] = bf16_hi(u.x);
-  v[2] = bf16_lo(u.y);
-  v[3] = bf16_hi(u.y);
-  v[4] = bf16_lo(u.z);
-  v[5] = bf16_hi(u.z);
-  v[6] = bf16_lo(u.w);
-  v[7] = bf16_hi(u.w);
+// Four pairs a lane: a[i], b[i] the elements of pair i, two pairs to a register
+// pair.  Half layout: u = a0 a1 a2 a3, v = b0 b1 b2 b3; interleaved: u v = a0 b0
+// a1 b1 ...
+struct Pairs {
+  uint64_t a[2], b[2];
+};
+
+template <bool INTER>
+__device__ __forceinline__ Pairs unpack(uint2 u, uint2 v) {
+  Pairs x;
+  if constexpr (INTER) {
+    x.a[0] = f2_pack(bf16_lo(u.x), bf16_lo(u.y));
+    x.b[0] = f2_pack(bf16_hi(u.x), bf16_hi(u.y));
+    x.a[1] = f2_pack(bf16_lo(v.x), bf16_lo(v.y));
+    x.b[1] = f2_pack(bf16_hi(v.x), bf16_hi(v.y));
+  } else {
+    x.a[0] = f2_pack(bf16_lo(u.x), bf16_hi(u.x));
+    x.a[1] = f2_pack(bf16_lo(u.y), bf16_hi(u.y));
+    x.b[0] = f2_pack(bf16_lo(v.x), bf16_hi(v.x));
+    x.b[1] = f2_pack(bf16_lo(v.y), bf16_hi(v.y));
+  }
+  return x;
 }
 
-// Rows of one of q and k: U rounds of them (kThreads / (D / 8) rows each) from
-// round first on, already loaded in u.
-template <int D, int U>
-__device__ __forceinline__ void norm_rope_rows(const uint4 (&u)[U], const float (&co)[8], const float (&sn)[8],
-                                               bool normed, const QkParams& p, int src, uint32_t partner_bits,
-                                               int row0, int rows, uint4* out, int c) {
-  constexpr int L = D / 8, R = kThreads / L;
-#pragma unroll
-  for (int n = 0; n < U; ++n) {
-    const int row = row0 + n * R;
-    uint4 v;
-    if (p.inter) {
-      v.x = __funnelshift_l(u[n].x, u[n].x, 16);
-      v.y = __funnelshift_l(u[n].y, u[n].y, 16);
-      v.z = __funnelshift_l(u[n].z, u[n].z, 16);
-      v.w = __funnelshift_l(u[n].w, u[n].w, 16);
-    } else {
-      v.x = __shfl_sync(0xffffffffu, u[n].x, src);
-      v.y = __shfl_sync(0xffffffffu, u[n].y, src);
-      v.z = __shfl_sync(0xffffffffu, u[n].z, src);
-      v.w = __shfl_sync(0xffffffffu, u[n].w, src);
-    }
-    v.x &= partner_bits;  // an element that is not rotated has no partner
-    v.y &= partner_bits;
-    v.z &= partner_bits;
-    v.w &= partner_bits;
-    float x[8], y[8];
-    unpack8(u[n], x);
-    unpack8(v, y);
-    float inv = 1.f;
-    if (normed) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      inv = rsqrtf(ss * (1.f / D) + p.eps);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = inv * fmaf(y[e], sn[e], x[e] * co[e]);
-    if (row < rows)
-      out[static_cast<long long>(row) * L + c] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+template <bool INTER>
+__device__ __forceinline__ void pack(const Pairs& x, uint2& u, uint2& v) {
+  float a[4], b[4];
+  f2_unpack(x.a[0], a[0], a[1]);
+  f2_unpack(x.a[1], a[2], a[3]);
+  f2_unpack(x.b[0], b[0], b[1]);
+  f2_unpack(x.b[1], b[2], b[3]);
+  if constexpr (INTER) {
+    u = make_uint2(pack_bf16x2(a[0], b[0]), pack_bf16x2(a[1], b[1]));
+    v = make_uint2(pack_bf16x2(a[2], b[2]), pack_bf16x2(a[3], b[3]));
+  } else {
+    u = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    v = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
   }
 }
 
-// QU: rounds of q rows loaded at once (the rows beyond them in further turns)
-template <int D, int QU>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant__ RopeTable tab, const QkParams p) {
-  constexpr int L = D / 8;              // lanes a row
-  constexpr int R = kThreads / L;       // rows of the CTA at a time
-  __shared__ float2 cs[kMaxPairs];
-  const long long t = blockIdx.x;
-  const int c = threadIdx.x % L, group = threadIdx.x / L;
-  // the rounds of this CTA: of all q rounds, then the k rounds
-  const int q_rounds = (p.nq + R - 1) / R, k_rounds = (p.nkv + R - 1) / R;
-  const int share = (q_rounds + k_rounds + gridDim.y - 1) / gridDim.y;
-  const int first = blockIdx.y * share, last = min(q_rounds + k_rounds, first + share);
-  const uint4* q = p.q + t * p.q_stride;
-  const uint4* k = p.k + t * p.k_stride;
-  uint4 u[QU], uk[1];
-  auto load = [&](auto& v, const uint4* x, int row0, int rows) {
-#pragma unroll
-    for (int n = 0; n < static_cast<int>(sizeof(v) / sizeof(v[0])); ++n) {
-      const int row = row0 + n * R;
-      v[n] = make_uint4(0, 0, 0, 0);
-      if (row < rows) v[n] = x[static_cast<long long>(row) * L + c];
-    }
-  };
-  const int q_last = min(last, q_rounds);          // q rounds [first, q_last)
-  const int k_first = max(first, q_rounds) - q_rounds, k_last = last - q_rounds;
-  const int q_end = min(p.nq, q_last * R);          // q rows of this CTA end here
-  if (first < q_last) load(u, q, first * R + group, q_end);
-  if (k_first < k_last) load(uk, k, k_first * R + group, p.nkv);
+// y_a = x_a aa + x_b ab,  y_b = x_b bb + x_a ba
+struct Factors {
+  uint64_t aa[2], ab[2], bb[2], ba[2];
+};
+
+// PARTIAL: some elements are not rotated; their lanes keep x' out of the sums (an
+// infinity times a zero sine would be a NaN).
+template <int D, bool INTER, bool PARTIAL>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_qk_norm_rope(const __grid_constant__ RopeTable tab, const QkParams p) {
+  constexpr int L = D / 8;   // lanes a row
+  constexpr int R = 32 / L;  // rows a round
+  __shared__ float2 cs_all[kWarps][kMaxPairs];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % L, sub = lane / L;
+  float2* cs = cs_all[warp];
   const int pairs = p.rot / 2;
-  if (threadIdx.x < pairs) {
-    // the position in two floats (the low part is zero below 2^24)
-    const int pos = p.positions[t];
-    const float ph = static_cast<float>(pos);
-    const float pl = static_cast<float>(static_cast<long long>(pos) - static_cast<long long>(ph));
-    const float2 r = tab.rev[threadIdx.x];
-    const float m = ph * r.x;
-    const float e = fmaf(ph, r.x, -m) + (ph * r.y + pl * r.x);
-    float sn, co;
-    sincospif(2.f * ((m - rintf(m)) + e), &sn, &co);
-    cs[threadIdx.x] = make_float2(co * p.factor, sn * p.factor);
-  }
-  __syncthreads();
-  // the eight elements of this lane: rotated ones take pairs pair0 .. (half
-  // layout: eight pairs and a partner lane; interleaved: four pairs of its own)
-  const bool rotated = c * 8 < p.rot;
-  const bool upper = !p.inter && rotated && c * 8 >= pairs;
-  const int partner = !rotated || p.inter ? c : upper ? c - pairs / 8 : c + pairs / 8;
-  float co[8], sn[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int pair = p.inter ? c * 4 + e / 2 : c * 8 + e - (upper ? pairs : 0);
-    const float2 v = rotated ? cs[pair] : make_float2(1.f, 0.f);
-    co[e] = v.x;
-    sn[e] = (p.inter ? !(e & 1) : !upper) ? -v.y : v.y;
-  }
-  const int lane = threadIdx.x & 31, src = (lane / L) * L + partner;
-  const uint32_t partner_bits = rotated ? 0xffffffffu : 0u;
-  // the factors with a norm's weights
-  auto weighted = [&](const uint4* w, float (&cw)[8], float (&sw)[8]) {
-    float wx[8], wy[8];
-    const uint4 wu = w[c];
-    unpack8(wu, wx);
-    uint4 wv = w[partner];
-    if (p.inter) {
-      wv.x = __funnelshift_l(wu.x, wu.x, 16);
-      wv.y = __funnelshift_l(wu.y, wu.y, 16);
-      wv.z = __funnelshift_l(wu.z, wu.z, 16);
-      wv.w = __funnelshift_l(wu.w, wu.w, 16);
-    }
-    unpack8(wv, wy);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cw[e] = co[e] * wx[e];
-      sw[e] = sn[e] * wy[e];
-    }
-  };
-  float cw[8], sw[8];
-  auto factors = [&](const uint4* w) {
-    if (w != nullptr) {
-      weighted(w, cw, sw);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cw[e] = co[e];
-        sw[e] = sn[e];
+  const bool rotated = !PARTIAL || c * 8 < p.rot;
+  // the lane's two 8-byte chunks of a row
+  const int at0 = INTER ? 2 * c : rotated ? c : p.rot / 4 + 2 * (c - p.rot / 8);
+  const int at1 = INTER || !rotated ? at0 + 1 : c + p.rot / 8;
+  const uint64_t keep = rotated ? ~0ull : 0ull;
+  const int q_rounds = (p.nq + R - 1) / R, rounds = q_rounds + (p.nkv + R - 1) / R;
+  const int share = (rounds + p.parts - 1) / p.parts;
+  const long long units = static_cast<long long>(p.T) * p.parts;
+  for (long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp; unit < units;
+       unit += static_cast<long long>(gridDim.x) * kWarps) {
+    const long long t = p.parts == 1 ? unit : unit / p.parts;
+    const int first = static_cast<int>(unit - t * p.parts) * share, last = min(rounds, first + share);
+    if (first >= last) continue;
+    // a row of q, then of k; rounds do not mix the two
+    auto load = [&](int r, uint2& u, uint2& v) {
+      const bool is_k = r >= q_rounds;
+      const int row = (is_k ? r - q_rounds : r) * R + sub;
+      u = v = make_uint2(0, 0);
+      if (r < last && row < (is_k ? p.nkv : p.nq)) {
+        const uint2* src = (is_k ? p.k + t * p.k_stride : p.q + t * p.q_stride) + row * (D / 4);
+        u = src[at0];
+        v = src[at1];
       }
+    };
+    uint2 u[kRounds], v[kRounds];
+#pragma unroll
+    for (int n = 0; n < kRounds; ++n) load(first + n, u[n], v[n]);
+    if (pairs > 0) {
+      // the position in two floats (the low part is zero below 2^24)
+      const int pos = p.positions[t];
+      const float ph = static_cast<float>(pos);
+      const float pl = static_cast<float>(static_cast<long long>(pos) - static_cast<long long>(ph));
+      __syncwarp();
+      for (int i = lane; i < pairs; i += 32) {
+        const float2 rev = tab.rev[i];
+        const float m = ph * rev.x;
+        const float e = fmaf(ph, rev.x, -m) + (ph * rev.y + pl * rev.x);
+        float sn, co;
+        sincospif(2.f * ((m - rintf(m)) + e), &sn, &co);
+        cs[i] = make_float2(co * p.factor, sn * p.factor);
+      }
+      __syncwarp();
     }
-  };
-  if (first < q_last) {
-    factors(p.qw);
-    uint4* out = p.q_out + t * p.q_out_stride;
-    for (int r = first; r < q_last; r += QU) {
-      if (r > first) load(u, q, r * R + group, q_end);
-      norm_rope_rows<D, QU>(u, cw, sw, p.qw != nullptr, p, src, partner_bits, r * R + group, q_end, out, c);
-    }
-  }
-  if (k_first < k_last) {
-    factors(p.kw);
-    uint4* out = p.k_out + t * p.k_out_stride;
-    const int k_end = min(p.nkv, k_last * R);
-    for (int r = k_first; r < k_last; ++r) {
-      if (r > k_first) load(uk, k, r * R + group, k_end);
-      norm_rope_rows<D, 1>(uk, cw, sw, p.kw != nullptr, p, src, partner_bits, r * R + group, k_end, out, c);
+    Factors f;
+    auto factors = [&](const uint2* w) {
+      uint64_t co[2], sn[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 x = rotated && pairs > 0 ? cs[4 * c + 2 * i] : make_float2(1.f, 0.f);
+        const float2 y = rotated && pairs > 0 ? cs[4 * c + 2 * i + 1] : make_float2(1.f, 0.f);
+        co[i] = f2_pack(x.x, y.x);
+        sn[i] = f2_pack(x.y, y.y);
+      }
+      const uint64_t minus = f2_pack(-1.f, -1.f);
+      if (w != nullptr) {
+        const Pairs n = unpack<INTER>(w[at0], w[at1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f.aa[i] = f2_mul(co[i], n.a[i]);
+          f.bb[i] = f2_mul(co[i], n.b[i]);
+          f.ab[i] = f2_mul(f2_mul(sn[i], n.b[i]), minus);
+          f.ba[i] = f2_mul(sn[i], n.a[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f.aa[i] = f.bb[i] = co[i];
+          f.ab[i] = f2_mul(sn[i], minus);
+          f.ba[i] = sn[i];
+        }
+      }
+    };
+    auto finish = [&](int r, uint2 u0, uint2 v0) {
+      const bool is_k = r >= q_rounds;
+      const Pairs x = unpack<INTER>(u0, v0);
+      float inv = 1.f;
+      if ((is_k ? p.kw : p.qw) != nullptr) {
+        uint64_t s2 = f2_mul(x.a[0], x.a[0]);
+        s2 = f2_fma(x.a[1], x.a[1], s2);
+        s2 = f2_fma(x.b[0], x.b[0], s2);
+        s2 = f2_fma(x.b[1], x.b[1], s2);
+        float s0, s1;
+        f2_unpack(s2, s0, s1);
+        float ss = s0 + s1;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        inv = rsqrtf(ss * (1.f / D) + p.eps);
+      }
+      const uint64_t inv2 = f2_pack(inv, inv);
+      Pairs y;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t xb = PARTIAL ? x.b[i] & keep : x.b[i], xa = PARTIAL ? x.a[i] & keep : x.a[i];
+        y.a[i] = f2_mul(inv2, f2_fma(x.a[i], f.aa[i], f2_mul(xb, f.ab[i])));
+        y.b[i] = f2_mul(inv2, f2_fma(x.b[i], f.bb[i], f2_mul(xa, f.ba[i])));
+      }
+      const int row = (is_k ? r - q_rounds : r) * R + sub;
+      if (row < (is_k ? p.nkv : p.nq)) {
+        uint2* dst = (is_k ? p.k_out + t * p.k_out_stride : p.q_out + t * p.q_out_stride) + row * (D / 4);
+        pack<INTER>(y, u0, v0);
+        dst[at0] = u0;
+        dst[at1] = v0;
+      }
+    };
+    if (first < q_rounds) factors(p.qw);
+    for (int r = first; r < last; r += kRounds) {
+      uint2 un[kRounds], vn[kRounds];
+      if (r + kRounds < last) {
+#pragma unroll
+        for (int n = 0; n < kRounds; ++n) load(r + kRounds + n, un[n], vn[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < kRounds; ++n) {
+        if (r + n >= last) break;
+        if (r + n == q_rounds || (r + n == first && first > q_rounds)) factors(p.kw);
+        finish(r + n, u[n], v[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < kRounds; ++n) {
+        u[n] = un[n];
+        v[n] = vn[n];
+      }
     }
   }
 }
@@ -257,34 +280,41 @@ int qk_norm_rope_launch(const QkNormRopeArgs& a, cudaStream_t s) {
   if (a.T <= 0) return 0;
   const LlamaQkNormRopeConfig& c = *a.cfg;
   QkParams p{};
-  p.q = static_cast<const uint4*>(a.q);
-  p.k = static_cast<const uint4*>(a.k);
-  p.qw = static_cast<const uint4*>(a.q_norm_w);
-  p.kw = static_cast<const uint4*>(a.k_norm_w);
-  p.q_out = static_cast<uint4*>(a.q_out);
-  p.k_out = static_cast<uint4*>(a.k_out);
+  p.q = static_cast<const uint2*>(a.q);
+  p.k = static_cast<const uint2*>(a.k);
+  p.qw = static_cast<const uint2*>(a.q_norm_w);
+  p.kw = static_cast<const uint2*>(a.k_norm_w);
+  p.q_out = static_cast<uint2*>(a.q_out);
+  p.k_out = static_cast<uint2*>(a.k_out);
   p.positions = a.positions;
-  p.q_stride = a.q_stride / 8;
-  p.k_stride = a.k_stride / 8;
-  p.q_out_stride = a.q_out_stride / 8;
-  p.k_out_stride = a.k_out_stride / 8;
+  p.q_stride = a.q_stride / 4;
+  p.k_stride = a.k_stride / 4;
+  p.q_out_stride = a.q_out_stride / 4;
+  p.k_out_stride = a.k_out_stride / 4;
+  p.T = a.T;
   p.nq = c.n_heads;
   p.nkv = c.n_kv_heads;
   p.rot = c.rotary_dim;
-  p.inter = c.interleaved;
   p.eps = c.rms_eps;
   p.factor = c.rope_scaling == LLAMA_ROPE_YARN ? c.rs_attention_factor : 1.f;
   const RopeTable tab = rope_table(c);
-  const int per = kThreads / (c.head_dim / 8);
-  const int q_rounds = (p.nq + per - 1) / per, k_rounds = (p.nkv + per - 1) / per;
-  // few tokens: a CTA for every round of rows of a token, so that they run side by side
-  const bool split = static_cast<long long>(a.T) * (q_rounds + k_rounds) <= 8LL * num_sms();
-  const dim3 grid(a.T, split ? q_rounds + k_rounds : 1);
+  // Few tokens: a token's rounds are shared by several warps (two rounds each at least), so that they run side by
+  // side; from 16 warps an SM on, a warp a token.
+  const int per = 32 / (c.head_dim / 8);
+  const int rounds = (p.nq + per - 1) / per + (p.nkv + per - 1) / per;
+  const long long want = 16LL * num_sms() / a.T;
+  const int most = (rounds + 1) / 2;
+  p.parts = want < 1 ? 1 : want > most ? most : static_cast<int>(want);
+  const long long ctas = (static_cast<long long>(a.T) * p.parts + kWarps - 1) / kWarps, full = 1LL * kCtasPerSm * num_sms();
+  const dim3 grid(static_cast<unsigned>(ctas < full ? ctas : full));
   auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kThreads), 0, s, false, tab, p); };
-  const bool one = split || q_rounds == 1;
-  if (c.head_dim == 128)
-    return one ? go(k_qk_norm_rope<128, 1>) : q_rounds == 2 ? go(k_qk_norm_rope<128, 2>) : go(k_qk_norm_rope<128, 4>);
-  return one ? go(k_qk_norm_rope<64, 1>) : q_rounds == 2 ? go(k_qk_norm_rope<64, 2>) : go(k_qk_norm_rope<64, 4>);
+  const bool partial = p.rot < c.head_dim;
+  if (c.head_dim == 128) {
+    if (c.interleaved) return partial ? go(k_qk_norm_rope<128, true, true>) : go(k_qk_norm_rope<128, true, false>);
+    return partial ? go(k_qk_norm_rope<128, false, true>) : go(k_qk_norm_rope<128, false, false>);
+  }
+  if (c.interleaved) return partial ? go(k_qk_norm_rope<64, true, true>) : go(k_qk_norm_rope<64, true, false>);
+  return partial ? go(k_qk_norm_rope<64, false, true>) : go(k_qk_norm_rope<64, false, false>);
 }
 
 }  // namespace llama
