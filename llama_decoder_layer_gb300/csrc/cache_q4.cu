@@ -38,73 +38,103 @@ struct Shape {
   int chunks, rows, parts;
 };
 
-// This thread's chunk (head h, chunk c of it) and its first token; -1: none.
+// This thread's chunk c of head h (c < 0: none) and the first of its U tokens, `rows` apart.
+struct Place {
+  long long t0;
+  int h, c;
+};
+
 template <int D, int U>
-__device__ __forceinline__ long long place(const Shape& g, int& h, int& c, bool& is_v) {
+__device__ __forceinline__ Place place(const Shape& g) {
   constexpr int C = D / 8;
-  const int part = blockIdx.y >> 1, row = threadIdx.x / g.chunks;
-  const int r = g.parts > 1 ? part * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)
+  const int row = threadIdx.x / g.chunks;
+  const int r = g.parts > 1 ? static_cast<int>((blockIdx.y >> 1) * blockDim.x + threadIdx.x)
                             : static_cast<int>(threadIdx.x) - row * g.chunks;
-  is_v = blockIdx.y & 1;
-  h = r / C;
-  c = r % C;
-  if (r >= g.chunks) return -1;
-  return static_cast<long long>(blockIdx.x) * g.rows * U + (g.parts > 1 ? 0 : row);
+  Place x;
+  x.h = r / C;
+  x.c = r < g.chunks ? r % C : -1;
+  x.t0 = static_cast<long long>(blockIdx.x) * g.rows * U + (g.parts > 1 ? 0 : row);
+  return x;
 }
 
-// the slots of this thread's tokens: -1 where there is nothing to do
+// the slots of this thread's tokens; -1 where there is nothing to do
 template <int U>
-__device__ __forceinline__ void load_slots(const CacheQ4Args& a, const Shape& g, long long t0, bool reports,
+__device__ __forceinline__ void load_slots(const CacheQ4Args& a, const Shape& g, const Place& x, bool reports,
                                            int (&slot)[U]) {
+  bool past = false;
 #pragma unroll
   for (int n = 0; n < U; ++n) {
-    const long long t = t0 + n * g.rows;
-    slot[n] = t0 >= 0 && t < a.T ? a.slots[t] : -1;
+    const long long t = x.t0 + n * g.rows;
+    slot[n] = x.c >= 0 && t < a.T ? a.slots[t] : -1;
   }
 #pragma unroll
-  for (int n = 0; n < U; ++n)
-    if (slot[n] >= a.num_blocks * kQ4Block) {
-      if (reports) report_error(a.err, kErrGuard, kWhereSlot);
-      slot[n] = -1;
-    }
+  for (int n = 0; n < U; ++n) {
+    const bool over = slot[n] >= a.num_blocks * kQ4Block;
+    past |= over;
+    slot[n] = over ? -1 : slot[n];
+  }
+  if (past && reports) report_error(a.err, kErrGuard, kWhereSlot);
 }
 
-template <int D, int U>
-__global__ void __launch_bounds__(kMaxThreads) k_kv_write_q4(const CacheQ4Args a, const Shape g) {
-  int h, c, slot[U];
-  bool is_v;
-  const long long t0 = place<D, U>(g, h, c, is_v);
-  const long long stride = is_v ? a.v_stride : a.k_stride;
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? a.v : a.k) + t0 * stride + h * D + c * 8;
+// What depends on the chunk alone in the places of its codes and its scale, and the step from tile to tile.
+template <int D, bool V>
+struct Bytes {
+  int code, scale;
+  __device__ __forceinline__ explicit Bytes(int c)
+      : code(q4_code_at<D>(V, 0, c)), scale(q4_scale_at<D>(V, 0, c >> 1)) {}
+  __device__ __forceinline__ int code_at(int k) const { return code + q4_code_at<D>(V, k, 0); }
+  __device__ __forceinline__ int scale_at(int k) const { return scale + q4_scale_at<D>(V, k, 0) - 8 * D; }
+};
+
+template <int D, int U, bool V>
+__device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g) {
+  const Place x = place<D, U>(g);
+  const long long stride = V ? a.v_stride : a.k_stride, step = g.rows * stride;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(V ? a.v : a.k) + x.t0 * stride + x.h * D + x.c * 8;
   uint4 u[U];
 #pragma unroll
   for (int n = 0; n < U; ++n) {  // before the slots are known: every row may be read
     u[n] = make_uint4(0, 0, 0, 0);
-    if (t0 >= 0 && t0 + n * g.rows < a.T) u[n] = *reinterpret_cast<const uint4*>(src + n * g.rows * stride);
+    if (x.c >= 0 && x.t0 + n * g.rows < a.T) u[n] = *reinterpret_cast<const uint4*>(src + n * step);
   }
-  load_slots<U>(a, g, t0, h == 0 && c == 0 && !is_v, slot);
-  const float inv_g = is_v ? a.inv_v_scale : a.inv_k_scale;
-  uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + static_cast<size_t>(h) * q4_tile_bytes(D);
+  int slot[U];
+  load_slots<U>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
+  float top[U];
+  bool nan = false;
 #pragma unroll
   for (int n = 0; n < U; ++n) {
-    uint32_t w[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
-    __nv_bfloat162 top = __habs2(*reinterpret_cast<__nv_bfloat162*>(&w[0]));
-#pragma unroll
-    for (int e = 1; e < 4; ++e) top = __hmax2_nan(top, __habs2(*reinterpret_cast<__nv_bfloat162*>(&w[e])));
-    float amax = __bfloat162float(__hmax_nan(__low2bfloat16(top), __high2bfloat16(top)));
-    if (amax != amax) {  // rare: NaN counts as zero
-      amax = 0.f;
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&u[n]);
+    __nv_bfloat162 m = __hmax2_nan(__habs2(w[0]), __habs2(w[1]));
+    m = __hmax2_nan(m, __hmax2_nan(__habs2(w[2]), __habs2(w[3])));
+    top[n] = __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+    nan |= top[n] != top[n];
+  }
+  if (nan) {  // rare: a NaN counts as zero
+#pragma unroll 1
+    for (int n = 0; n < U; ++n) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&u[n]);
+      float m = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if ((w[e] & 0x7FFFu) > 0x7F80u) w[e] &= 0xFFFF0000u;
         if ((w[e] & 0x7FFF0000u) > 0x7F800000u) w[e] &= 0xFFFFu;
-        amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+        m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
       }
+      top[n] = m;
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // the group's other half is in the next lane
+  }
+  __syncwarp();
+  const float inv_g = V ? a.inv_v_scale : a.inv_k_scale;
+  const Bytes<D, V> at(x.c);
+  uint8_t* cache = static_cast<uint8_t*>(V ? a.v_cache : a.k_cache) + static_cast<size_t>(x.h) * q4_tile_bytes(D);
+  const uint32_t block_bytes = static_cast<uint32_t>(a.n_kv) * q4_tile_bytes(D);
+#pragma unroll
+  for (int n = 0; n < U; ++n) {
+    const float amax = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 1));  // the group's other half: the next lane
     const uint32_t s8 = f32_to_e4m3_by_f16(amax * (inv_g * (1.f / 6.f)));
     const float inv = s8 == 0 ? 0.f : __fdividef(inv_g, f16_lo(e4m3x2_to_f16(s8)));
     constexpr float kSnap = 1.5f * 1024.f;  // sums with it are multiples of 2^-13 below 2^10
+    const uint32_t w[4] = {u[n].x, u[n].y, u[n].z, u[n].w};
     float y[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -114,45 +144,62 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_write_q4(const CacheQ4Args a
     }
     const uint32_t code = s8 == 0 ? 0u : f32x8_to_e2m1(y);
     const uint32_t next = __shfl_down_sync(0xffffffffu, s8, 2);  // the next group's scale (K stores two at D = 128)
-    if (slot[n] >= 0) {
-      const int k = slot[n] & 15, s = c >> 1;
-      uint8_t* tile = cache + static_cast<size_t>(slot[n] >> 4) * (static_cast<size_t>(a.n_kv) * q4_tile_bytes(D));
-      *reinterpret_cast<uint32_t*>(tile + q4_code_at<D>(is_v, k, c)) = code;
-      if (D == 128 && !is_v) {
-        if ((c & 3) == 0)
-          *reinterpret_cast<uint16_t*>(tile + q4_k_scale_at<D>(k, s)) = static_cast<uint16_t>(s8 | (next << 8));
-      } else if ((c & 1) == 0) {
-        tile[q4_scale_at<D>(is_v, k, s)] = static_cast<uint8_t>(s8);
-      }
+    const int k = slot[n] & 15;
+    uint8_t* tile = cache + static_cast<size_t>(static_cast<uint32_t>(slot[n]) >> 4) * block_bytes;
+    if (slot[n] >= 0) *reinterpret_cast<uint32_t*>(tile + at.code_at(k)) = code;
+    if (D == 128 && !V) {
+      if (slot[n] >= 0 && (x.c & 3) == 0)
+        *reinterpret_cast<uint16_t*>(tile + at.scale_at(k)) = static_cast<uint16_t>(s8 | (next << 8));
+    } else {
+      if (slot[n] >= 0 && (x.c & 1) == 0) tile[at.scale_at(k)] = static_cast<uint8_t>(s8);
     }
   }
 }
 
-template <int D, int U>
-__global__ void __launch_bounds__(kMaxThreads) k_kv_read_q4(const CacheQ4Args a, const Shape g) {
-  int h, c, slot[U];
-  bool is_v;
-  const long long t0 = place<D, U>(g, h, c, is_v);
-  load_slots<U>(a, g, t0, h == 0 && c == 0 && !is_v, slot);
+template <int D, int U, bool V>
+__device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) {
+  const Place x = place<D, U>(g);
+  int slot[U];
+  load_slots<U>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
+  const Bytes<D, V> at(x.c);
   const uint8_t* cache =
-      static_cast<const uint8_t*>(is_v ? a.v_cache : a.k_cache) + static_cast<size_t>(h) * q4_tile_bytes(D);
+      static_cast<const uint8_t*>(V ? a.v_cache : a.k_cache) + static_cast<size_t>(x.h) * q4_tile_bytes(D);
+  const uint32_t block_bytes = static_cast<uint32_t>(a.n_kv) * q4_tile_bytes(D);
   uint32_t code[U], s8[U];
 #pragma unroll
   for (int n = 0; n < U; ++n) {
-    code[n] = s8[n] = 0;
-    if (slot[n] < 0) continue;
     const int k = slot[n] & 15;
-    const uint8_t* tile =
-        cache + static_cast<size_t>(slot[n] >> 4) * (static_cast<size_t>(a.n_kv) * q4_tile_bytes(D));
-    code[n] = *reinterpret_cast<const uint32_t*>(tile + q4_code_at<D>(is_v, k, c));
-    s8[n] = tile[q4_scale_at<D>(is_v, k, c >> 1)];
+    const uint8_t* tile = cache + static_cast<size_t>(static_cast<uint32_t>(slot[n]) >> 4) * block_bytes;
+    code[n] = s8[n] = 0;
+    if (slot[n] >= 0) {
+      code[n] = *reinterpret_cast<const uint32_t*>(tile + at.code_at(k));
+      s8[n] = tile[at.scale_at(k)];
+    }
   }
-  const long long stride = is_v ? a.v_stride : a.k_stride;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(is_v ? a.v_out : a.k_out) + t0 * stride + h * D + c * 8;
-  const float scale = is_v ? a.v_scale : a.k_scale;
+  const long long stride = V ? a.v_stride : a.k_stride, step = g.rows * stride;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(V ? a.v_out : a.k_out) + x.t0 * stride + x.h * D + x.c * 8;
+  const float scale = V ? a.v_scale : a.k_scale;
 #pragma unroll
-  for (int n = 0; n < U; ++n)
-    if (slot[n] >= 0) *reinterpret_cast<uint4*>(dst + n * g.rows * stride) = q4_to_bf16(code[n], s8[n], scale);
+  for (int n = 0; n < U; ++n) {
+    const uint4 v = q4_to_bf16(code[n], s8[n], scale);
+    if (slot[n] >= 0) *reinterpret_cast<uint4*>(dst + n * step) = v;
+  }
+}
+
+template <int D, int U>
+__global__ void __launch_bounds__(kMaxThreads) k_kv_write_q4(const CacheQ4Args a, const Shape g) {
+  if (blockIdx.y & 1)
+    write_rows<D, U, true>(a, g);
+  else
+    write_rows<D, U, false>(a, g);
+}
+
+template <int D, int U>
+__global__ void __launch_bounds__(kMaxThreads) k_kv_read_q4(const CacheQ4Args a, const Shape g) {
+  if (blockIdx.y & 1)
+    read_rows<D, U, true>(a, g);
+  else
+    read_rows<D, U, false>(a, g);
 }
 
 // U = 4 tokens a thread where that still gives every SM four CTAs, else one
