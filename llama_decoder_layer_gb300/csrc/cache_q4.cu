@@ -40,38 +40,47 @@ struct Shape {
 
 // This thread's chunk c of head h (c < 0: none) and the first of its U tokens, `rows` apart.
 struct Place {
-  long long t0;
+  uint32_t t0;
   int h, c;
 };
 
-template <int D, int U>
+// v, known to be the same in every lane of the warp if WHOLE
+template <bool WHOLE>
+__device__ __forceinline__ int warp_value(int v) {
+  return WHOLE ? __shfl_sync(0xffffffffu, v, 0) : v;
+}
+
+// WHOLE: a row is a whole number of warps, so that its token, slot and tile are a warp's (and cost a lane nothing)
+template <int D, int U, bool WHOLE>
 __device__ __forceinline__ Place place(const Shape& g) {
   constexpr int C = D / 8;
-  const int row = threadIdx.x / g.chunks;
+  const int row = warp_value<WHOLE>(threadIdx.x / g.chunks);
   const int r = g.parts > 1 ? static_cast<int>((blockIdx.y >> 1) * blockDim.x + threadIdx.x)
                             : static_cast<int>(threadIdx.x) - row * g.chunks;
   Place x;
   x.h = r / C;
   x.c = r < g.chunks ? r % C : -1;
-  x.t0 = static_cast<long long>(blockIdx.x) * g.rows * U + (g.parts > 1 ? 0 : row);
+  x.t0 = blockIdx.x * static_cast<uint32_t>(g.rows * U) + (g.parts > 1 ? 0 : row);  // below T + rows * U < 2^32
   return x;
 }
 
 // the slots of this thread's tokens; -1 where there is nothing to do
-template <int U>
+template <int U, bool WHOLE>
 __device__ __forceinline__ void load_slots(const CacheQ4Args& a, const Shape& g, const Place& x, bool reports,
                                            int (&slot)[U]) {
   bool past = false;
 #pragma unroll
   for (int n = 0; n < U; ++n) {
-    const long long t = x.t0 + n * g.rows;
-    slot[n] = x.c >= 0 && t < a.T ? a.slots[t] : -1;
+    const uint32_t t = x.t0 + n * g.rows;
+    slot[n] = t < static_cast<uint32_t>(a.T) ? a.slots[t] : -1;
   }
 #pragma unroll
   for (int n = 0; n < U; ++n) {
+    slot[n] = warp_value<WHOLE>(slot[n]);
     const bool over = slot[n] >= a.num_blocks * kQ4Block;
     past |= over;
-    slot[n] = over ? -1 : slot[n];
+    if (over) slot[n] = -1;
+    if (!WHOLE && x.c < 0) slot[n] = -1;
   }
   if (past && reports) report_error(a.err, kErrGuard, kWhereSlot);
 }
@@ -86,19 +95,19 @@ struct Bytes {
   __device__ __forceinline__ int scale_at(int k) const { return scale + q4_scale_at<D>(V, k, 0) - 8 * D; }
 };
 
-template <int D, int U, bool V>
+template <int D, int U, bool WHOLE, bool V>
 __device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g) {
-  const Place x = place<D, U>(g);
+  const Place x = place<D, U, WHOLE>(g);
   const long long stride = V ? a.v_stride : a.k_stride, step = g.rows * stride;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(V ? a.v : a.k) + x.t0 * stride + x.h * D + x.c * 8;
   uint4 u[U];
 #pragma unroll
   for (int n = 0; n < U; ++n) {  // before the slots are known: every row may be read
     u[n] = make_uint4(0, 0, 0, 0);
-    if (x.c >= 0 && x.t0 + n * g.rows < a.T) u[n] = *reinterpret_cast<const uint4*>(src + n * step);
+    if ((WHOLE || x.c >= 0) && x.t0 + n * g.rows < static_cast<uint32_t>(a.T)) u[n] = *reinterpret_cast<const uint4*>(src + n * step);
   }
   int slot[U];
-  load_slots<U>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
+  load_slots<U, WHOLE>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
   float top[U];
   bool nan = false;
 #pragma unroll
@@ -156,11 +165,11 @@ __device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g)
   }
 }
 
-template <int D, int U, bool V>
+template <int D, int U, bool WHOLE, bool V>
 __device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) {
-  const Place x = place<D, U>(g);
+  const Place x = place<D, U, WHOLE>(g);
   int slot[U];
-  load_slots<U>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
+  load_slots<U, WHOLE>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
   const Bytes<D, V> at(x.c);
   const uint8_t* cache =
       static_cast<const uint8_t*>(V ? a.v_cache : a.k_cache) + static_cast<size_t>(x.h) * q4_tile_bytes(D);
@@ -186,25 +195,26 @@ __device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) 
   }
 }
 
-template <int D, int U>
+template <int D, int U, bool WHOLE>
 __global__ void __launch_bounds__(kMaxThreads) k_kv_write_q4(const CacheQ4Args a, const Shape g) {
   if (blockIdx.y & 1)
-    write_rows<D, U, true>(a, g);
+    write_rows<D, U, WHOLE, true>(a, g);
   else
-    write_rows<D, U, false>(a, g);
+    write_rows<D, U, WHOLE, false>(a, g);
 }
 
-template <int D, int U>
+template <int D, int U, bool WHOLE>
 __global__ void __launch_bounds__(kMaxThreads) k_kv_read_q4(const CacheQ4Args a, const Shape g) {
   if (blockIdx.y & 1)
-    read_rows<D, U, true>(a, g);
+    read_rows<D, U, WHOLE, true>(a, g);
   else
-    read_rows<D, U, false>(a, g);
+    read_rows<D, U, WHOLE, false>(a, g);
 }
 
 // U = 4 tokens a thread where that still gives every SM four CTAs, else one
-template <typename K4, typename K1>
-int launch(K4 four, K1 one, const CacheQ4Args& a, cudaStream_t s) {
+using Kernel = void (*)(const CacheQ4Args, const Shape);
+
+int launch(Kernel four, Kernel one, Kernel four_whole, Kernel one_whole, const CacheQ4Args& a, cudaStream_t s) {
   Shape g{};
   g.chunks = a.n_kv * (a.head_dim / 8);
   int threads = g.chunks;  // the least number of whole rows that is a number of whole warps (chunks is a multiple of 8)
@@ -222,22 +232,27 @@ int launch(K4 four, K1 one, const CacheQ4Args& a, cudaStream_t s) {
   const long long ctas = (static_cast<long long>(a.T) + g.rows - 1) / g.rows, ctas4 = (ctas + 3) / 4;
   const bool u4 = ctas4 * 2 * g.parts >= 4LL * num_sms();
   const dim3 grid(static_cast<unsigned>(u4 ? ctas4 : ctas), 2 * g.parts);
-  return u4 ? launch_kernel(four, grid, dim3(threads), 0, s, false, a, g)
-            : launch_kernel(one, grid, dim3(threads), 0, s, false, a, g);
+  const bool whole = g.chunks % 32 == 0 && (g.parts == 1 || g.chunks % threads == 0);
+  return launch_kernel(whole ? (u4 ? four_whole : one_whole) : (u4 ? four : one), grid, dim3(threads), 0, s, false, a,
+                       g);
 }
 
 }  // namespace
 
 int kv_write_q4_launch(const CacheQ4Args& a, cudaStream_t s) {
   if (a.T <= 0) return 0;
-  return a.head_dim == 128 ? launch(k_kv_write_q4<128, 4>, k_kv_write_q4<128, 1>, a, s)
-                           : launch(k_kv_write_q4<64, 4>, k_kv_write_q4<64, 1>, a, s);
+  return a.head_dim == 128 ? launch(k_kv_write_q4<128, 4, false>, k_kv_write_q4<128, 1, false>,
+                                    k_kv_write_q4<128, 4, true>, k_kv_write_q4<128, 1, true>, a, s)
+                           : launch(k_kv_write_q4<64, 4, false>, k_kv_write_q4<64, 1, false>,
+                                    k_kv_write_q4<64, 4, true>, k_kv_write_q4<64, 1, true>, a, s);
 }
 
 int kv_read_q4_launch(const CacheQ4Args& a, cudaStream_t s) {
   if (a.T <= 0) return 0;
-  return a.head_dim == 128 ? launch(k_kv_read_q4<128, 4>, k_kv_read_q4<128, 1>, a, s)
-                           : launch(k_kv_read_q4<64, 4>, k_kv_read_q4<64, 1>, a, s);
+  return a.head_dim == 128 ? launch(k_kv_read_q4<128, 4, false>, k_kv_read_q4<128, 1, false>,
+                                    k_kv_read_q4<128, 4, true>, k_kv_read_q4<128, 1, true>, a, s)
+                           : launch(k_kv_read_q4<64, 4, false>, k_kv_read_q4<64, 1, false>,
+                                    k_kv_read_q4<64, 4, true>, k_kv_read_q4<64, 1, true>, a, s);
 }
 
 }  // namespace llama

@@ -68,14 +68,15 @@ def unpack_tiles(tiles, d, is_v):
 
 def pack_rows(tiles, slots, code, s8, d, is_v):
     """Rows (codes [n, n_kv, d], scale bits [n, n_kv, d/16]) at slots >= 0 of tiles [blocks, n_kv, 9d], in place."""
-    for i, slot in enumerate(slots):
-        if slot < 0:
-            continue
-        b, k = divmod(int(slot), 16)
-        for e in range(0, d, 2):
-            tiles[b, :, code_place(d, k, e, is_v)] = code[i, :, e] | (code[i, :, e + 1] << 4)
-        for s in range(d // 16):
-            tiles[b, :, scale_place(d, k, s, is_v)] = s8[i, :, s]
+    slots = np.asarray(slots, dtype=np.int64)
+    keep = slots >= 0
+    b, k = slots[keep] // 16, slots[keep] % 16
+    code, s8 = code[keep], s8[keep]
+    heads = np.arange(tiles.shape[1])[None, :]
+    for e in range(0, d, 2):
+        tiles[b[:, None], heads, code_place(d, k, e, is_v)[:, None]] = code[:, :, e] | (code[:, :, e + 1] << 4)
+    for s in range(d // 16):
+        tiles[b[:, None], heads, scale_place(d, k, s, is_v)[:, None]] = s8[:, :, s]
 
 
 def cache_rows(tiles, slots, d, is_v, g):

@@ -71,7 +71,7 @@ def hard_rows(n, nkv, d, seed, g):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("T,nkv", [(1, 1), (5, 3), (16, 8), (37, 2), (300, 5)])
+@pytest.mark.parametrize("T,nkv", [(1, 1), (5, 3), (16, 8), (37, 2), (300, 5), (9, 64), (40, 33), (3, 70), (5300, 8), (20011, 3)])
 @pytest.mark.parametrize("kexp,vexp", [(0, 0), (-5, 3)])
 def test_write_and_read_bit_for_bit(d, T, nkv, kexp, vexp):
     blocks = T // 16 + 4
