@@ -1350,16 +1350,8 @@ int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, At
   // caller's stream forks to it after the previous kernel and joins it before
   // the next.  Otherwise everything runs in order on the caller's stream.
   cudaStream_t sd = s;
-  cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
-  if (a.max_query_len >= 2 && a.overlap) {
-    cudaStream_t side = side_stream();
-    if (side != nullptr && fork_join_events(&ev_fork, &ev_join) && cudaEventRecord(ev_fork, s) == cudaSuccess &&
-        cudaStreamWaitEvent(side, ev_fork, 0) == cudaSuccess) {
-      sd = side;
-    } else {
-      cudaGetLastError();
-    }
-  }
+  cudaEvent_t ev_join = nullptr;
+  if (a.max_query_len >= 2 && a.overlap) sd = side_fork(s, &ev_join);
   const bool forked = sd != s;
   if (joined) *joined = forked;
   // the first kernel on each stream takes the caller's dependency mode (none
@@ -1384,9 +1376,8 @@ int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, At
   if (e == cudaSuccess && a.max_query_len >= 2)
     e = static_cast<cudaError_t>(launch_prefill_d<D>(a, tk, tv, p, tc, tile_tokens, items, pdl_s, s));
   if (forked) {  // join even after a failed launch, so the caller's stream never runs ahead of the side stream
-    const cudaError_t j1 = cudaEventRecord(ev_join, sd);
-    const cudaError_t j2 = j1 == cudaSuccess ? cudaStreamWaitEvent(s, ev_join, 0) : j1;
-    if (e == cudaSuccess) e = j2;
+    const cudaError_t j = static_cast<cudaError_t>(side_join(s, sd, ev_join));
+    if (e == cudaSuccess) e = j;
   }
   return e;
 }
@@ -1458,6 +1449,21 @@ int attention_launch(const AttnArgs& a, cudaStream_t s, bool* joined) {
   if (a.head_dim == 128) return launch_d<128>(a, tk, tv, p, s, joined);
   if (a.head_dim == 64) return launch_d<64>(a, tk, tv, p, s, joined);
   return cudaErrorInvalidValue;
+}
+
+cudaStream_t side_fork(cudaStream_t s, cudaEvent_t* join) {
+  cudaEvent_t fork = nullptr;
+  cudaStream_t side = side_stream();
+  if (side != nullptr && fork_join_events(&fork, join) && cudaEventRecord(fork, s) == cudaSuccess &&
+      cudaStreamWaitEvent(side, fork, 0) == cudaSuccess)
+    return side;
+  cudaGetLastError();
+  return s;
+}
+
+int side_join(cudaStream_t s, cudaStream_t side, cudaEvent_t join) {
+  const cudaError_t e = cudaEventRecord(join, side);
+  return e == cudaSuccess ? cudaStreamWaitEvent(s, join, 0) : e;
 }
 
 int prefill_tile_tokens(const AttnArgs& a) {

@@ -63,6 +63,7 @@ struct Q4Params {
   const uint8_t *k_cache, *v_cache;
   const int32_t *qsl, *seq_lens, *positions, *block_table;
   int T, B, max_blocks, num_blocks, nq, nkv, group, max_query_len, max_seq_len;
+  int rows_lo, rows_hi;  // the sequences of the launch: those of so many query rows
   float scale_log2, v_scale;
   float* part_o;   // [CTA][2][kMaxRows][D]
   float2* part_ml; // [CTA][2][kMaxRows]: maximum, sum
@@ -79,7 +80,7 @@ __device__ __forceinline__ int decode_blocks(const Q4Params& p, int b, int& t0, 
   len = p.seq_lens[b];
   rows = n * p.group;
   bad = n > p.max_query_len || t0 < 0 || t0 > p.T - n;  // n rows of q and out from t0 on, as the launch was sized for
-  if (bad || n < 1 || (n > 1 && (n > kMaxRows || rows > kMaxRows))) return 0;
+  if (bad || n < 1 || (n > 1 && (n > kMaxRows || rows > kMaxRows)) || rows < p.rows_lo || rows > p.rows_hi) return 0;
   const int nblk = (len + kQ4Block - 1) / kQ4Block;
   bad = len < 1 || len > p.max_seq_len || nblk > p.max_blocks;
   return bad ? 0 : nblk;
@@ -855,8 +856,9 @@ Layout layout(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int he
   return L;
 }
 
+// the sequences of rows_lo .. rows_hi query rows, on at most ctas_per_sm CTAs an SM
 template <int D, int NT>
-int launch_decode(Q4Params p, int grid, bool pdl, cudaStream_t s) {
+int launch_decode(Q4Params p, int rows_lo, int rows_hi, int ctas_per_sm, bool pdl, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
@@ -864,7 +866,11 @@ int launch_decode(Q4Params p, int grid, bool pdl, cudaStream_t s) {
                                 static_cast<int>(decode_smem<D, NT>()));
   });
   if (attr != cudaSuccess) return attr;
+  p.rows_lo = rows_lo;
+  p.rows_hi = rows_hi;
   const long long pieces = static_cast<long long>(p.B) * p.nkv;
+  const long long want = pieces * ((p.max_seq_len + kQ4Block - 1) / kQ4Block + kPieceCost) / kMinShare + 1;
+  const int full = num_sms() * ctas_per_sm, grid = want < full ? static_cast<int>(want) : full;
   p.cut_by_piece = pieces <= grid;
   const cudaError_t e =
       launch_kernel(k_attn_q4_decode<D, NT>, dim3(grid), dim3(kThreads), decode_smem<D, NT>(), s, pdl, p);
@@ -881,59 +887,65 @@ template <int D>
 int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStream_t s) {
   const AttnArgs& a = q4.a;
   const int mq = a.max_query_len;
-  const bool long_seqs = mq > 1 && (mq > kMaxRows || mq * p.group > kMaxRows);
-  int e = 0;
-  bool pdl = false;
-  if (long_seqs) {
-    PrefillQ4 f{};
-    f.qsl = a.qsl;
-    f.seq_lens = a.seq_lens;
-    f.block_table = a.block_table;
-    f.T = a.T;
-    f.B = a.B;
-    f.max_query_len = mq;
-    f.max_blocks = a.max_blocks;
-    f.num_blocks = a.num_blocks;
-    f.nkv = a.nkv;
-    f.group = p.group;
-    f.max_seq_len = a.max_seq_len;
-    f.prefill_blocks = q4.prefill_blocks;
-    f.tile_tokens = prefill_tile_tokens(a);
-    f.max_items = (a.T + f.tile_tokens - 1) / f.tile_tokens + a.B;
-    f.stride = L.stride;
-    f.base = reinterpret_cast<int32_t*>(q4.ws + L.base);
-    f.items = reinterpret_cast<uint32_t*>(q4.ws + L.items);
-    f.table = reinterpret_cast<int32_t*>(q4.ws + L.table);
-    f.k_cache = p.k_cache;
-    f.v_cache = p.v_cache;
-    f.k_copy = reinterpret_cast<__nv_bfloat16*>(q4.ws + L.k_copy);
-    f.v_copy = reinterpret_cast<__nv_bfloat16*>(q4.ws + L.v_copy);
-    f.k_scale = q4.k_scale;
-    f.v_scale = q4.v_scale;
-    f.err = a.err;
-    if ((e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(1024), 0, s, pdl, f))) return e;
-    pdl = true;
-    if (q4.prefill_blocks > 0) {
-      if ((e = launch_kernel(k_q4_expand<D>, dim3(q4.prefill_blocks), dim3(256), 0, s, true, f))) return e;
-      AttnArgs c = a;
-      c.k_cache = f.k_copy;
-      c.v_cache = f.v_copy;
-      c.block_table = f.table;
-      c.max_blocks = L.stride;
-      c.num_blocks = q4.prefill_blocks;
-      if ((e = prefill_items_launch(c, f.items, f.max_items, true, s))) return e;
-    }
-  }
   // rows a sequence of the decode path may have
-  const int toks = mq > 1 ? min(mq, kMaxRows / p.group > 1 ? kMaxRows / p.group : 1) : 1;
-  const long long bound = static_cast<long long>(a.B) * a.nkv * L.stride;
-  const long long want = (bound + kMinShare - 1) / kMinShare;
-  if (toks * p.group <= 8) {
-    const int full = num_sms() * kCtasPerSm;
-    return launch_decode<D, 1>(p, want < full ? static_cast<int>(want) : full, pdl, s);
+  const int toks = mq > 1 ? min(mq, max(kMaxRows / p.group, 1)) : 1, rows = toks * p.group;
+  if (mq <= 1 || (mq <= kMaxRows && mq * p.group <= kMaxRows))
+    return rows <= 8 ? launch_decode<D, 1>(p, 1, 8, kCtasPerSm, false, s)
+                     : launch_decode<D, 2>(p, 1, kMaxRows, 3, false, s);
+
+  // Longer sequences too: the decode kernels (bound by HBM) run on the side stream beside the expansion and the
+  // prefill kernel (bound by its softmax and the tensor cores).
+  PrefillQ4 f{};
+  f.T = a.T;
+  f.qsl = a.qsl;
+  f.seq_lens = a.seq_lens;
+  f.block_table = a.block_table;
+  f.B = a.B;
+  f.max_query_len = mq;
+  f.max_blocks = a.max_blocks;
+  f.num_blocks = a.num_blocks;
+  f.nkv = a.nkv;
+  f.group = p.group;
+  f.max_seq_len = a.max_seq_len;
+  f.prefill_blocks = q4.prefill_blocks;
+  f.tile_tokens = prefill_tile_tokens(a);
+  f.max_items = (a.T + f.tile_tokens - 1) / f.tile_tokens + a.B;
+  f.stride = L.stride;
+  f.base = reinterpret_cast<int32_t*>(q4.ws + L.base);
+  f.items = reinterpret_cast<uint32_t*>(q4.ws + L.items);
+  f.table = reinterpret_cast<int32_t*>(q4.ws + L.table);
+  f.k_cache = p.k_cache;
+  f.v_cache = p.v_cache;
+  f.k_copy = reinterpret_cast<__nv_bfloat16*>(q4.ws + L.k_copy);
+  f.v_copy = reinterpret_cast<__nv_bfloat16*>(q4.ws + L.v_copy);
+  f.k_scale = q4.k_scale;
+  f.v_scale = q4.v_scale;
+  f.err = a.err;
+  cudaEvent_t join = nullptr;
+  const cudaStream_t side = side_fork(s, &join);
+  int e;
+  if (p.group > 8) {
+    e = launch_decode<D, 2>(p, 1, kMaxRows, 3, false, side);
+  } else {
+    e = launch_decode<D, 1>(p, 1, 8, kCtasPerSm, false, side);
+    if (e == 0 && rows > 8) e = launch_decode<D, 2>(p, 9, kMaxRows, 3, true, side);
   }
-  const int full = num_sms() * 3;
-  return launch_decode<D, 2>(p, want < full ? static_cast<int>(want) : full, pdl, s);
+  if (e == 0) e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(1024), 0, s, side == s, f);
+  if (e == 0 && q4.prefill_blocks > 0) {
+    e = launch_kernel(k_q4_expand<D>, dim3(q4.prefill_blocks), dim3(256), 0, s, true, f);
+    AttnArgs c = a;
+    c.k_cache = f.k_copy;
+    c.v_cache = f.v_copy;
+    c.block_table = f.table;
+    c.max_blocks = L.stride;
+    c.num_blocks = q4.prefill_blocks;
+    if (e == 0) e = prefill_items_launch(c, f.items, f.max_items, true, s);
+  }
+  if (side != s) {  // join even after a failed launch, so that the caller's stream never runs ahead of the side stream
+    const int j = side_join(s, side, join);
+    if (e == 0) e = j;
+  }
+  return e;
 }
 
 }  // namespace
