@@ -48,8 +48,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 16;        // query rows (new tokens x group) of the decode path
 constexpr int kCtasPerSm = 4;
+constexpr int kRankStep = 46;       // half the share lost from one CTA of an SM to the next, in 1/1024 of the mean
 constexpr int kMinShare = 8;        // blocks a CTA takes at least: two a warp
-constexpr int kPieceCost = 4;       // what a (sequence, KV head) costs a CTA beside its blocks, in blocks
+constexpr int kPieceCost = 6;       // what a (sequence, KV head) costs a CTA beside its blocks, in blocks
 constexpr float kMaxStep = 8.f;     // log2 by which a score may pass the running maximum
 constexpr float kWeightBias = 6.f;  // weights are stored times 2^6
 constexpr float kMinusInf = -INFINITY;
@@ -63,6 +64,7 @@ struct Q4Params {
   const uint8_t *k_cache, *v_cache;
   const int32_t *qsl, *seq_lens, *positions, *block_table;
   int T, B, max_blocks, num_blocks, nq, nkv, group, max_query_len, max_seq_len;
+  int sms;
   int rows_lo, rows_hi;  // the sequences of the launch: those of so many query rows
   float scale_log2, v_scale;
   float* part_o;   // [CTA][2][kMaxRows][D]
@@ -155,6 +157,40 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// How the units are cut into the CTAs' ranges.  An SM's warp schedulers favour the
+// warps of the CTA that came first: with equal ranges the four CTAs of an SM ended
+// after 86, 94, 103 and 112 us (128-sequence batch), the last ones on a half-empty
+// SM.  So the CTAs of rank r (the r-th on their SM: the grid fills the SMs in
+// turn) get a share that falls with r.
+struct Split {
+  long long total, mean;
+  int per_rank, ranks;
+  __device__ __forceinline__ Split(long long units, int sms) : total(units) {
+    const int grid = gridDim.x;
+    mean = units < 0x7fffffffLL ? (static_cast<uint32_t>(units) + grid - 1) / grid : (units + grid - 1) / grid;
+    const bool ranked = grid > sms && grid % sms == 0 && mean >= 2 * kMinShare;
+    per_rank = ranked ? sms : grid;
+    ranks = ranked ? grid / sms : 1;
+    if (mean < kMinShare) mean = kMinShare;
+  }
+  // the shares sum to the mean's (their parts of it are opposite in pairs, rounded down, plus one)
+  __device__ __forceinline__ long long share(int r) const {
+    return mean + ((mean * kRankStep * (ranks - 1 - 2 * r)) >> 10) + (ranks > 1);
+  }
+  __device__ __forceinline__ long long begin(int cta) const {
+    long long at = 0;
+#pragma unroll
+    for (int r = 0; r < kCtasPerSm; ++r)
+      if (r < ranks) at += min(max(cta - r * per_rank, 0), per_rank) * share(r);
+    return at;
+  }
+  __device__ __forceinline__ int cta_of(long long unit) const {
+    int r = 0;
+    while (r < ranks - 1 && unit >= per_rank * share(r)) unit -= per_rank * share(r++);
+    return r * per_rank + static_cast<int>(unit / share(r));
+  }
+};
+
 // Where a CTA's range begins or ends.
 struct Place {
   long long blocks;  // blocks before it
@@ -213,11 +249,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     all += sums[w];
   }
   auto units_of = [&](long long v) { return ((v >> 17) + kPieceCost * (v & 0x1FFFF)) * p.nkv; };
-  const long long total = units_of(all);
-  long long share = total < 0x7fffffffLL ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x
-                                         : (total + gridDim.x - 1) / gridDim.x;
-  if (share < kMinShare) share = kMinShare;
-  const long long begin = share * blockIdx.x, end = min(total, begin + share);
+  const Split split(units_of(all), p.sms);
+  const long long begin = split.begin(blockIdx.x), end = min(split.total, split.begin(blockIdx.x + 1));
   if (threadIdx.x == 0 && !p.cut_by_piece) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (begin >= end) return;
   {
@@ -285,11 +318,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
   const uint8_t* const ks_lane = p.k_cache + 8 * D + (D == 128 ? lane * 4 : (lane >> 1) * 4);
   const uint8_t* const vs_lane = p.v_cache + 8 * D + ((D == 128 ? g : g >> 1) * 4 + t) * 4;
   const uint32_t ring_c = ring + lane * (4 * KW), ring_s = ring + 4 * CB + lane * 4;
-  auto issue = [&]() {
+  auto issue = [&](uint32_t st) {
     if (issued < mine_n) {
       if (issued % 32 == 0) look_up();
       const size_t at = static_cast<size_t>(__shfl_sync(0xffffffffu, tile, issued % 32)) * TB;
-      const uint32_t st = (issued % S) * STB;
       copy_async<4 * KW>(ring_c + st, k_lane + at);
       copy_async<4 * KW>(ring_c + st + CB, k_lane + at + 4 * D);
       copy_async<4>(ring_s + st, ks_lane + at);
@@ -300,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     ++issued;
     copy_commit();
   };
+  auto after = [](uint32_t st) { return st == (S - 1) * STB ? 0u : st + STB; };  // the next stage
 
   // ---- pieces: blocks cj .. of (cb, ch)
   int t0, rows, len, nblk;
@@ -327,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
   };
   if (NT == 1) load_q();  // before the ring is filled: behind those copies it would wait for all of them
 #pragma unroll 1
-  for (int i = 0; i < S; ++i) issue();
-  int used = 0;  // blocks this warp has taken
+  for (int i = 0; i < S; ++i) issue(i * STB);
+  uint32_t stage = 0;  // of the warp's next block
   int left = count;
   int first = 0;  // index in the range of the piece's first block
   while (left > 0) {
@@ -378,11 +411,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     auto step = [&](int i, auto blocks) {
       constexpr int N = decltype(blocks)::value;
       float s[N][NT][4];
+      uint32_t at[N];
+#pragma unroll
+      for (int x = 0; x < N; ++x) at[x] = x == 0 ? stage : after(at[x - 1]);
       copy_wait<S - N>();
       // ---- S^T = K Q^T
 #pragma unroll
       for (int x = 0; x < N; ++x) {
-        const uint32_t st = ((used + x) % S) * STB;
+        const uint32_t st = at[x];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[x][nt][0] = s[x][nt][1] = s[x][nt][2] = s[x][nt][3] = 0.f;
         uint32_t wa[KW], wb[KW];
@@ -421,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
       }
       // ---- weights: score c of a tile is column c & 1 (row 2t + (c & 1)), key g + 8 (c >> 1)
       const int key0 = (cj + i) * kQ4Block;
-      if (key0 + (N - 1) * kWarps * kQ4Block + kQ4Block - 1 > lim_lo) {
+      const bool edge = key0 + (N - 1) * kWarps * kQ4Block + kQ4Block - 1 > lim_lo;
+      if (edge) {
 #pragma unroll
         for (int x = 0; x < N; ++x)
 #pragma unroll
@@ -484,14 +521,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int x = 0; x < N; ++x) {
-        const uint32_t st = ((used + x) % S) * STB;
+        const uint32_t st = at[x];
         uint32_t v0[KW], v1[KW];
         lds_words(v0, ring_c + st + 2 * CB);
         lds_words(v1, ring_c + st + 3 * CB);
         const uint32_t sw = lds_u32(ring_s + st + 128);
         uint32_t s0 = e4m3x2_to_f16(sw), s1 = e4m3x2_to_f16(sw >> 16);
         const int k0 = key0 + x * kWarps * kQ4Block;
-        if (k0 + kQ4Block > len) {  // tokens past the sequence: their bytes may be anything
+        if (edge && k0 + kQ4Block > len) {  // tokens past the sequence: their bytes may be anything
           const int k = k0 + 2 * t;
           s0 = (k < len ? s0 & 0xFFFFu : 0u) | (k + 1 < len ? s0 & 0xFFFF0000u : 0u);
           s1 = (k + 8 < len ? s1 & 0xFFFFu : 0u) | (k + 9 < len ? s1 & 0xFFFF0000u : 0u);
@@ -512,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
           }
         }
       }
-      used += N;
 #pragma unroll
-      for (int x = 0; x < N; ++x) issue();  // the stages just read take the next blocks
+      for (int x = 0; x < N; ++x) issue(at[x]);  // the stages just read take the next blocks
+      stage = after(at[N - 1]);
     };
     // the warp's blocks of the piece: range indices congruent to warp
     constexpr int kStep = 2;
@@ -542,8 +579,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     const bool whole = cj == 0 && n == nblk;
     const int slot = cj == 0 ? 1 : 0;  // a piece that begins here, or one continued from the CTA before
     if (threadIdx.x == 0 && cj == 0 && (n < nblk || p.cut_by_piece))
-      p.cut[p.cut_by_piece ? cb * p.nkv + ch : blockIdx.x] = make_int4(
-          n < nblk ? cb : -1, ch, static_cast<int>((unit + kPieceCost + nblk - 1) / share), blockIdx.x);
+      p.cut[p.cut_by_piece ? cb * p.nkv + ch : blockIdx.x] =
+          make_int4(n < nblk ? cb : -1, ch, split.cta_of(unit + kPieceCost + nblk - 1), blockIdx.x);
     const int out_t0 = t0, out_rows = rows, out_len = len, out_h = ch;
     left -= n;
     first += n;
@@ -866,6 +903,7 @@ int launch_decode(Q4Params p, int rows_lo, int rows_hi, int ctas_per_sm, bool pd
                                 static_cast<int>(decode_smem<D, NT>()));
   });
   if (attr != cudaSuccess) return attr;
+  p.sms = num_sms();
   p.rows_lo = rows_lo;
   p.rows_hi = rows_hi;
   const long long pieces = static_cast<long long>(p.B) * p.nkv;
