@@ -58,6 +58,12 @@ constexpr float kMinusInf = -INFINITY;
 template <int D>
 constexpr int stages() { return D == 128 ? 4 : 8; }  // a power of two
 
+// A piece that spans CTAs, for k_attn_q4_combine.
+struct Cut {
+  int first, last;  // its CTAs; last < 0: nothing to join
+  int t0, rows, len, h, unused[2];
+};
+
 struct Q4Params {
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
@@ -69,7 +75,7 @@ struct Q4Params {
   float scale_log2, v_scale;
   float* part_o;   // [CTA][2][kMaxRows][D]
   float2* part_ml; // [CTA][2][kMaxRows]: maximum, sum
-  int4* cut;       // sequence (or -1: nothing to join), KV head, last CTA, first CTA of a piece
+  Cut* cut;
   int cut_by_piece;  // cut is indexed by sequence * nkv + KV head (else by the piece's first CTA)
   int* err;
 };
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
   auto units_of = [&](long long v) { return ((v >> 17) + kPieceCost * (v & 0x1FFFF)) * p.nkv; };
   const Split split(units_of(all), p.sms);
   const long long begin = split.begin(blockIdx.x), end = min(split.total, split.begin(blockIdx.x + 1));
-  if (threadIdx.x == 0 && !p.cut_by_piece) p.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !p.cut_by_piece) p.cut[blockIdx.x].last = -1;
   if (begin >= end) return;
   {
     const long long first_unit = units_of(excl), last_unit = first_unit + units_of(mine);
@@ -580,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     const int slot = cj == 0 ? 1 : 0;  // a piece that begins here, or one continued from the CTA before
     if (threadIdx.x == 0 && cj == 0 && (n < nblk || p.cut_by_piece))
       p.cut[p.cut_by_piece ? cb * p.nkv + ch : blockIdx.x] =
-          make_int4(n < nblk ? cb : -1, ch, split.cta_of(unit + kPieceCost + nblk - 1), blockIdx.x);
+          Cut{static_cast<int>(blockIdx.x), n < nblk ? split.cta_of(unit + kPieceCost + nblk - 1) : -1, t0, rows, len, ch,
+              {0, 0}};
     const int out_t0 = t0, out_rows = rows, out_len = len, out_h = ch;
     left -= n;
     first += n;
@@ -643,76 +650,99 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
 // so that a few long pieces have many warps; beyond that one entry per decode CTA
 // (the piece that begins in it and ends in a later one).
 constexpr int kCombineWarps = 16;
+constexpr int kCombineBatch = 4;  // parts a warp loads at once
 
 template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) k_attn_q4_combine(const Q4Params p) {
   __shared__ float so[kCombineWarps][D];
-  __shared__ float sl[kCombineWarps];
+  __shared__ float2 sml[kCombineWarps];
   pdl_wait();
-  int t0, rows, len;
-  bool bad;
-  if (p.cut_by_piece && decode_blocks(p, blockIdx.x / p.nkv, t0, rows, len, bad) == 0) return;
-  const int4 cut = p.cut[blockIdx.x];
-  if (cut.x < 0) return;
-  decode_blocks(p, cut.x, t0, rows, len, bad);
-  const int first = cut.w, parts = cut.z - first + 1;
+  const Cut cut = p.cut[blockIdx.x];
+  // (an entry per piece is written for the sequences of this launch only)
+  if (p.cut_by_piece && plan_blocks(p, blockIdx.x / p.nkv) == 0) return;
+  if (cut.last < 0) return;
+  const int rows = cut.rows, parts = cut.last - cut.first + 1;
   const int gy = gridDim.y, y = blockIdx.y;
   const int mine = y < rows ? (rows - y + gy - 1) / gy : 0;  // rows y, y + gy, ...
   if (mine == 0) return;
   const int wpr = mine <= 1 ? 16 : mine <= 2 ? 8 : mine <= 4 ? 4 : mine <= 8 ? 2 : 1;  // warps a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = y + (warp / wpr) * gy, sub = warp % wpr;
-  auto at = [&](int i) { return (static_cast<size_t>(first + i) * 2 + (i == 0 ? 1 : 0)) * kMaxRows + r; };
   constexpr int E = D / 32;
-  float L = 0.f, O[E];
+  float M = kMinusInf, L = 0.f, O[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) O[e] = 0.f;
+  const int tok = cut.t0 + r / p.group;
+  int pos = -1;
   if (r < rows) {
-    float M = kMinusInf;
-    for (int i = lane; i < parts; i += 32) M = fmaxf(M, p.part_ml[at(i)].x);
+    pos = p.positions[tok];
+    for (int i0 = sub; i0 < parts; i0 += wpr * kCombineBatch) {
+      float2 ml[kCombineBatch];
+      float x[kCombineBatch][E];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    const float mb = M == kMinusInf ? 0.f : M;
-#pragma unroll 8
-    for (int i = sub; i < parts; i += wpr) {
-      const float2 ml = p.part_ml[at(i)];
-      const float* src = p.part_o + at(i) * D + lane * E;
-      float x[E];
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        x[0] = v.x, x[1] = v.y;
+      for (int n = 0; n < kCombineBatch; ++n) {
+        const int i = i0 + n * wpr;
+        ml[n] = make_float2(kMinusInf, 0.f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[n][e] = 0.f;
+        if (i < parts) {
+          const size_t at = (static_cast<size_t>(cut.first + i) * 2 + (i == 0 ? 1 : 0)) * kMaxRows + r;
+          ml[n] = p.part_ml[at];
+          const float* src = p.part_o + at * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            x[n][0] = v.x, x[n][1] = v.y, x[n][2] = v.z, x[n][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            x[n][0] = v.x, x[n][1] = v.y;
+          }
+        }
       }
-      const float f = fast_exp2(ml.x - mb);
-      L += ml.y * f;
+      float m = M;
 #pragma unroll
-      for (int e = 0; e < E; ++e) O[e] += x[e] * f;
+      for (int n = 0; n < kCombineBatch; ++n) m = fmaxf(m, ml[n].x);
+      const float mb = m == kMinusInf ? 0.f : m, a = fast_exp2(M - mb);
+      M = m;
+      L *= a;
+#pragma unroll
+      for (int e = 0; e < E; ++e) O[e] *= a;
+#pragma unroll
+      for (int n = 0; n < kCombineBatch; ++n) {
+        const float f = fast_exp2(ml[n].x - mb);
+        L += ml[n].y * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) O[e] += x[n][e] * f;
+      }
     }
   }
   if (wpr > 1) {
 #pragma unroll
     for (int e = 0; e < E; ++e) so[warp][lane * E + e] = O[e];
-    if (lane == 0) sl[warp] = L;
+    if (lane == 0) sml[warp] = make_float2(M, L);
     __syncthreads();
     if (sub != 0) return;
-    for (int w = 1; w < wpr; ++w) {
-      L += sl[warp + w];
+    float m = M;
+    for (int w = 1; w < wpr; ++w) m = fmaxf(m, sml[warp + w].x);
+    const float mb = m == kMinusInf ? 0.f : m, a = fast_exp2(M - mb);
+    L *= a;
 #pragma unroll
-      for (int e = 0; e < E; ++e) O[e] += so[warp + w][lane * E + e];
+    for (int e = 0; e < E; ++e) O[e] *= a;
+    for (int w = 1; w < wpr; ++w) {
+      const float2 ml = sml[warp + w];
+      const float f = fast_exp2(ml.x - mb);
+      L += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) O[e] += so[warp + w][lane * E + e] * f;
     }
   }
   if (r >= rows) return;
-  const int tok = t0 + r / p.group;
-  const int pos = p.positions[tok];
-  if (pos < 0 || pos >= len) {
-    if (cut.y == 0 && lane == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
+  if (pos < 0 || pos >= cut.len) {
+    if (cut.h == 0 && lane == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
     return;
   }
   const float inv = p.v_scale / L;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
-      p.out + (static_cast<size_t>(tok) * p.nq + cut.y * p.group + r % p.group) * D + lane * E);
+      p.out + (static_cast<size_t>(tok) * p.nq + cut.h * p.group + r % p.group) * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(O[e] * inv, O[e + 1] * inv);
 }
@@ -875,7 +905,7 @@ Layout layout(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int he
   L.part_ml = off;
   off += up(rows * sizeof(float2));
   L.cut = off;
-  off += up(static_cast<size_t>(L.grid) * sizeof(int4));
+  off += up(static_cast<size_t>(L.grid) * sizeof(Cut));
   if (prefill_blocks > 0) {
     const size_t copy = up(static_cast<size_t>(prefill_blocks) * nkv * kQ4Block * head_dim * 2);
     L.table = off;
@@ -1018,7 +1048,7 @@ int attention_q4_launch(const AttnQ4Args& q4, cudaStream_t s) {
   p.v_scale = q4.v_scale;
   p.part_o = reinterpret_cast<float*>(q4.ws + L.part_o);
   p.part_ml = reinterpret_cast<float2*>(q4.ws + L.part_ml);
-  p.cut = reinterpret_cast<int4*>(q4.ws + L.cut);
+  p.cut = reinterpret_cast<Cut*>(q4.ws + L.cut);
   p.err = a.err;
   return a.head_dim == 128 ? launch_d<128>(q4, p, L, s) : launch_d<64>(q4, p, L, s);
 }
