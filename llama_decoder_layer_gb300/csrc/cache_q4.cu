@@ -38,10 +38,12 @@ struct Shape {
   int chunks, rows, parts;
 };
 
-// This thread's chunk c of head h (c < 0: none) and the first of its U tokens, `rows` apart.
+// This thread's chunk c of head h, and the first of its U tokens, `rows` apart.
+// Threads and tokens past the end load what the last ones do and store nothing.
 struct Place {
   uint32_t t0;
   int h, c;
+  bool there;
 };
 
 // v, known to be the same in every lane of the warp if WHOLE
@@ -55,13 +57,20 @@ template <int D, int U, bool WHOLE>
 __device__ __forceinline__ Place place(const Shape& g) {
   constexpr int C = D / 8;
   const int row = warp_value<WHOLE>(threadIdx.x / g.chunks);
-  const int r = g.parts > 1 ? static_cast<int>((blockIdx.y >> 1) * blockDim.x + threadIdx.x)
-                            : static_cast<int>(threadIdx.x) - row * g.chunks;
+  const int at = g.parts > 1 ? static_cast<int>((blockIdx.y >> 1) * blockDim.x + threadIdx.x)
+                             : static_cast<int>(threadIdx.x) - row * g.chunks;
+  const int r = WHOLE ? at : min(at, g.chunks - 1);
   Place x;
   x.h = r / C;
-  x.c = r < g.chunks ? r % C : -1;
+  x.c = r % C;
+  x.there = WHOLE || at == r;
   x.t0 = blockIdx.x * static_cast<uint32_t>(g.rows * U) + (g.parts > 1 ? 0 : row);  // below T + rows * U < 2^32
   return x;
+}
+
+// token t0 + n rows, or the last one
+__device__ __forceinline__ uint32_t token(const CacheQ4Args& a, const Shape& g, const Place& x, int n) {
+  return min(x.t0 + n * g.rows, static_cast<uint32_t>(a.T) - 1);
 }
 
 // the slots of this thread's tokens; -1 where there is nothing to do
@@ -70,17 +79,13 @@ __device__ __forceinline__ void load_slots(const CacheQ4Args& a, const Shape& g,
                                            int (&slot)[U]) {
   bool past = false;
 #pragma unroll
-  for (int n = 0; n < U; ++n) {
-    const uint32_t t = x.t0 + n * g.rows;
-    slot[n] = t < static_cast<uint32_t>(a.T) ? a.slots[t] : -1;
-  }
+  for (int n = 0; n < U; ++n) slot[n] = a.slots[token(a, g, x, n)];
 #pragma unroll
   for (int n = 0; n < U; ++n) {
     slot[n] = warp_value<WHOLE>(slot[n]);
     const bool over = slot[n] >= a.num_blocks * kQ4Block;
     past |= over;
-    if (over) slot[n] = -1;
-    if (!WHOLE && x.c < 0) slot[n] = -1;
+    if (over || x.t0 + n * g.rows >= static_cast<uint32_t>(a.T) || (!WHOLE && !x.there)) slot[n] = -1;
   }
   if (past && reports) report_error(a.err, kErrGuard, kWhereSlot);
 }
@@ -98,16 +103,14 @@ struct Bytes {
 template <int D, int U, bool WHOLE, bool V>
 __device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g) {
   const Place x = place<D, U, WHOLE>(g);
-  const long long stride = V ? a.v_stride : a.k_stride, step = g.rows * stride;
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(V ? a.v : a.k) + x.t0 * stride + x.h * D + x.c * 8;
+  const long long stride = V ? a.v_stride : a.k_stride;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(V ? a.v : a.k) + x.h * D + x.c * 8;
   uint4 u[U];
 #pragma unroll
-  for (int n = 0; n < U; ++n) {  // before the slots are known: every row may be read
-    u[n] = make_uint4(0, 0, 0, 0);
-    if ((WHOLE || x.c >= 0) && x.t0 + n * g.rows < static_cast<uint32_t>(a.T)) u[n] = *reinterpret_cast<const uint4*>(src + n * step);
-  }
+  for (int n = 0; n < U; ++n)  // before the slots are known: every row may be read
+    u[n] = *reinterpret_cast<const uint4*>(src + token(a, g, x, n) * stride);
   int slot[U];
-  load_slots<U, WHOLE>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
+  load_slots<U, WHOLE>(a, g, x, !V && x.h == 0 && x.c == 0 && x.there, slot);
   float top[U];
   bool nan = false;
 #pragma unroll
@@ -119,7 +122,7 @@ __device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g)
     nan |= top[n] != top[n];
   }
   if (nan) {  // rare: a NaN counts as zero
-#pragma unroll 1
+#pragma unroll
     for (int n = 0; n < U; ++n) {
       uint32_t* w = reinterpret_cast<uint32_t*>(&u[n]);
       float m = 0.f;
@@ -169,7 +172,7 @@ template <int D, int U, bool WHOLE, bool V>
 __device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) {
   const Place x = place<D, U, WHOLE>(g);
   int slot[U];
-  load_slots<U, WHOLE>(a, g, x, !V && x.h == 0 && x.c == 0, slot);
+  load_slots<U, WHOLE>(a, g, x, !V && x.h == 0 && x.c == 0 && x.there, slot);
   const Bytes<D, V> at(x.c);
   const uint8_t* cache =
       static_cast<const uint8_t*>(V ? a.v_cache : a.k_cache) + static_cast<size_t>(x.h) * q4_tile_bytes(D);
@@ -177,21 +180,18 @@ __device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) 
   uint32_t code[U], s8[U];
 #pragma unroll
   for (int n = 0; n < U; ++n) {
-    const int k = slot[n] & 15;
-    const uint8_t* tile = cache + static_cast<size_t>(static_cast<uint32_t>(slot[n]) >> 4) * block_bytes;
-    code[n] = s8[n] = 0;
-    if (slot[n] >= 0) {
-      code[n] = *reinterpret_cast<const uint32_t*>(tile + at.code_at(k));
-      s8[n] = tile[at.scale_at(k)];
-    }
+    const uint32_t from = max(slot[n], 0);  // (a skipped row reads slot 0's bytes and stores nothing)
+    const uint8_t* tile = cache + static_cast<size_t>(from >> 4) * block_bytes;
+    code[n] = *reinterpret_cast<const uint32_t*>(tile + at.code_at(from & 15));
+    s8[n] = tile[at.scale_at(from & 15)];
   }
-  const long long stride = V ? a.v_stride : a.k_stride, step = g.rows * stride;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(V ? a.v_out : a.k_out) + x.t0 * stride + x.h * D + x.c * 8;
+  const long long stride = V ? a.v_stride : a.k_stride;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(V ? a.v_out : a.k_out) + x.h * D + x.c * 8;
   const float scale = V ? a.v_scale : a.k_scale;
 #pragma unroll
   for (int n = 0; n < U; ++n) {
     const uint4 v = q4_to_bf16(code[n], s8[n], scale);
-    if (slot[n] >= 0) *reinterpret_cast<uint4*>(dst + n * step) = v;
+    if (slot[n] >= 0) *reinterpret_cast<uint4*>(dst + token(a, g, x, n) * stride) = v;
   }
 }
 
