@@ -321,19 +321,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
   // the next block's copies: every lane fetches the bytes it will use
   const uint8_t* const k_lane = p.k_cache + lane * (4 * KW);
   const uint8_t* const v_lane = p.v_cache + lane * (4 * KW);
-  const uint8_t* const ks_lane = p.k_cache + 8 * D + (D == 128 ? lane * 4 : (lane >> 1) * 4);
-  const uint8_t* const vs_lane = p.v_cache + 8 * D + ((D == 128 ? g : g >> 1) * 4 + t) * 4;
-  const uint32_t ring_c = ring + lane * (4 * KW), ring_s = ring + 4 * CB + lane * 4;
+  const uint32_t ring_c = ring + lane * (4 * KW);
+  const uint32_t ring_ks = ring + 4 * CB + (D == 128 ? lane : lane >> 1) * 4;
+  const uint32_t ring_vs = ring + 4 * CB + 128 + ((D == 128 ? g : g >> 1) * 4 + t) * 4;
   auto issue = [&](uint32_t st) {
     if (issued < mine_n) {
       if (issued % 32 == 0) look_up();
       const size_t at = static_cast<size_t>(__shfl_sync(0xffffffffu, tile, issued % 32)) * TB;
-      copy_async<4 * KW>(ring_c + st, k_lane + at);
-      copy_async<4 * KW>(ring_c + st + CB, k_lane + at + 4 * D);
-      copy_async<4>(ring_s + st, ks_lane + at);
-      copy_async<4 * KW>(ring_c + st + 2 * CB, v_lane + at);
-      copy_async<4 * KW>(ring_c + st + 3 * CB, v_lane + at + 4 * D);
-      copy_async<4>(ring_s + st + 128, vs_lane + at);
+      const uint8_t *kp = k_lane + at, *vp = v_lane + at;
+      copy_async<4 * KW>(ring_c + st, kp);
+      copy_async<4 * KW>(ring_c + st + CB, kp + 4 * D);
+      copy_async<4 * KW>(ring_c + st + 2 * CB, vp);
+      copy_async<4 * KW>(ring_c + st + 3 * CB, vp + 4 * D);
+      if (lane < 8) {  // the scales, for all lanes
+        copy_async<4 * KW>(ring_c + st + 4 * CB, kp + 8 * D);
+        copy_async<4 * KW>(ring_c + st + 4 * CB + 128, vp + 8 * D);
+      }
     }
     ++issued;
     copy_commit();
@@ -421,6 +424,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
 #pragma unroll
       for (int x = 0; x < N; ++x) at[x] = x == 0 ? stage : after(at[x - 1]);
       copy_wait<S - N>();
+      __syncwarp();  // the scales came by other lanes' copies
       // ---- S^T = K Q^T
 #pragma unroll
       for (int x = 0; x < N; ++x) {
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
         uint32_t wa[KW], wb[KW];
         lds_words(wa, ring_c + st);
         lds_words(wb, ring_c + st + CB);
-        const uint32_t sw = lds_u32(ring_s + st);
+        const uint32_t sw = lds_u32(ring_ks + st);
         uint32_t sa[2], sb[2];  // scales of rows g and g + 8, doubled, for the lane's first and second 16 elements
         if constexpr (D == 128) {
           const uint32_t a = e4m3x2_to_f16(sw), b = e4m3x2_to_f16(sw >> 16);
@@ -531,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
         uint32_t v0[KW], v1[KW];
         lds_words(v0, ring_c + st + 2 * CB);
         lds_words(v1, ring_c + st + 3 * CB);
-        const uint32_t sw = lds_u32(ring_s + st + 128);
+        const uint32_t sw = lds_u32(ring_vs + st);
         uint32_t s0 = e4m3x2_to_f16(sw), s1 = e4m3x2_to_f16(sw >> 16);
         const int k0 = key0 + x * kWarps * kQ4Block;
         if (edge && k0 + kQ4Block > len) {  // tokens past the sequence: their bytes may be anything
@@ -555,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
           }
         }
       }
+      __syncwarp();
 #pragma unroll
       for (int x = 0; x < N; ++x) issue(at[x]);  // the stages just read take the next blocks
       stage = after(at[N - 1]);
