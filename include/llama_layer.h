@@ -50,10 +50,11 @@
  *     it on the stream finishes (programmatic dependent launch) and reads
  *     that kernel's results only after it has completed.  The first kernel
  *     of llama_layer_forward, llama_stack_forward and llama_moe_layer_forward
- *     (an embedding gather or a norm) reads nothing before then, so work
- *     queued before the call is complete before any of its data is read;
- *     the other entry points' first kernels start only after everything
- *     queued before them has completed.
+ *     (an embedding gather or a norm) reads nothing before then, nor does any
+ *     kernel of kv_cache_write_q4, kv_cache_read_q4, llama_paged_attention_q4
+ *     and llama_qk_norm_rope, so work queued before the call is complete
+ *     before any of its data is read; the other entry points' first kernels
+ *     start only after everything queued before them has completed.
  *   - A workspace belongs to one call at a time: calls that may overlap on the
  *     GPU need separate workspaces.  Its contents need not be initialised.
  *   - A call returns LLAMA_OK, or a status code without launching anything

@@ -653,7 +653,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
 // Joins the parts of every piece that spans CTAs, in order.  Up to as many pieces
 // as decode CTAs: one entry of `cut` per piece and grid.y CTAs share its rows,
 // so that a few long pieces have many warps; beyond that one entry per decode CTA
-// (the piece that begins in it and ends in a later one).
+// (the piece that begins in it and ends in a later one).  It lets no later kernel
+// start early: CTAs of a next call's decode kernel that came one by one into
+// freed slots would not be ranked by their SM (128-sequence batch 135 us instead
+// of 122).
 constexpr int kCombineWarps = 16;
 constexpr int kCombineBatch = 4;  // parts a warp loads at once
 
@@ -963,8 +966,8 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   // rows a sequence of the decode path may have
   const int toks = mq > 1 ? min(mq, max(kMaxRows / p.group, 1)) : 1, rows = toks * p.group;
   if (mq <= 1 || (mq <= kMaxRows && mq * p.group <= kMaxRows))
-    return rows <= 8 ? launch_decode<D, 1>(p, 1, 8, kCtasPerSm, false, s)
-                     : launch_decode<D, 2>(p, 1, kMaxRows, 3, false, s);
+    return rows <= 8 ? launch_decode<D, 1>(p, 1, 8, kCtasPerSm, true, s)
+                     : launch_decode<D, 2>(p, 1, kMaxRows, 3, true, s);
 
   // Longer sequences too: the decode kernels (bound by HBM) run on the side stream beside the expansion and the
   // prefill kernel (bound by its softmax and the tensor cores).

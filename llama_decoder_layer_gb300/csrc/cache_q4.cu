@@ -197,6 +197,7 @@ __device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) 
 
 template <int D, int U, bool WHOLE>
 __global__ void __launch_bounds__(kMaxThreads) k_kv_write_q4(const CacheQ4Args a, const Shape g) {
+  pdl_wait();
   if (blockIdx.y & 1)
     write_rows<D, U, WHOLE, true>(a, g);
   else
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_write_q4(const CacheQ4Args a
 
 template <int D, int U, bool WHOLE>
 __global__ void __launch_bounds__(kMaxThreads) k_kv_read_q4(const CacheQ4Args a, const Shape g) {
+  pdl_wait();
   if (blockIdx.y & 1)
     read_rows<D, U, WHOLE, true>(a, g);
   else
@@ -233,7 +235,7 @@ int launch(Kernel four, Kernel one, Kernel four_whole, Kernel one_whole, const C
   const bool u4 = ctas4 * 2 * g.parts >= 4LL * num_sms();
   const dim3 grid(static_cast<unsigned>(u4 ? ctas4 : ctas), 2 * g.parts);
   const bool whole = g.chunks % 32 == 0 && (g.parts == 1 || g.chunks % threads == 0);
-  return launch_kernel(whole ? (u4 ? four_whole : one_whole) : (u4 ? four : one), grid, dim3(threads), 0, s, false, a,
+  return launch_kernel(whole ? (u4 ? four_whole : one_whole) : (u4 ? four : one), grid, dim3(threads), 0, s, true, a,
                        g);
 }
 

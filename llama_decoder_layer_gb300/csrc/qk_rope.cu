@@ -109,6 +109,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_qk_norm_rope(const __g
   constexpr int L = D / 8;   // lanes a row
   constexpr int R = 32 / L;  // rows a round
   __shared__ float2 cs_all[kWarps][kMaxPairs];
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % L, sub = lane / L;
   float2* cs = cs_all[warp];
   const int pairs = p.rot / 2;
@@ -307,7 +308,7 @@ int qk_norm_rope_launch(const QkNormRopeArgs& a, cudaStream_t s) {
   p.parts = want < 1 ? 1 : want > most ? most : static_cast<int>(want);
   const long long ctas = (static_cast<long long>(a.T) * p.parts + kWarps - 1) / kWarps, full = 1LL * kCtasPerSm * num_sms();
   const dim3 grid(static_cast<unsigned>(ctas < full ? ctas : full));
-  auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kThreads), 0, s, false, tab, p); };
+  auto go = [&](auto kernel) { return launch_kernel(kernel, grid, dim3(kThreads), 0, s, true, tab, p); };
   const bool partial = p.rot < c.head_dim;
   if (c.head_dim == 128) {
     if (c.interleaved) return partial ? go(k_qk_norm_rope<128, true, true>) : go(k_qk_norm_rope<128, true, false>);
