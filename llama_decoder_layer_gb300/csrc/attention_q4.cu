@@ -50,6 +50,7 @@ constexpr int kMaxRows = 16;        // query rows (new tokens x group) of the de
 constexpr int kCtasPerSm = 4;
 constexpr int kRankStep = 46;       // half the share lost from one CTA of an SM to the next, in 1/1024 of the mean
 constexpr int kMinShare = 8;        // blocks a CTA takes at least: two a warp
+constexpr int kWholeBlocks = 64;    // pieces of up to so many blocks stay whole where the SMs hold them all
 constexpr int kPieceCost = 6;       // what a (sequence, KV head) costs a CTA beside its blocks, in blocks
 constexpr float kMaxStep = 8.f;     // log2 by which a score may pass the running maximum
 constexpr float kWeightBias = 6.f;  // weights are stored times 2^6
@@ -71,6 +72,7 @@ struct Q4Params {
   const int32_t *qsl, *seq_lens, *positions, *block_table;
   int T, B, max_blocks, num_blocks, nq, nkv, group, max_query_len, max_seq_len;
   int sms;
+  int whole;  // every CTA takes one (sequence, KV head)
   int rows_lo, rows_hi;  // the sequences of the launch: those of so many query rows
   float scale_log2, v_scale;
   float* part_o;   // [CTA][2][kMaxRows][D]
@@ -171,6 +173,7 @@ __device__ __forceinline__ void copy_wait() {
 struct Split {
   long long total, mean;
   int per_rank, ranks;
+  Split() = default;
   __device__ __forceinline__ Split(long long units, int sms) : total(units) {
     const int grid = gridDim.x;
     mean = units < 0x7fffffffLL ? (static_cast<uint32_t>(units) + grid - 1) / grid : (units + grid - 1) / grid;
@@ -227,78 +230,93 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
   pdl_wait();
   pdl_trigger();
 
-  // ---- the CTA's range: exclusive sums of the sequences' blocks (and their
-  // number, in the low 17 bits: at most 65535), a run of sequences per thread.  A
-  // piece (sequence, KV head) counts kPieceCost units before those of its blocks.
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int bfirst = min(p.B, static_cast<int>(threadIdx.x) * per), blast = min(p.B, bfirst + per);
-  long long mine = 0;
-  for (int b = bfirst; b < blast; ++b) {
+  // ---- the CTA's range of blocks: its first one (sequence cb, KV head ch, block cj
+  // of first_n) and how many
+  int cb, ch, cj = 0, first_n, count;
+  long long unit = 0;      // of the piece's start
+  Split split;
+  if (p.whole) {  // few short pieces: one a CTA
+    cb = blockIdx.x / p.nkv;
+    ch = blockIdx.x - cb * p.nkv;
     int t0, rows, len;
     bool bad;
-    const int n = decode_blocks(p, b, t0, rows, len, bad);
-    if (n > 0) mine += (static_cast<long long>(n) << 17) + 1;
-    if (bad && blockIdx.x == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
-  }
-  long long incl = mine;
+    first_n = count = uniform(decode_blocks(p, cb, t0, rows, len, bad));
+    if (bad && ch == 0 && threadIdx.x == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
+    if (count == 0) return;
+  } else {
+    // Exclusive sums of the sequences' blocks (and their number, in the low 17 bits: at most 65535), a run of
+    // sequences per thread.  A piece (sequence, KV head) counts kPieceCost units before those of its blocks.
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int bfirst = min(p.B, static_cast<int>(threadIdx.x) * per), blast = min(p.B, bfirst + per);
+    long long mine = 0;
+    for (int b = bfirst; b < blast; ++b) {
+      int t0, rows, len;
+      bool bad;
+      const int n = decode_blocks(p, b, t0, rows, len, bad);
+      if (n > 0) mine += (static_cast<long long>(n) << 17) + 1;
+      if (bad && blockIdx.x == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
+    }
+    long long incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  long long excl = incl - mine, all = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    long long excl = incl - mine, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) excl += sums[w];
-    all += sums[w];
-  }
-  auto units_of = [&](long long v) { return ((v >> 17) + kPieceCost * (v & 0x1FFFF)) * p.nkv; };
-  const Split split(units_of(all), p.sms);
-  const long long begin = split.begin(blockIdx.x), end = min(split.total, split.begin(blockIdx.x + 1));
-  if (threadIdx.x == 0 && !p.cut_by_piece) p.cut[blockIdx.x].last = -1;
-  if (begin >= end) return;
-  {
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) excl += sums[w];
+      all += sums[w];
+    }
+    auto units_of = [&](long long v) { return ((v >> 17) + kPieceCost * (v & 0x1FFFF)) * p.nkv; };
+    split = Split(units_of(all), p.sms);
+    const long long begin = split.begin(blockIdx.x), end = min(split.total, split.begin(blockIdx.x + 1));
+    if (threadIdx.x == 0 && !p.cut_by_piece) p.cut[blockIdx.x].last = -1;
+    if (begin >= end) return;
     const long long first_unit = units_of(excl), last_unit = first_unit + units_of(mine);
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       const long long at = which == 0 ? begin : end - 1;  // the end by its last unit
       if (at < first_unit || at >= last_unit) continue;
-      long long unit = first_unit, blocks = (excl >> 17) * p.nkv;
+      long long from = first_unit, blocks = (excl >> 17) * p.nkv;
       for (int b = bfirst; b < blast; ++b) {
         const int n = per == 1 ? static_cast<int>(mine >> 17) : plan_blocks(p, b);
         if (n == 0) continue;
         const long long units = static_cast<long long>(n + kPieceCost) * p.nkv;
-        if (at < unit + units) {
+        if (at < from + units) {
           Place x;
           x.b = b;
           x.nblk = n;
-          x.h = static_cast<int>(static_cast<uint32_t>(at - unit) / static_cast<uint32_t>(n + kPieceCost));
-          x.unit = unit + static_cast<long long>(x.h) * (n + kPieceCost);
+          x.h = static_cast<int>(static_cast<uint32_t>(at - from) / static_cast<uint32_t>(n + kPieceCost));
+          x.unit = from + static_cast<long long>(x.h) * (n + kPieceCost);
           // blocks before unit `at` (for the end: before the unit after it)
           x.j = max(0, static_cast<int>(at - x.unit) + which - kPieceCost);
           x.blocks = blocks + static_cast<long long>(x.h) * n + x.j;
           range[which] = x;
           break;
         }
-        unit += units;
+        from += units;
         blocks += static_cast<long long>(n) * p.nkv;
       }
     }
+    __syncthreads();
+    cb = uniform(range[0].b);
+    ch = uniform(range[0].h);
+    cj = uniform(range[0].j);
+    first_n = uniform(range[0].nblk);
+    count = uniform(static_cast<int>(range[1].blocks - range[0].blocks));
+    unit = range[0].unit;
+    if (count <= 0) return;
   }
-  __syncthreads();
-  const int count = uniform(static_cast<int>(range[1].blocks - range[0].blocks));
-  if (count <= 0) return;
 
   // ---- the warp's blocks: warp, warp + 4, ... of the range.  Lane i looks up
   // the tiles of blocks i, 32 + i, ... of those, 32 at once.
-  int cb = uniform(range[0].b), ch = uniform(range[0].h), cj = uniform(range[0].j);
-  long long unit = range[0].unit;
   const uint32_t ring = smem_u32(smem) + warp * S * STB;
   const int mine_n = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
   int issued = 0;
-  int pb = cb, pn = range[0].nblk, tile = 0;
+  int pb = cb, pn = first_n, tile = 0;
   uint32_t px = static_cast<uint32_t>(ch) * pn + cj + warp + kWarps * lane;  // block within sequence pb, over its heads
   auto look_up = [&]() {
     if (issued + lane < mine_n) {
@@ -947,6 +965,12 @@ int launch_decode(Q4Params p, int rows_lo, int rows_hi, int ctas_per_sm, bool pd
   const long long pieces = static_cast<long long>(p.B) * p.nkv;
   const long long want = pieces * ((p.max_seq_len + kQ4Block - 1) / kQ4Block + kPieceCost) / kMinShare + 1;
   const int full = num_sms() * ctas_per_sm, grid = want < full ? static_cast<int>(want) : full;
+  // Few short pieces are not split: finding the ranges and joining the parts cost about as much as kWholeBlocks blocks
+  // (one sequence of 777 tokens: 7.5 us split into 13 CTAs and joined, 7.4 whole, with one launch instead of two).
+  p.whole = pieces <= full && (p.max_seq_len + kQ4Block - 1) / kQ4Block <= kWholeBlocks;
+  if (p.whole)
+    return launch_kernel(k_attn_q4_decode<D, NT>, dim3(static_cast<unsigned>(pieces)), dim3(kThreads),
+                         decode_smem<D, NT>(), s, pdl, p);
   p.cut_by_piece = pieces <= grid;
   const cudaError_t e =
       launch_kernel(k_attn_q4_decode<D, NT>, dim3(grid), dim3(kThreads), decode_smem<D, NT>(), s, pdl, p);

@@ -226,7 +226,7 @@ class Case:
     """A batch of (new tokens, total length) sequences over random 4-bit caches; slots past a sequence's end hold
     random bytes, NaN scales among them."""
 
-    def __init__(self, seqs, nq, nkv, d, seed=0, kg=1.0, vg=1.0, extra_tokens=0, qmul=1.0):
+    def __init__(self, seqs, nq, nkv, d, seed=0, kg=1.0, vg=1.0, extra_tokens=0, qmul=1.0, bound=0):
         r = np.random.default_rng(seed)
         self.seqs, self.nq, self.nkv, self.d, self.kg, self.vg = seqs, nq, nkv, d, kg, vg
         nblk = [-(-t // 16) for _, t in seqs]
@@ -252,7 +252,7 @@ class Case:
         self.cfg = lb.LayerConfig(nq * d, nq, nkv, d, 4 * nq * d, 1e-5, 1e4)
         t32 = lambda x: torch.as_tensor(np.asarray(x, dtype=np.int32), device=DEV)  # noqa: E731
         self.batch = lb.Batch(t32(self.pos), t32(self.qsl), t32([t for _, t in seqs]), t32(self.table), blocks,
-                              max(n for n, _ in seqs), max(t for _, t in seqs))
+                              max(n for n, _ in seqs), max(bound, max(t for _, t in seqs)))
         self.pre = lb.prefill_blocks([n for n, _ in seqs], [t for _, t in seqs], nq // nkv)
         self.kc, self.vc = (torch.from_numpy(t).to(DEV) for t in tiles)
         self.qd = self.q.to(DEV)
@@ -284,25 +284,34 @@ class Case:
 HEADS = [(8, 2, 64), (64, 8, 128), (1, 1, 128), (16, 1, 64), (5, 1, 128), (12, 2, 128), (24, 2, 64), (3, 3, 64)]
 
 
+# max_seq_len, the bound the caller gives: up to 1024 a (sequence, KV head) stays whole, above it may be split
+BOUNDS = [0, 5000]
+
+
+@pytest.mark.parametrize("bound", BOUNDS)
 @pytest.mark.parametrize("nq,nkv,d", HEADS)
-def test_attention_one_token_each(nq, nkv, d):
-    c = Case([(1, n) for n in (1, 2, 15, 16, 17, 33, 64, 65, 100, 257, 530)], nq, nkv, d, seed=d + nq)
+def test_attention_one_token_each(nq, nkv, d, bound):
+    c = Case([(1, n) for n in (1, 2, 15, 16, 17, 33, 64, 65, 100, 257, 530)], nq, nkv, d, seed=d + nq, bound=bound)
     c.run()
     ok()
     c.check()
 
 
+@pytest.mark.parametrize("bound", BOUNDS)
 @pytest.mark.parametrize("nq,nkv,d", HEADS)
-def test_attention_a_few_new_tokens(nq, nkv, d):
-    c = Case([(n, n + p) for n, p in ((2, 0), (3, 14), (1, 40), (2, 301), (4, 77), (16, 5))], nq, nkv, d, seed=d + nq)
+def test_attention_a_few_new_tokens(nq, nkv, d, bound):
+    c = Case([(n, n + p) for n, p in ((2, 0), (3, 14), (1, 40), (2, 301), (4, 77), (16, 5))], nq, nkv, d, seed=d + nq,
+             bound=bound)
     c.run()
     ok()
     c.check()
 
 
+@pytest.mark.parametrize("bound", BOUNDS)
 @pytest.mark.parametrize("nq,nkv,d", HEADS)
-def test_attention_prompts_and_single_tokens_in_one_batch(nq, nkv, d):
-    c = Case([(1, 70), (33, 33), (1, 1), (70, 201), (17, 18), (2, 400), (129, 130), (1, 300)], nq, nkv, d, seed=nq)
+def test_attention_prompts_and_single_tokens_in_one_batch(nq, nkv, d, bound):
+    c = Case([(1, 70), (33, 33), (1, 1), (70, 201), (17, 18), (2, 400), (129, 130), (1, 300)], nq, nkv, d, seed=nq,
+             bound=bound)
     c.run()
     ok()
     c.check()
@@ -348,17 +357,19 @@ def test_rows_behind_the_last_sequence_stay():
         c.check()
 
 
-def test_a_sequence_without_new_tokens_is_passed_over():
-    c = Case([(1, 40), (0, 77), (1, 3), (0, 5), (20, 31), (0, 16)], 8, 2, 64)
+@pytest.mark.parametrize("bound", BOUNDS)
+def test_a_sequence_without_new_tokens_is_passed_over(bound):
+    c = Case([(1, 40), (0, 77), (1, 3), (0, 5), (20, 31), (0, 16)], 8, 2, 64, bound=bound)
     c.run()
     ok()
     c.check()
 
 
-def test_bad_positions_lengths_and_blocks_are_reported():
+@pytest.mark.parametrize("bound", BOUNDS)
+def test_bad_positions_lengths_and_blocks_are_reported(bound):
     for new in (1, 30):
         for what in ("past", "negative", "long", "blocks"):
-            c = Case([(new, 40), (new, 100), (new, 60)], 8, 2, 128, seed=11)
+            c = Case([(new, 40), (new, 100), (new, 60)], 8, 2, 128, seed=11, bound=bound)
             if what == "past":
                 c.batch.positions[c.qsl[2] - 1] = 100
             elif what == "negative":
@@ -401,8 +412,9 @@ def test_same_result_on_every_run_and_on_another_stream():
     c.check(a)
 
 
-def test_captured_and_replayed_with_new_lengths():
-    c = Case([(1, 900), (1, 40), (1, 333)], 8, 2, 128, seed=14)
+@pytest.mark.parametrize("bound", BOUNDS)
+def test_captured_and_replayed_with_new_lengths(bound):
+    c = Case([(1, 900), (1, 40), (1, 333)], 8, 2, 128, seed=14, bound=bound)
     c.run()
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -417,6 +429,40 @@ def test_captured_and_replayed_with_new_lengths():
         g.replay()
         ok()
         c.check()
+
+
+def test_a_mixed_batch_captured_and_replayed():
+    # the decode kernels' side stream joins the capture
+    c = Case([(1, 900), (40, 77), (1, 40), (3, 333)], 8, 2, 128, seed=16)
+    want = c.run().clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+        c.run()
+    for _ in range(3):
+        c.out.fill_(5.0)
+        g.replay()
+        ok()
+        assert torch.equal(c.out, want)
+    c.check()
+
+
+def test_calls_back_to_back_on_two_streams():
+    # each with a workspace of its own, many calls in flight
+    a = Case([(1, 2000), (1, 70)], 16, 2, 128, seed=17)
+    b = Case([(1, 3000), (2, 500)], 8, 2, 64, seed=18)
+    wa, wb = a.run().clone(), b.run().clone()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(40):
+        with torch.cuda.stream(s):
+            a.run()
+        with torch.cuda.stream(t):
+            b.run()
+    torch.cuda.synchronize()
+    ok()
+    assert torch.equal(a.out, wa) and torch.equal(b.out, wb)
 
 
 def test_caches_over_four_gigabytes():
