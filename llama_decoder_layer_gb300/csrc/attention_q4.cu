@@ -676,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
 // freed slots would not be ranked by their SM (128-sequence batch 135 us instead
 // of 122).
 constexpr int kCombineWarps = 16;
-constexpr int kCombineBatch = 4;  // parts a warp loads at once
+constexpr int kCombineBatch = 2;  // parts a warp loads at once (four take registers that keep its CTAs out of the
+                                  // SMs beside prefill CTAs: 226 instead of 220 us for the mixed batch)
 
 template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) k_attn_q4_combine(const Q4Params p) {
@@ -808,7 +809,7 @@ __global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
     __syncthreads();
     long long before = 0;
     all = 0;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
       if (w < warp) before += tot[w];
       all += tot[w];
     }
@@ -949,9 +950,11 @@ Layout layout(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int he
   return L;
 }
 
-// the sequences of rows_lo .. rows_hi query rows, on at most ctas_per_sm CTAs an SM
+// The sequences of rows_lo .. rows_hi query rows.  alone: nothing else runs beside the kernel, so that its CTAs fill the
+// SMs in turn (see Split).
 template <int D, int NT>
-int launch_decode(Q4Params p, int rows_lo, int rows_hi, int ctas_per_sm, bool pdl, cudaStream_t s) {
+int launch_decode(Q4Params p, int rows_lo, int rows_hi, bool alone, bool pdl, cudaStream_t s) {
+  constexpr int ctas_per_sm = NT == 1 ? kCtasPerSm : 3;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
@@ -959,12 +962,12 @@ int launch_decode(Q4Params p, int rows_lo, int rows_hi, int ctas_per_sm, bool pd
                                 static_cast<int>(decode_smem<D, NT>()));
   });
   if (attr != cudaSuccess) return attr;
-  p.sms = num_sms();
   p.rows_lo = rows_lo;
   p.rows_hi = rows_hi;
   const long long pieces = static_cast<long long>(p.B) * p.nkv;
   const long long want = pieces * ((p.max_seq_len + kQ4Block - 1) / kQ4Block + kPieceCost) / kMinShare + 1;
   const int full = num_sms() * ctas_per_sm, grid = want < full ? static_cast<int>(want) : full;
+  p.sms = alone ? num_sms() : grid;
   // Few short pieces are not split: finding the ranges and joining the parts cost about as much as kWholeBlocks blocks
   // (one sequence of 777 tokens: 7.5 us split into 13 CTAs and joined, 7.4 whole, with one launch instead of two).
   p.whole = pieces <= full && (p.max_seq_len + kQ4Block - 1) / kQ4Block <= kWholeBlocks;
@@ -990,8 +993,7 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   // rows a sequence of the decode path may have
   const int toks = mq > 1 ? min(mq, max(kMaxRows / p.group, 1)) : 1, rows = toks * p.group;
   if (mq <= 1 || (mq <= kMaxRows && mq * p.group <= kMaxRows))
-    return rows <= 8 ? launch_decode<D, 1>(p, 1, 8, kCtasPerSm, true, s)
-                     : launch_decode<D, 2>(p, 1, kMaxRows, 3, true, s);
+    return rows <= 8 ? launch_decode<D, 1>(p, 1, 8, true, true, s) : launch_decode<D, 2>(p, 1, kMaxRows, true, true, s);
 
   // Longer sequences too: the decode kernels (bound by HBM) run on the side stream beside the expansion and the
   // prefill kernel (bound by its softmax and the tensor cores).
@@ -1025,12 +1027,13 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   const cudaStream_t side = side_fork(s, &join);
   int e;
   if (p.group > 8) {
-    e = launch_decode<D, 2>(p, 1, kMaxRows, 3, false, side);
+    e = launch_decode<D, 2>(p, 1, kMaxRows, false, false, side);
   } else {
-    e = launch_decode<D, 1>(p, 1, 8, kCtasPerSm, false, side);
-    if (e == 0 && rows > 8) e = launch_decode<D, 2>(p, 9, kMaxRows, 3, true, side);
+    e = launch_decode<D, 1>(p, 1, 8, false, false, side);
+    if (e == 0 && rows > 8) e = launch_decode<D, 2>(p, 9, kMaxRows, false, true, side);
   }
-  if (e == 0) e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(1024), 0, s, side == s, f);
+  const int plan_threads = a.B < 1024 ? (a.B + 31) / 32 * 32 : 1024;
+  if (e == 0) e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(plan_threads), 0, s, side == s, f);
   if (e == 0 && q4.prefill_blocks > 0) {
     e = launch_kernel(k_q4_expand<D>, dim3(q4.prefill_blocks), dim3(256), 0, s, true, f);
     AttnArgs c = a;
