@@ -855,54 +855,57 @@ __global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
   for (long long i = items_before + threadIdx.x; i < p.max_items; i += blockDim.x) p.items[i] = kNoPrefillItem;
 }
 
-// One CTA per block of the copy: K and V of all KV heads in bf16 (exact), zero
-// past the sequence's end, and its entry of the copy's block table.
+// CTA (x, y): K (y = 0) or V of all KV heads of block x of the copy in bf16
+// (exact), zero past the sequence's end; and the block's entry in the copy's table.
+constexpr int kExpandThreads = 256;
+
+template <int D, bool V>
+__device__ __forceinline__ void expand_block(const PrefillQ4& p, int s, int blk, int tokens) {
+  // chunks of 8 elements, (head, token, chunk); kUnroll of a thread's loads in flight at once
+  constexpr int C = D / 8, kUnroll = 4;
+  const int total = p.nkv * kQ4Block * C;
+  const uint8_t* tiles = (V ? p.v_cache : p.k_cache) + static_cast<size_t>(blk) * p.nkv * q4_tile_bytes(D);
+  uint4* dst = reinterpret_cast<uint4*>((V ? p.v_copy : p.k_copy) + static_cast<size_t>(s) * p.nkv * kQ4Block * D);
+  const float g = V ? p.v_scale : p.k_scale;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kExpandThreads * kUnroll) {
+    uint32_t code[kUnroll], s8[kUnroll];
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n) {
+      const int i = min(i0 + n * kExpandThreads, total - 1);
+      const int c = i % C, k = (i / C) % kQ4Block;
+      const uint8_t* tile = tiles + (i / (C * kQ4Block)) * q4_tile_bytes(D);
+      code[n] = *reinterpret_cast<const uint32_t*>(tile + q4_code_at<D>(V, k, c));
+      s8[n] = k < tokens ? tile[q4_scale_at<D>(V, k, c >> 1)] : 0u;  // (unwritten tokens: any bytes; codes are finite)
+    }
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n)
+      if (i0 + n * kExpandThreads < total) dst[i0 + n * kExpandThreads] = q4_to_bf16(code[n], s8[n], g);
+  }
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) k_q4_expand(const PrefillQ4 p) {
+__global__ void __launch_bounds__(kExpandThreads) k_q4_expand(const PrefillQ4 p) {
   pdl_wait();
   pdl_trigger();
   const int s = blockIdx.x;
   if (s >= p.base[p.B]) return;
-  int lo = 0, hi = p.B - 1;  // the last sequence with base <= s
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.base[mid] <= s) lo = mid; else hi = mid - 1;
+  int upto = 0;  // sequences whose blocks begin at or before s: the last of them holds it
+  for (int b0 = 0; b0 < p.B; b0 += kExpandThreads) {
+    const int b = b0 + threadIdx.x;
+    upto += __syncthreads_count(b < p.B && p.base[b] <= s);
   }
-  const int b = lo, j = s - p.base[b], len = p.seq_lens[b];
+  const int b = upto - 1, j = s - p.base[b], len = p.seq_lens[b];
   if (j >= p.stride || j * kQ4Block >= len) return;
-  if (threadIdx.x == 0) p.table[static_cast<size_t>(b) * p.stride + j] = s;
+  if (threadIdx.x == 0 && blockIdx.y == 0) p.table[static_cast<size_t>(b) * p.stride + j] = s;
   int blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + j];
   if (blk < 0 || blk >= p.num_blocks) {
     if (threadIdx.x == 0) report_error(p.err, kErrGuard, kWhereBlockTable);
     blk = 0;
   }
-  // chunks of 8 elements, K then V: (head, token, chunk); all of a thread's loads in flight at once
-  constexpr int C = D / 8, kUnroll = 4;
-  const int half = p.nkv * kQ4Block * C;
-  for (int i0 = threadIdx.x; i0 < 2 * half; i0 += blockDim.x * kUnroll) {
-    uint32_t code[kUnroll], s8[kUnroll];
-#pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      const int i = i0 + n * blockDim.x;
-      const bool is_v = i >= half;
-      const int x = is_v ? i - half : i, c = x % C, k = (x / C) % kQ4Block, h = x / (C * kQ4Block);
-      code[n] = s8[n] = 0;
-      if (i < 2 * half && j * kQ4Block + k < len) {
-        const uint8_t* tile =
-            (is_v ? p.v_cache : p.k_cache) + (static_cast<size_t>(blk) * p.nkv + h) * q4_tile_bytes(D);
-        code[n] = *reinterpret_cast<const uint32_t*>(tile + q4_code_at<D>(is_v, k, c));
-        s8[n] = tile[q4_scale_at<D>(is_v, k, c >> 1)];
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      const int i = i0 + n * blockDim.x;
-      if (i >= 2 * half) break;
-      const bool is_v = i >= half;
-      __nv_bfloat16* dst = (is_v ? p.v_copy : p.k_copy) + static_cast<size_t>(s) * p.nkv * kQ4Block * D;
-      reinterpret_cast<uint4*>(dst)[is_v ? i - half : i] = q4_to_bf16(code[n], s8[n], is_v ? p.v_scale : p.k_scale);
-    }
-  }
+  if (blockIdx.y)
+    expand_block<D, true>(p, s, blk, len - j * kQ4Block);
+  else
+    expand_block<D, false>(p, s, blk, len - j * kQ4Block);
 }
 
 // ---------------------------------------------------------------------------
@@ -1035,7 +1038,7 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   const int plan_threads = a.B < 1024 ? (a.B + 31) / 32 * 32 : 1024;
   if (e == 0) e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(plan_threads), 0, s, side == s, f);
   if (e == 0 && q4.prefill_blocks > 0) {
-    e = launch_kernel(k_q4_expand<D>, dim3(q4.prefill_blocks), dim3(256), 0, s, true, f);
+    e = launch_kernel(k_q4_expand<D>, dim3(q4.prefill_blocks, 2), dim3(kExpandThreads), 0, s, true, f);
     AttnArgs c = a;
     c.k_cache = f.k_copy;
     c.v_cache = f.v_copy;
