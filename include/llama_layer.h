@@ -343,7 +343,8 @@ int kv_cache_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
  * n_kv_heads, head_dim and block_size matter (it is checked as a whole).  Rows
  * of out behind the last sequence are left as they were; a token whose position
  * is negative or not below its seq_lens is reported as a device guard and its
- * row left.
+ * row left (in one of the longer sequences below its row is undefined, and the
+ * rows of up to 127 tokens beside it may be left).
  * Sequences with one new token, or with so few that new * n_heads / n_kv_heads
  * <= 16 (draft tokens to verify), read the 4-bit cache directly.  For longer
  * ones the workspace takes a 16-bit copy of the sequence's K and V, of

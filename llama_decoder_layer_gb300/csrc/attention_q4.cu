@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) k_attn_q4_combine(const Q4
 // longer sequences
 // ---------------------------------------------------------------------------
 struct PrefillQ4 {
-  const int32_t *qsl, *seq_lens, *block_table;
+  const int32_t *qsl, *seq_lens, *positions, *block_table;
   int T, B, max_blocks, num_blocks, nkv, group, max_query_len, max_seq_len, prefill_blocks;
   int tile_tokens, max_items, stride;
   int32_t* base;    // [B + 1] blocks of the copy before each sequence
@@ -846,6 +846,7 @@ __global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
     if (b < p.B) p.base[b] = static_cast<int32_t>(base < p.prefill_blocks ? base : p.prefill_blocks);
     const long long item = items_before + scan(tiles, all) - tiles;
     items_before += all;
+    if (item + tiles > p.max_items) report_error(p.err, kErrGuard, kWhereQueryLen);  // (sequences that overlap)
     for (int j = 0; j < tiles; ++j)
       if (item + j < p.max_items)
         p.items[item + j] = (static_cast<uint32_t>(b) << 16) | static_cast<uint32_t>(tiles - 1 - j);
@@ -857,6 +858,8 @@ __global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
 
 // CTA (x, y): K (y = 0) or V of all KV heads of block x of the copy in bf16
 // (exact), zero past the sequence's end; and the block's entry in the copy's table.
+// Bad positions of the sequence's tokens are reported here, by the CTAs of its
+// first blocks (the prefill kernels look at the largest of a tile only).
 constexpr int kExpandThreads = 256;
 
 template <int D, bool V>
@@ -896,7 +899,15 @@ __global__ void __launch_bounds__(kExpandThreads) k_q4_expand(const PrefillQ4 p)
   }
   const int b = upto - 1, j = s - p.base[b], len = p.seq_lens[b];
   if (j >= p.stride || j * kQ4Block >= len) return;
-  if (threadIdx.x == 0 && blockIdx.y == 0) p.table[static_cast<size_t>(b) * p.stride + j] = s;
+  if (blockIdx.y == 0) {
+    if (threadIdx.x == 0) p.table[static_cast<size_t>(b) * p.stride + j] = s;
+    const int t0 = p.qsl[b], n = p.qsl[b + 1] - t0;
+    const long long step = static_cast<long long>((len + kQ4Block - 1) / kQ4Block) * kExpandThreads;
+    for (long long i = static_cast<long long>(j) * kExpandThreads + threadIdx.x; i < n; i += step) {
+      const int pos = p.positions[t0 + i];
+      if (pos < 0 || pos >= len) report_error(p.err, kErrGuard, kWhereQueryLen);
+    }
+  }
   int blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + j];
   if (blk < 0 || blk >= p.num_blocks) {
     if (threadIdx.x == 0) report_error(p.err, kErrGuard, kWhereBlockTable);
@@ -1004,6 +1015,7 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   f.T = a.T;
   f.qsl = a.qsl;
   f.seq_lens = a.seq_lens;
+  f.positions = a.positions;
   f.block_table = a.block_table;
   f.B = a.B;
   f.max_query_len = mq;

@@ -1,7 +1,8 @@
 // Host-side kernel launch with an optional programmatic dependency on the
 // kernel before it on the stream (see pdl_wait / pdl_trigger in common.cuh).
 // The first kernel of a public call is launched without it, so it starts only
-// after everything the caller queued earlier has completed; the kernels after
+// after everything the caller queued earlier has completed (but for the calls
+// whose first kernel touches nothing before its pdl_wait); the kernels after
 // it in the same call overlap their prologues (barrier setup, tensor-memory
 // allocation, weight prefetch) with the tail of their predecessor.
 #pragma once

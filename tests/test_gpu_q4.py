@@ -388,6 +388,20 @@ def test_bad_positions_lengths_and_blocks_are_reported(bound):
             assert np.abs(got[rest] - want[rest]).max() < 0.05 * np.abs(want).max(), (new, what)
 
 
+@pytest.mark.parametrize("nq,nkv,d", [(8, 2, 64), (8, 2, 128), (5, 1, 128)])
+@pytest.mark.parametrize("new,at", [(30, 7), (300, 299)])
+def test_one_negative_position_in_a_longer_sequence(nq, nkv, d, new, at):
+    c = Case([(1, 40), (new, new + 17), (1, 60)], nq, nkv, d, seed=20)
+    c.batch.positions[1 + at] = -1
+    c.run()
+    guard()
+    got = f64(c.out).reshape(-1, nq, d)
+    want, spread, flat = R.attention(f64(c.q), c.pos, c.qsl, c.table, c.tiles[0], c.tiles[1], 1.0, 1.0)
+    rest = np.delete(np.arange(len(c.pos)), 1 + at)
+    tol = 2.0 ** -8 * np.abs(want) + 2 * (2.0 ** -8 + 2.0 ** -12) * spread + 2.0 ** -31 * flat
+    assert np.all((np.abs(got - want) <= tol)[rest])
+
+
 def test_too_few_prefill_blocks_are_reported():
     c = Case([(1, 40), (50, 60), (20, 100)], 8, 2, 128, seed=12)
     c.run(pre=4)  # room for the first prompt (4 blocks), not for the second (7)
@@ -446,6 +460,45 @@ def test_a_mixed_batch_captured_and_replayed():
         ok()
         assert torch.equal(c.out, want)
     c.check()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_the_cache_written_right_behind_a_mixed_batch(captured):
+    # the write starts while the batch's last kernels end, those of the side stream too, and must not reach the cache
+    c = Case([(1, 900), (40, 77), (1, 40), (200, 333), (3, 50)], 32, 4, 128, seed=19)
+    slots = torch.from_numpy(np.concatenate([[c.table[b][j // 16] * 16 + j % 16 for j in range(t)]
+                                             for b, (_, t) in enumerate(c.seqs)]).astype(np.int32)).to(DEV)
+    g = torch.Generator(device=DEV).manual_seed(19)
+    rows = [torch.randn(len(slots), 4, 128, generator=g, device=DEV).bfloat16() for _ in range(4)]
+    outs = [torch.empty_like(c.out) for _ in range(4)]
+
+    def write(i):
+        lb.kv_cache_write_q4(rows[2 * i], rows[2 * i + 1], slots, c.kc, c.vc)
+
+    def chain():
+        for n in range(4):
+            write(n % 2)
+            c.run(out=outs[n])
+
+    want = []
+    for i in range(2):
+        write(i)
+        torch.cuda.synchronize()
+        want.append(c.run().clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            chain()
+        chain = graph.replay
+    for _ in range(5):
+        for o in outs:
+            o.fill_(5.0)
+        chain()
+        ok()
+        for n in range(4):
+            assert torch.equal(outs[n], want[n % 2]), n
 
 
 def test_calls_back_to_back_on_two_streams():
