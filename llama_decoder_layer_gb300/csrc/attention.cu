@@ -63,6 +63,8 @@ struct AttnParams {
   float* part_o;
   float2* part_ml;
   uint32_t* pre_items;  // prefill work list: (sequence << 16) | q-tile, 0xFFFFFFFF past the end
+  const int32_t* n_items;  // its length (split prefill)
+  int split_ctas;          // CTAs that the parts of a split prefill may take
   int* err;
 };
 
@@ -483,7 +485,35 @@ __global__ void __launch_bounds__(1024) k_attn_plan(const int32_t* __restrict__ 
 
 constexpr int kPreMaxHeads = 8;  // q heads (consumer warps) per prefill CTA
 
-template <int D>
+// Few query tiles over many keys: a CTA each would leave SMs idle and walk its
+// keys alone.  So the keys of a tile are split over as many CTAs as bring the
+// whole to split_ctas (those that run at once), two key tiles each at least, and
+// k_attn_prefill_join joins the parts.  CTA i takes part i % parts of unit i / parts,
+// a unit being a query tile of the work list and its KV head (and chunk of heads).
+constexpr int kPreMaxParts = 16;
+constexpr int kPartRows = 128;  // query rows of a CTA at most, in either prefill kernel
+
+struct PrefillPart {
+  int units, parts, unit, part;
+};
+
+__device__ __forceinline__ PrefillPart prefill_part(const AttnParams& p, int per_item) {
+  PrefillPart x;
+  x.units = *p.n_items * per_item;
+  x.parts = min(kPreMaxParts, max(1, p.split_ctas / max(x.units, 1)));
+  x.unit = blockIdx.x / x.parts;
+  x.part = blockIdx.x - x.unit * x.parts;
+  return x;
+}
+
+// its key tiles first .. last - 1 of n
+__device__ __forceinline__ void part_tiles(const PrefillPart& x, int n, int& first, int& last) {
+  const int per = max(2, (n + x.parts - 1) / x.parts);
+  first = x.part * per;
+  last = min(n, first + per);
+}
+
+template <int D, bool SPLIT = false>
 __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
     k_attn_prefill(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, AttnParams p) {
   constexpr int TB = tile_bytes(D);      // one 16-key block of K (or V)
@@ -501,10 +531,18 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
   pdl_wait();
   pdl_trigger();
   const int n_hc = (p.group + kPreMaxHeads - 1) / kPreMaxHeads;  // head chunks per KV head
-  const uint32_t item = p.pre_items[blockIdx.y];
+  int bx = blockIdx.x, by = blockIdx.y;
+  PrefillPart part{};
+  if constexpr (SPLIT) {
+    part = prefill_part(p, p.nkv * n_hc);
+    if (part.unit >= part.units) return;
+    by = part.unit / (p.nkv * n_hc);
+    bx = part.unit - by * (p.nkv * n_hc);
+  }
+  const uint32_t item = p.pre_items[by];
   if (item == kNoItem) return;
   const int b = static_cast<int>(item >> 16), qt = static_cast<int>(item & 0xFFFFu);
-  const int kvh = blockIdx.x / n_hc, hc = blockIdx.x % n_hc;
+  const int kvh = bx / n_hc, hc = bx % n_hc;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = min(kPreMaxHeads, p.group - hc * kPreMaxHeads);  // q heads of this CTA
   const int h_first = kvh * p.group + hc * kPreMaxHeads;
@@ -516,14 +554,22 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
   const int nrows = min(16, qlen - qt * 16);
 
   // largest position of the tile (keys needed: 0 .. p_hi)
-  int p_hi = -1;
-  for (int r = 0; r < nrows; ++r) p_hi = max(p_hi, p.positions[tq + r]);
+  const int pos_l = lane < nrows ? p.positions[tq + lane] : -1;
+  const int p_hi = __reduce_max_sync(0xffffffffu, max(pos_l, -1));
   const int n_keys = p_hi + 1;
   if (n_keys > p.seq_lens[b] || (n_keys + kBS - 1) / kBS > p.max_blocks) {
     if (kvh == 0 && threadIdx.x == 0) report_error(p.err, kErrGuard, kWhereQueryLen);
     return;
   }
-  const int ntiles = (n_keys + kPreKeys - 1) / kPreKeys;
+  int ntiles = (n_keys + kPreKeys - 1) / kPreKeys, kt0 = 0;  // key tiles kt0 .. ntiles - 1
+  const size_t part_row = static_cast<size_t>(blockIdx.x) * kPartRows + warp * 16;
+  if constexpr (SPLIT) {
+    part_tiles(part, ntiles, kt0, ntiles);
+    if (part.parts > 1 && kt0 >= ntiles) {  // no keys for this part
+      if (warp < G && lane < 16) p.part_ml[part_row + lane] = make_float2(-INFINITY, 0.f);
+      return;
+    }
+  }
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kPreStages;
 
   if (warp < G) {
@@ -554,16 +600,30 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
       const int nblk = (n_keys + kBS - 1) / kBS;
       uint32_t uses[kPreStages] = {};
       bool ok = true;
-      for (int kt = 0; kt < ntiles && ok; ++kt) {
-        const int st = kt % kPreStages;
-        if (!mbar_wait(empty0 + 8 * st, ((kt / kPreStages) & 1) ^ 1, abort_flag)) {
+      // a tile's block numbers are read a tile ahead, all four at once, so that their latency does not stand before
+      // the copies
+      int ahead[4];
+      auto look_ahead = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ahead[i] = bt[min(kt * 4 + i, nblk - 1)];
+      };
+      if (kt0 < ntiles) look_ahead(kt0);
+      for (int kt = kt0; kt < ntiles && ok; ++kt) {
+        int blocks[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) blocks[i] = ahead[i];
+        if (kt + 1 < ntiles) look_ahead(kt + 1);
+        const int st = (kt - kt0) % kPreStages;
+        if (!mbar_wait(empty0 + 8 * st, (((kt - kt0) / kPreStages) & 1) ^ 1, abort_flag)) {
           ok = false;
           break;
         }
         int nload = min(4, nblk - kt * 4);
         mbar_arrive_expect_tx(full0 + 8 * st, nload * 2 * TB);
-        for (int i = 0; i < nload; ++i) {
-          int blk = bt[kt * 4 + i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i >= nload) break;
+          int blk = blocks[i];
           if (blk < 0 || blk >= p.num_blocks) {
             report_error(p.err, kErrGuard, kWhereBlockTable);
             blk = 0;
@@ -599,10 +659,9 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
     for (int kk = 0; kk < D / 16; ++kk) ldsm_x4(base + kk * 32, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3]);
   }
   const int g = lane >> 2;
-  const int pos0 = g < nrows ? p.positions[tq + g] : -1;      // row g
-  const int pos1 = g + 8 < nrows ? p.positions[tq + g + 8] : -1;  // row g + 8
-  int p_lo = p_hi;
-  for (int r = 0; r < nrows; ++r) p_lo = min(p_lo, p.positions[tq + r]);
+  const int pos0 = __shfl_sync(0xffffffffu, pos_l, g);      // row g
+  const int pos1 = __shfl_sync(0xffffffffu, pos_l, g + 8);  // row g + 8
+  const int p_lo = __reduce_min_sync(0xffffffffu, lane < nrows ? pos_l : p_hi);
 
   float o[D / 8][4];
 #pragma unroll
@@ -610,9 +669,9 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
   bool ok = true;
 
-  for (int kt = 0; kt < ntiles; ++kt) {
-    const int st = kt % kPreStages;
-    if (!mbar_wait(full0 + 8 * st, (kt / kPreStages) & 1, abort_flag)) {
+  for (int kt = kt0; kt < ntiles; ++kt) {
+    const int st = (kt - kt0) % kPreStages;
+    if (!mbar_wait(full0 + 8 * st, ((kt - kt0) / kPreStages) & 1, abort_flag)) {
       ok = false;
       break;
     }
@@ -642,57 +701,100 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
         }
       }
     }
-    // scale to the log2 domain; causal mask (keys past n_keys are past every
-    // row's position, so the same test removes them)
     const int kq = kbase + 2 * (lane & 3);
-    if (need_mask) {
+    if constexpr (SPLIT) {
+      // as below, in fewer instructions: raw scores up to the exponent's multiply-add, the hardware's exp2, and O
+      // rescaled only when a maximum moved
+      if (need_mask) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int key = kq + n * 8 + (c & 1);
-          const int lim = c < 2 ? pos0 : pos1;
-          s[n][c] = key <= lim ? s[n][c] * p.scale_log2 : -INFINITY;
+          for (int c = 0; c < 4; ++c)
+            if (kq + n * 8 + (c & 1) > (c < 2 ? pos0 : pos1)) s[n][c] = -INFINITY;
+      }
+      float mx0 = fmaxf(s[0][0], s[0][1]), mx1 = fmaxf(s[0][2], s[0][3]);
+#pragma unroll
+      for (int n = 1; n < 8; ++n) {
+        mx0 = fmax3(mx0, s[n][0], s[n][1]);
+        mx1 = fmax3(mx1, s[n][2], s[n][3]);
+      }
+      const float nm0 = fmaxf(m0, quad_max(mx0) * p.scale_log2), nm1 = fmaxf(m1, quad_max(mx1) * p.scale_log2);
+      const float b0 = nm0 == -INFINITY ? 0.f : nm0, b1 = nm1 == -INFINITY ? 0.f : nm1;
+      if (__any_sync(0xffffffffu, nm0 > m0 || nm1 > m1)) {
+        const float a0 = fast_exp2(m0 - b0), a1 = fast_exp2(m1 - b1);
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][0] *= a0;
+          o[n][1] *= a0;
+          o[n][2] *= a1;
+          o[n][3] *= a1;
         }
+      }
+      m0 = nm0;
+      m1 = nm1;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        s[n][0] = fast_exp2(fmaf(s[n][0], p.scale_log2, -b0));
+        s[n][1] = fast_exp2(fmaf(s[n][1], p.scale_log2, -b0));
+        s[n][2] = fast_exp2(fmaf(s[n][2], p.scale_log2, -b1));
+        s[n][3] = fast_exp2(fmaf(s[n][3], p.scale_log2, -b1));
+        l0 += s[n][0] + s[n][1];
+        l1 += s[n][2] + s[n][3];
+      }
     } else {
+      // scale to the log2 domain; causal mask (keys past n_keys are past every
+      // row's position, so the same test removes them)
+      if (need_mask) {
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[n][c] *= p.scale_log2;
-    }
-    // online softmax once per tile: new row maxima, rescale of O and l
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+          for (int c = 0; c < 4; ++c) {
+            const int key = kq + n * 8 + (c & 1);
+            const int lim = c < 2 ? pos0 : pos1;
+            s[n][c] = key <= lim ? s[n][c] * p.scale_log2 : -INFINITY;
+          }
+      } else {
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
-      mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
-    }
-    mx0 = quad_max(mx0);
-    mx1 = quad_max(mx1);
-    const float nm0 = fmaxf(m0, mx0), nm1 = fmaxf(m1, mx1);
-    const float b0 = nm0 == -INFINITY ? 0.f : nm0;
-    const float b1 = nm1 == -INFINITY ? 0.f : nm1;
-    const float a0 = exp2f(m0 - b0), a1 = exp2f(m1 - b1);
-    m0 = nm0;
-    m1 = nm1;
-    float ls0 = 0.f, ls1 = 0.f;
+        for (int n = 0; n < 8; ++n)
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      s[n][0] = exp2f(s[n][0] - b0);
-      s[n][1] = exp2f(s[n][1] - b0);
-      s[n][2] = exp2f(s[n][2] - b1);
-      s[n][3] = exp2f(s[n][3] - b1);
-      ls0 += s[n][0] + s[n][1];
-      ls1 += s[n][2] + s[n][3];
-    }
-    l0 = l0 * a0 + ls0;
-    l1 = l1 * a1 + ls1;
+          for (int c = 0; c < 4; ++c) s[n][c] *= p.scale_log2;
+      }
+      // online softmax once per tile: new row maxima, rescale of O and l
+      float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-      o[n][0] *= a0;
-      o[n][1] *= a0;
-      o[n][2] *= a1;
-      o[n][3] *= a1;
+      for (int n = 0; n < 8; ++n) {
+        mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
+        mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
+      }
+      mx0 = quad_max(mx0);
+      mx1 = quad_max(mx1);
+      const float nm0 = fmaxf(m0, mx0), nm1 = fmaxf(m1, mx1);
+      const float b0 = nm0 == -INFINITY ? 0.f : nm0;
+      const float b1 = nm1 == -INFINITY ? 0.f : nm1;
+      const float a0 = exp2f(m0 - b0), a1 = exp2f(m1 - b1);
+      m0 = nm0;
+      m1 = nm1;
+      float ls0 = 0.f, ls1 = 0.f;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        s[n][0] = exp2f(s[n][0] - b0);
+        s[n][1] = exp2f(s[n][1] - b0);
+        s[n][2] = exp2f(s[n][2] - b1);
+        s[n][3] = exp2f(s[n][3] - b1);
+        ls0 += s[n][0] + s[n][1];
+        ls1 += s[n][2] + s[n][3];
+      }
+      l0 = l0 * a0 + ls0;
+      l1 = l1 * a1 + ls1;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] *= a0;
+        o[n][1] *= a0;
+        o[n][2] *= a1;
+        o[n][3] *= a1;
+      }
     }
     // O += P V, one 16-key block per k-step
     {
@@ -736,6 +838,21 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
   }
   l0 = quad_sum(l0);
   l1 = quad_sum(l1);
+  if constexpr (SPLIT) {
+    if (part.parts > 1) {
+      if ((lane & 3) == 0) {
+        p.part_ml[part_row + g] = make_float2(m0, l0);
+        p.part_ml[part_row + g + 8] = make_float2(m1, l1);
+      }
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        const int col = n * 8 + 2 * (lane & 3);
+        *reinterpret_cast<float2*>(p.part_o + (part_row + g) * D + col) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(p.part_o + (part_row + g + 8) * D + col) = make_float2(o[n][2], o[n][3]);
+      }
+      return;
+    }
+  }
   const float i0 = l0 > 0.f ? 1.f / l0 : 0.f;
   const float i1 = l1 > 0.f ? 1.f / l1 : 0.f;
   const int h = h_first + warp;
@@ -749,6 +866,69 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
       *reinterpret_cast<uint32_t*>(p.out + (static_cast<size_t>(tq + g + 8) * p.nq + h) * D + col) =
           pack_bf16x2(o[n][2] * i1, o[n][3] * i1);
   }
+}
+
+// Joins the parts of a unit's query rows (see prefill_part) in order, a warp per row: rows 16 blockIdx.y on.  TC: rows
+// are token * group + head, else head * 16 + token.  Tiles that the parts left out (a position past the sequence) are left
+// out here too.
+template <int D, bool TC>
+__global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
+  pdl_wait();
+  const int n_hc = TC ? 1 : (p.group + kPreMaxHeads - 1) / kPreMaxHeads;
+  const PrefillPart part = prefill_part(p, p.nkv * n_hc);
+  const int unit = blockIdx.x, r = blockIdx.y * 16 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (part.parts == 1 || unit >= part.units) return;
+  const int by = unit / (p.nkv * n_hc), bx = unit - by * (p.nkv * n_hc);
+  const uint32_t item = p.pre_items[by];
+  if (item == kNoItem) return;
+  const int b = static_cast<int>(item >> 16), qt = static_cast<int>(item & 0xFFFFu);
+  const int kvh = bx / n_hc, hc = bx % n_hc;
+  const int tile = TC ? kPartRows / p.group : 16;
+  const int tok = TC ? r / p.group : r % 16, head = TC ? r % p.group : r / 16;
+  const int tq = p.qsl[b] + qt * tile, nrows = min(tile, p.qsl[b + 1] - tq);
+  if (tok >= nrows || head >= min(TC ? p.group : kPreMaxHeads, p.group - hc * kPreMaxHeads)) return;
+  int hi = -1;
+  for (int i = lane; i < nrows; i += 32) hi = max(hi, p.positions[tq + i]);
+  const int n_keys = __reduce_max_sync(0xffffffffu, hi) + 1;
+  if (n_keys > p.seq_lens[b] || (n_keys + kBS - 1) / kBS > p.max_blocks || (TC && n_keys < 1)) return;
+  constexpr int E = D / 32;
+  const size_t first = static_cast<size_t>(unit) * part.parts * kPartRows + r;
+  // lane i has part i's maximum and sum, and its weight in the whole (zero: nothing was stored, or all of it was masked)
+  const float2 ml = lane < part.parts ? p.part_ml[first + static_cast<size_t>(lane) * kPartRows] : make_float2(-INFINITY, 0.f);
+  float m = ml.x;
+#pragma unroll
+  for (int o = kPreMaxParts / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = __shfl_sync(0xffffffffu, m, 0);
+  const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+  float L = 0.f, O[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) O[e] = 0.f;
+  for (int i0 = 0; i0 < part.parts; i0 += 4) {
+    float x[4][E];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const size_t at = first + static_cast<size_t>(min(i0 + n, part.parts - 1)) * kPartRows;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + lane * E + e);
+        x[n][e] = v.x;
+        x[n][e + 1] = v.y;
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float fi = __shfl_sync(0xffffffffu, f, i0 + n), li = __shfl_sync(0xffffffffu, ml.y, i0 + n);  // zero past the parts
+      if (fi == 0.f) continue;
+      L += li * fi;
+#pragma unroll
+      for (int e = 0; e < E; ++e) O[e] += x[n][e] * fi;
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(
+      p.out + (static_cast<size_t>(tq + tok) * p.nq + kvh * p.group + hc * kPreMaxHeads + head) * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(O[e] * inv, O[e + 1] * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -790,6 +970,7 @@ static_assert(kTcKeys == 64 || kTcKeys == 128, "the softmax handles 64- or 128-k
 constexpr int kTcSmem = 2 * kTcQHalf + (kTcKStages + kTcVStages) * kTcTileBytes + 256 + kTcSlack;
 constexpr float kRescaleLog2 = 8.0f;               // lazy rescale threshold (factor 256)
 
+template <bool SPLIT = false>
 __global__ void __launch_bounds__(kTcThreads, 2)
     k_attn_prefill_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, AttnParams p) {
@@ -829,11 +1010,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   int* p_hi_s = reinterpret_cast<int*>(tmem_slot + 2);
   int* p_lo_s = reinterpret_cast<int*>(tmem_slot + 3);
 
-  const uint32_t item = p.pre_items[blockIdx.y];
+  int kvh = blockIdx.x, by = blockIdx.y;
+  PrefillPart part{};
+  if constexpr (SPLIT) {
+    part = prefill_part(p, p.nkv);
+    if (part.unit >= part.units) return;
+    by = part.unit / p.nkv;
+    kvh = part.unit - by * p.nkv;
+  }
+  const uint32_t item = p.pre_items[by];
   if (item == kNoItem) return;
   const int G = p.group, QT = 128 / G;
   const int b = static_cast<int>(item >> 16), qt = static_cast<int>(item & 0xFFFFu);
-  const int kvh = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t0 = p.qsl[b];
   const int qlen = p.qsl[b + 1] - t0;
@@ -859,7 +1047,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     return;
   }
   const int nblk = (n_keys + kBS - 1) / kBS;
-  const int ntiles = (n_keys + kTcKeys - 1) / kTcKeys;
+  int ntiles = (n_keys + kTcKeys - 1) / kTcKeys, kt0 = 0;  // key tiles kt0 .. kt0 + ntiles - 1
+  if constexpr (SPLIT) {
+    part_tiles(part, ntiles, kt0, ntiles);
+    ntiles -= kt0;
+    if (ntiles <= 0) {  // no keys for this part
+      if (threadIdx.x < kPartRows)
+        p.part_ml[static_cast<size_t>(blockIdx.x) * kPartRows + threadIdx.x] = make_float2(-INFINITY, 0.f);
+      return;
+    }
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -916,7 +1113,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         int blks[kTcKeys / kBS];
 #pragma unroll
         for (int i = 0; i < kTcKeys / kBS; ++i) {
-          const int jb = j * (kTcKeys / kBS) + i;
+          const int jb = (kt0 + j) * (kTcKeys / kBS) + i;
           blks[i] = bt[jb < nblk ? jb : 0];
         }
         if (!mbar_wait(empty0 + 8 * st, ((j / nst) & 1) ^ 1, abort_flag)) {
@@ -1048,7 +1245,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       // S of this tile: masked, scaled row maximum (four independent max
       // chains; eight and sixteen measured no faster), 64 columns per load;
       // t keeps the last 64 columns read
-      const int kbase = j * kTcKeys;
+      const int kbase = (kt0 + j) * kTcKeys;
       const bool full_tile = kbase + kTcKeys - 1 <= pos_lo;  // CTA-uniform
       const int lim = pos - kbase;                           // column e is visible when e <= lim
       const uint32_t s_addr = lane_addr + st * kTcKeys;
@@ -1188,10 +1385,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       *abort_flag = 1;
     } else {
       tc_fence_after();
+      if (SPLIT && part.parts > 1) {
+        const size_t at = static_cast<size_t>(blockIdx.x) * kPartRows + r;
+        p.part_ml[at] = make_float2(m_run, l);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float o[32];
+          tmem_ld32(lane_addr + kOCol + c * 32, o);
+          float4* d4 = reinterpret_cast<float4*>(p.part_o + at * 128 + c * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) d4[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16* dst = p.out + (static_cast<size_t>(tq + tok) * p.nq + kvh * G + hq) * 128;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < (SPLIT && part.parts > 1 ? 0 : 4); ++c) {
         float o[32];
         tmem_ld32(lane_addr + kOCol + c * 32, o);
         if (row_ok) {
@@ -1389,12 +1598,12 @@ int launch_prefill_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap
     static std::once_flag tc_once;
     static cudaError_t tc_attr = cudaSuccess;
     std::call_once(tc_once, [] {
-      tc_attr = cudaFuncSetAttribute(k_attn_prefill_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+      tc_attr = cudaFuncSetAttribute(k_attn_prefill_tc<>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
     });
     if (tc_attr != cudaSuccess) return tc_attr;
     CUtensorMap tq;
     if (!make_q_tmap(&tq, a.q, a.T, a.nq, p.group, tile_tokens)) return cudaErrorInvalidValue;
-    return launch_kernel(k_attn_prefill_tc, dim3(a.nkv, items), dim3(kTcThreads), kTcSmem, s, pdl, tq, tk,
+    return launch_kernel(k_attn_prefill_tc<>, dim3(a.nkv, items), dim3(kTcThreads), kTcSmem, s, pdl, tq, tk,
                          tv, p);
   }
   const int n_hc = (p.group + kPreMaxHeads - 1) / kPreMaxHeads;
@@ -1471,8 +1680,38 @@ int prefill_tile_tokens(const AttnArgs& a) {
   return prefill_on_tc(a.head_dim, group) ? 128 / group : 16;
 }
 
-int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int n_items, bool pdl, cudaStream_t s) {
-  if (n_items > 65535) return cudaErrorInvalidValue;  // grid y
+namespace {
+
+// CTAs that run at once, by their shared memory: 50 KB (head_dim 64), 99 KB (128), 97 KB (tensor memory)
+int prefill_split_ctas(int head_dim) { return num_sms() * (head_dim == 64 ? 4 : 2); }
+
+template <int D, bool TC, typename Kernel, typename... Maps>
+int launch_prefill_split(Kernel kernel, int smem, int threads, const AttnParams& p, int n_items, bool pdl, cudaStream_t s,
+                         const Maps&... maps) {
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [&] { attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (attr != cudaSuccess) return attr;
+  const long long units =
+      static_cast<long long>(n_items) * p.nkv * (TC ? 1 : (p.group + kPreMaxHeads - 1) / kPreMaxHeads);
+  const unsigned ctas = static_cast<unsigned>(units > p.split_ctas ? units : p.split_ctas);
+  const cudaError_t e = launch_kernel(kernel, dim3(ctas), dim3(threads), smem, s, pdl, maps..., p);
+  if (e != cudaSuccess) return e;
+  // units of two parts or more
+  const unsigned joins = static_cast<unsigned>(units < p.split_ctas / 2 ? units : p.split_ctas / 2);
+  const unsigned rows16 = TC || p.group > kPreMaxHeads ? 8 : p.group;
+  return launch_kernel(k_attn_prefill_join<D, TC>, dim3(joins, rows16), dim3(512), 0, s, true, p);
+}
+
+}  // namespace
+
+size_t prefill_split_bytes(int head_dim) {
+  return static_cast<size_t>(prefill_split_ctas(head_dim)) * kPartRows * (head_dim * sizeof(float) + sizeof(float2));
+}
+
+int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int max_items, const int32_t* n_items, void* parts,
+                         bool pdl, cudaStream_t s) {
+  if (max_items > 65535) return cudaErrorInvalidValue;  // grid y
   const long long rows = static_cast<long long>(a.num_blocks) * a.nkv * kBS;
   CUtensorMap tk, tv;
   if (!make_cache_tmap(&tk, a.k_cache, rows, a.head_dim)) return cudaErrorInvalidValue;
@@ -1483,8 +1722,34 @@ int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int n_items, 
   const int tile = prefill_tile_tokens(a);
   const cudaError_t attr = a.head_dim == 128 ? set_attributes<128>() : set_attributes<64>();
   if (attr != cudaSuccess) return attr;
-  if (a.head_dim == 128) return launch_prefill_d<128>(a, tk, tv, p, tc, tile, n_items, pdl, s);
-  return launch_prefill_d<64>(a, tk, tv, p, tc, tile, n_items, pdl, s);
+  // Keys are split where the batch's tokens, were they all of prompts, would leave a unit two CTAs or more, and where the
+  // keys pay for the parts' way through memory and one more launch.  64 new tokens, whole against split (us):
+  //   after                             500          4000         32000
+  //   64 / 8 heads x 128 (tc)      18.8 / 25.4   61.0 / 38.3    411 / 110
+  //   10 / 2 heads x 128           32.5 / 21.7    158 / 30.4   1206 / 120
+  //   8 / 2 heads x 64             20.4 / 16.6    105 / 22.5    655 / 80
+  // (17 tokens after 300 of the last two: 23.5 / 19.9 and 15.8 / 15.7)
+  const int hc = tc ? 1 : (p.group + kPreMaxHeads - 1) / kPreMaxHeads;
+  p.split_ctas = prefill_split_ctas(a.head_dim);
+  if (static_cast<long long>((a.T + tile - 1) / tile) * a.nkv * hc * 2 <= p.split_ctas &&
+      a.max_seq_len > (tc ? 2048 : 256)) {
+    p.n_items = n_items;
+    p.part_o = static_cast<float*>(parts);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(p.split_ctas) * kPartRows * a.head_dim);
+    const int threads = ((p.group < kPreMaxHeads ? p.group : kPreMaxHeads) + 1) * 32;
+    if (a.head_dim == 64)
+      return launch_prefill_split<64, false>(k_attn_prefill<64, true>, static_cast<int>(prefill_smem<64>()), threads, p,
+                                             max_items, pdl, s, tk, tv);
+    if (!tc)
+      return launch_prefill_split<128, false>(k_attn_prefill<128, true>, static_cast<int>(prefill_smem<128>()), threads,
+                                              p, max_items, pdl, s, tk, tv);
+    CUtensorMap tq;
+    if (!make_q_tmap(&tq, a.q, a.T, a.nq, p.group, tile)) return cudaErrorInvalidValue;
+    return launch_prefill_split<128, true>(k_attn_prefill_tc<true>, kTcSmem, kTcThreads, p, max_items, pdl, s, tq, tk,
+                                           tv);
+  }
+  if (a.head_dim == 128) return launch_prefill_d<128>(a, tk, tv, p, tc, tile, max_items, pdl, s);
+  return launch_prefill_d<64>(a, tk, tv, p, tc, tile, max_items, pdl, s);
 }
 
 }  // namespace llama

@@ -56,6 +56,7 @@ constexpr int kCtasPerSm = 4;
 constexpr int kRankStep = 46;       // half the share lost from one CTA of an SM to the next, in 1/1024 of the mean
 constexpr int kMinShare = 8;        // blocks a CTA takes at least: two a warp
 constexpr int kWholeBlocks = 64;    // pieces of up to so many blocks stay whole where the SMs hold them all
+constexpr int kFewBlocks = 16384;   // blocks that the decode kernel for 16 rows takes at most 8 us for
 constexpr int kPieceCost = 6;       // what a (sequence, KV head) costs a CTA beside its blocks, in blocks
 constexpr float kMaxStep = 8.f;     // log2 by which a score may pass the running maximum
 constexpr float kWeightBias = 6.f;  // weights are stored times 2^6
@@ -789,7 +790,7 @@ struct PrefillQ4 {
   const int32_t *qsl, *seq_lens, *positions, *block_table;
   int T, B, max_blocks, num_blocks, nkv, group, max_query_len, max_seq_len, prefill_blocks;
   int tile_tokens, max_items, stride;
-  int32_t* base;    // [B + 1] blocks of the copy before each sequence
+  int32_t* base;    // [B + 1] blocks of the copy before each sequence; then the length of the work list
   uint32_t* items;  // the prefill kernels' work list
   int32_t* table;   // [B, stride] block table of the copy
   const uint8_t *k_cache, *v_cache;
@@ -859,8 +860,10 @@ __global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
       if (item + j < p.max_items)
         p.items[item + j] = (static_cast<uint32_t>(b) << 16) | static_cast<uint32_t>(tiles - 1 - j);
   }
-  if (threadIdx.x == 0)
+  if (threadIdx.x == 0) {
     p.base[p.B] = static_cast<int32_t>(blocks_before < p.prefill_blocks ? blocks_before : p.prefill_blocks);
+    p.base[p.B + 1] = static_cast<int32_t>(items_before < p.max_items ? items_before : p.max_items);
+  }
   for (long long i = items_before + threadIdx.x; i < p.max_items; i += blockDim.x) p.items[i] = kNoPrefillItem;
 }
 
@@ -938,7 +941,7 @@ size_t decode_smem() {
 }
 
 struct Layout {
-  size_t part_o, part_ml, cut, base, items, table, k_copy, v_copy, total;
+  size_t part_o, part_ml, cut, base, items, table, k_copy, v_copy, parts, total;
   int grid, max_items, stride;
 };
 
@@ -964,9 +967,11 @@ Layout layout(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int he
     off += copy;
     L.v_copy = off;
     off += copy;
+    L.parts = off;
+    off += up(prefill_split_bytes(head_dim));
   }
   L.base = off;
-  off += up((static_cast<size_t>(B) + 1) * 4);
+  off += up((static_cast<size_t>(B) + 2) * 4);
   L.items = off;
   off += up(static_cast<size_t>(L.max_items) * 4);
   L.total = off;
@@ -993,7 +998,8 @@ int launch_decode(Q4Params p, int rows_lo, int rows_hi, bool alone, bool pdl, cu
   p.sms = alone ? num_sms() : grid;
   // Few short pieces are not split: finding the ranges and joining the parts cost about as much as kWholeBlocks blocks
   // (one sequence of 777 tokens: 7.5 us split into 13 CTAs and joined, 7.4 whole, with one launch instead of two).
-  p.whole = pieces <= full && (p.max_seq_len + kQ4Block - 1) / kQ4Block <= kWholeBlocks;
+  // Beside prefill kernels, which take longer, four times as many.
+  p.whole = pieces <= full && (p.max_seq_len + kQ4Block - 1) / kQ4Block <= (alone ? 1 : 4) * kWholeBlocks;
   if (p.whole)
     return launch_kernel(k_attn_q4_decode<D, NT>, dim3(static_cast<unsigned>(pieces)), dim3(kThreads),
                          decode_smem<D, NT>(), s, pdl, p);
@@ -1050,8 +1056,11 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   cudaEvent_t join = nullptr;
   const cudaStream_t side = side_fork(s, &join);
   int e;
-  if (p.group > 8) {
-    e = launch_decode<D, 2>(p, 1, kMaxRows, false, false, side);
+  // Few blocks in all: one launch for 1 .. 16 rows is done before two of 8 and 16 are launched.
+  const bool few = static_cast<long long>(a.B) * a.nkv * L.stride <= kFewBlocks;
+  if (p.group > 8 || few) {
+    e = rows <= 8 ? launch_decode<D, 1>(p, 1, 8, false, false, side)
+                  : launch_decode<D, 2>(p, 1, kMaxRows, false, false, side);
   } else {
     e = launch_decode<D, 1>(p, 1, 8, false, false, side);
     if (e == 0 && rows > 8) e = launch_decode<D, 2>(p, 9, kMaxRows, false, true, side);
@@ -1066,7 +1075,7 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
     c.block_table = f.table;
     c.max_blocks = L.stride;
     c.num_blocks = q4.prefill_blocks;
-    if (e == 0) e = prefill_items_launch(c, f.items, f.max_items, true, s);
+    if (e == 0) e = prefill_items_launch(c, f.items, f.max_items, f.base + a.B + 1, q4.ws + L.parts, true, s);
   }
   if (side != s) {  // join even after a failed launch, so that the caller's stream never runs ahead of the side stream
     const int j = side_join(s, side, join);

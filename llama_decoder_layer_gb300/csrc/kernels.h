@@ -176,11 +176,14 @@ cudaStream_t side_fork(cudaStream_t s, cudaEvent_t* join);
 int side_join(cudaStream_t s, cudaStream_t side, cudaEvent_t join);
 
 // The prefill kernels alone, over a work list of (sequence << 16 | query tile)
-// entries on the device, kNoPrefillItem past the end, tiles of
-// prefill_tile_tokens(a) tokens.
+// entries on the device, *n_items of them and kNoPrefillItem up to max_items, tiles of
+// prefill_tile_tokens(a) tokens.  parts: 256-aligned, prefill_split_bytes(...), for
+// few tiles whose keys are split over several CTAs.
 constexpr uint32_t kNoPrefillItem = 0xFFFFFFFFu;
 int prefill_tile_tokens(const AttnArgs& a);
-int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int n_items, bool pdl, cudaStream_t s);
+size_t prefill_split_bytes(int head_dim);
+int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int max_items, const int32_t* n_items, void* parts,
+                         bool pdl, cudaStream_t s);
 
 // Sparse MoE block: workspace layout (byte offsets from a 256-aligned base)
 // and the launch sequence.

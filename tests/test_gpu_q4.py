@@ -317,6 +317,16 @@ def test_attention_prompts_and_single_tokens_in_one_batch(nq, nkv, d, bound):
     c.check()
 
 
+@pytest.mark.parametrize("nq,nkv,d", HEADS)
+@pytest.mark.parametrize("seqs", [[(70, 900), (1, 60), (33, 400), (18, 131)], [(20, 5000)], [(600, 1300), (2, 9)]])
+def test_attention_few_prompt_rows_over_many_keys(nq, nkv, d, seqs):
+    # (head shapes off the tensor-memory kernel: the keys of a tile split over several CTAs, some without any)
+    c = Case(seqs, nq, nkv, d, seed=nq + d)
+    c.run()
+    ok()
+    c.check()
+
+
 @pytest.mark.parametrize("nq,nkv,d,lens", [(32, 4, 128, (20000, 3, 9000)), (8, 8, 64, (30001,)), (64, 8, 128, (5000, 1))])
 def test_attention_long_contexts(nq, nkv, d, lens):
     c = Case([(1, n) for n in lens], nq, nkv, d, seed=3)
