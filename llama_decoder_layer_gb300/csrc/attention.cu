@@ -1731,8 +1731,9 @@ int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int max_items
   // (17 tokens after 300 of the last two: 23.5 / 19.9 and 15.8 / 15.7)
   const int hc = tc ? 1 : (p.group + kPreMaxHeads - 1) / kPreMaxHeads;
   p.split_ctas = prefill_split_ctas(a.head_dim);
-  if (static_cast<long long>((a.T + tile - 1) / tile) * a.nkv * hc * 2 <= p.split_ctas &&
-      a.max_seq_len > (tc ? 2048 : 256)) {
+  const long long pool = static_cast<long long>(a.num_blocks) * kBS;  // keys of all prompts
+  const long long tokens = pool < a.T ? pool : a.T, keys = pool < a.max_seq_len ? pool : a.max_seq_len;
+  if ((tokens + tile - 1) / tile * a.nkv * hc * 2 <= p.split_ctas && keys > (tc ? 2048 : 256)) {
     p.n_items = n_items;
     p.part_o = static_cast<float*>(parts);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(p.split_ctas) * kPartRows * a.head_dim);

@@ -33,7 +33,8 @@
 //   tile is read by all query tiles, so decoding it there would repeat the work
 //   and load the softmax's pipes.  Of a batch of 32 decoding sequences of up to
 //   16384 tokens and two prompts of 2048 tokens, 216 us, the decode kernels take
-//   60, plan and expansion 14 (beside them) and the prefill kernel 139.
+//   60, plan and expansion 14 (beside them) and the prefill kernel 139.  Few new
+//   tokens after many keys: the prefill kernels' keys are split over CTAs.
 #include <math.h>
 
 #include <mutex>
@@ -1019,10 +1020,9 @@ template <int D>
 int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStream_t s) {
   const AttnArgs& a = q4.a;
   const int mq = a.max_query_len;
-  // rows a sequence of the decode path may have
-  const int toks = mq > 1 ? min(mq, max(kMaxRows / p.group, 1)) : 1, rows = toks * p.group;
-  if (mq <= 1 || (mq <= kMaxRows && mq * p.group <= kMaxRows))
-    return rows <= 8 ? launch_decode<D, 1>(p, 1, 8, true, true, s) : launch_decode<D, 2>(p, 1, kMaxRows, true, true, s);
+  if (mq <= 1 || (mq <= kMaxRows && mq * p.group <= kMaxRows))  // every sequence takes the decode path
+    return max(mq, 1) * p.group <= 8 ? launch_decode<D, 1>(p, 1, 8, true, true, s)
+                                     : launch_decode<D, 2>(p, 1, kMaxRows, true, true, s);
 
   // Longer sequences too: the decode kernels (bound by HBM) run on the side stream beside the expansion and the
   // prefill kernel (bound by its softmax and the tensor cores).
@@ -1041,7 +1041,7 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   f.max_seq_len = a.max_seq_len;
   f.prefill_blocks = q4.prefill_blocks;
   f.tile_tokens = prefill_tile_tokens(a);
-  f.max_items = (a.T + f.tile_tokens - 1) / f.tile_tokens + a.B;
+  f.max_items = (a.T + f.tile_tokens - 1) / f.tile_tokens + min(a.B, q4.prefill_blocks);  // (a block a sequence at least)
   f.stride = L.stride;
   f.base = reinterpret_cast<int32_t*>(q4.ws + L.base);
   f.items = reinterpret_cast<uint32_t*>(q4.ws + L.items);
@@ -1059,11 +1059,10 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   // Few blocks in all: one launch for 1 .. 16 rows is done before two of 8 and 16 are launched.
   const bool few = static_cast<long long>(a.B) * a.nkv * L.stride <= kFewBlocks;
   if (p.group > 8 || few) {
-    e = rows <= 8 ? launch_decode<D, 1>(p, 1, 8, false, false, side)
-                  : launch_decode<D, 2>(p, 1, kMaxRows, false, false, side);
+    e = launch_decode<D, 2>(p, 1, kMaxRows, false, false, side);
   } else {
     e = launch_decode<D, 1>(p, 1, 8, false, false, side);
-    if (e == 0 && rows > 8) e = launch_decode<D, 2>(p, 9, kMaxRows, false, true, side);
+    if (e == 0) e = launch_decode<D, 2>(p, 9, kMaxRows, false, true, side);
   }
   const int plan_threads = a.B < 1024 ? (a.B + 31) / 32 * 32 : 1024;
   if (e == 0) e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(plan_threads), 0, s, side == s, f);

@@ -175,10 +175,11 @@ int attention_q4_launch(const AttnQ4Args& a, cudaStream_t s);
 cudaStream_t side_fork(cudaStream_t s, cudaEvent_t* join);
 int side_join(cudaStream_t s, cudaStream_t side, cudaEvent_t join);
 
-// The prefill kernels alone, over a work list of (sequence << 16 | query tile)
-// entries on the device, *n_items of them and kNoPrefillItem up to max_items, tiles of
-// prefill_tile_tokens(a) tokens.  parts: 256-aligned, prefill_split_bytes(...), for
-// few tiles whose keys are split over several CTAs.
+// The prefill kernels alone, over a cache that holds the prompts' blocks only
+// and a work list of (sequence << 16 | query tile) entries on the device, *n_items
+// of them and kNoPrefillItem up to max_items, tiles of prefill_tile_tokens(a)
+// tokens.  parts: 256-aligned, prefill_split_bytes(...), for few tiles whose keys
+// are split over several CTAs.
 constexpr uint32_t kNoPrefillItem = 0xFFFFFFFFu;
 int prefill_tile_tokens(const AttnArgs& a);
 size_t prefill_split_bytes(int head_dim);

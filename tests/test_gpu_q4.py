@@ -455,6 +455,27 @@ def test_captured_and_replayed_with_new_lengths(bound):
         c.check()
 
 
+@pytest.mark.parametrize("nq,nkv,d", [(8, 2, 64), (16, 2, 128), (5, 1, 128)])
+def test_a_chunk_over_many_keys_replayed_with_new_lengths(nq, nkv, d):
+    # more and fewer key tiles than parts, and parts without a key
+    c = Case([(40, 3000), (1, 40), (40, 2500)], nq, nkv, d, seed=22)
+    c.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+    for lens in ((3000, 40, 2500), (40, 1, 41), (130, 17, 2500), (2999, 33, 65)):
+        c.seqs = [(40, lens[0]), (1, lens[1]), (40, lens[2])]
+        c.pos = np.concatenate([np.arange(t - n, t) for n, t in c.seqs]).astype(np.int32)
+        c.batch.positions.copy_(torch.from_numpy(c.pos))
+        c.batch.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.out.fill_(5.0)
+        c.ws.random_(0, 255)
+        g.replay()
+        ok()
+        c.check()
+
+
 def test_a_mixed_batch_captured_and_replayed():
     # the decode kernels' side stream joins the capture
     c = Case([(1, 900), (40, 77), (1, 40), (3, 333)], 8, 2, 128, seed=16)
