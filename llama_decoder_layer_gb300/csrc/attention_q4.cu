@@ -32,8 +32,8 @@
 //   (k_q4_expand) over which the prefill kernels of the bf16 cache run: every
 //   tile is read by all query tiles, so decoding it there would repeat the work
 //   and load the softmax's pipes.  Of a batch of 32 decoding sequences of up to
-//   16384 tokens and two prompts of 2048 tokens, 216 us, the decode kernels take
-//   60, plan and expansion 14 (beside them) and the prefill kernel 139.  Few new
+//   16384 tokens and two prompts of 2048 tokens, 212 us, the expansion takes 9, the
+//   decode kernels (on a side stream) 60 and the prefill kernel 139.  Few new
 //   tokens after many keys: the prefill kernels' keys are split over CTAs.
 #include <math.h>
 
@@ -800,51 +800,53 @@ struct PrefillQ4 {
   int* err;
 };
 
+// inclusive sum of v over the CTA, and the whole sum
+__device__ __forceinline__ long long cta_scan(long long v, long long* tot, long long& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) tot[warp] = v;
+  __syncthreads();
+  long long before = 0;
+  all = 0;
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+    if (w < warp) before += tot[w];
+    all += tot[w];
+  }
+  return before + v;
+}
+
+// Blocks of sequence b on the prefill path (n new tokens); 0 if it takes the decode path or is out of bounds (*bad).
+__device__ __forceinline__ long long prefill_seq_blocks(const PrefillQ4& p, int b, int& n, bool& bad) {
+  const int t0 = p.qsl[b], len = p.seq_lens[b];
+  n = p.qsl[b + 1] - t0;
+  bad = false;
+  if (n <= 1 || (n <= kMaxRows && n * p.group <= kMaxRows)) return 0;
+  const long long blocks = (static_cast<long long>(len) + kQ4Block - 1) / kQ4Block;
+  bad = n > p.max_query_len || t0 < 0 || t0 > p.T - n || len < 1 || len > p.max_seq_len || blocks > p.max_blocks;
+  return bad ? 0 : blocks;
+}
+
 // One CTA: where each prefill sequence's blocks go in the copy, and its query
 // tiles (longest causal range first within a sequence).  A sequence that is out
 // of bounds or does not fit the copy is reported and left out.
-__global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
-  __shared__ long long tot[32];
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto scan = [&](long long v, long long& all) {  // inclusive sum over the CTA, and the whole sum
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    __syncthreads();
-    if (lane == 31) tot[warp] = v;
-    __syncthreads();
-    long long before = 0;
-    all = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-      if (w < warp) before += tot[w];
-      all += tot[w];
-    }
-    return before + v;
-  };
+__device__ __forceinline__ void plan_prefill(const PrefillQ4& p, long long* tot) {
   long long blocks_before = 0, items_before = 0, all;
   for (int b0 = 0; b0 < p.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
     int n = 0;
     long long blocks = 0;
     if (b < p.B) {
-      const int t0 = p.qsl[b];
-      n = p.qsl[b + 1] - t0;
-      if (n > 1 && (n > kMaxRows || n * p.group > kMaxRows)) {
-        const int len = p.seq_lens[b];
-        blocks = (static_cast<long long>(len) + kQ4Block - 1) / kQ4Block;
-        if (n > p.max_query_len || t0 < 0 || t0 > p.T - n || len < 1 || len > p.max_seq_len ||
-            blocks > p.max_blocks) {
-          // n > max_query_len and t0 are reported by the decode kernel, which looks at every sequence
-          if (n <= p.max_query_len) report_error(p.err, kErrGuard, kWhereQueryLen);
-          blocks = 0;
-        }
-      }
+      bool bad;
+      blocks = prefill_seq_blocks(p, b, n, bad);
+      // n > max_query_len and t0 are reported by the decode kernel, which looks at every sequence
+      if (bad && n <= p.max_query_len) report_error(p.err, kErrGuard, kWhereQueryLen);
     }
-    const long long base = blocks_before + scan(blocks, all) - blocks;
+    const long long base = blocks_before + cta_scan(blocks, tot, all) - blocks;
     blocks_before += all;
     int tiles = 0;
     if (blocks > 0) {
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
         tiles = (n + p.tile_tokens - 1) / p.tile_tokens;
     }
     if (b < p.B) p.base[b] = static_cast<int32_t>(base < p.prefill_blocks ? base : p.prefill_blocks);
-    const long long item = items_before + scan(tiles, all) - tiles;
+    const long long item = items_before + cta_scan(tiles, tot, all) - tiles;
     items_before += all;
     if (item + tiles > p.max_items) report_error(p.err, kErrGuard, kWhereQueryLen);  // (sequences that overlap)
     for (int j = 0; j < tiles; ++j)
@@ -868,11 +870,24 @@ __global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
   for (long long i = items_before + threadIdx.x; i < p.max_items; i += blockDim.x) p.items[i] = kNoPrefillItem;
 }
 
+__global__ void __launch_bounds__(1024) k_attn_q4_plan(const PrefillQ4 p) {
+  __shared__ long long tot[32];
+  pdl_wait();
+  pdl_trigger();
+  plan_prefill(p, tot);
+}
+
 // CTA (x, y): K (y = 0) or V of all KV heads of block x of the copy in bf16
 // (exact), zero past the sequence's end; and the block's entry in the copy's table.
 // 256 blocks of 8 heads x 128: 9.2 us for 21 MB, launch and look-up included.
 // Bad positions of the sequence's tokens are reported here, by the CTAs of its
 // first blocks (the prefill kernels look at the largest of a tile only).
+//   PLANNED: after k_attn_q4_plan.  Else, with up to kScanSeqs sequences, every CTA
+// finds its sequence itself and one more makes the plan: a launch less, and the
+// expansion starts before the decode kernels fill the SMs (mixed batch above: 215
+// us with the plan and the decode kernels before it, 212 so; a batch of 80 new tokens
+// 20.7 and 17.5).
+constexpr int kScanSeqs = 512;
 constexpr int kExpandThreads = 256;
 
 template <int D, bool V>
@@ -899,18 +914,49 @@ __device__ __forceinline__ void expand_block(const PrefillQ4& p, int s, int blk,
   }
 }
 
-template <int D>
+template <int D, bool PLANNED>
 __global__ void __launch_bounds__(kExpandThreads) k_q4_expand(const PrefillQ4 p) {
+  __shared__ long long tot[kExpandThreads / 32];
+  __shared__ int found[2];  // block s's sequence and its block there
   pdl_wait();
   pdl_trigger();
   const int s = blockIdx.x;
-  if (s >= p.base[p.B]) return;
-  int upto = 0;  // sequences whose blocks begin at or before s: the last of them holds it
-  for (int b0 = 0; b0 < p.B; b0 += kExpandThreads) {
-    const int b = b0 + threadIdx.x;
-    upto += __syncthreads_count(b < p.B && p.base[b] <= s);
+  int b, j;
+  if constexpr (PLANNED) {
+    if (s >= p.base[p.B]) return;
+    int upto = 0;  // sequences whose blocks begin at or before s: the last of them holds it
+    for (int b0 = 0; b0 < p.B; b0 += kExpandThreads) {
+      const int i = b0 + threadIdx.x;
+      upto += __syncthreads_count(i < p.B && p.base[i] <= s);
+    }
+    b = upto - 1;
+    j = s - p.base[b];
+  } else {
+    if (s == p.prefill_blocks) {
+      if (blockIdx.y == 0) plan_prefill(p, tot);
+      return;
+    }
+    if (threadIdx.x == 0) found[0] = -1;
+    long long before = 0, all;
+    for (int b0 = 0; b0 < p.B; b0 += kExpandThreads) {
+      const int i = b0 + threadIdx.x;
+      int n;
+      bool bad;
+      const long long blocks = i < p.B ? prefill_seq_blocks(p, i, n, bad) : 0;
+      const long long base = before + cta_scan(blocks, tot, all) - blocks;
+      before += all;
+      if (base <= s && s < base + blocks) {
+        found[0] = i;
+        found[1] = static_cast<int>(s - base);
+      }
+      if (before > s) break;
+    }
+    __syncthreads();
+    b = found[0];
+    j = found[1];
+    if (b < 0) return;
   }
-  const int b = upto - 1, j = s - p.base[b], len = p.seq_lens[b];
+  const int len = p.seq_lens[b];
   if (j >= p.stride || j * kQ4Block >= len) return;
   if (blockIdx.y == 0) {
     if (threadIdx.x == 0) p.table[static_cast<size_t>(b) * p.stride + j] = s;
@@ -1056,25 +1102,31 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   cudaEvent_t join = nullptr;
   const cudaStream_t side = side_fork(s, &join);
   int e;
+  if (q4.prefill_blocks == 0 || a.B > kScanSeqs) {
+    e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(a.B < 1024 ? (a.B + 31) / 32 * 32 : 1024), 0, s, side == s, f);
+    if (e == 0 && q4.prefill_blocks > 0)
+      e = launch_kernel(k_q4_expand<D, true>, dim3(q4.prefill_blocks, 2), dim3(kExpandThreads), 0, s, true, f);
+  } else {
+    e = launch_kernel(k_q4_expand<D, false>, dim3(q4.prefill_blocks + 1, 2), dim3(kExpandThreads), 0, s, side == s, f);
+  }
   // Few blocks in all: one launch for 1 .. 16 rows is done before two of 8 and 16 are launched.
   const bool few = static_cast<long long>(a.B) * a.nkv * L.stride <= kFewBlocks;
-  if (p.group > 8 || few) {
-    e = launch_decode<D, 2>(p, 1, kMaxRows, false, false, side);
-  } else {
-    e = launch_decode<D, 1>(p, 1, 8, false, false, side);
-    if (e == 0) e = launch_decode<D, 2>(p, 9, kMaxRows, false, true, side);
+  if (e == 0) {
+    if (p.group > 8 || few) {
+      e = launch_decode<D, 2>(p, 1, kMaxRows, false, false, side);
+    } else {
+      e = launch_decode<D, 1>(p, 1, 8, false, false, side);
+      if (e == 0) e = launch_decode<D, 2>(p, 9, kMaxRows, false, true, side);
+    }
   }
-  const int plan_threads = a.B < 1024 ? (a.B + 31) / 32 * 32 : 1024;
-  if (e == 0) e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(plan_threads), 0, s, side == s, f);
   if (e == 0 && q4.prefill_blocks > 0) {
-    e = launch_kernel(k_q4_expand<D>, dim3(q4.prefill_blocks, 2), dim3(kExpandThreads), 0, s, true, f);
     AttnArgs c = a;
     c.k_cache = f.k_copy;
     c.v_cache = f.v_copy;
     c.block_table = f.table;
     c.max_blocks = L.stride;
     c.num_blocks = q4.prefill_blocks;
-    if (e == 0) e = prefill_items_launch(c, f.items, f.max_items, f.base + a.B + 1, q4.ws + L.parts, true, s);
+    e = prefill_items_launch(c, f.items, f.max_items, f.base + a.B + 1, q4.ws + L.parts, side != s, s);
   }
   if (side != s) {  // join even after a failed launch, so that the caller's stream never runs ahead of the side stream
     const int j = side_join(s, side, join);
