@@ -422,6 +422,29 @@ def test_too_few_prefill_blocks_are_reported():
     assert np.all(got[51:] == 5.0)
 
 
+@pytest.mark.parametrize("many", [300, 700])
+def test_prompts_among_many_sequences(many):
+    r = np.random.default_rng(23)
+    seqs = [(1, int(n)) for n in r.integers(1, 40, many)]
+    for at, s in ((3, (40, 77)), (many // 2, (18, 18)), (many - 2, (33, 300)), (many, (70, 71))):
+        seqs.insert(at, s)
+    c = Case(seqs, 8, 2, 64, seed=24)
+    c.run()
+    ok()
+    c.check()
+
+
+def test_prompts_without_prefill_blocks_are_reported():
+    c = Case([(1, 40), (50, 60), (2, 9)], 8, 2, 128, seed=25)
+    c.run(pre=0)
+    guard()
+    got = f64(c.out).reshape(-1, 8, 128)
+    want, spread, _ = R.attention(f64(c.q), c.pos, c.qsl, c.table, c.tiles[0], c.tiles[1], 1.0, 1.0)
+    rest = np.r_[0:1, 51:53]
+    assert np.all(np.abs(got - want)[rest] <= 2.0 ** -8 * np.abs(want[rest]) + 2.0 ** -9 * spread[rest])
+    assert np.all(got[1:51] == 5.0)
+
+
 def test_same_result_on_every_run_and_on_another_stream():
     c = Case([(1, 3000), (1, 17), (33, 500), (2, 999), (1, 1200)], 32, 4, 128, seed=13)
     a = c.run().clone()
