@@ -490,7 +490,7 @@ constexpr int kPreMaxHeads = 8;  // q heads (consumer warps) per prefill CTA
 // whole to split_ctas (those that run at once), two key tiles each at least, and
 // k_attn_prefill_join joins the parts.  CTA i takes part i % parts of unit i / parts,
 // a unit being a query tile of the work list and its KV head (and chunk of heads).
-constexpr int kPreMaxParts = 16;
+constexpr int kPreMaxParts = 32;  // (a lane each in the join)
 constexpr int kPartRows = 128;  // query rows of a CTA at most, in either prefill kernel
 
 struct PrefillPart {
@@ -506,9 +506,12 @@ __device__ __forceinline__ PrefillPart prefill_part(const AttnParams& p, int per
   return x;
 }
 
-// its key tiles first .. last - 1 of n
+// key tiles a part, of n
+__device__ __forceinline__ int tiles_per_part(const PrefillPart& x, int n) { return max(2, (n + x.parts - 1) / x.parts); }
+
+// the part's key tiles first .. last - 1 of n
 __device__ __forceinline__ void part_tiles(const PrefillPart& x, int n, int& first, int& last) {
-  const int per = max(2, (n + x.parts - 1) / x.parts);
+  const int per = tiles_per_part(x, n);
   first = x.part * per;
   last = min(n, first + per);
 }
@@ -565,10 +568,7 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
   const size_t part_row = static_cast<size_t>(blockIdx.x) * kPartRows + warp * 16;
   if constexpr (SPLIT) {
     part_tiles(part, ntiles, kt0, ntiles);
-    if (part.parts > 1 && kt0 >= ntiles) {  // no keys for this part
-      if (warp < G && lane < 16) p.part_ml[part_row + lane] = make_float2(-INFINITY, 0.f);
-      return;
-    }
+    if (part.parts > 1 && kt0 >= ntiles) return;  // no keys for this part
   }
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kPreStages;
 
@@ -878,6 +878,25 @@ __global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
   const PrefillPart part = prefill_part(p, p.nkv * n_hc);
   const int unit = blockIdx.x, r = blockIdx.y * 16 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (part.parts == 1 || unit >= part.units) return;
+  constexpr int E = D / 32;
+  const size_t first = static_cast<size_t>(unit) * part.parts * kPartRows + r;
+  // lane i has part i's maximum and sum, and its weight in the whole (zero if all of it was masked)
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < part.parts) ml = p.part_ml[first + static_cast<size_t>(lane) * kPartRows];
+  float x[4][E];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const size_t at = first + static_cast<size_t>(min(i0 + n, part.parts - 1)) * kPartRows;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + lane * E + e);
+        x[n][e] = v.x;
+        x[n][e + 1] = v.y;
+      }
+    }
+  };
+  load(0);  // on their way while the row is looked up (rows and parts that are not there have a place all the same)
   const int by = unit / (p.nkv * n_hc), bx = unit - by * (p.nkv * n_hc);
   const uint32_t item = p.pre_items[by];
   if (item == kNoItem) return;
@@ -891,10 +910,9 @@ __global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
   for (int i = lane; i < nrows; i += 32) hi = max(hi, p.positions[tq + i]);
   const int n_keys = __reduce_max_sync(0xffffffffu, hi) + 1;
   if (n_keys > p.seq_lens[b] || (n_keys + kBS - 1) / kBS > p.max_blocks || (TC && n_keys < 1)) return;
-  constexpr int E = D / 32;
-  const size_t first = static_cast<size_t>(unit) * part.parts * kPartRows + r;
-  // lane i has part i's maximum and sum, and its weight in the whole (zero: nothing was stored, or all of it was masked)
-  const float2 ml = lane < part.parts ? p.part_ml[first + static_cast<size_t>(lane) * kPartRows] : make_float2(-INFINITY, 0.f);
+  const int tiles = (n_keys + kPreKeys - 1) / kPreKeys, per = tiles_per_part(part, tiles);
+  const int used = (tiles + per - 1) / per;  // parts with keys
+  if (lane >= used) ml = make_float2(-INFINITY, 0.f);
   float m = ml.x;
 #pragma unroll
   for (int o = kPreMaxParts / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -903,18 +921,8 @@ __global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
   float L = 0.f, O[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) O[e] = 0.f;
-  for (int i0 = 0; i0 < part.parts; i0 += 4) {
-    float x[4][E];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const size_t at = first + static_cast<size_t>(min(i0 + n, part.parts - 1)) * kPartRows;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(p.part_o + at * D + lane * E + e);
-        x[n][e] = v.x;
-        x[n][e + 1] = v.y;
-      }
-    }
+  for (int i0 = 0; i0 < used; i0 += 4) {
+    if (i0 > 0) load(i0);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float fi = __shfl_sync(0xffffffffu, f, i0 + n), li = __shfl_sync(0xffffffffu, ml.y, i0 + n);  // zero past the parts
@@ -967,6 +975,7 @@ constexpr int kTcKStages = 2;                     // K ring (three stages measur
 constexpr int kTcVStages = 2;                     // V ring
 static_assert(kTcSBufs * kTcKeys + 128 <= 256, "S buffers and O must fit 256 tensor-memory columns");
 static_assert(kTcKeys == 64 || kTcKeys == 128, "the softmax handles 64- or 128-key tiles");
+static_assert(kTcKeys == kPreKeys, "k_attn_prefill_join counts the tiles of either kernel");
 constexpr int kTcSmem = 2 * kTcQHalf + (kTcKStages + kTcVStages) * kTcTileBytes + 256 + kTcSlack;
 constexpr float kRescaleLog2 = 8.0f;               // lazy rescale threshold (factor 256)
 
@@ -1051,11 +1060,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   if constexpr (SPLIT) {
     part_tiles(part, ntiles, kt0, ntiles);
     ntiles -= kt0;
-    if (ntiles <= 0) {  // no keys for this part
-      if (threadIdx.x < kPartRows)
-        p.part_ml[static_cast<size_t>(blockIdx.x) * kPartRows + threadIdx.x] = make_float2(-INFINITY, 0.f);
-      return;
-    }
+    if (ntiles <= 0) return;  // no keys for this part
   }
 
   if (threadIdx.x == 0) {
@@ -1682,8 +1687,9 @@ int prefill_tile_tokens(const AttnArgs& a) {
 
 namespace {
 
-// CTAs that run at once, by their shared memory: 50 KB (head_dim 64), 99 KB (128), 97 KB (tensor memory)
-int prefill_split_ctas(int head_dim) { return num_sms() * (head_dim == 64 ? 4 : 2); }
+// CTAs that run at once: 99 KB of shared memory each with head_dim 128.  (64: four of 50 KB would fit, with a warp more a
+// scheduler for each to wait for; chunks of 421 after 1033: one 22.4 us with four, 18.6 with three, three 33.5 and 32.1.)
+int prefill_split_ctas(int head_dim) { return num_sms() * (head_dim == 64 ? 3 : 2); }
 
 template <int D, bool TC, typename Kernel, typename... Maps>
 int launch_prefill_split(Kernel kernel, int smem, int threads, const AttnParams& p, int n_items, bool pdl, cudaStream_t s,
