@@ -1729,12 +1729,12 @@ int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int max_items
   const cudaError_t attr = a.head_dim == 128 ? set_attributes<128>() : set_attributes<64>();
   if (attr != cudaSuccess) return attr;
   // Keys are split where the batch's tokens, were they all of prompts, would leave a unit two CTAs or more, and where the
-  // keys pay for the parts' way through memory and one more launch.  64 new tokens, whole against split (us):
+  // keys pay for the parts' way through memory and one more launch.  64 new tokens, whole against split (us, the whole call):
   //   after                             500          4000         32000
-  //   64 / 8 heads x 128 (tc)      18.8 / 25.4   61.0 / 38.3    411 / 110
-  //   10 / 2 heads x 128           32.5 / 21.7    158 / 30.4   1206 / 120
-  //   8 / 2 heads x 64             20.4 / 16.6    105 / 22.5    655 / 80
-  // (17 tokens after 300 of the last two: 23.5 / 19.9 and 15.8 / 15.7)
+  //   64 / 8 heads x 128 (tc)      15.9 / 20.3   60 / 29      411 / 104
+  //   10 / 2 heads x 128           29.6 / 20.1   181 / 28.4   1417 / 80
+  //   8 / 2 heads x 64             17.8 / 13.8   85 / 18.5    833 / 53
+  // (17 tokens after 300 of the last two: 20.2 / 15.6 and 13.0 / 12.9; 256 after 1000 of the first: 24.2 / 33.6)
   const int hc = tc ? 1 : (p.group + kPreMaxHeads - 1) / kPreMaxHeads;
   p.split_ctas = prefill_split_ctas(a.head_dim);
   const long long pool = static_cast<long long>(a.num_blocks) * kBS;  // keys of all prompts
