@@ -22,6 +22,9 @@
 //   tensor-memory MMA (S and O accumulate in TMEM, P goes back to TMEM as the
 //   A operand of P V); other shapes: k_attn_prefill, one CTA per (sequence,
 //   KV head, 16 query tokens), warp w owns q head w of the group, mma.sync.
+//   The longer sequences of the 4-bit cache run through these too, over a copy
+//   of their blocks; few query tiles with their keys split over CTAs
+//   (k_attn_prefill_join).
 // * In a batch with prefill sequences the decode kernels run on a side stream
 //   beside the prefill kernel (HBM-bound next to tensor-bound work).
 //
@@ -1731,7 +1734,7 @@ int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int max_items
   // Keys are split where the batch's tokens, were they all of prompts, would leave a unit two CTAs or more, and where the
   // keys pay for the parts' way through memory and one more launch.  64 new tokens, whole against split (us, the whole call):
   //   after                             500          4000         32000
-  //   64 / 8 heads x 128 (tc)      15.9 / 20.3   60 / 29      411 / 104
+  //   64 / 8 heads x 128 (tc)      15.9 / 20.3   55 / 29      404 / 104
   //   10 / 2 heads x 128           29.6 / 20.1   181 / 28.4   1417 / 80
   //   8 / 2 heads x 64             17.8 / 13.8   85 / 18.5    833 / 53
   // (17 tokens after 300 of the last two: 20.2 / 15.6 and 13.0 / 12.9; 256 after 1000 of the first: 24.2 / 33.6)
