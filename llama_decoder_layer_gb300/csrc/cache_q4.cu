@@ -27,6 +27,7 @@
 // next tokens while they quantise (one after the other they took 39 us, a third of
 // it waiting for their rows; reading has too little to do between its loads and
 // stores to gain from it).
+#include "cache_rows.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -36,20 +37,9 @@ namespace llama {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
-
-// A launch's shape: `chunks` chunks of 8 elements a token row (K or V); a CTA
-// covers `rows` rows at a time, or 1 / parts of one.
-struct Shape {
-  int chunks, rows, parts;
-};
-
-// This thread's chunk c of head h, and the first of its U tokens, `rows` apart.
-// Threads and tokens past the end load what the last ones do and store nothing.
-struct Place {
-  uint32_t t0;
+// This thread's chunk c of head h.
+struct Place : RowPlace {
   int h, c;
-  bool there;
 };
 
 // v, known to be the same in every lane of the warp if WHOLE
@@ -58,30 +48,26 @@ __device__ __forceinline__ int warp_value(int v) {
   return WHOLE ? __shfl_sync(0xffffffffu, v, 0) : v;
 }
 
-// WHOLE: a row is a whole number of warps, so that its token, slot and tile are a warp's (and cost a lane nothing)
+// WHOLE: g.whole
 template <int D, int U, bool WHOLE>
-__device__ __forceinline__ Place place(const Shape& g) {
+__device__ __forceinline__ Place place(const RowShape& g) {
   constexpr int C = D / 8;
   const int row = warp_value<WHOLE>(threadIdx.x / g.chunks);
-  const int at = g.parts > 1 ? static_cast<int>((blockIdx.y >> 1) * blockDim.x + threadIdx.x)
-                             : static_cast<int>(threadIdx.x) - row * g.chunks;
-  const int r = WHOLE ? at : min(at, g.chunks - 1);
-  Place x;
-  x.h = r / C;
-  x.c = r % C;
-  x.there = WHOLE || at == r;
-  x.t0 = blockIdx.x * static_cast<uint32_t>(g.rows * U) + (g.parts > 1 ? 0 : row);  // below T + rows * U < 2^32
+  Place x{row_place(g, U, blockIdx.x, blockIdx.y >> 1, blockDim.x, threadIdx.x, row), 0, 0};
+  if (WHOLE) x.there = true;
+  x.h = x.at / C;
+  x.c = x.at % C;
   return x;
 }
 
 // token t0 + n rows, or the last one
-__device__ __forceinline__ uint32_t token(const CacheQ4Args& a, const Shape& g, const Place& x, int n) {
+__device__ __forceinline__ uint32_t token(const CacheQ4Args& a, const RowShape& g, const Place& x, int n) {
   return min(x.t0 + n * g.rows, static_cast<uint32_t>(a.T) - 1);
 }
 
 // the slots of this thread's tokens; -1 where there is nothing to do
 template <int U, bool WHOLE>
-__device__ __forceinline__ void load_slots(const CacheQ4Args& a, const Shape& g, const Place& x, bool reports,
+__device__ __forceinline__ void load_slots(const CacheQ4Args& a, const RowShape& g, const Place& x, bool reports,
                                            int (&slot)[U]) {
   bool past = false;
 #pragma unroll
@@ -121,7 +107,7 @@ template <int D, int U, bool WHOLE, bool V>
 struct Spots {
   int slot[WHOLE ? 1 : U];
 
-  __device__ __forceinline__ void load(const CacheQ4Args& a, const Shape& g, const Place& x, bool reports) {
+  __device__ __forceinline__ void load(const CacheQ4Args& a, const RowShape& g, const Place& x, bool reports) {
     if constexpr (WHOLE) {
       const int n = threadIdx.x % U;
       slot[0] = a.slots[token(a, g, x, n)];
@@ -154,13 +140,13 @@ struct Spots {
 };
 
 template <int D, int U, bool WHOLE, bool V>
-__device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g) {
+__device__ __forceinline__ void write_rows(const CacheQ4Args& a, const RowShape& g) {
   Place x = place<D, U, WHOLE>(g);
   const long long stride = V ? a.v_stride : a.k_stride;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(V ? a.v : a.k) + x.h * D + x.c * 8;
   constexpr int C = D / 8;
   const bool reports = !V && x.there && x.h * C + x.c == (WHOLE ? static_cast<int>(threadIdx.x & 31) : 0);
-  const uint32_t step = gridDim.x * static_cast<uint32_t>(g.rows * U);  // at most 2^31 + 2^17
+  const uint32_t step = row_step(g, U, gridDim.x);
   const float inv_g = V ? a.inv_v_scale : a.inv_k_scale;
   using To = Spots<D, U, WHOLE, V>;
   // this chunk's codes and scale in the tile of token 0 of block 0 (the tokens' own part is added to them)
@@ -179,7 +165,8 @@ __device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g)
     const To to = to_next;
 #pragma unroll
     for (int n = 0; n < U; ++n) u[n] = next[n];
-    more = x.t0 < static_cast<uint32_t>(a.T) && static_cast<uint32_t>(a.T) - x.t0 > step;
+    more = row_more(x, a.T, step);
+    x.cta += step;
     x.t0 += step;
     if (more) {  // on their way while these are quantised
 #pragma unroll
@@ -242,7 +229,7 @@ __device__ __forceinline__ void write_rows(const CacheQ4Args& a, const Shape& g)
 }
 
 template <int D, int U, bool WHOLE, bool V>
-__device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) {
+__device__ __forceinline__ void read_rows(const CacheQ4Args& a, const RowShape& g) {
   const Place x = place<D, U, WHOLE>(g);
   int slot[U];
   load_slots<U, WHOLE>(a, g, x, !V && x.h == 0 && x.c == 0 && x.there, slot);
@@ -269,7 +256,7 @@ __device__ __forceinline__ void read_rows(const CacheQ4Args& a, const Shape& g) 
 }
 
 template <int D, int U, bool WHOLE>
-__global__ void __launch_bounds__(kMaxThreads, WHOLE ? 2 : 1) k_kv_write_q4(const CacheQ4Args a, const Shape g) {
+__global__ void __launch_bounds__(kMaxRowThreads, WHOLE ? 2 : 1) k_kv_write_q4(const CacheQ4Args a, const RowShape g) {
   pdl_wait();
   if (blockIdx.y & 1)
     write_rows<D, U, WHOLE, true>(a, g);
@@ -278,7 +265,7 @@ __global__ void __launch_bounds__(kMaxThreads, WHOLE ? 2 : 1) k_kv_write_q4(cons
 }
 
 template <int D, int U, bool WHOLE>
-__global__ void __launch_bounds__(kMaxThreads) k_kv_read_q4(const CacheQ4Args a, const Shape g) {
+__global__ void __launch_bounds__(kMaxRowThreads) k_kv_read_q4(const CacheQ4Args a, const RowShape g) {
   pdl_wait();
   if (blockIdx.y & 1)
     read_rows<D, U, WHOLE, true>(a, g);
@@ -286,34 +273,15 @@ __global__ void __launch_bounds__(kMaxThreads) k_kv_read_q4(const CacheQ4Args a,
     read_rows<D, U, WHOLE, false>(a, g);
 }
 
-// U = 4 tokens a thread where that still gives every SM four CTAs, else one
-using Kernel = void (*)(const CacheQ4Args, const Shape);
+using Kernel = void (*)(const CacheQ4Args, const RowShape);
 
 int launch(Kernel four, Kernel one, Kernel four_whole, Kernel one_whole, bool loops, const CacheQ4Args& a, cudaStream_t s) {
-  Shape g{};
-  g.chunks = a.n_kv * (a.head_dim / 8);
-  int threads = g.chunks;  // the least number of whole rows that is a number of whole warps (chunks is a multiple of 8)
-  while (threads % 32) threads += g.chunks;
-  if (threads <= kMaxThreads) {
-    while (threads < 256 && threads * 2 <= kMaxThreads) threads *= 2;
-    g.rows = threads / g.chunks;
-    g.parts = 1;
-  } else {
-    threads = 256;
-    g.rows = 1;
-    g.parts = (g.chunks + threads - 1) / threads;
-  }
+  const RowShape g = row_shape(a.n_kv, a.head_dim);
   if (g.parts > 32767) return cudaErrorInvalidValue;
-  const long long ctas = (static_cast<long long>(a.T) + g.rows - 1) / g.rows, ctas4 = (ctas + 3) / 4;
-  const bool u4 = ctas4 * 2 * g.parts >= 4LL * num_sms();
-  const bool whole = g.chunks % 32 == 0 && (g.parts == 1 || g.chunks % threads == 0);
-  long long wide = u4 ? ctas4 : ctas;
-  if (loops) {  // no more CTAs than run at once (their registers: 64 a thread, or 80)
-    const long long fit = static_cast<long long>(num_sms()) * ((whole ? 1024 : 768) / threads) / (2 * g.parts);
-    if (wide > fit) wide = fit < 1 ? 1 : fit;
-  }
-  const dim3 grid(static_cast<unsigned>(wide), 2 * g.parts);
-  return launch_kernel(whole ? (u4 ? four_whole : one_whole) : (u4 ? four : one), grid, dim3(threads), 0, s, true, a,
+  const RowGrid r = row_grid(g, a.T, num_sms(), loops);
+  const dim3 grid(static_cast<unsigned>(r.ctas), 2 * g.parts);
+  const bool u4 = r.u == 4;
+  return launch_kernel(g.whole ? (u4 ? four_whole : one_whole) : (u4 ? four : one), grid, dim3(g.threads), 0, s, true, a,
                        g);
 }
 

@@ -1,0 +1,14 @@
+"""Rows of the 4-bit cache whose warps hold several tokens, at sizes where the
+writing CTAs go round more than once and their last tokens end inside a warp."""
+
+import pytest
+
+from test_gpu_q4 import test_write_and_read_bit_for_bit as write_and_read
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,nkv,d", [(3649, 2, 64), (3650, 2, 64), (3655, 1, 128), (7299, 1, 64), (609, 5, 128),
+                                     (1217, 3, 128), (1219, 3, 128), (4001, 3, 64)])
+def test_the_last_tokens_end_inside_a_warp(T, nkv, d):
+    write_and_read(d, T, nkv, 0, -3)
