@@ -34,8 +34,8 @@ inline RowShape row_shape(int n_kv, int head_dim) {
     while (threads < 256 && threads * 2 <= kMaxRowThreads) threads *= 2;
     g.rows = threads / g.chunks;
     g.parts = 1;
-  } else {
-    threads = 256;
+  } else {  // one row, or 256 threads' part of it; the last warp's threads past the row idle
+    threads = g.chunks < 256 ? (g.chunks + 31) / 32 * 32 : 256;
     g.rows = 1;
     g.parts = (g.chunks + threads - 1) / threads;
   }
@@ -78,7 +78,7 @@ LLAMA_HOST_DEVICE RowPlace row_place(const RowShape& g, int U, uint32_t block, i
   RowPlace x;
   const int at = g.parts > 1 ? part * threads + thread : thread - row * g.chunks;
   x.at = g.whole ? at : at < g.chunks ? at : g.chunks - 1;
-  x.there = x.at == at;
+  x.there = x.at == at && row < g.rows;
   x.cta = block * static_cast<uint32_t>(g.rows * U);
   x.t0 = x.cta + (g.parts > 1 ? 0 : row);  // below T + rows * U < 2^32
   return x;

@@ -12,3 +12,9 @@ pytestmark = pytest.mark.gpu
                                      (1217, 3, 128), (1219, 3, 128), (4001, 3, 64)])
 def test_the_last_tokens_end_inside_a_warp(T, nkv, d):
     write_and_read(d, T, nkv, 0, -3)
+
+
+@pytest.mark.parametrize("T", [1, 40, 3001])
+@pytest.mark.parametrize("nkv", [17, 23, 31])
+def test_heads_that_no_number_of_whole_rows_makes_warps_of(T, nkv):
+    write_and_read(64, T, nkv, 2, 0)

@@ -41,3 +41,14 @@ def test_the_lanes_of_a_warp_go_round_together(walk, n_kv, d, T, more):
     r = walk(n_kv, d, T + more)
     assert not r["whole"] and r["steps"] > 1
     assert r["uneven"] == 0 and r["strangers"] == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n_kv", list(range(1, 36)) + [48, 63, 64, 65, 70])
+@pytest.mark.parametrize("T", [1, 5, 40, 700])
+@pytest.mark.parametrize("loops", [False, True])
+def test_every_chunk_of_every_token_has_one_thread(walk, n_kv, d, T, loops):
+    for sms in (152, 4):  # (few SMs: four tokens a thread, and steps)
+        r = walk(n_kv, d, T, sms, loops)
+        assert r["missed"] == 0 and r["twice"] == 0 and r["out_of_range"] == 0, (sms, r)
+        assert r["uneven"] == 0 and r["strangers"] == 0, (sms, r)
