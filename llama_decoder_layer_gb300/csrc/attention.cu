@@ -920,7 +920,8 @@ __global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
 #pragma unroll
   for (int o = kPreMaxParts / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   m = __shfl_sync(0xffffffffu, m, 0);
-  const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+  // (a part's maximum ignores scores that are NaN, its sum does not: a part with nothing but those weighs NaN)
+  const float f = ml.x == -INFINITY ? ml.y * 0.f : exp2f(ml.x - m);
   float L = 0.f, O[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) O[e] = 0.f;
@@ -929,13 +930,13 @@ __global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float fi = __shfl_sync(0xffffffffu, f, i0 + n), li = __shfl_sync(0xffffffffu, ml.y, i0 + n);  // zero past the parts
-      if (fi == 0.f) continue;
       L += li * fi;
+      if (fi == 0.f) continue;
 #pragma unroll
       for (int e = 0; e < E; ++e) O[e] += x[n][e] * fi;
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
       p.out + (static_cast<size_t>(tq + tok) * p.nq + kvh * p.group + hc * kPreMaxHeads + head) * D + lane * E);
 #pragma unroll
