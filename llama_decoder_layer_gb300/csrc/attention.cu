@@ -68,6 +68,7 @@ struct AttnParams {
   uint32_t* pre_items;  // prefill work list: (sequence << 16) | q-tile, 0xFFFFFFFF past the end
   const int32_t* n_items;  // its length (split prefill)
   int split_ctas;          // CTAs that the parts of a split prefill may take
+  float no_weight;         // a prefill row whose weights sum to zero is its sum times this: 0, or NaN (scores all -inf)
   int* err;
 };
 
@@ -856,8 +857,9 @@ __global__ void __launch_bounds__((kPreMaxHeads + 1) * 32)
       return;
     }
   }
-  const float i0 = l0 > 0.f ? 1.f / l0 : 0.f;
-  const float i1 = l1 > 0.f ? 1.f / l1 : 0.f;
+  // (a row with a negative position sees no key: zero)
+  const float i0 = l0 > 0.f ? 1.f / l0 : pos0 >= 0 ? p.no_weight : 0.f;
+  const float i1 = l1 > 0.f ? 1.f / l1 : pos1 >= 0 ? p.no_weight : 0.f;
   const int h = h_first + warp;
 #pragma unroll
   for (int n = 0; n < D / 8; ++n) {
@@ -936,7 +938,7 @@ __global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
       for (int e = 0; e < E; ++e) O[e] += x[n][e] * fi;
     }
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const float inv = L != 0.f ? 1.f / L : p.positions[tq + tok] >= 0 ? p.no_weight : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
       p.out + (static_cast<size_t>(tq + tok) * p.nq + kvh * p.group + hc * kPreMaxHeads + head) * D + lane * E);
 #pragma unroll
@@ -1406,7 +1408,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           for (int q = 0; q < 8; ++q) d4[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l > 0.f ? 1.f / l : pos >= 0 ? p.no_weight : 0.f;
       __nv_bfloat16* dst = p.out + (static_cast<size_t>(tq + tok) * p.nq + kvh * G + hq) * 128;
 #pragma unroll 1
       for (int c = 0; c < (SPLIT && part.parts > 1 ? 0 : 4); ++c) {
@@ -1727,6 +1729,7 @@ int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int max_items
   if (!make_cache_tmap(&tk, a.k_cache, rows, a.head_dim)) return cudaErrorInvalidValue;
   if (!make_cache_tmap(&tv, a.v_cache, rows, a.head_dim)) return cudaErrorInvalidValue;
   AttnParams p = base_params(a);
+  p.no_weight = NAN;  // the softmax of nothing but -inf, as where single tokens are decoded
   p.pre_items = const_cast<uint32_t*>(items);
   const bool tc = prefill_on_tc(a.head_dim, p.group);
   const int tile = prefill_tile_tokens(a);

@@ -50,3 +50,22 @@ def test_a_query_row_that_is_not_finite(path, x):
     c.run()
     ok()
     check_with_nan_rows(c, rows)
+
+
+@pytest.mark.parametrize("path", PATHS)
+def test_a_query_row_all_of_whose_scores_are_minus_infinity(path):
+    # softmax of nothing but -inf: NaN by the formula
+    seqs, nq, nkv, d, bound = PATHS[path]
+    c = Case(seqs, nq, nkv, d, seed=32, bound=bound)
+    for k in range(16):  # element 0 of every key: positive (code 7)
+        c.tiles[0][..., R.code_place(d, k, 0, False)] &= 0xF0
+        c.tiles[0][..., R.code_place(d, k, 0, False)] |= 7
+    c.kc = torch.from_numpy(c.tiles[0]).cuda()
+    n = seqs[0][0]
+    rows = {(0, 1), (n - 1, nq - 1), (n, 0)}
+    for t, h in rows:
+        c.q[t, h, 0] = -np.inf
+    c.qd = c.q.cuda()
+    c.run()
+    ok()
+    check_with_nan_rows(c, rows)
