@@ -404,10 +404,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
     // q as the 8-column operand
     uint32_t bq[NT][D / 8];
     float sc[NT][2];
-    int lim_lo = 0x7fffffff;
+    int lim_lo = 0x7fffffff, seen = 0;  // the least position of a row; keys that any row sees
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (qpos[nt] < 0 || qpos[nt] >= len) qpos[nt] = len - 1;  // such a row is not stored
+      if (qpos[nt] < 0 || qpos[nt] >= len)
+        qpos[nt] = len - 1;  // such a row is not stored
+      else if (nt * 8 + g < rows)
+        seen = max(seen, qpos[nt] + 1);
       lim_lo = min(lim_lo, qpos[nt]);
       float amax = 0.f;
       const uint32_t* w = reinterpret_cast<const uint32_t*>(qu[nt]);
@@ -428,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
       }
     }
     lim_lo = __reduce_min_sync(0xffffffffu, lim_lo);
+    seen = __reduce_max_sync(0xffffffffu, seen);
 
     // thr: the unscaled score that moves the maximum, base: what is subtracted
     // from the scaled ones (the maximum less the weights' 2^6)
@@ -563,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 3) k_attn_q4_
         const uint32_t sw = lds_u32(ring_vs + st);
         uint32_t s0 = e4m3x2_to_f16(sw), s1 = e4m3x2_to_f16(sw >> 16);
         const int k0 = key0 + x * kWarps * kQ4Block;
-        if (edge && k0 + kQ4Block > len) {  // tokens past the sequence: their bytes may be anything
+        if (edge && k0 + kQ4Block > seen) {  // tokens that no row sees may never have been written: any bytes, NaN scales
           const int k = k0 + 2 * t;
-          s0 = (k < len ? s0 & 0xFFFFu : 0u) | (k + 1 < len ? s0 & 0xFFFF0000u : 0u);
-          s1 = (k + 8 < len ? s1 & 0xFFFFu : 0u) | (k + 9 < len ? s1 & 0xFFFF0000u : 0u);
+          s0 = (k < seen ? s0 & 0xFFFFu : 0u) | (k + 1 < seen ? s0 & 0xFFFF0000u : 0u);
+          s1 = (k + 8 < seen ? s1 & 0xFFFFu : 0u) | (k + 9 < seen ? s1 & 0xFFFF0000u : 0u);
         }
 #pragma unroll
         for (int w = 0; w < KW / 2; ++w) {
