@@ -423,13 +423,18 @@ def paged_attention_q4(cfg: LayerConfig, batch: Batch, q: torch.Tensor, k_cache:
 
 
 _ROPE_TYPES = {"default": 0, "llama3": 1, "linear": 2, "yarn": 3}
+_ROPE_KEYS = frozenset(("rope_type", "type", "factor", "low_freq_factor", "high_freq_factor", "beta_slow", "beta_fast",
+                        "attention_factor", "original_max_position_embeddings"))
+_PLAIN_ROPE = (0, 1.0, 1.0, 4.0, 0, 1.0)  # QkNormRopeConfig._scaling() without a block
 
 
 @dataclass
 class QkNormRopeConfig:
     """Heads, norm and rotary embedding of qk_norm_rope.  rotary_dim None: the
     whole head.  rope_scaling: None, or a config.json block with rope_type (or
-    type) linear, llama3 or yarn and that type's parameters."""
+    type) linear, llama3 or yarn and that type's parameters, factor among them.
+    A block with other parameters (mscale, mscale_all_dim, truncate false, a
+    rope_theta that is not this one's, ..) is refused."""
 
     n_heads: int
     n_kv_heads: int
@@ -440,24 +445,35 @@ class QkNormRopeConfig:
     rope_theta: float = 10000.0
     rope_scaling: Optional[dict] = None
 
-    def c(self) -> LlamaQkNormRopeConfig:
-        s = self.rope_scaling or {}
+    def _scaling(self):
+        """rope_scaling's type, factor, low and high, original positions, attention factor."""
+        s = self.rope_scaling
+        if None in s.values():
+            s = {k: v for k, v in s.items() if v is not None}
         kind = s.get("rope_type", s.get("type", "default"))
         if kind not in _ROPE_TYPES:
             raise LlamaError(LLAMA_ERR_ARG, f"rope_type {kind!r}")
+        if not _ROPE_KEYS.issuperset(s):
+            for k, v in s.items():
+                if k not in _ROPE_KEYS and (k, v) not in (("truncate", True), ("rope_theta", self.rope_theta)):
+                    raise LlamaError(LLAMA_ERR_ARG, f"rope_scaling {k!r}")
+        if kind != "default" and "factor" not in s:
+            raise LlamaError(LLAMA_ERR_ARG, f"rope_scaling of type {kind!r} without a factor")
         factor = float(s.get("factor", 1.0))
-        low, high = s.get("low_freq_factor", 1.0), s.get("high_freq_factor", 4.0)
-        attn = 1.0
+        low, high, attn = s.get("low_freq_factor", 1.0), s.get("high_freq_factor", 4.0), 1.0
         if kind == "yarn":
             low, high = s.get("beta_slow", 1.0), s.get("beta_fast", 32.0)
             attn = s.get("attention_factor")
             if attn is None:
                 attn = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+        return (_ROPE_TYPES[kind], factor, float(low), float(high), int(s.get("original_max_position_embeddings", 0)),
+                float(attn))
+
+    def c(self) -> LlamaQkNormRopeConfig:
         return LlamaQkNormRopeConfig(
             self.n_heads, self.n_kv_heads, self.head_dim,
             self.head_dim if self.rotary_dim is None else self.rotary_dim, 1 if self.interleaved else 0, self.rms_eps,
-            self.rope_theta, _ROPE_TYPES[kind], factor, float(low), float(high),
-            int(s.get("original_max_position_embeddings", 0)), float(attn))
+            self.rope_theta, *(self._scaling() if self.rope_scaling else _PLAIN_ROPE))
 
 
 def qk_norm_rope(cfg: QkNormRopeConfig, q_norm: Optional[torch.Tensor], k_norm: Optional[torch.Tensor],
