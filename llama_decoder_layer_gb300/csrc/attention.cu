@@ -1539,16 +1539,8 @@ bool fork_join_events(cudaEvent_t* fork, cudaEvent_t* join) {
 
 template <int D>
 cudaError_t set_attributes() {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(k_attn_decode<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(decode_smem<D>()));
-    if (attr == cudaSuccess)
-      attr = cudaFuncSetAttribute(k_attn_prefill<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(prefill_smem<D>()));
-  });
-  return attr;
+  static SmemLimits limits;
+  return limits.raise({smem_need(k_attn_decode<D>, decode_smem<D>()), smem_need(k_attn_prefill<D>, prefill_smem<D>())});
 }
 
 // the tensor-memory prefill kernel serves this shape
@@ -1606,12 +1598,9 @@ template <int D>
 int launch_prefill_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, bool tc,
                      int tile_tokens, int items, bool pdl, cudaStream_t s) {
   if (tc) {
-    static std::once_flag tc_once;
-    static cudaError_t tc_attr = cudaSuccess;
-    std::call_once(tc_once, [] {
-      tc_attr = cudaFuncSetAttribute(k_attn_prefill_tc<>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-    });
-    if (tc_attr != cudaSuccess) return tc_attr;
+    static SmemLimits limits;
+    const cudaError_t attr = limits.raise({smem_need(k_attn_prefill_tc<>, kTcSmem)});
+    if (attr != cudaSuccess) return attr;
     CUtensorMap tq;
     if (!make_q_tmap(&tq, a.q, a.T, a.nq, p.group, tile_tokens)) return cudaErrorInvalidValue;
     return launch_kernel(k_attn_prefill_tc<>, dim3(a.nkv, items), dim3(kTcThreads), kTcSmem, s, pdl, tq, tk,
@@ -1700,9 +1689,8 @@ int prefill_split_ctas(int head_dim) { return num_sms() * (head_dim == 64 ? 3 : 
 template <int D, bool TC, typename Kernel, typename... Maps>
 int launch_prefill_split(Kernel kernel, int smem, int threads, const AttnParams& p, int n_items, bool pdl, cudaStream_t s,
                          const Maps&... maps) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] { attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  static SmemLimits limits;  // (one kernel for each D and TC)
+  const cudaError_t attr = limits.raise({smem_need(kernel, smem)});
   if (attr != cudaSuccess) return attr;
   const long long units =
       static_cast<long long>(n_items) * p.nkv * (TC ? 1 : (p.group + kPreMaxHeads - 1) / kPreMaxHeads);

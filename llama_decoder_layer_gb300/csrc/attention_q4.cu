@@ -37,7 +37,6 @@
 //   tokens after many keys: the prefill kernels' keys are split over CTAs.
 #include <math.h>
 
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1034,12 +1033,8 @@ Layout layout(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int he
 template <int D, int NT>
 int launch_decode(Q4Params p, int rows_lo, int rows_hi, bool alone, bool pdl, cudaStream_t s) {
   constexpr int ctas_per_sm = NT == 1 ? kCtasPerSm : 3;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(k_attn_q4_decode<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(decode_smem<D, NT>()));
-  });
+  static SmemLimits limits;
+  const cudaError_t attr = limits.raise({smem_need(k_attn_q4_decode<D, NT>, decode_smem<D, NT>())});
   if (attr != cudaSuccess) return attr;
   p.rows_lo = rows_lo;
   p.rows_hi = rows_hi;

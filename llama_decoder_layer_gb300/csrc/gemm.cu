@@ -1391,20 +1391,13 @@ bool make_tmap_bf16(CUtensorMap* m, const void* base, int rows, int cols, int bo
 
 template <int EPI>
 cudaError_t set_smem_attrs() {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = cudaFuncSetAttribute(k_gemm_tc<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
-    if constexpr (EPI == kEpiSwiGlu)
-      if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_gemm_tc<EPI, kNarrowBN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   kMaxSmemBytes);
-    if (err == cudaSuccess)
-      err = cudaFuncSetAttribute(k_gemm_cluster<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemBytes);
-    if (err == cudaSuccess)
-      err = cudaFuncSetAttribute(k_gemm_pair<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, PAIR_SMEM_BYTES);
-  });
-  return err;
+  static SmemLimits limits;
+  if constexpr (EPI == kEpiSwiGlu)
+    return limits.raise({smem_need(k_gemm_tc<EPI>, kMaxSmemBytes), smem_need(k_gemm_tc<EPI, kNarrowBN>, kMaxSmemBytes),
+                         smem_need(k_gemm_cluster<EPI>, kMaxSmemBytes), smem_need(k_gemm_pair<EPI>, PAIR_SMEM_BYTES)});
+  else
+    return limits.raise({smem_need(k_gemm_tc<EPI>, kMaxSmemBytes), smem_need(k_gemm_cluster<EPI>, kMaxSmemBytes),
+                         smem_need(k_gemm_pair<EPI>, PAIR_SMEM_BYTES)});
 }
 
 // 2-CTA clusters of k_gemm_pair<EPI> resident at once (one per TPC with both

@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <utility>
 
 namespace llama {
@@ -22,6 +23,41 @@ inline cudaError_t counted(cudaError_t e) {
   if (e == cudaSuccess) g_launch_count.fetch_add(1, std::memory_order_relaxed);
   return e;
 }
+
+// A kernel and the dynamic shared memory it is launched with.
+struct SmemNeed {
+  const void* kernel;
+  size_t bytes;
+};
+template <typename... KArgs>
+SmemNeed smem_need(void (*kernel)(KArgs...), size_t bytes) {
+  return {reinterpret_cast<const void*>(kernel), bytes};
+}
+
+// Raises the dynamic shared-memory limit of a set of kernels, once on every
+// device: the limit is the current device's, so a flag for the whole process
+// would leave the others without it.  An error is not kept: the next call tries
+// again.  (Two threads may both do it; the limits are the same.)
+class SmemLimits {
+ public:
+  cudaError_t raise(std::initializer_list<SmemNeed> needs) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kDevs;
+    if (known && done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    for (const SmemNeed& n : needs) {
+      e = cudaFuncSetAttribute(n.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(n.bytes));
+      if (e != cudaSuccess) return e;
+    }
+    if (known) done_[dev].store(true, std::memory_order_release);
+    return cudaSuccess;
+  }
+
+ private:
+  static constexpr int kDevs = 64;
+  std::atomic<bool> done_[kDevs] = {};
+};
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool pdl,
