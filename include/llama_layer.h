@@ -65,9 +65,10 @@
  *     runs past its limit (2 s) is recorded and the kernel winds down.
  *     llama_get_device_error() reports and clears the word.
  *   - The library keeps no other state than that error word (one per device),
- *     cached kernel attributes and SM counts, one non-blocking side stream
- *     per device (decode attention beside prefill attention in mixed
- *     batches), a fork/join event pair per host thread and device, a launch
+ *     cached kernel attributes and SM counts, non-blocking side streams with
+ *     a fork/join event pair each (decode attention beside prefill attention
+ *     in mixed batches; one per device, and more only while several host
+ *     threads issue such calls at once or captures are open), a launch
  *     counter, and the fixed scratch array of llama_paged_attention_noalloc.
  */
 #ifndef LLAMA_LAYER_H_

@@ -1499,44 +1499,6 @@ template <int D>
 int launch_prefill_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const AttnParams& p, bool tc,
                      int tile_tokens, int items, bool pdl, cudaStream_t s);
 
-// One non-blocking stream per device, created on first use and kept for the
-// life of the process.
-cudaStream_t side_stream() {
-  constexpr int kDevs = 64;
-  static cudaStream_t st[kDevs] = {};
-  static std::mutex mu;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return nullptr;
-  std::lock_guard<std::mutex> lock(mu);
-  if (st[dev] == nullptr && cudaStreamCreateWithFlags(&st[dev], cudaStreamNonBlocking) != cudaSuccess) {
-    cudaGetLastError();
-    st[dev] = nullptr;
-  }
-  return st[dev];
-}
-
-// The fork and join events of the current host thread on the current device,
-// created on first use and reused by every later call of that thread (a
-// stream wait takes the event's state when it is enqueued, so re-recording
-// afterwards does not disturb it).  Creating them outside any stream capture
-// (the first call of a thread is eager) keeps the call capture-safe.
-bool fork_join_events(cudaEvent_t* fork, cudaEvent_t* join) {
-  constexpr int kDevs = 64;
-  thread_local cudaEvent_t ev[kDevs][2] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return false;
-  for (int i = 0; i < 2; ++i) {
-    if (ev[dev][i] == nullptr && cudaEventCreateWithFlags(&ev[dev][i], cudaEventDisableTiming) != cudaSuccess) {
-      ev[dev][i] = nullptr;
-      cudaGetLastError();
-      return false;
-    }
-  }
-  *fork = ev[dev][0];
-  *join = ev[dev][1];
-  return true;
-}
-
 template <int D>
 cudaError_t set_attributes() {
   static SmemLimits limits;
@@ -1558,13 +1520,12 @@ int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, At
   const int tile_tokens = tc ? 128 / p.group : 16;  // tensor-core prefill: 128 rows = tokens x group heads
   const int items = (a.T + tile_tokens - 1) / tile_tokens + a.B;
   // With prefill sequences in the batch, the decode kernels (HBM-bound) run on
-  // the library's side stream beside the prefill kernel (tensor-bound): the
+  // a side stream beside the prefill kernel (tensor-bound): the
   // caller's stream forks to it after the previous kernel and joins it before
   // the next.  Otherwise everything runs in order on the caller's stream.
-  cudaStream_t sd = s;
-  cudaEvent_t ev_join = nullptr;
-  if (a.max_query_len >= 2 && a.overlap) sd = side_fork(s, &ev_join);
-  const bool forked = sd != s;
+  SideStream* const side = a.max_query_len >= 2 && a.overlap ? side_fork(s) : nullptr;
+  const bool forked = side != nullptr;
+  const cudaStream_t sd = forked ? side->stream : s;
   if (joined) *joined = forked;
   // the first kernel on each stream takes the caller's dependency mode (none
   // after a fork), the ones after it overlap their predecessor
@@ -1588,7 +1549,7 @@ int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, At
   if (e == cudaSuccess && a.max_query_len >= 2)
     e = static_cast<cudaError_t>(launch_prefill_d<D>(a, tk, tv, p, tc, tile_tokens, items, pdl_s, s));
   if (forked) {  // join even after a failed launch, so the caller's stream never runs ahead of the side stream
-    const cudaError_t j = static_cast<cudaError_t>(side_join(s, sd, ev_join));
+    const cudaError_t j = static_cast<cudaError_t>(side_join(s, side));
     if (e == cudaSuccess) e = j;
   }
   return e;
@@ -1660,19 +1621,91 @@ int attention_launch(const AttnArgs& a, cudaStream_t s, bool* joined) {
   return cudaErrorInvalidValue;
 }
 
-cudaStream_t side_fork(cudaStream_t s, cudaEvent_t* join) {
-  cudaEvent_t fork = nullptr;
-  cudaStream_t side = side_stream();
-  if (side != nullptr && fork_join_events(&fork, join) && cudaEventRecord(fork, s) == cudaSuccess &&
-      cudaStreamWaitEvent(side, fork, 0) == cudaSuccess)
-    return side;
-  cudaGetLastError();
+namespace {
+
+constexpr unsigned long long kNoCapture = ~0ull;
+
+// The number of the capture that s takes part in, or kNoCapture; false if that
+// cannot be told, or the capture has failed.
+bool capture_of(cudaStream_t s, unsigned long long* id) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamGetCaptureInfo(s, &st, id) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  if (st == cudaStreamCaptureStatusNone) *id = kNoCapture;
+  return st != cudaStreamCaptureStatusInvalidated;
+}
+
+// The side streams of a device, created when needed and kept for the life of the
+// process.  A call has one for itself from its fork to its join, so that calls of
+// several host threads do not queue into each other's, and takes none that
+// belongs to another capture than its own (a stream that was forked into a
+// capture stays in it until the capture ends): an eager call beside an open
+// capture would break it, or end up in its graph.  One after the other, calls
+// get the same one.
+constexpr int kSideDevs = 64, kSides = 16;
+
+struct Sides {
+  std::mutex mu;
+  SideStream side[kSideDevs][kSides];
+};
+
+Sides& sides() {
+  static Sides s;
   return s;
 }
 
-int side_join(cudaStream_t s, cudaStream_t side, cudaEvent_t join) {
-  const cudaError_t e = cudaEventRecord(join, side);
-  return e == cudaSuccess ? cudaStreamWaitEvent(s, join, 0) : e;
+// (the calling thread may be capturing: creating these is no part of it)
+bool create(SideStream* x) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return false;
+  const bool ok =
+      (x->fork || cudaEventCreateWithFlags(&x->fork, cudaEventDisableTiming) == cudaSuccess) &&
+      (x->join || cudaEventCreateWithFlags(&x->join, cudaEventDisableTiming) == cudaSuccess) &&
+      cudaStreamCreateWithFlags(&x->stream, cudaStreamNonBlocking) == cudaSuccess;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  return ok;
+}
+
+}  // namespace
+
+SideStream* side_fork(cudaStream_t s) {
+  int dev = 0;
+  unsigned long long mine = 0, its = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kSideDevs || !capture_of(s, &mine)) return nullptr;
+  SideStream* x = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(sides().mu);
+    for (SideStream& y : sides().side[dev]) {
+      if (y.taken) continue;
+      if (y.stream == nullptr) {
+        if (create(&y)) x = &y;
+        break;
+      }
+      if (capture_of(y.stream, &its) && (its == kNoCapture || its == mine)) {
+        x = &y;
+        break;
+      }
+    }
+    if (x) x->taken = true;
+  }
+  if (x && cudaEventRecord(x->fork, s) == cudaSuccess && cudaStreamWaitEvent(x->stream, x->fork, 0) == cudaSuccess)
+    return x;
+  cudaGetLastError();
+  if (x) {
+    std::lock_guard<std::mutex> lock(sides().mu);
+    x->taken = false;
+  }
+  return nullptr;
+}
+
+int side_join(cudaStream_t s, SideStream* x) {
+  cudaError_t e = cudaEventRecord(x->join, x->stream);
+  if (e == cudaSuccess) e = cudaStreamWaitEvent(s, x->join, 0);
+  std::lock_guard<std::mutex> lock(sides().mu);
+  x->taken = false;
+  return e;
 }
 
 int prefill_tile_tokens(const AttnArgs& a) {

@@ -1098,8 +1098,8 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   f.k_scale = q4.k_scale;
   f.v_scale = q4.v_scale;
   f.err = a.err;
-  cudaEvent_t join = nullptr;
-  const cudaStream_t side = side_fork(s, &join);
+  SideStream* const forked = side_fork(s);
+  const cudaStream_t side = forked ? forked->stream : s;
   int e;
   if (q4.prefill_blocks == 0 || a.B > kScanSeqs) {
     e = launch_kernel(k_attn_q4_plan, dim3(1), dim3(a.B < 1024 ? (a.B + 31) / 32 * 32 : 1024), 0, s, side == s, f);
@@ -1127,8 +1127,8 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
     c.num_blocks = q4.prefill_blocks;
     e = prefill_items_launch(c, f.items, f.max_items, f.base + a.B + 1, q4.ws + L.parts, side != s, s);
   }
-  if (side != s) {  // join even after a failed launch, so that the caller's stream never runs ahead of the side stream
-    const int j = side_join(s, side, join);
+  if (forked) {  // join even after a failed launch, so that the caller's stream never runs ahead of the side stream
+    const int j = side_join(s, forked);
     if (e == 0) e = j;
   }
   return e;

@@ -170,10 +170,15 @@ struct AttnQ4Args {
 size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int nq, int nkv, int head_dim);
 int attention_q4_launch(const AttnQ4Args& a, cudaStream_t s);
 
-// The library's side stream of the current device, forked off s (work queued on s before is complete before what
-// is queued on it), or s itself if that fails; side_join makes s wait for it.
-cudaStream_t side_fork(cudaStream_t s, cudaEvent_t* join);
-int side_join(cudaStream_t s, cudaStream_t side, cudaEvent_t join);
+// A side stream of the current device, forked off s (work queued on s before is complete before what is queued on it) and
+// the caller's until side_join, which makes s wait for it; null if there is none, and s has to do.
+struct SideStream {
+  cudaStream_t stream;
+  cudaEvent_t fork, join;
+  bool taken;
+};
+SideStream* side_fork(cudaStream_t s);
+int side_join(cudaStream_t s, SideStream* side);
 
 // The prefill kernels alone, over a cache that holds the prompts' blocks only
 // and a work list of (sequence << 16 | query tile) entries on the device, *n_items
