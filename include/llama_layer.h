@@ -306,8 +306,8 @@ size_t llama_paged_attention_noalloc_limit(void);
  * so g is chosen to bring the largest |x| well below 2688 g and the typical
  * ones above 0.1 g (1 suits normed keys; a calibrated factor is rounded to a
  * power of two, which loses nothing but range).  A NaN is stored as zero and
- * an infinity saturates, so a cache never holds one.  A tile never written
- * may hold any bytes.  The same k_scale and v_scale go to every call on a
+ * an infinity saturates, so a cache never holds one.  A tile, or a token of it,
+ * never written may hold any bytes.  The same k_scale and v_scale go to every call on a
  * cache.  The order of the bytes in a tile:
  *   code of K element e of token k:  byte k * d/2 + e/2
  *   code of V element e of token k:  byte (k/8) * 4d + (e/w * 4 + k%8/2) * w
@@ -346,12 +346,19 @@ int kv_cache_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
  * is negative or not below its seq_lens is reported as a device guard and its
  * row left (in one of the longer sequences below its row is undefined, and the
  * rows of up to 127 tokens beside it may be left).
+ * A query row with a NaN or an infinity gives a row of NaN, and no other.
  * Sequences with one new token, or with so few that new * n_heads / n_kv_heads
- * <= 16 (draft tokens to verify), read the 4-bit cache directly.  For longer
- * ones the workspace takes a 16-bit copy of the sequence's K and V, of
- * prefill_blocks blocks at least for all of them: the sum over those sequences
- * of ceil(seq_lens/16).  A sequence that does not fit any more is reported as a
- * device guard and its rows left.  prefill_blocks 0 suits batches without them. */
+ * <= 16 (draft tokens to verify), read the 4-bit cache directly, with softmax
+ * weights rounded to fp16 (11 bits).  For longer ones the workspace takes a
+ * 16-bit copy of the sequence's K and V, of prefill_blocks blocks at least for
+ * all of them: the sum over those sequences of ceil(seq_lens/16).  Their weights
+ * are rounded to bf16 (8 bits), as over the bf16 cache; sums are fp32 in either.
+ * The copy is made anew by every call, whole contexts included: it takes 3.6
+ * times the bytes of the cache's part and moves 4.6 bytes an element instead of
+ * 0.56, so that a few draft tokens of more than 16 query rows over long contexts
+ * cost more than over a bf16 cache.  A sequence that does not fit any more is
+ * reported as a device guard and its rows left.  prefill_blocks 0 suits batches
+ * without them. */
 int llama_paged_attention_q4(const LlamaLayerConfig* cfg, const LlamaBatch* batch, const void* q, const void* k_cache,
                              const void* v_cache, float k_scale, float v_scale, int prefill_blocks, void* out,
                              void* workspace, size_t workspace_bytes, llama_stream_t stream);

@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(512) k_attn_prefill_join(AttnParams p) {
 #pragma unroll
   for (int o = kPreMaxParts / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   m = __shfl_sync(0xffffffffu, m, 0);
-  // (a part's maximum ignores scores that are NaN, its sum does not: a part with nothing but those weighs NaN)
+  // (a part's maximum ignores scores that are NaN, its sum does not: a part with none but those weighs NaN)
   const float f = ml.x == -INFINITY ? ml.y * 0.f : exp2f(ml.x - m);
   float L = 0.f, O[E];
 #pragma unroll
@@ -1520,9 +1520,8 @@ int launch_d(const AttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, At
   const int tile_tokens = tc ? 128 / p.group : 16;  // tensor-core prefill: 128 rows = tokens x group heads
   const int items = (a.T + tile_tokens - 1) / tile_tokens + a.B;
   // With prefill sequences in the batch, the decode kernels (HBM-bound) run on
-  // a side stream beside the prefill kernel (tensor-bound): the
-  // caller's stream forks to it after the previous kernel and joins it before
-  // the next.  Otherwise everything runs in order on the caller's stream.
+  // a side stream beside the prefill kernel (tensor-bound): the caller's stream
+  // forks to it after the previous kernel and joins it before the next.  Otherwise everything runs in order on the caller's stream.
   SideStream* const side = a.max_query_len >= 2 && a.overlap ? side_fork(s) : nullptr;
   const bool forked = side != nullptr;
   const cudaStream_t sd = forked ? side->stream : s;
@@ -1757,11 +1756,12 @@ int prefill_items_launch(const AttnArgs& a, const uint32_t* items, int max_items
   const cudaError_t attr = a.head_dim == 128 ? set_attributes<128>() : set_attributes<64>();
   if (attr != cudaSuccess) return attr;
   // Keys are split where the batch's tokens, were they all of prompts, would leave a unit two CTAs or more, and where the
-  // keys pay for the parts' way through memory and one more launch.  64 new tokens, whole against split (us, the whole call):
+  // keys pay for the parts' way through memory and one more launch.  64 new tokens, whole against split (us, the whole
+  // call, from a graph):
   //   after                             500          4000         32000
-  //   64 / 8 heads x 128 (tc)      15.9 / 20.3   55 / 29      404 / 104
-  //   10 / 2 heads x 128           29.6 / 20.1   181 / 28.4   1417 / 80
-  //   8 / 2 heads x 64             17.8 / 13.8   85 / 18.5    833 / 53
+  //   64 / 8 heads x 128 (tc)      15.7 / 20.3   55 / 29      402 / 103
+  //   10 / 2 heads x 128           29.2 / 20.3   159 / 28     1432 / 80
+  //   8 / 2 heads x 64             16.8 / 14.4   80 / 18.4    827 / 53
   // (17 tokens after 300 of the last two: 20.2 / 15.6 and 13.0 / 12.9; 256 after 1000 of the first: 24.2 / 33.6)
   const int hc = tc ? 1 : (p.group + kPreMaxHeads - 1) / kPreMaxHeads;
   p.split_ctas = prefill_split_ctas(a.head_dim);

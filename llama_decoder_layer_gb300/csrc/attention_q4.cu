@@ -5,7 +5,7 @@
 //
 // * Sequences of one new token, or of so few that new * g <= 16 rows share a
 //   pass over the keys: k_attn_q4_decode, bound by the cache's bytes up to 8 rows
-//   and by instruction issue with 16.  128 sequences of 512 .. 8192 tokens, 64
+//   and by the latency of its chains at 12 warps an SM with 16.  128 sequences of 512 .. 8192 tokens, 64
 //   query and 8 KV heads x 128, 649 MB: 120 us, 5.4 TB/s, 80% of the copy rate (the
 //   copies alone take 117, the arithmetic alone 115).  Four sequences of up to
 //   131072 tokens with two new tokens each, 32 and 4 heads, 194 MB: 55 us, 3.5 TB/s.
@@ -53,10 +53,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 16;        // query rows (new tokens x group) of the decode path
 constexpr int kCtasPerSm = 4;
-constexpr int kRankStep = 46;       // half the share lost from one CTA of an SM to the next, in 1/1024 of the mean
+constexpr int kRankStep = 46;       // half the share lost from one CTA of an SM to the next, in 1/1024 of the mean (0, 32,
+                                    // 46, 60: 131.0, 128.7, 126.9, 129.0 us, 128 sequences of 703 MB in a graph)
 constexpr int kMinShare = 8;        // blocks a CTA takes at least: two a warp
 constexpr int kWholeBlocks = 64;    // pieces of up to so many blocks stay whole where the SMs hold them all
-constexpr int kFewBlocks = 16384;   // blocks that the decode kernel for 16 rows takes at most 8 us for
+constexpr int kFewBlocks = 16384;   // blocks up to which a batch with prompts decodes in one launch, of the 16-row kernel
 constexpr int kPieceCost = 6;       // what a (sequence, KV head) costs a CTA beside its blocks, in blocks
 constexpr float kMaxStep = 8.f;     // log2 by which a score may pass the running maximum
 constexpr float kWeightBias = 6.f;  // weights are stored times 2^6
@@ -1043,7 +1044,7 @@ int launch_decode(Q4Params p, int rows_lo, int rows_hi, bool alone, bool pdl, cu
   const int full = num_sms() * ctas_per_sm, grid = want < full ? static_cast<int>(want) : full;
   p.sms = alone ? num_sms() : grid;
   // Few short pieces are not split: finding the ranges and joining the parts cost about as much as kWholeBlocks blocks
-  // (one sequence of 777 tokens: 7.5 us split into 13 CTAs and joined, 7.4 whole, with one launch instead of two).
+  // (one sequence of 777 tokens, from a graph: 7.6 us split into 13 CTAs and joined, 6.9 whole, with one launch not two).
   // Beside prefill kernels, which take longer, four times as many.
   p.whole = pieces <= full && (p.max_seq_len + kQ4Block - 1) / kQ4Block <= (alone ? 1 : 4) * kWholeBlocks;
   if (p.whole)
@@ -1108,7 +1109,9 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
   } else {
     e = launch_kernel(k_q4_expand<D, false>, dim3(q4.prefill_blocks + 1, 2), dim3(kExpandThreads), 0, s, side == s, f);
   }
-  // Few blocks in all: one launch for 1 .. 16 rows is done before two of 8 and 16 are launched.
+  // Few blocks in all: one launch for 1 .. 16 rows, not one of 8 and one of 16 rows (eight sequences each of one and of two
+  // tokens beside a chunk of 64, 64 / 8 heads x 128, 8568 blocks: 19.5 us, with two 34.5; 8 / 2 x 64, 8500 blocks: 25 and
+  // 23).  Many blocks of single tokens are the 8-row kernel's (262144: 60 us, the 16-row kernel takes 80 for two tokens).
   const bool few = static_cast<long long>(a.B) * a.nkv * L.stride <= kFewBlocks;
   if (e == 0) {
     if (p.group > 8 || few) {
