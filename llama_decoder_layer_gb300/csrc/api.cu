@@ -639,8 +639,7 @@ int kv_cache_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
 size_t llama_paged_attention_q4_workspace_size(const LlamaLayerConfig* cfg, int max_tokens, int max_seqs,
                                                int max_seq_len, int prefill_blocks) {
   if (check_cfg(cfg) != LLAMA_OK || max_tokens < 0 || max_seqs < 0 || max_seq_len < 0 || prefill_blocks < 0) return 0;
-  return attn_q4_workspace_bytes(max_tokens, max_seqs, max_seq_len, prefill_blocks, cfg->n_heads, cfg->n_kv_heads,
-                                 cfg->head_dim) + 256;
+  return attn_q4_workspace_bytes(max_tokens, max_seqs, max_seq_len, prefill_blocks, cfg->n_kv_heads, cfg->head_dim) + 256;
 }
 
 int llama_paged_attention_q4(const LlamaLayerConfig* cfg, const LlamaBatch* batch, const void* q, const void* k_cache,
@@ -658,7 +657,7 @@ int llama_paged_attention_q4(const LlamaLayerConfig* cfg, const LlamaBatch* batc
   if ((static_cast<long long>(batch->max_seq_len) / cfg->block_size + 16) * cfg->n_kv_heads > 0x7fffffffLL)
     return LLAMA_ERR_UNSUPPORTED;
   const size_t need = attn_q4_workspace_bytes(batch->num_tokens, batch->num_seqs, batch->max_seq_len, prefill_blocks,
-                                              cfg->n_heads, cfg->n_kv_heads, cfg->head_dim);
+                                              cfg->n_kv_heads, cfg->head_dim);
   if (workspace == nullptr || workspace_bytes < need + 256) return LLAMA_ERR_WORKSPACE;
   AttnQ4Args a{};
   a.a = attn_args(*cfg, *batch, q, k_cache, v_cache, out, nullptr, 0, device_error_word(), false);

@@ -69,7 +69,7 @@ constexpr int stages() { return D == 128 ? 4 : 8; }  // a power of two
 // A piece that spans CTAs, for k_attn_q4_combine.
 struct Cut {
   int first, last;  // its CTAs; last < 0: nothing to join
-  int t0, rows, len, h, unused[2];
+  int t0, rows, len, h, unused[2];  // (32 bytes)
 };
 
 struct Q4Params {
@@ -1139,7 +1139,7 @@ int launch_d(const AttnQ4Args& q4, const Q4Params& p, const Layout& L, cudaStrea
 
 }  // namespace
 
-size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int, int nkv, int head_dim) {
+size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int head_dim) {
   return layout(T, B, max_seq_len, prefill_blocks, nkv, head_dim).total;
 }
 

@@ -167,7 +167,7 @@ struct AttnQ4Args {
   int prefill_blocks;  // bound on the blocks of the sequences that take the prefill path
   uint8_t* ws;         // 256-aligned, attn_q4_workspace_bytes(...)
 };
-size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int nq, int nkv, int head_dim);
+size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int head_dim);
 int attention_q4_launch(const AttnQ4Args& a, cudaStream_t s);
 
 // A side stream of the current device, forked off s (work queued on s before is complete before what is queued on it) and
