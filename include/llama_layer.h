@@ -14,8 +14,10 @@
  * llama_paged_attention), sampling with temperature, top-k and top-p
  * (llama_sample), a KV cache held in 4 bits with the attention over it
  * (kv_cache_write_q4, kv_cache_read_q4, llama_paged_attention_q4) and the norm
- * and rotation of query and key heads before it (llama_qk_norm_rope), the
- * Qwen3-MoE sparse block and decoder layer
+ * and rotation of query and key heads before it (llama_qk_norm_rope),
+ * activations and weights held in 8 or 4 bits with the projections over them
+ * (llama_quantize_mx, llama_fused_add_rmsnorm_mx, llama_linear_mx,
+ * llama_gate_up_silu_mx), the Qwen3-MoE sparse block and decoder layer
  * (llama_moe_forward, llama_moe_layer_forward), norm weights folded into the
  * projections (llama_fold_norm_weights) and a self-test of the device-side
  * failure path (llama_selftest_wait_timeout).
@@ -51,10 +53,11 @@
  *     that kernel's results only after it has completed.  The first kernel
  *     of llama_layer_forward, llama_stack_forward and llama_moe_layer_forward
  *     (an embedding gather or a norm) reads nothing before then, nor does any
- *     kernel of kv_cache_write_q4, kv_cache_read_q4, llama_paged_attention_q4
- *     and llama_qk_norm_rope, so work queued before the call is complete
- *     before any of its data is read; the other entry points' first kernels
- *     start only after everything queued before them has completed.
+ *     kernel of kv_cache_write_q4, kv_cache_read_q4, llama_paged_attention_q4,
+ *     llama_qk_norm_rope and the calls on microscaled matrices (_mx), so work
+ *     queued before the call is complete before any of its data is read; the
+ *     other entry points' first kernels start only after everything queued
+ *     before them has completed.
  *   - A workspace belongs to one call at a time: calls that may overlap on the
  *     GPU need separate workspaces.  Its contents need not be initialised.
  *   - A call returns LLAMA_OK, or a status code without launching anything
@@ -407,6 +410,79 @@ int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, c
                        const int32_t* positions, int num_tokens, const void* q, int64_t q_stride, const void* k,
                        int64_t k_stride, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
                        llama_stream_t stream);
+
+/* Microscaled matrices: activations and weights held in 8 or 4 bits, for
+ * projections whose bytes bound a step.  A matrix [rows, cols] is two arrays,
+ * its codes and its scales, one scale for every group of neighbouring elements
+ * of a row; a value is code * scale * g:
+ *   LLAMA_MX_NVFP4  e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), an e4m3
+ *                   scale for 16 elements, g a power of two (2^-32 .. 2^32) for
+ *                   the matrix;
+ *   LLAMA_MX_FP4    e2m1 codes, an e8m0 scale (a power of two) for 32 elements;
+ *   LLAMA_MX_FP8    e4m3 codes (up to 448), an e8m0 scale for 32 elements.
+ * (g is 1 for the last two.)  Codes lie row by row with no gaps, 4-bit ones two to
+ * a byte, the even element in the low half.  Scales lie in tiles of 128 rows x 4
+ * groups, 512 bytes each, the tiles of a row of tiles side by side:
+ *   byte of (row r, group s) = ((r/128) * ceil(groups/4) + s/4) * 512
+ *                              + r%32 * 16 + r%128/32 * 4 + s%4
+ * so llama_mx_scale_bytes() counts whole tiles.  Rows past the last one of a
+ * scale array may hold any bytes and are left as they are; bytes of groups
+ * past a row's last, up to a multiple of four, are zero (the calls below write
+ * them so).  cols is a multiple of 32, both arrays are 16-byte aligned.
+ * Quantising: s = e4m3(max |x| / (6 g)) for nvfp4, else the smallest power of two
+ * with which no element of the group is beyond the largest code;
+ * code = round(x / (s g)); both to nearest, ties to even, saturating (what rounds
+ * to zero may keep its sign).  nvfp4's s reaches from 2^-9 to 448, so g is chosen
+ * to bring the largest |x| below 2688 g and the typical ones above 0.1 g.  A group
+ * with a NaN or an infinity gets a NaN scale and reads back as NaN; its row's
+ * products are NaN and no other row's.  The pages have no counterpart: they keep
+ * the model's type throughout. */
+enum { LLAMA_MX_BF16 = 0, LLAMA_MX_NVFP4 = 1, LLAMA_MX_FP4 = 2, LLAMA_MX_FP8 = 3 };
+size_t llama_mx_code_bytes(int format, int rows, int cols);   /* 0 for an unsupported matrix */
+size_t llama_mx_scale_bytes(int format, int rows, int cols);  /* 0 for an unsupported matrix */
+
+/* x [rows, cols] bf16, x_stride elements from row to row (a multiple of 8, at
+ * least cols), quantised.  The result is that of the exact quotients. */
+int llama_quantize_mx(int format, const void* x, int64_t x_stride, int rows, int cols, float g, void* codes,
+                      void* scales, llama_stream_t stream);
+
+/* The values of a matrix as bf16, to y [rows, cols] with the given stride:
+ * exact (values below bf16's smallest, 2^-133, are rounded). */
+int llama_dequantize_mx(int format, const void* codes, const void* scales, int rows, int cols, float g, void* y,
+                        int64_t y_stride, llama_stream_t stream);
+
+/* llama_fused_add_rmsnorm with its output quantised: r = bf16(x (+ residual_in));
+ * r / sqrt(mean(r^2) + eps) * gamma, per row of length H, goes to codes and
+ * scales.  The norm's fp32 result is quantised without a rounding to bf16
+ * before.  residual_out may be NULL or alias x / residual_in.  H is a multiple
+ * of 32 up to 16384. */
+int llama_fused_add_rmsnorm_mx(int format, const void* x, const void* residual_in, void* residual_out, void* codes,
+                               void* scales, float g, const void* gamma, int rows, int H, float eps,
+                               llama_stream_t stream);
+
+/* y[M, N] = alpha x[M, K] w[N, K]^T for microscaled x and w of one format, their
+ * codes and scales; alpha holds the matrices' g's (g_x * g_w, and any other
+ * factor).  y bf16 (out_fp32 = 0) or fp32, rounded once from fp32 sums.  K is a
+ * multiple of 32, N of 8.  A result does not depend on M or on other rows, but
+ * for the order of its sums: with few tiles K is split over several SMs, in a
+ * fixed order, so a call repeats bit for bit.  The workspace
+ * (llama_linear_mx_workspace_size) is the call's while it runs. */
+int llama_linear_mx(int format, const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                    int M, int N, int K, float alpha, void* y, int out_fp32, void* workspace, size_t workspace_bytes,
+                    llama_stream_t stream);
+size_t llama_linear_mx_workspace_size(void);
+
+/* a[M, I] = silu(alpha_gate x w_gate^T) * (alpha_up x w_up^T), the gate_up
+ * projection with SiluAndMul in its epilogue, for microscaled x [M, K] and w_gate,
+ * w_up [I, K] of one format (two matrices, so that either's scales begin a
+ * tile).  a is bf16 (out_format LLAMA_MX_BF16; out_scales NULL, I a multiple of 8)
+ * or a microscaled matrix, for the down projection to read: codes to a, scales
+ * to out_scales, with out_g (I a multiple of 32).  The fp32 sums are rounded once,
+ * at the end. */
+int llama_gate_up_silu_mx(int format, const void* x_codes, const void* x_scales, const void* gate_codes,
+                          const void* gate_scales, const void* up_codes, const void* up_scales, int M, int I, int K,
+                          float alpha_gate, float alpha_up, int out_format, float out_g, void* a, void* out_scales,
+                          void* workspace, size_t workspace_bytes, llama_stream_t stream);
 
 /* Sampling beyond greedy ([LLAMA-70B] Sampler, sample(): temperature scaling,
  * the top-k / top-p sampler, greedy rows below a temperature threshold, the

@@ -27,6 +27,11 @@ LLAMA_ERR_DEVICE_GUARD = 5
 LLAMA_ERR_TIMEOUT = 6
 LLAMA_ERR_SCRATCH_LIMIT = 7
 
+LLAMA_MX_BF16 = 0
+LLAMA_MX_NVFP4 = 1
+LLAMA_MX_FP4 = 2
+LLAMA_MX_FP8 = 3
+
 
 class LlamaError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -98,6 +103,15 @@ SIGNATURES = {
     "llama_paged_attention_q4_workspace_size": (_SZ, [_P_CFG, _I, _I, _I, _I]),
     "llama_qk_norm_rope": (_I, [ctypes.POINTER(LlamaQkNormRopeConfig), _VP, _VP, _VP, _I, _VP, _I64, _VP, _I64, _VP,
                                 _I64, _VP, _I64, _VP]),
+    "llama_mx_code_bytes": (_SZ, [_I, _I, _I]),
+    "llama_mx_scale_bytes": (_SZ, [_I, _I, _I]),
+    "llama_quantize_mx": (_I, [_I, _VP, _I64, _I, _I, _F, _VP, _VP, _VP]),
+    "llama_dequantize_mx": (_I, [_I, _VP, _VP, _I, _I, _F, _VP, _I64, _VP]),
+    "llama_fused_add_rmsnorm_mx": (_I, [_I, _VP, _VP, _VP, _VP, _VP, _F, _VP, _I, _I, _F, _VP]),
+    "llama_linear_mx": (_I, [_I, _VP, _VP, _VP, _VP, _I, _I, _I, _F, _VP, _I, _VP, _SZ, _VP]),
+    "llama_linear_mx_workspace_size": (_SZ, []),
+    "llama_gate_up_silu_mx": (_I, [_I, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _F, _F, _I, _F, _VP, _VP, _VP, _SZ,
+                                   _VP]),
     "llama_get_device_error": (_I, [_VP, ctypes.POINTER(ctypes.c_int)]),
     "llama_status_string": (ctypes.c_char_p, [_I]),
     "llama_num_sms": (_I, []),
@@ -496,6 +510,142 @@ def qk_norm_rope(cfg: QkNormRopeConfig, q_norm: Optional[torch.Tensor], k_norm: 
             raise LlamaError(LLAMA_ERR_ARG, where)
     st = lib().llama_qk_norm_rope(cfg.c(), _ptr(q_norm), _ptr(k_norm), _ptr(positions), T, q.data_ptr(), qs,
                                   k.data_ptr(), ks, q_out.data_ptr(), qos, k_out.data_ptr(), kos, _stream(stream))
+    if st:
+        raise LlamaError(st, where)
+
+
+class MxMatrix:
+    """A microscaled matrix [rows, cols]: its format (LLAMA_MX_NVFP4, _FP4 or
+    _FP8), its codes [rows, bytes of a row] and scales, both uint8, and its factor
+    g (``scale``, a power of two; 1 but for LLAMA_MX_NVFP4); see the header.  The
+    tensors are the caller's."""
+
+    __slots__ = ("format", "rows", "cols", "codes", "scales", "scale", "device")
+
+    def __init__(self, format: int, cols: int, codes: torch.Tensor, scales: torch.Tensor, scale: float = 1.0):
+        where = "MxMatrix"
+        rows = int(codes.shape[0])
+        n = lib().llama_mx_scale_bytes(format, rows, cols)
+        if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.dim() != 2 or
+                not codes.is_contiguous() or not scales.is_contiguous() or codes.device != scales.device or
+                (n == 0 and rows > 0) or codes.numel() != lib().llama_mx_code_bytes(format, rows, cols) or
+                scales.numel() < n):
+            raise LlamaError(LLAMA_ERR_ARG, where)
+        self.format, self.rows, self.cols = format, rows, cols
+        self.codes, self.scales, self.scale, self.device = codes, scales, float(scale), codes.device
+
+    @staticmethod
+    def empty(format: int, rows: int, cols: int, scale: float = 1.0, device="cuda") -> "MxMatrix":
+        if format not in (LLAMA_MX_NVFP4, LLAMA_MX_FP4, LLAMA_MX_FP8) or rows < 0 or cols < 1:
+            raise LlamaError(LLAMA_ERR_ARG, "MxMatrix")
+        if cols % 32:
+            raise LlamaError(LLAMA_ERR_UNSUPPORTED, "MxMatrix")
+        u8 = dict(dtype=torch.uint8, device=device)
+        return MxMatrix(format, cols, torch.empty(rows, cols if format == LLAMA_MX_FP8 else cols // 2, **u8),
+                        torch.empty(int(lib().llama_mx_scale_bytes(format, rows, cols)), **u8), scale)
+
+
+def _check_here(where: str, *things) -> None:
+    """Tensors (and matrices) on the current CUDA device, where the call runs."""
+    for t in things:
+        if t is not None and (t.device.type != "cuda" or t.device.index != torch._C._cuda_getDevice()):
+            raise LlamaError(LLAMA_ERR_ARG, where)
+
+
+def _rows_bf16(t: torch.Tensor, shape, where: str) -> int:
+    """Elements from one row to the next of t [rows, cols] bf16, whose rows are dense."""
+    if t.dtype is torch.bfloat16 and t.dim() == 2 and t.shape == shape:
+        row, col = t.stride()
+        if col == 1 or shape[1] == 1:
+            return row if shape[0] > 1 else shape[1]
+    raise LlamaError(LLAMA_ERR_ARG, where)
+
+
+def quantize_mx(x: torch.Tensor, out: MxMatrix, stream=None) -> None:
+    """x [rows, cols] bf16 (any stride between rows) quantised into out; see
+    llama_quantize_mx in the header."""
+    where = "llama_quantize_mx"
+    stride = _rows_bf16(x, (out.rows, out.cols), where)
+    _check_here(where, x, out)
+    st = lib().llama_quantize_mx(out.format, x.data_ptr(), stride, out.rows, out.cols, out.scale, out.codes.data_ptr(),
+                                 out.scales.data_ptr(), _stream(stream))
+    if st:
+        raise LlamaError(st, where)
+
+
+def dequantize_mx(m: MxMatrix, out: torch.Tensor, stream=None) -> None:
+    """The values of m as bf16, into out [rows, cols] (any stride between
+    rows); see llama_dequantize_mx in the header."""
+    where = "llama_dequantize_mx"
+    stride = _rows_bf16(out, (m.rows, m.cols), where)
+    _check_here(where, m, out)
+    st = lib().llama_dequantize_mx(m.format, m.codes.data_ptr(), m.scales.data_ptr(), m.rows, m.cols, m.scale,
+                                   out.data_ptr(), stride, _stream(stream))
+    if st:
+        raise LlamaError(st, where)
+
+
+def fused_add_rmsnorm_mx(x: torch.Tensor, residual_in: Optional[torch.Tensor], residual_out: Optional[torch.Tensor],
+                         out: MxMatrix, gamma: torch.Tensor, eps: float, stream=None) -> None:
+    """fused_add_rmsnorm with the normed rows quantised into out; see
+    llama_fused_add_rmsnorm_mx in the header."""
+    where = "llama_fused_add_rmsnorm_mx"
+    shape = (out.rows, out.cols)
+    for t in (x, residual_in, residual_out):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_contiguous()):
+            raise LlamaError(LLAMA_ERR_ARG, where)
+    if gamma.dtype is not torch.bfloat16 or gamma.numel() != out.cols or not gamma.is_contiguous():
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    _check_here(where, x, residual_in, residual_out, out, gamma)
+    st = lib().llama_fused_add_rmsnorm_mx(out.format, x.data_ptr(), _ptr(residual_in), _ptr(residual_out),
+                                          out.codes.data_ptr(), out.scales.data_ptr(), out.scale, gamma.data_ptr(),
+                                          out.rows, out.cols, eps, _stream(stream))
+    if st:
+        raise LlamaError(st, where)
+
+
+def linear_mx_workspace_size() -> int:
+    """Bytes of workspace of linear_mx and gate_up_silu_mx."""
+    return int(lib().llama_linear_mx_workspace_size())
+
+
+def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, workspace: torch.Tensor, alpha: float = 1.0,
+              stream=None) -> None:
+    """out [M, N] (bf16 or fp32) = alpha x w^T for x [M, K] and w [N, K] of one
+    format; see llama_linear_mx in the header."""
+    where = "llama_linear_mx"
+    if (w.format != x.format or w.cols != x.cols or out.shape != (x.rows, w.rows) or not out.is_contiguous() or
+            out.dtype not in (torch.bfloat16, torch.float32) or workspace.dtype is not torch.uint8):
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    _check_here(where, x, w, out, workspace)
+    st = lib().llama_linear_mx(x.format, x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(),
+                               w.scales.data_ptr(), x.rows, w.rows, x.cols, alpha * (x.scale * w.scale),
+                               out.data_ptr(), 1 if out.dtype is torch.float32 else 0, workspace.data_ptr(),
+                               workspace.numel(), _stream(stream))
+    if st:
+        raise LlamaError(st, where)
+
+
+def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, workspace: torch.Tensor, alpha_gate: float = 1.0,
+                    alpha_up: float = 1.0, stream=None) -> None:
+    """out = silu(alpha_gate x gate^T) * (alpha_up x up^T) for x [M, K] and gate,
+    up [I, K] of one format; out a bf16 tensor [M, I] or an MxMatrix; see
+    llama_gate_up_silu_mx in the header."""
+    where = "llama_gate_up_silu_mx"
+    mx = isinstance(out, MxMatrix)
+    if (gate.format != x.format or up.format != x.format or gate.cols != x.cols or up.cols != x.cols or
+            up.rows != gate.rows or workspace.dtype is not torch.uint8 or
+            ((out.rows, out.cols) if mx else out.shape) != (x.rows, gate.rows) or
+            (not mx and (out.dtype is not torch.bfloat16 or not out.is_contiguous()))):
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    _check_here(where, x, gate, up, out, workspace)
+    to = (out.format, out.scale, out.codes.data_ptr(), out.scales.data_ptr()) if mx else (
+        LLAMA_MX_BF16, 1.0, out.data_ptr(), None)
+    st = lib().llama_gate_up_silu_mx(x.format, x.codes.data_ptr(), x.scales.data_ptr(), gate.codes.data_ptr(),
+                                     gate.scales.data_ptr(), up.codes.data_ptr(), up.scales.data_ptr(), x.rows,
+                                     gate.rows, x.cols, alpha_gate * (x.scale * gate.scale),
+                                     alpha_up * (x.scale * up.scale), *to, workspace.data_ptr(), workspace.numel(),
+                                     _stream(stream))
     if st:
         raise LlamaError(st, where)
 

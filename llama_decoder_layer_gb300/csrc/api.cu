@@ -25,6 +25,7 @@
 #include "kernels.h"
 #include "launch.cuh"
 #include "llama_layer.h"
+#include "mx.cuh"
 #include "q4.cuh"
 
 namespace llama {
@@ -716,6 +717,184 @@ int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, c
   a.q_out_stride = q_out_stride;
   a.k_out_stride = k_out_stride;
   return cuda_status(qk_norm_rope_launch(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Whether a matrix of a format is one, and its scale tiles along a row.
+static int check_mx(int format, int rows, int cols) {
+  if (format < LLAMA_MX_NVFP4 || format > LLAMA_MX_FP8 || rows < 0 || cols < 1) return LLAMA_ERR_ARG;
+  if (cols % 32) return LLAMA_ERR_UNSUPPORTED;
+  // groups are counted in 32 bits on the device
+  if (static_cast<long long>(rows) * ((cols / mx_group(format) + 3) / 4 * 4) > 0x7fffff00LL) return LLAMA_ERR_UNSUPPORTED;
+  return LLAMA_OK;
+}
+
+static int mx_ktiles(int format, int cols) { return (cols / mx_group(format) + kMxTileGroups - 1) / kMxTileGroups; }
+
+// g of a matrix: a power of two for nvfp4, 1 for the others
+static bool mx_factor_ok(int format, float g) { return format == LLAMA_MX_NVFP4 ? q4_scale_ok(g) : g == 1.f; }
+
+size_t llama_mx_code_bytes(int format, int rows, int cols) {
+  if (check_mx(format, rows, cols)) return 0;
+  return static_cast<size_t>(rows) * (cols / 8 * mx_bits(format));
+}
+
+size_t llama_mx_scale_bytes(int format, int rows, int cols) {
+  if (check_mx(format, rows, cols)) return 0;
+  return static_cast<size_t>((rows + kMxTileRows - 1) / kMxTileRows) * mx_ktiles(format, cols) * kMxTileBytes;
+}
+
+// The checks that quantising and reading back share; fills the arguments.
+static int mx_rows_args(int format, const void* v, int64_t stride, int rows, int cols, float g, const void* codes,
+                        const void* scales, MxRowsArgs* a) {
+  const int st = check_mx(format, rows, cols);
+  if (st) return st;
+  if (!mx_factor_ok(format, g)) return LLAMA_ERR_ARG;
+  if (rows == 0) return LLAMA_OK;
+  if (!v || !codes || !scales || stride < cols) return LLAMA_ERR_ARG;
+  if (stride % 8 || !a16(v) || !a16(codes) || !a16(scales)) return LLAMA_ERR_UNSUPPORTED;
+  a->x_stride = stride;
+  a->rows = rows;
+  a->groups = cols / mx_group(format);
+  a->ktiles = mx_ktiles(format, cols);
+  a->g = g;
+  a->inv_g = 1.f / g;
+  a->sixth = a->inv_g * (1.f / 6.f);
+  return LLAMA_OK;
+}
+
+int llama_quantize_mx(int format, const void* x, int64_t x_stride, int rows, int cols, float g, void* codes,
+                      void* scales, llama_stream_t stream) {
+  MxRowsArgs a{};
+  const int st = mx_rows_args(format, x, x_stride, rows, cols, g, codes, scales, &a);
+  if (st || rows == 0) return st;
+  a.x = x;
+  a.codes = codes;
+  a.scales = scales;
+  return cuda_status(quantize_mx_launch(format, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int llama_dequantize_mx(int format, const void* codes, const void* scales, int rows, int cols, float g, void* y,
+                        int64_t y_stride, llama_stream_t stream) {
+  MxRowsArgs a{};
+  const int st = mx_rows_args(format, y, y_stride, rows, cols, g, codes, scales, &a);
+  if (st || rows == 0) return st;
+  a.y = y;
+  a.codes = const_cast<void*>(codes);
+  a.scales = const_cast<void*>(scales);
+  return cuda_status(dequantize_mx_launch(format, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int llama_fused_add_rmsnorm_mx(int format, const void* x, const void* residual_in, void* residual_out, void* codes,
+                               void* scales, float g, const void* gamma, int rows, int H, float eps,
+                               llama_stream_t stream) {
+  const int st = check_mx(format, rows, H);
+  if (st) return st;
+  if (!(eps >= 0.f) || !mx_factor_ok(format, g)) return LLAMA_ERR_ARG;
+  if (H > 16384) return LLAMA_ERR_UNSUPPORTED;
+  if (rows == 0) return LLAMA_OK;
+  if (!x || !codes || !scales || !gamma) return LLAMA_ERR_ARG;
+  if (!a16(x) || !a16(codes) || !a16(scales) || !a16(gamma) || (residual_in && !a16(residual_in)) ||
+      (residual_out && !a16(residual_out)))
+    return LLAMA_ERR_UNSUPPORTED;
+  MxNormArgs a{};
+  a.x = x;
+  a.res_in = residual_in;
+  a.gamma = gamma;
+  a.res_out = residual_out;
+  a.codes = codes;
+  a.scales = scales;
+  a.rows = rows;
+  a.cols = H;
+  a.ktiles = mx_ktiles(format, H);
+  a.eps = eps;
+  a.inv_g = 1.f / g;
+  a.sixth = a.inv_g * (1.f / 6.f);
+  return cuda_status(add_rmsnorm_mx_launch(format, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t llama_linear_mx_workspace_size(void) { return gemm_mx_partials_bytes(num_sms()) + 256; }
+
+// The checks that the two products share (of w, `n_w` matrices).
+static int check_mx_product(int format, int M, int N, int K, const MxOperand& x, const MxOperand* w, int n_w,
+                            const float* alpha) {
+  int st = check_mx(format, M, K);
+  if (!st) st = check_mx(format, N, K);
+  if (st) return st;
+  if (N < 1) return LLAMA_ERR_ARG;
+  for (int i = 0; i < n_w; ++i)
+    if (!(fabsf(alpha[i]) < INFINITY)) return LLAMA_ERR_ARG;
+  if (M == 0) return LLAMA_OK;
+  if (!x.codes || !x.scales) return LLAMA_ERR_ARG;
+  for (int i = 0; i < n_w; ++i)
+    if (!w[i].codes || !w[i].scales) return LLAMA_ERR_ARG;
+  if (!a16(x.codes) || !a16(x.scales)) return LLAMA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_w; ++i)
+    if (!a16(w[i].codes) || !a16(w[i].scales)) return LLAMA_ERR_UNSUPPORTED;
+  // output tiles are counted in 32 bits
+  if (static_cast<long long>((M + 127LL) / 128) * ((N + 127LL) / 128) > 0x3fffffffLL) return LLAMA_ERR_UNSUPPORTED;
+  return LLAMA_OK;
+}
+
+static int mx_product(MxGemmArgs& g, void* workspace, llama_stream_t stream) {
+  g.partials = reinterpret_cast<float*>(ws_base(workspace));
+  g.partials_bytes = gemm_mx_partials_bytes(num_sms());
+  g.err = device_error_word();
+  return cuda_status(gemm_mx_launch(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int llama_linear_mx(int format, const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
+                    int M, int N, int K, float alpha, void* y, int out_fp32, void* workspace, size_t workspace_bytes,
+                    llama_stream_t stream) {
+  MxGemmArgs g{};
+  g.fmt = format;
+  g.x = {x_codes, x_scales};
+  g.w[0] = {w_codes, w_scales};
+  g.alpha[0] = alpha;
+  const int st = check_mx_product(format, M, N, K, g.x, g.w, 1, g.alpha);
+  if (st || M == 0) return st;
+  if (!y) return LLAMA_ERR_ARG;
+  if (N % 8 || !a16(y)) return LLAMA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < llama_linear_mx_workspace_size()) return LLAMA_ERR_WORKSPACE;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.out = y;
+  g.out_f32 = out_fp32 != 0;
+  return mx_product(g, workspace, stream);
+}
+
+int llama_gate_up_silu_mx(int format, const void* x_codes, const void* x_scales, const void* gate_codes,
+                          const void* gate_scales, const void* up_codes, const void* up_scales, int M, int I, int K,
+                          float alpha_gate, float alpha_up, int out_format, float out_g, void* a, void* out_scales,
+                          void* workspace, size_t workspace_bytes, llama_stream_t stream) {
+  MxGemmArgs g{};
+  g.fmt = format;
+  g.x = {x_codes, x_scales};
+  g.w[0] = {gate_codes, gate_scales};
+  g.w[1] = {up_codes, up_scales};
+  g.alpha[0] = alpha_gate;
+  g.alpha[1] = alpha_up;
+  if (out_format < LLAMA_MX_BF16 || out_format > LLAMA_MX_FP8) return LLAMA_ERR_ARG;
+  const int st = check_mx_product(format, M, I, K, g.x, g.w, 2, g.alpha);
+  if (st) return st;
+  if (out_format == LLAMA_MX_BF16 ? out_scales != nullptr : !mx_factor_ok(out_format, out_g)) return LLAMA_ERR_ARG;
+  if (I % 8 || (out_format != LLAMA_MX_BF16 && check_mx(out_format, M, I))) return LLAMA_ERR_UNSUPPORTED;
+  if (M == 0) return LLAMA_OK;
+  if (!a || (out_format != LLAMA_MX_BF16 && !out_scales)) return LLAMA_ERR_ARG;
+  if (!a16(a) || (out_scales && !a16(out_scales))) return LLAMA_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < llama_linear_mx_workspace_size()) return LLAMA_ERR_WORKSPACE;
+  g.M = M;
+  g.N = I;
+  g.K = K;
+  g.silu = true;
+  g.out_fmt = out_format;
+  g.out = a;
+  g.out_scales = out_scales;
+  if (out_format != LLAMA_MX_BF16) {
+    g.out_inv_g = 1.f / out_g;
+    g.out_sixth = g.out_inv_g * (1.f / 6.f);
+  }
+  return mx_product(g, workspace, stream);
 }
 
 int llama_sample(const float* logits, int rows, int vocab, const float* temperature, const int32_t* top_k,

@@ -323,6 +323,39 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
+// D[tmem] (+)= (A * SA)[smem desc] * (B * SB)[smem desc]^T, microscaled operands with their scales in tensor memory
+// (sa, sb): FMT_BITS 8: e4m3 and one scale a K step of 32; 4: e2m1, a K step of 64 with VEC scales (2: e8m0, 4: e4m3)
+template <int FMT_BITS, int VEC, bool PAIR>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa,
+                                          uint32_t sb, uint32_t accumulate) {
+#define LLAMA_TC_MMA_MX(GROUP, KIND)                                                                     \
+  asm volatile(                                                                                          \
+      "{\n\t.reg .pred p;\n\t"                                                                           \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                                        \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem), \
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)                              \
+      : "memory")
+  if constexpr (FMT_BITS == 8) {
+    if constexpr (PAIR) LLAMA_TC_MMA_MX("2", "mxf8f6f4.block_scale.scale_vec::1X");
+    else LLAMA_TC_MMA_MX("1", "mxf8f6f4.block_scale.scale_vec::1X");
+  } else if constexpr (VEC == 2) {
+    if constexpr (PAIR) LLAMA_TC_MMA_MX("2", "mxf4.block_scale.scale_vec::2X");
+    else LLAMA_TC_MMA_MX("1", "mxf4.block_scale.scale_vec::2X");
+  } else {
+    if constexpr (PAIR) LLAMA_TC_MMA_MX("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    else LLAMA_TC_MMA_MX("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  }
+#undef LLAMA_TC_MMA_MX
+}
+
+// One scale tile (32 rows of 16 bytes) from shared memory into four 32-bit columns of tensor memory, the same in each
+// of the four lane quarters.  Copies and MMAs issued by one thread run in the order of their issue.
+template <bool PAIR>
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // arrive once on the mbarrier when all previously issued tcgen05.mma of this
 // thread have completed
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -535,6 +568,32 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int M, int N) {
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Instruction descriptor of the microscaled kinds: A and B e4m3 (type 0) or e2m1 (1, bits 7-9 and 10-12), both K-major,
+// N >> 3 in bits 17-22, the scales' type in bit 23 (0 e4m3, 1 e8m0), M >> 4 in bits 24-28; which byte of a scale word
+// the instruction starts at goes into bits 4-5 (B) and 29-30 (A).
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int bits, bool e8m0) {
+  return (bits == 4 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (e8m0 ? 1u << 23 : 0u) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_mx_scale(uint32_t idesc, uint32_t byte) {
+  return idesc | (byte << 4) | (byte << 29);
+}
+
+// Shared-memory descriptor of a scale tile: no swizzle, 8 rows of 16 bytes in a row (128 bytes from one such block to
+// the next), descriptor version 1.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) | (1ull << 46);
+}
+
+// Untiled copy of bytes (a multiple of 16, both addresses 16-byte aligned) into shared memory, completion as
+// transaction bytes on the mbarrier
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,540 @@
+// Products of microscaled matrices (the formats are in mx.cuh) on the block-scaled
+// tensor-core instructions:
+//   y = alpha x w^T                                    (llama_linear_mx)
+//   a = silu(alpha_0 x w_gate^T) * (alpha_1 x w_up^T)  (llama_gate_up_silu_mx)
+// x [M, K] and w [N, K] are codes with scales; sums are fp32 in tensor memory, and
+// each result is rounded once: to bf16, or with its row's neighbours to the
+// codes and scales of a microscaled matrix that the next product reads.
+//
+// Tiles are 128 rows of x by NB columns (rows of w).  A stage of the operand ring holds 128 bytes of every row (256 e2m1 or
+// 128 e4m3 elements, one swizzle row) and the scale tiles that belong to them; the issuing thread copies these into tensor
+// memory and then issues the stage's four MMAs, in order.
+//
+// With 256 columns two accumulators do not fit beside the scales (512 columns of tensor memory), so the second starts at
+// column 192: the MMAs of the next tile may begin once the epilogue has read the 64 columns that the two share, which it
+// reads first.
+#include <cuda.h>
+#include <math.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "mx.cuh"
+
+namespace llama {
+
+namespace {
+
+constexpr int BM = 128;
+constexpr int kRowBytes = 128;    // of every row of a stage
+constexpr int kThreads = 192;     // warp 0 copies, warp 1 MMAs, warps 2-5 epilogue
+constexpr int kTmemCols = 512;
+constexpr int kMaxStages = 8;
+constexpr int kMaxSmemBytes = 232448;              // the opt-in limit per CTA (227 KB)
+constexpr int kRingBudget = kMaxSmemBytes - 2048;  // the rest: barriers, alignment slack
+
+enum MxEpilogue : int { kMxBf16 = 0, kMxF32 = 1, kMxSilu = 2, kMxSiluNvfp4 = 3, kMxSiluFp4 = 4, kMxSiluFp8 = 5 };
+
+__host__ __device__ constexpr bool is_silu(int epi) { return epi >= kMxSilu; }
+// the format that the output is quantised to; 0: none
+__host__ __device__ constexpr int out_fmt(int epi) {
+  return epi == kMxSiluNvfp4 ? kMxNvfp4 : epi == kMxSiluFp4 ? kMxFp4 : epi == kMxSiluFp8 ? kMxFp8 : 0;
+}
+
+// What a format makes of a stage.
+template <int FMT>
+struct Stage {
+  static constexpr int kBits = mx_bits(FMT);
+  static constexpr int kElems = kRowBytes * 8 / kBits;
+  static constexpr int kTiles = kElems / mx_group(FMT) / kMxTileGroups;  // scale tiles of 128 rows
+  static constexpr int kStepElems = 256 / kBits;                        // an MMA's part of K: 32 bytes of a row
+  static constexpr int kSteps = kElems / kStepElems;
+  static constexpr int kStepScales = kStepElems / mx_group(FMT);  // scales of a row in an MMA: 4, 2 or 1
+  static constexpr int kPerTile = kMxTileGroups / kStepScales;    // MMAs that take their scales from one tile
+  static constexpr bool kE8m0 = FMT != kMxNvfp4;
+};
+
+struct MxGemmParams {
+  int M, N, kb;             // kb: stages along K
+  int last_steps;           // MMAs of the last one
+  int ktiles, w_tiles;      // scale tiles along K, and row tiles of w
+  int tiles_m, tiles_n, tiles, group_m;
+  int stages;
+  const uint8_t *x_scales, *w_scales[2];
+  float alpha[2];
+  void* out;
+  uint8_t* out_scales;
+  int out_ktiles;
+  float out_inv_g, out_sixth;
+  int* err;
+};
+
+__device__ __forceinline__ void tile_coords(const MxGemmParams& p, int tile, int& tm, int& tn) {
+  const int group = p.group_m * p.tiles_n;
+  const int g = tile / group;
+  const int first_m = g * p.group_m;
+  const int gm = min(p.tiles_m - first_m, p.group_m);
+  const int r = tile - g * group;
+  tm = first_m + r % gm;
+  tn = r / gm;
+}
+
+template <int FMT, int NB>
+struct Ring {
+  static constexpr int kA = BM * kRowBytes, kB = NB * kRowBytes;
+  static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = kSa * (NB / kMxTileRows);
+  static constexpr int kBytes = kA + kB + kSa + kSb;  // of a stage
+  static constexpr int kStages = kRingBudget / kBytes < kMaxStages ? kRingBudget / kBytes : kMaxStages;
+  static constexpr int kSmem = kStages * kBytes + 2048;
+};
+
+// Tensor memory: two accumulators, then the scales of a stage.
+template <int FMT, int NB>
+struct Tmem {
+  static constexpr int kAcc = NB == 256 ? 192 : NB;  // from the first accumulator to the second
+  static constexpr int kSa = kAcc + NB, kSb = kSa + 4 * Stage<FMT>::kTiles;
+  static_assert(kSb + 4 * (NB / 128) * Stage<FMT>::kTiles <= kTmemCols, "tensor memory");
+};
+
+// ---------------------------------------------------------------------------
+// Epilogue: 32 output columns of a thread's row at a time.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* o, const float (&v)[32], int n) {
+  if (n >= 32) {
+    uint4* d = reinterpret_cast<uint4*>(o);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      d[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < n) o[e] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+// 32 results to codes, at columns n .. n + 31 of the row; `words` collects the tile's scale words (128 columns).
+template <int OF>
+__device__ __forceinline__ void store_codes32(const MxGemmParams& p, int row, int n, const float (&v)[32],
+                                              uint32_t (&words)[2]) {
+  constexpr int G = mx_group(OF), kGroups = 32 / G;
+  uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * (p.N / 8 * mx_bits(OF)) + n / 8 * mx_bits(OF);
+  uint32_t w[mx_bits(OF)];
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < G; ++e) top = max(top, abs_bits(v[g * G + e]));
+    const MxScale s = mx_scale<OF, false>(top, p.out_sixth, p.out_inv_g);
+    const int at = n % 128 / G + g;  // among the tile's groups
+    words[0] |= at < 4 ? s.byte << (at * 8) : 0u;
+    words[1] |= at < 4 ? 0u : s.byte << (at * 8 - 32);
+#pragma unroll
+    for (int c = 0; c < G / 8; ++c) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = v[g * G + c * 8 + e];
+      const uint2 u = mx_codes8<OF, false>(x, s.factor);
+      const int i = g * (G / 8) + c;
+      if constexpr (OF == kMxFp8) {
+        w[2 * i] = u.x;
+        w[2 * i + 1] = u.y;
+      } else {
+        w[i] = u.x;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < mx_bits(OF) / 4; ++i)
+    reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// Columns [32 u, 32 u + 32) of the tile's outputs (silu: NB / 2 of them).  ld(column, v) returns 32 accumulator columns of
+// the thread's row; it is called by whole warps.
+template <int EPI, int NB, class Loader>
+__device__ __forceinline__ void epilogue_unit(const MxGemmParams& p, int row, int tn, int u, const Loader& ld,
+                                              uint32_t (&words)[2]) {
+  const int n = tn * (is_silu(EPI) ? NB / 2 : NB) + 32 * u;
+  if (n >= p.N) return;
+  float v[32];
+  ld(32 * u, v);
+  if constexpr (is_silu(EPI)) {
+    float up[32];
+    ld(NB / 2 + 32 * u, up);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float g = v[e] * p.alpha[0];
+      v[e] = g / (1.0f + __expf(-g)) * (up[e] * p.alpha[1]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] *= p.alpha[0];
+  }
+  if (row >= p.M) return;
+  if constexpr (out_fmt(EPI) != 0) {
+    store_codes32<out_fmt(EPI)>(p, row, n, v, words);
+  } else if constexpr (EPI == kMxF32) {
+    float* o = static_cast<float*>(p.out) + static_cast<size_t>(row) * p.N + n;
+    if (n + 32 <= p.N) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        reinterpret_cast<float4*>(o)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (n + e < p.N) o[e] = v[e];
+    }
+  } else {
+    store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(row) * p.N + n, v, p.N - n);
+  }
+}
+
+// the scale words of a tile's 128 outputs of the row
+template <int EPI>
+__device__ __forceinline__ void store_words(const MxGemmParams& p, int row, int tn, const uint32_t (&words)[2]) {
+  constexpr int kWords = out_fmt(EPI) == kMxNvfp4 ? 2 : 1;
+  if (row >= p.M) return;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    if (tn * kWords + i < p.out_ktiles)
+      *reinterpret_cast<uint32_t*>(p.out_scales + mx_scale_at(row, tn * kWords + i, p.out_ktiles)) = words[i];
+}
+
+struct TmemLoader {
+  uint32_t taddr;
+  __device__ __forceinline__ void operator()(int col, float (&v)[32]) const { tmem_ld32(taddr + col, v); }
+};
+
+// ---------------------------------------------------------------------------
+// Persistent, one CTA an SM, whole tiles in a grouped raster.
+// ---------------------------------------------------------------------------
+template <int FMT, int EPI, int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gemm_mx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
+              const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ MxGemmParams p) {
+  using S = Stage<FMT>;
+  using R = Ring<FMT, NB>;
+  using T = Tmem<FMT, NB>;
+  static_assert(!is_silu(EPI) || NB == 256, "SiLU tiles hold 128 gate and 128 up columns");
+  constexpr int nst = R::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  const uint32_t sbase = raw_addr + pad;
+  const uint32_t scales = sbase + nst * (R::kA + R::kB);  // behind the swizzled tiles
+  uint8_t* meta = smem_raw + pad + nst * R::kBytes;
+  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull[2], tempty[2], drain
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * nst + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * nst + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * nst + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 4);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB0);
+    if (is_silu(EPI)) tma_prefetch_desc(&tmB1);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_first();
+    int stage = 0;
+    uint32_t phase = 0;
+    long long used = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
+      int tm, tn;
+      tile_coords(p, t, tm, tn);
+      for (int kb = 0; kb < p.kb; ++kb) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
+          const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
+          const int kt = kb * S::kTiles;
+          const uint32_t bytes = min(S::kTiles, p.ktiles - kt) * kMxTileBytes;  // of the scales of 128 rows
+          int pieces = 1;  // 128-row pieces of w that are there
+          if (NB == 256 && (is_silu(EPI) || 2 * tn + 1 < p.w_tiles)) pieces = 2;
+          mbar_arrive_expect_tx(full_bar(stage), R::kA + R::kB + bytes * (1 + pieces));
+          tma_load_2d(sa, &tmA, full_bar(stage), kb * kRowBytes, tm * BM, pol_a);
+          bulk_load(ssa, p.x_scales + (static_cast<size_t>(tm) * p.ktiles + kt) * kMxTileBytes, bytes, full_bar(stage), pol_a);
+#pragma unroll
+          for (int i = 0; i < NB / 128; ++i) {
+            const int rt = is_silu(EPI) ? tn : tn * (NB / 128) + i;  // 128 rows of w
+            tma_load_2d(sb + i * 128 * kRowBytes, is_silu(EPI) && i ? &tmB1 : &tmB0, full_bar(stage), kb * kRowBytes, rt * 128,
+                        pol_b);
+            if (i < pieces)
+              bulk_load(ssb + i * R::kSa,
+                        p.w_scales[is_silu(EPI) ? i : 0] + (static_cast<size_t>(rt) * p.ktiles + kt) * kMxTileBytes, bytes,
+                        full_bar(stage), pol_b);
+          }
+        }
+        __syncwarp();
+        ++used;
+        if (++stage == nst) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0) pdl_trigger();
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmProducer);
+      *abort_flag = 1;
+    }
+    // every copy has landed before the CTA can exit: use u of stage s completes its phase u
+    for (int s = 0; s < nst; ++s) {
+      const long long uses = (used - s + nst - 1) / nst;
+      if (uses > 0) mbar_wait(full_bar(s), static_cast<uint32_t>(uses - 1) & 1u, nullptr);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    constexpr uint32_t idesc = idesc_mx(BM, NB, S::kBits, S::kE8m0);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true, issued = false;
+    int n_tiles = 0;
+    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++n_tiles) {
+      // NB 256: the other accumulator's shared columns have been read; else: all of this one
+      const int wait_acc = NB == 256 ? acc ^ 1 : acc;
+      const uint32_t wait_phase = NB == 256 ? (acc ? acc_phase : acc_phase ^ 1u) : acc_phase ^ 1u;
+      if (!mbar_wait(tempty_bar(wait_acc), wait_phase, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * T::kAcc;
+      for (int kb = 0; kb < p.kb; ++kb) {
+        if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
+          const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
+#pragma unroll
+          for (int i = 0; i < S::kTiles; ++i) {
+            tc_copy_scales<false>(tmem_base + T::kSa + 4 * i, smem_desc_scales(ssa + i * kMxTileBytes));
+#pragma unroll
+            for (int j = 0; j < NB / 128; ++j)
+              tc_copy_scales<false>(tmem_base + T::kSb + (NB / 128) * 4 * i + 4 * j,
+                                    smem_desc_scales(ssb + j * R::kSa + i * kMxTileBytes));
+          }
+          const int steps = kb + 1 < p.kb ? S::kSteps : p.last_steps;
+#pragma unroll
+          for (int k = 0; k < S::kSteps; ++k) {
+            if (k >= steps) break;
+            const int i = k / S::kPerTile;
+            tc_mma_mx<S::kBits, S::kStepScales, false>(
+                d_tmem, smem_desc_sw128(sa + 32 * k), smem_desc_sw128(sb + 32 * k),
+                idesc_mx_scale(idesc, k % S::kPerTile * S::kStepScales), tmem_base + T::kSa + 4 * i,
+                tmem_base + T::kSb + (NB / 128) * 4 * i, kb > 0 || k > 0 ? 1u : 0u);
+          }
+          tc_commit(empty_bar(stage));
+          issued = true;
+        }
+        __syncwarp();
+        if (++stage == nst) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (lane == 0) tc_commit(tfull_bar(acc));
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmMma);
+      *abort_flag = 1;
+    }
+    // all MMAs and copies this thread issued must finish before tensor memory is freed
+    if (lane == 0 && issued) tc_commit(drain_bar);
+    __syncwarp();
+    if (__shfl_sync(0xffffffffu, issued ? 1 : 0, 0)) mbar_wait(drain_bar, 0, nullptr);
+  } else {
+    // ---------------- epilogue ----------------
+    const int quad = warp & 3;  // tensor-memory lane quarter this warp may access
+    constexpr int kUnits = (is_silu(EPI) ? NB / 2 : NB) / 32;
+    constexpr int kShared = NB == 256 ? kUnits / (is_silu(EPI) ? 2 : 4) : kUnits;  // units that touch shared columns
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
+      int tm, tn;
+      tile_coords(p, t, tm, tn);
+      if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int row = tm * BM + quad * 32 + lane;
+      const TmemLoader ld{tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc};
+      uint32_t words[2] = {0, 0};
+      // the first accumulator's shared columns are its last, the second's its first
+      const int first = NB == 256 && acc == 0 ? kUnits - kShared : 0;
+#pragma unroll 1
+      for (int i = 0; i < kUnits; ++i) {
+        epilogue_unit<EPI, NB>(p, row, tn, (first + i) % kUnits, ld, words);
+        if (i == kShared - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty_bar(acc));
+        }
+      }
+      if constexpr (out_fmt(EPI) != 0) store_words<EPI>(p, row, tn, words);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
+      *abort_flag = 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// [rows, row_bytes] bytes in boxes of box_rows x 128 bytes, 128-byte swizzle; bytes out of range read as zero
+bool make_tmap(CUtensorMap* m, const void* base, int rows, long long row_bytes, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  cuuint32_t box[2] = {kRowBytes, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int EPI, int NB>
+int launch_typed(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const MxGemmParams& p, int grid,
+                 cudaStream_t s) {
+  static SmemLimits limits;
+  const cudaError_t e = limits.raise({smem_need(k_gemm_mx<FMT, EPI, NB>, Ring<FMT, NB>::kSmem)});
+  if (e != cudaSuccess) return e;
+  return launch_kernel(k_gemm_mx<FMT, EPI, NB>, dim3(grid), dim3(kThreads), Ring<FMT, NB>::kSmem, s, true, ta, tb0, tb1, p);
+}
+
+template <int FMT>
+int launch_fmt(const MxGemmArgs& a, cudaStream_t s) {
+  using S = Stage<FMT>;
+  MxGemmParams p{};
+  const long long row_bytes = static_cast<long long>(a.K) * S::kBits / 8;
+  p.M = a.M;
+  p.N = a.N;
+  p.kb = static_cast<int>((row_bytes + kRowBytes - 1) / kRowBytes);
+  p.last_steps = (a.K - (p.kb - 1) * S::kElems + S::kStepElems - 1) / S::kStepElems;
+  p.ktiles = (a.K / mx_group(FMT) + kMxTileGroups - 1) / kMxTileGroups;
+  p.w_tiles = (a.N + kMxTileRows - 1) / kMxTileRows;
+  p.x_scales = static_cast<const uint8_t*>(a.x.scales);
+  for (int i = 0; i < 2; ++i) {
+    p.w_scales[i] = static_cast<const uint8_t*>(a.w[i].scales);
+    p.alpha[i] = a.alpha[i];
+  }
+  p.out = a.out;
+  p.out_scales = static_cast<uint8_t*>(a.out_scales);
+  if (a.out_fmt) p.out_ktiles = (a.N / mx_group(a.out_fmt) + kMxTileGroups - 1) / kMxTileGroups;
+  p.out_inv_g = a.out_inv_g;
+  p.out_sixth = a.out_sixth;
+  p.err = a.err;
+  constexpr int NB = 256;
+  p.tiles_m = (a.M + BM - 1) / BM;
+  p.tiles_n = a.silu ? (a.N + NB / 2 - 1) / (NB / 2) : (a.N + NB - 1) / NB;
+  p.tiles = p.tiles_m * p.tiles_n;
+  p.group_m = p.tiles_m < 24 ? p.tiles_m : 24;
+  const int sms = num_sms(), grid = p.tiles < sms ? p.tiles : sms;
+  CUtensorMap ta, tb0, tb1;
+  if (!make_tmap(&ta, a.x.codes, a.M, row_bytes, BM) || !make_tmap(&tb0, a.w[0].codes, a.N, row_bytes, 128))
+    return cudaErrorInvalidValue;
+  tb1 = tb0;
+  if (a.silu && !make_tmap(&tb1, a.w[1].codes, a.N, row_bytes, 128)) return cudaErrorInvalidValue;
+  if (!a.silu)
+    return a.out_f32 ? launch_typed<FMT, kMxF32, NB>(ta, tb0, tb1, p, grid, s)
+                     : launch_typed<FMT, kMxBf16, NB>(ta, tb0, tb1, p, grid, s);
+  switch (a.out_fmt) {
+    case 0:
+      return launch_typed<FMT, kMxSilu, NB>(ta, tb0, tb1, p, grid, s);
+    case kMxNvfp4:
+      return launch_typed<FMT, kMxSiluNvfp4, NB>(ta, tb0, tb1, p, grid, s);
+    case kMxFp4:
+      return launch_typed<FMT, kMxSiluFp4, NB>(ta, tb0, tb1, p, grid, s);
+    default:
+      return launch_typed<FMT, kMxSiluFp8, NB>(ta, tb0, tb1, p, grid, s);
+  }
+}
+
+}  // namespace
+
+size_t gemm_mx_partials_bytes(int) { return 256; }
+
+int gemm_mx_launch(const MxGemmArgs& a, cudaStream_t s) {
+  if (a.M <= 0) return 0;
+  switch (a.fmt) {
+    case kMxNvfp4:
+      return launch_fmt<kMxNvfp4>(a, s);
+    case kMxFp4:
+      return launch_fmt<kMxFp4>(a, s);
+    case kMxFp8:
+      return launch_fmt<kMxFp8>(a, s);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace llama

@@ -170,6 +170,46 @@ struct AttnQ4Args {
 size_t attn_q4_workspace_bytes(int T, int B, int max_seq_len, int prefill_blocks, int nkv, int head_dim);
 int attention_q4_launch(const AttnQ4Args& a, cudaStream_t s);
 
+// Microscaled matrices (mx.cuh; quant_mx.cu, gemm_mx.cu).  fmt: LLAMA_MX_NVFP4, _FP4 or _FP8.
+struct MxRowsArgs {
+  const void* x;  // quantise: [rows, groups * group] bf16, x_stride elements from row to row
+  void* y;        // read back: the same, written
+  long long x_stride;
+  void *codes, *scales;
+  int rows, groups, ktiles;  // groups of a row, and their tiles of four
+  float g, inv_g, sixth;     // sixth: 1 / (6 g)
+};
+int quantize_mx_launch(int fmt, const MxRowsArgs& a, cudaStream_t s);
+int dequantize_mx_launch(int fmt, const MxRowsArgs& a, cudaStream_t s);
+
+struct MxNormArgs {
+  const void *x, *res_in, *gamma;
+  void *res_out, *codes, *scales;
+  int rows, cols, ktiles;
+  float eps, inv_g, sixth;
+};
+int add_rmsnorm_mx_launch(int fmt, const MxNormArgs& a, cudaStream_t s);
+
+struct MxOperand {
+  const void *codes, *scales;
+};
+struct MxGemmArgs {
+  int fmt;             // of x and w
+  MxOperand x, w[2];   // [M, K]; [N, K] (silu: gate and up, each [N, K])
+  float alpha[2];      // the product with w[i] is multiplied by it
+  int M, N, K;
+  bool silu;           // out = silu(x w0^T) * (x w1^T)
+  int out_fmt;         // 0: bf16, or the format that out is quantised to (silu)
+  bool out_f32;        // fp32 instead of bf16 (no silu)
+  void *out, *out_scales;  // [M, N], or codes and scales
+  float out_inv_g, out_sixth;
+  float* partials;
+  size_t partials_bytes;
+  int* err;
+};
+size_t gemm_mx_partials_bytes(int num_sms);
+int gemm_mx_launch(const MxGemmArgs& a, cudaStream_t s);
+
 // A side stream of the current device, forked off s (work queued on s before is complete before what is queued on it) and
 // the caller's until side_join, which makes s wait for it; null if there is none, and s has to do.
 struct SideStream {

@@ -1,0 +1,250 @@
+// Microscaled matrices (the formats are in mx.cuh): quantising bf16 rows,
+// reading them back, and the fused residual add + RMSNorm whose output is
+// quantised, for a product of microscaled matrices to read.
+#include "common.cuh"
+#include "kernels.h"
+#include "launch.cuh"
+#include "mx.cuh"
+
+namespace llama {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// A thread's group: its row, its number in the row, and whether the row has it (a row's last scale word is filled up
+// with zeros).  Four lanes in a row have the groups of one scale word.
+struct MxPlace {
+  int row, grp;
+  bool there;
+};
+__device__ __forceinline__ MxPlace mx_place(const MxRowsArgs& a) {
+  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  MxPlace p;
+  const uint32_t padded = static_cast<uint32_t>(a.ktiles) * kMxTileGroups;
+  const bool in = i < static_cast<long long>(a.rows) * padded;
+  const uint32_t n = in ? static_cast<uint32_t>(i) : 0u;
+  p.row = static_cast<int>(n / padded);
+  p.grp = static_cast<int>(n - static_cast<uint32_t>(p.row) * padded);
+  p.there = in && p.grp < a.groups;
+  if (!in) p.row = -1;
+  return p;
+}
+
+// the word of four lanes' scale bytes
+__device__ __forceinline__ uint32_t scale_word(uint32_t byte) {
+  uint32_t w = byte << ((threadIdx.x & 3) * 8);
+  w |= __shfl_xor_sync(0xffffffffu, w, 1);
+  w |= __shfl_xor_sync(0xffffffffu, w, 2);
+  return w;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
+  v[0] = bf16_lo(u.x);
+  v[1] = bf16_hi(u.x);
+  v[2] = bf16_lo(u.y);
+  v[3] = bf16_hi(u.y);
+  v[4] = bf16_lo(u.z);
+  v[5] = bf16_hi(u.z);
+  v[6] = bf16_lo(u.w);
+  v[7] = bf16_hi(u.w);
+}
+
+// One thread a group.
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) k_quantize_mx(const MxRowsArgs a) {
+  constexpr int G = mx_group(FMT), C = G / 8;
+  pdl_wait();
+  const MxPlace p = mx_place(a);
+  uint4 u[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) u[c] = make_uint4(0, 0, 0, 0);
+  if (p.there) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + p.row * a.x_stride) + p.grp * C;
+#pragma unroll
+    for (int c = 0; c < C; ++c) u[c] = src[c];
+  }
+  float x[C][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    unpack8(u[c], x[c]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, abs_bits(x[c][e]));
+  }
+  const MxScale s = mx_scale<FMT, true>(top, a.sixth, a.inv_g);
+  if (p.there) {
+    uint8_t* dst = static_cast<uint8_t*>(a.codes) + static_cast<size_t>(p.row) * (a.groups * (G * mx_bits(FMT) / 8)) +
+                   p.grp * (G * mx_bits(FMT) / 8);
+    uint2 w[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) w[c] = mx_codes8<FMT, true>(x[c], s.factor);
+    if constexpr (FMT == kMxNvfp4) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0].x, w[1].x);
+    } else if constexpr (FMT == kMxFp4) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
+    } else {
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+      reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+    }
+  }
+  const uint32_t word = scale_word(p.there ? s.byte : 0u);
+  if (p.row >= 0 && (threadIdx.x & 3) == 0)
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) + mx_scale_at(p.row, p.grp >> 2, a.ktiles)) = word;
+}
+
+// bf16(code * scale * g), one thread a group.
+template <int FMT>
+__global__ void __launch_bounds__(kThreads) k_dequantize_mx(const MxRowsArgs a) {
+  constexpr int G = mx_group(FMT), C = G / 8;
+  pdl_wait();
+  const MxPlace p = mx_place(a);
+  if (!p.there) return;
+  const uint8_t* src = static_cast<const uint8_t*>(a.codes) +
+                       static_cast<size_t>(p.row) * (a.groups * (G * mx_bits(FMT) / 8)) + p.grp * (G * mx_bits(FMT) / 8);
+  const uint8_t byte = static_cast<const uint8_t*>(a.scales)[mx_scale_at(p.row, p.grp >> 2, a.ktiles) + (p.grp & 3)];
+  uint32_t w[G * mx_bits(FMT) / 32];
+  if constexpr (FMT == kMxNvfp4) {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < G * mx_bits(FMT) / 128; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  }
+  const float s = FMT == kMxNvfp4 ? e4m3_value(byte) * a.g : e8m0_value(byte);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + p.row * a.x_stride) + p.grp * C;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float v[8];
+    mx_values8<FMT>(FMT == kMxFp8 ? make_uint2(w[2 * c], w[2 * c + 1]) : make_uint2(w[c], 0), v);
+    dst[c] = make_uint4(pack_bf16x2(v[0] * s, v[1] * s), pack_bf16x2(v[2] * s, v[3] * s),
+                        pack_bf16x2(v[4] * s, v[5] * s), pack_bf16x2(v[6] * s, v[7] * s));
+  }
+}
+
+// The residual add and RMSNorm of rowops.cu (one CTA a row, the row in registers), its output quantised: a thread has
+// chunks of 8 elements, 2 or 4 lanes a group.  The norm's fp32 result is quantised as it is, without a rounding to bf16
+// before.
+template <int FMT, int MAXC>
+__global__ void __launch_bounds__(kThreads) k_add_rmsnorm_mx(const MxNormArgs a) {
+  constexpr int L = mx_group(FMT) / 8;  // lanes a group
+  __shared__ float red[kThreads / 32];
+  pdl_wait();
+  const int row = blockIdx.x, nch = a.cols >> 3;
+  const size_t base = static_cast<size_t>(row) * nch;
+  const uint4* x = static_cast<const uint4*>(a.x) + base;
+  const uint4* res = static_cast<const uint4*>(a.res_in) + base;
+  float v[MAXC][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < MAXC; ++c) {
+    const int i = threadIdx.x + c * kThreads;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
+    if (i < nch) {
+      unpack8(x[i], v[c]);
+      if (a.res_in != nullptr) {
+        float r[8];
+        unpack8(res[i], r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[c][e] += r[e];
+      }
+      // the new residual is a bf16 tensor; the norm is taken of that tensor
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[c][e] = round_bf16(v[c][e]);
+        ss += v[c][e] * v[c][e];
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
+  __syncthreads();
+  ss = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) ss += red[w];
+  const float inv = rsqrtf(ss / static_cast<float>(a.cols) + a.eps);
+  uint4* res_out = static_cast<uint4*>(a.res_out) + base;
+  uint8_t* codes = static_cast<uint8_t*>(a.codes) + base * mx_bits(FMT);
+#pragma unroll
+  for (int c = 0; c < MAXC; ++c) {
+    const int i = threadIdx.x + c * kThreads;
+    if (c * kThreads >= nch) break;  // the same for the whole CTA
+    const bool there = i < nch;
+    float h[8];
+    uint32_t top = 0;
+    if (there) {
+      if (a.res_out != nullptr)
+        res_out[i] = make_uint4(pack_bf16x2(v[c][0], v[c][1]), pack_bf16x2(v[c][2], v[c][3]),
+                                pack_bf16x2(v[c][4], v[c][5]), pack_bf16x2(v[c][6], v[c][7]));
+      float g[8];
+      unpack8(static_cast<const uint4*>(a.gamma)[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[e] = v[c][e] * inv * g[e];
+        top = max(top, abs_bits(h[e]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = 0.f;
+    }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const MxScale s = mx_scale<FMT, false>(top, a.sixth, a.inv_g);
+    if (there) {
+      const uint2 w = mx_codes8<FMT, false>(h, s.factor);
+      if constexpr (FMT == kMxFp8) reinterpret_cast<uint2*>(codes)[i] = w;
+      else reinterpret_cast<uint32_t*>(codes)[i] = w.x;
+    }
+    // the scale bytes of 4 L lanes
+    uint32_t word = (there ? s.byte : 0u) << ((threadIdx.x / L & 3) * 8);
+#pragma unroll
+    for (int o = L; o < 4 * L; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+    if (there && (threadIdx.x & (4 * L - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) + mx_scale_at(row, i / (4 * L), a.ktiles)) = word;
+  }
+}
+
+template <int FMT>
+int norm_typed(const MxNormArgs& a, cudaStream_t s) {
+  const int per = (a.cols / 8 + kThreads - 1) / kThreads;
+  auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(a.rows), dim3(kThreads), 0, s, true, a); };
+  if (per <= 1) return go(k_add_rmsnorm_mx<FMT, 1>);
+  if (per <= 2) return go(k_add_rmsnorm_mx<FMT, 2>);
+  if (per <= 4) return go(k_add_rmsnorm_mx<FMT, 4>);
+  if (per <= 8) return go(k_add_rmsnorm_mx<FMT, 8>);
+  return cudaErrorInvalidValue;
+}
+
+unsigned group_ctas(const MxRowsArgs& a) {
+  const long long n = static_cast<long long>(a.rows) * a.ktiles * kMxTileGroups;
+  return static_cast<unsigned>((n + kThreads - 1) / kThreads);
+}
+
+}  // namespace
+
+int quantize_mx_launch(int fmt, const MxRowsArgs& a, cudaStream_t s) {
+  auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(group_ctas(a)), dim3(kThreads), 0, s, true, a); };
+  return fmt == kMxNvfp4 ? go(k_quantize_mx<kMxNvfp4>) : fmt == kMxFp4 ? go(k_quantize_mx<kMxFp4>) : go(k_quantize_mx<kMxFp8>);
+}
+
+int dequantize_mx_launch(int fmt, const MxRowsArgs& a, cudaStream_t s) {
+  auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(group_ctas(a)), dim3(kThreads), 0, s, true, a); };
+  return fmt == kMxNvfp4 ? go(k_dequantize_mx<kMxNvfp4>)
+         : fmt == kMxFp4 ? go(k_dequantize_mx<kMxFp4>)
+                         : go(k_dequantize_mx<kMxFp8>);
+}
+
+int add_rmsnorm_mx_launch(int fmt, const MxNormArgs& a, cudaStream_t s) {
+  return fmt == kMxNvfp4 ? norm_typed<kMxNvfp4>(a, s) : fmt == kMxFp4 ? norm_typed<kMxFp4>(a, s) : norm_typed<kMxFp8>(a, s);
+}
+
+}  // namespace llama
