@@ -437,52 +437,56 @@ int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, c
  * with a NaN or an infinity gets a NaN scale and reads back as NaN; its row's
  * products are NaN and no other row's.  The pages have no counterpart: they keep
  * the model's type throughout. */
-enum { LLAMA_MX_BF16 = 0, LLAMA_MX_NVFP4 = 1, LLAMA_MX_FP4 = 2, LLAMA_MX_FP8 = 3 };
+enum { LLAMA_MX_NVFP4 = 1, LLAMA_MX_FP4 = 2, LLAMA_MX_FP8 = 3 };
+typedef struct {
+  int format;   /* LLAMA_MX_NVFP4, LLAMA_MX_FP4 or LLAMA_MX_FP8 */
+  int rows;
+  int cols;
+  float g;      /* 1 unless the format is nvfp4 */
+  void* codes;  /* llama_mx_code_bytes() */
+  void* scales; /* llama_mx_scale_bytes() */
+} LlamaMxMatrix;
 size_t llama_mx_code_bytes(int format, int rows, int cols);   /* 0 for an unsupported matrix */
 size_t llama_mx_scale_bytes(int format, int rows, int cols);  /* 0 for an unsupported matrix */
 
-/* x [rows, cols] bf16, x_stride elements from row to row (a multiple of 8, at
- * least cols), quantised.  The result is that of the exact quotients. */
-int llama_quantize_mx(int format, const void* x, int64_t x_stride, int rows, int cols, float g, void* codes,
-                      void* scales, llama_stream_t stream);
+/* x [out->rows, out->cols] bf16, x_stride elements from row to row (a multiple
+ * of 8, at least cols), quantised into out.  The result is that of the exact
+ * quotients. */
+int llama_quantize_mx(const void* x, int64_t x_stride, const LlamaMxMatrix* out, llama_stream_t stream);
 
-/* The values of a matrix as bf16, to y [rows, cols] with the given stride:
- * exact (values below bf16's smallest, 2^-133, are rounded). */
-int llama_dequantize_mx(int format, const void* codes, const void* scales, int rows, int cols, float g, void* y,
-                        int64_t y_stride, llama_stream_t stream);
+/* The values of a matrix as bf16, to y [m->rows, m->cols] with the given
+ * stride: exact (values below bf16's smallest, 2^-133, are rounded). */
+int llama_dequantize_mx(const LlamaMxMatrix* m, void* y, int64_t y_stride, llama_stream_t stream);
 
 /* llama_fused_add_rmsnorm with its output quantised: r = bf16(x (+ residual_in));
- * r / sqrt(mean(r^2) + eps) * gamma, per row of length H, goes to codes and
- * scales.  The norm's fp32 result is quantised without a rounding to bf16
- * before.  residual_out may be NULL or alias x / residual_in.  H is a multiple
- * of 32 up to 16384. */
-int llama_fused_add_rmsnorm_mx(int format, const void* x, const void* residual_in, void* residual_out, void* codes,
-                               void* scales, float g, const void* gamma, int rows, int H, float eps,
-                               llama_stream_t stream);
+ * r / sqrt(mean(r^2) + eps) * gamma, for every row of x [out->rows, out->cols],
+ * goes to out.  The norm's fp32 result is quantised without a rounding to bf16
+ * before.  residual_out may be NULL or alias x / residual_in.  cols is a
+ * multiple of 32 up to 16384. */
+int llama_fused_add_rmsnorm_mx(const void* x, const void* residual_in, void* residual_out, const LlamaMxMatrix* out,
+                               const void* gamma, float eps, llama_stream_t stream);
 
-/* y[M, N] = alpha x[M, K] w[N, K]^T for microscaled x and w of one format, their
- * codes and scales; alpha holds the matrices' g's (g_x * g_w, and any other
- * factor).  y bf16 (out_fp32 = 0) or fp32, rounded once from fp32 sums.  K is a
- * multiple of 32, N of 8.  A result does not depend on M or on other rows, but
- * for the order of its sums: with few tiles K is split over several SMs, in a
- * fixed order, so a call repeats bit for bit.  The workspace
- * (llama_linear_mx_workspace_size) is the call's while it runs. */
-int llama_linear_mx(int format, const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
-                    int M, int N, int K, float alpha, void* y, int out_fp32, void* workspace, size_t workspace_bytes,
-                    llama_stream_t stream);
+/* y[M, N] = alpha g_x g_w x w^T for codes and scales of x [M, K] and w [N, K] of
+ * one format (their g's are in the product, and alpha is any other factor).  y
+ * bf16 (out_fp32 = 0) or fp32, rounded once from fp32 sums.  N is a multiple of
+ * 8.  No row of y depends on another row of x, but M decides how K is split over
+ * SMs (few tiles), and so the order of the sums; that order is fixed, so a call
+ * repeats bit for bit.  The workspace (llama_linear_mx_workspace_size) is the
+ * call's while it runs. */
+int llama_linear_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* w, float alpha, void* y, int out_fp32,
+                    void* workspace, size_t workspace_bytes, llama_stream_t stream);
 size_t llama_linear_mx_workspace_size(void);
 
-/* a[M, I] = silu(alpha_gate x w_gate^T) * (alpha_up x w_up^T), the gate_up
- * projection with SiluAndMul in its epilogue, for microscaled x [M, K] and w_gate,
- * w_up [I, K] of one format (two matrices, so that either's scales begin a
- * tile).  a is bf16 (out_format LLAMA_MX_BF16; out_scales NULL, I a multiple of 8)
- * or a microscaled matrix, for the down projection to read: codes to a, scales
- * to out_scales, with out_g (I a multiple of 32).  The fp32 sums are rounded once,
- * at the end. */
-int llama_gate_up_silu_mx(int format, const void* x_codes, const void* x_scales, const void* gate_codes,
-                          const void* gate_scales, const void* up_codes, const void* up_scales, int M, int I, int K,
-                          float alpha_gate, float alpha_up, int out_format, float out_g, void* a, void* out_scales,
-                          void* workspace, size_t workspace_bytes, llama_stream_t stream);
+/* a[M, I] = silu(x gate^T) * (x up^T), the gate_up projection with SiluAndMul in
+ * its epilogue, for x [M, K] and gate, up [I, K] of one format (two matrices, so
+ * that either's scales begin a tile), each product times its matrices' g's and
+ * alpha_gate or alpha_up.  Either y, bf16 [M, I] (I a multiple of 8), or out, a
+ * matrix [M, I] of any format for the down projection to read (I a multiple of
+ * 32), is given and the other NULL.  The fp32 results are rounded once, at the
+ * end. */
+int llama_gate_up_silu_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* gate, const LlamaMxMatrix* up, float alpha_gate,
+                          float alpha_up, void* y, const LlamaMxMatrix* out, void* workspace, size_t workspace_bytes,
+                          llama_stream_t stream);
 
 /* Sampling beyond greedy ([LLAMA-70B] Sampler, sample(): temperature scaling,
  * the top-k / top-p sampler, greedy rows below a temperature threshold, the

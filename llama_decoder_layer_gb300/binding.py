@@ -27,7 +27,6 @@ LLAMA_ERR_DEVICE_GUARD = 5
 LLAMA_ERR_TIMEOUT = 6
 LLAMA_ERR_SCRATCH_LIMIT = 7
 
-LLAMA_MX_BF16 = 0
 LLAMA_MX_NVFP4 = 1
 LLAMA_MX_FP4 = 2
 LLAMA_MX_FP8 = 3
@@ -79,9 +78,14 @@ class LlamaQkNormRopeConfig(ctypes.Structure):
                 ("rs_original_max_pos", ctypes.c_int), ("rs_attention_factor", ctypes.c_float)]
 
 
+class LlamaMxMatrix(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("g", ctypes.c_float),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
 # every entry point of include/llama_layer.h with its C signature
 _VP, _I, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
-_I64 = ctypes.c_int64
+_I64, _P_MX = ctypes.c_int64, ctypes.POINTER(LlamaMxMatrix)
 _P_CFG, _P_W, _P_B = ctypes.POINTER(LlamaLayerConfig), ctypes.POINTER(LlamaLayerWeights), ctypes.POINTER(LlamaBatch)
 SIGNATURES = {
     "llama_workspace_size": (_SZ, [_P_CFG, _I, _I, _I, _I]),
@@ -105,13 +109,12 @@ SIGNATURES = {
                                 _I64, _VP, _I64, _VP]),
     "llama_mx_code_bytes": (_SZ, [_I, _I, _I]),
     "llama_mx_scale_bytes": (_SZ, [_I, _I, _I]),
-    "llama_quantize_mx": (_I, [_I, _VP, _I64, _I, _I, _F, _VP, _VP, _VP]),
-    "llama_dequantize_mx": (_I, [_I, _VP, _VP, _I, _I, _F, _VP, _I64, _VP]),
-    "llama_fused_add_rmsnorm_mx": (_I, [_I, _VP, _VP, _VP, _VP, _VP, _F, _VP, _I, _I, _F, _VP]),
-    "llama_linear_mx": (_I, [_I, _VP, _VP, _VP, _VP, _I, _I, _I, _F, _VP, _I, _VP, _SZ, _VP]),
+    "llama_quantize_mx": (_I, [_VP, _I64, _P_MX, _VP]),
+    "llama_dequantize_mx": (_I, [_P_MX, _VP, _I64, _VP]),
+    "llama_fused_add_rmsnorm_mx": (_I, [_VP, _VP, _VP, _P_MX, _VP, _F, _VP]),
+    "llama_linear_mx": (_I, [_P_MX, _P_MX, _F, _VP, _I, _VP, _SZ, _VP]),
     "llama_linear_mx_workspace_size": (_SZ, []),
-    "llama_gate_up_silu_mx": (_I, [_I, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _F, _F, _I, _F, _VP, _VP, _VP, _SZ,
-                                   _VP]),
+    "llama_gate_up_silu_mx": (_I, [_P_MX, _P_MX, _P_MX, _F, _F, _VP, _P_MX, _VP, _SZ, _VP]),
     "llama_get_device_error": (_I, [_VP, ctypes.POINTER(ctypes.c_int)]),
     "llama_status_string": (ctypes.c_char_p, [_I]),
     "llama_num_sms": (_I, []),
@@ -517,22 +520,25 @@ def qk_norm_rope(cfg: QkNormRopeConfig, q_norm: Optional[torch.Tensor], k_norm: 
 class MxMatrix:
     """A microscaled matrix [rows, cols]: its format (LLAMA_MX_NVFP4, _FP4 or
     _FP8), its codes [rows, bytes of a row] and scales, both uint8, and its factor
-    g (``scale``, a power of two; 1 but for LLAMA_MX_NVFP4); see the header.  The
-    tensors are the caller's."""
+    g (``scale``, a power of two; 1 but for LLAMA_MX_NVFP4); see the header.  It
+    holds the caller's tensors, which keep their memory (no resize_ or set_) while
+    it lives."""
 
-    __slots__ = ("format", "rows", "cols", "codes", "scales", "scale", "device")
+    __slots__ = ("format", "rows", "cols", "codes", "scales", "scale", "shape", "index", "c", "ref")
 
     def __init__(self, format: int, cols: int, codes: torch.Tensor, scales: torch.Tensor, scale: float = 1.0):
         where = "MxMatrix"
-        rows = int(codes.shape[0])
+        rows = int(codes.shape[0]) if codes.dim() == 2 else -1
         n = lib().llama_mx_scale_bytes(format, rows, cols)
-        if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or codes.dim() != 2 or
+        if (rows < 0 or codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or
                 not codes.is_contiguous() or not scales.is_contiguous() or codes.device != scales.device or
                 (n == 0 and rows > 0) or codes.numel() != lib().llama_mx_code_bytes(format, rows, cols) or
                 scales.numel() < n):
             raise LlamaError(LLAMA_ERR_ARG, where)
-        self.format, self.rows, self.cols = format, rows, cols
-        self.codes, self.scales, self.scale, self.device = codes, scales, float(scale), codes.device
+        self.format, self.rows, self.cols, self.shape = format, rows, cols, (rows, cols)
+        self.codes, self.scales, self.scale, self.index = codes, scales, float(scale), codes.get_device()
+        self.c = LlamaMxMatrix(format, rows, cols, self.scale, codes.data_ptr(), scales.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
     @staticmethod
     def empty(format: int, rows: int, cols: int, scale: float = 1.0, device="cuda") -> "MxMatrix":
@@ -544,19 +550,28 @@ class MxMatrix:
         return MxMatrix(format, cols, torch.empty(rows, cols if format == LLAMA_MX_FP8 else cols // 2, **u8),
                         torch.empty(int(lib().llama_mx_scale_bytes(format, rows, cols)), **u8), scale)
 
+    def get_device(self) -> int:
+        return self.index
 
-def _check_here(where: str, *things) -> None:
-    """Tensors (and matrices) on the current CUDA device, where the call runs."""
+
+def _mx_stream(where: str, stream, *things) -> Optional[int]:
+    """The stream's handle, once every tensor and matrix is known to be on the
+    current CUDA device, where the call runs."""
     for t in things:
-        if t is not None and (t.device.type != "cuda" or t.device.index != torch._C._cuda_getDevice()):
+        if t.get_device() < 0:
             raise LlamaError(LLAMA_ERR_ARG, where)
+    here = torch._C._cuda_getDevice()
+    for t in things:
+        if t.get_device() != here:
+            raise LlamaError(LLAMA_ERR_ARG, where)
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
 
 
-def _rows_bf16(t: torch.Tensor, shape, where: str) -> int:
+def _row_stride(t: torch.Tensor, shape, where: str) -> int:
     """Elements from one row to the next of t [rows, cols] bf16, whose rows are dense."""
-    if t.dtype is torch.bfloat16 and t.dim() == 2 and t.shape == shape:
+    if t.dtype is torch.bfloat16 and t.shape == shape:
         row, col = t.stride()
-        if col == 1 or shape[1] == 1:
+        if col == 1:
             return row if shape[0] > 1 else shape[1]
     raise LlamaError(LLAMA_ERR_ARG, where)
 
@@ -565,10 +580,9 @@ def quantize_mx(x: torch.Tensor, out: MxMatrix, stream=None) -> None:
     """x [rows, cols] bf16 (any stride between rows) quantised into out; see
     llama_quantize_mx in the header."""
     where = "llama_quantize_mx"
-    stride = _rows_bf16(x, (out.rows, out.cols), where)
-    _check_here(where, x, out)
-    st = lib().llama_quantize_mx(out.format, x.data_ptr(), stride, out.rows, out.cols, out.scale, out.codes.data_ptr(),
-                                 out.scales.data_ptr(), _stream(stream))
+    stride = _row_stride(x, out.shape, where)
+    s = _mx_stream(where, stream, x, out)
+    st = lib().llama_quantize_mx(x.data_ptr(), stride, out.ref, s)
     if st:
         raise LlamaError(st, where)
 
@@ -577,10 +591,9 @@ def dequantize_mx(m: MxMatrix, out: torch.Tensor, stream=None) -> None:
     """The values of m as bf16, into out [rows, cols] (any stride between
     rows); see llama_dequantize_mx in the header."""
     where = "llama_dequantize_mx"
-    stride = _rows_bf16(out, (m.rows, m.cols), where)
-    _check_here(where, m, out)
-    st = lib().llama_dequantize_mx(m.format, m.codes.data_ptr(), m.scales.data_ptr(), m.rows, m.cols, m.scale,
-                                   out.data_ptr(), stride, _stream(stream))
+    stride = _row_stride(out, m.shape, where)
+    s = _mx_stream(where, stream, m, out)
+    st = lib().llama_dequantize_mx(m.ref, out.data_ptr(), stride, s)
     if st:
         raise LlamaError(st, where)
 
@@ -590,16 +603,15 @@ def fused_add_rmsnorm_mx(x: torch.Tensor, residual_in: Optional[torch.Tensor], r
     """fused_add_rmsnorm with the normed rows quantised into out; see
     llama_fused_add_rmsnorm_mx in the header."""
     where = "llama_fused_add_rmsnorm_mx"
-    shape = (out.rows, out.cols)
-    for t in (x, residual_in, residual_out):
-        if t is not None and (t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_contiguous()):
+    rows = [t for t in (x, residual_in, residual_out) if t is not None]
+    for t in rows:
+        if t.dtype is not torch.bfloat16 or t.shape != out.shape or not t.is_contiguous():
             raise LlamaError(LLAMA_ERR_ARG, where)
     if gamma.dtype is not torch.bfloat16 or gamma.numel() != out.cols or not gamma.is_contiguous():
         raise LlamaError(LLAMA_ERR_ARG, where)
-    _check_here(where, x, residual_in, residual_out, out, gamma)
-    st = lib().llama_fused_add_rmsnorm_mx(out.format, x.data_ptr(), _ptr(residual_in), _ptr(residual_out),
-                                          out.codes.data_ptr(), out.scales.data_ptr(), out.scale, gamma.data_ptr(),
-                                          out.rows, out.cols, eps, _stream(stream))
+    s = _mx_stream(where, stream, out, gamma, *rows)
+    st = lib().llama_fused_add_rmsnorm_mx(x.data_ptr(), _ptr(residual_in), _ptr(residual_out), out.ref,
+                                          gamma.data_ptr(), eps, s)
     if st:
         raise LlamaError(st, where)
 
@@ -614,14 +626,13 @@ def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, workspace: torch.Tens
     """out [M, N] (bf16 or fp32) = alpha x w^T for x [M, K] and w [N, K] of one
     format; see llama_linear_mx in the header."""
     where = "llama_linear_mx"
-    if (w.format != x.format or w.cols != x.cols or out.shape != (x.rows, w.rows) or not out.is_contiguous() or
-            out.dtype not in (torch.bfloat16, torch.float32) or workspace.dtype is not torch.uint8):
+    dtype = out.dtype
+    if (out.shape != (x.rows, w.rows) or not out.is_contiguous() or workspace.dtype is not torch.uint8 or
+            not workspace.is_contiguous() or (dtype is not torch.bfloat16 and dtype is not torch.float32)):
         raise LlamaError(LLAMA_ERR_ARG, where)
-    _check_here(where, x, w, out, workspace)
-    st = lib().llama_linear_mx(x.format, x.codes.data_ptr(), x.scales.data_ptr(), w.codes.data_ptr(),
-                               w.scales.data_ptr(), x.rows, w.rows, x.cols, alpha * (x.scale * w.scale),
-                               out.data_ptr(), 1 if out.dtype is torch.float32 else 0, workspace.data_ptr(),
-                               workspace.numel(), _stream(stream))
+    s = _mx_stream(where, stream, x, w, out, workspace)
+    st = lib().llama_linear_mx(x.ref, w.ref, alpha, out.data_ptr(), 1 if dtype is torch.float32 else 0,
+                               workspace.data_ptr(), workspace.numel(), s)
     if st:
         raise LlamaError(st, where)
 
@@ -632,20 +643,18 @@ def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, workspace: t
     up [I, K] of one format; out a bf16 tensor [M, I] or an MxMatrix; see
     llama_gate_up_silu_mx in the header."""
     where = "llama_gate_up_silu_mx"
-    mx = isinstance(out, MxMatrix)
-    if (gate.format != x.format or up.format != x.format or gate.cols != x.cols or up.cols != x.cols or
-            up.rows != gate.rows or workspace.dtype is not torch.uint8 or
-            ((out.rows, out.cols) if mx else out.shape) != (x.rows, gate.rows) or
-            (not mx and (out.dtype is not torch.bfloat16 or not out.is_contiguous()))):
+    y, to = None, None
+    if isinstance(out, MxMatrix):
+        to = out.ref
+    elif out.dtype is torch.bfloat16 and out.is_contiguous():
+        y = out.data_ptr()
+    else:
         raise LlamaError(LLAMA_ERR_ARG, where)
-    _check_here(where, x, gate, up, out, workspace)
-    to = (out.format, out.scale, out.codes.data_ptr(), out.scales.data_ptr()) if mx else (
-        LLAMA_MX_BF16, 1.0, out.data_ptr(), None)
-    st = lib().llama_gate_up_silu_mx(x.format, x.codes.data_ptr(), x.scales.data_ptr(), gate.codes.data_ptr(),
-                                     gate.scales.data_ptr(), up.codes.data_ptr(), up.scales.data_ptr(), x.rows,
-                                     gate.rows, x.cols, alpha_gate * (x.scale * gate.scale),
-                                     alpha_up * (x.scale * up.scale), *to, workspace.data_ptr(), workspace.numel(),
-                                     _stream(stream))
+    if out.shape != (x.rows, gate.rows) or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    s = _mx_stream(where, stream, x, gate, up, out, workspace)
+    st = lib().llama_gate_up_silu_mx(x.ref, gate.ref, up.ref, alpha_gate, alpha_up, y, to, workspace.data_ptr(),
+                                     workspace.numel(), s)
     if st:
         raise LlamaError(st, where)
 

@@ -719,8 +719,8 @@ int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, c
   return cuda_status(qk_norm_rope_launch(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// Whether a matrix of a format is one, and its scale tiles along a row.
-static int check_mx(int format, int rows, int cols) {
+// Whether there is a matrix of this format and size.
+static int check_mx_size(int format, int rows, int cols) {
   if (format < LLAMA_MX_NVFP4 || format > LLAMA_MX_FP8 || rows < 0 || cols < 1) return LLAMA_ERR_ARG;
   if (cols % 32) return LLAMA_ERR_UNSUPPORTED;
   // groups are counted in 32 bits on the device
@@ -730,171 +730,168 @@ static int check_mx(int format, int rows, int cols) {
 
 static int mx_ktiles(int format, int cols) { return (cols / mx_group(format) + kMxTileGroups - 1) / kMxTileGroups; }
 
-// g of a matrix: a power of two for nvfp4, 1 for the others
-static bool mx_factor_ok(int format, float g) { return format == LLAMA_MX_NVFP4 ? q4_scale_ok(g) : g == 1.f; }
+// A matrix's description; g: a power of two for nvfp4, 1 for the others.  (Its arrays: mx_arrays.)
+static int check_mx(const LlamaMxMatrix* m) {
+  if (m == nullptr) return LLAMA_ERR_ARG;
+  const int st = check_mx_size(m->format, m->rows, m->cols);
+  if (st) return st;
+  return (m->format == LLAMA_MX_NVFP4 ? q4_scale_ok(m->g) : m->g == 1.f) ? LLAMA_OK : LLAMA_ERR_ARG;
+}
+static int mx_arrays(const LlamaMxMatrix* m) {
+  if (!m->codes || !m->scales) return LLAMA_ERR_ARG;
+  return a16(m->codes) && a16(m->scales) ? LLAMA_OK : LLAMA_ERR_UNSUPPORTED;
+}
 
 size_t llama_mx_code_bytes(int format, int rows, int cols) {
-  if (check_mx(format, rows, cols)) return 0;
+  if (check_mx_size(format, rows, cols)) return 0;
   return static_cast<size_t>(rows) * (cols / 8 * mx_bits(format));
 }
 
 size_t llama_mx_scale_bytes(int format, int rows, int cols) {
-  if (check_mx(format, rows, cols)) return 0;
+  if (check_mx_size(format, rows, cols)) return 0;
   return static_cast<size_t>((rows + kMxTileRows - 1) / kMxTileRows) * mx_ktiles(format, cols) * kMxTileBytes;
 }
 
-// The checks that quantising and reading back share; fills the arguments.
-static int mx_rows_args(int format, const void* v, int64_t stride, int rows, int cols, float g, const void* codes,
-                        const void* scales, MxRowsArgs* a) {
-  const int st = check_mx(format, rows, cols);
-  if (st) return st;
-  if (!mx_factor_ok(format, g)) return LLAMA_ERR_ARG;
-  if (rows == 0) return LLAMA_OK;
-  if (!v || !codes || !scales || stride < cols) return LLAMA_ERR_ARG;
-  if (stride % 8 || !a16(v) || !a16(codes) || !a16(scales)) return LLAMA_ERR_UNSUPPORTED;
+// The checks that quantising and reading back share; fills the arguments (v: the bf16 rows).
+static int mx_rows_args(const LlamaMxMatrix* m, const void* v, int64_t stride, MxRowsArgs* a) {
+  int st = check_mx(m);
+  if (st || m->rows == 0) return st;
+  if (!v || stride < m->cols) return LLAMA_ERR_ARG;
+  if ((st = mx_arrays(m))) return st;
+  if (stride % 8 || !a16(v)) return LLAMA_ERR_UNSUPPORTED;
   a->x_stride = stride;
-  a->rows = rows;
-  a->groups = cols / mx_group(format);
-  a->ktiles = mx_ktiles(format, cols);
-  a->g = g;
-  a->inv_g = 1.f / g;
+  a->codes = m->codes;
+  a->scales = m->scales;
+  a->rows = m->rows;
+  a->groups = m->cols / mx_group(m->format);
+  a->ktiles = mx_ktiles(m->format, m->cols);
+  a->g = m->g;
+  a->inv_g = 1.f / m->g;
   a->sixth = a->inv_g * (1.f / 6.f);
   return LLAMA_OK;
 }
 
-int llama_quantize_mx(int format, const void* x, int64_t x_stride, int rows, int cols, float g, void* codes,
-                      void* scales, llama_stream_t stream) {
+int llama_quantize_mx(const void* x, int64_t x_stride, const LlamaMxMatrix* out, llama_stream_t stream) {
   MxRowsArgs a{};
-  const int st = mx_rows_args(format, x, x_stride, rows, cols, g, codes, scales, &a);
-  if (st || rows == 0) return st;
+  const int st = mx_rows_args(out, x, x_stride, &a);
+  if (st || out->rows == 0) return st;
   a.x = x;
-  a.codes = codes;
-  a.scales = scales;
-  return cuda_status(quantize_mx_launch(format, a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(quantize_mx_launch(out->format, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int llama_dequantize_mx(int format, const void* codes, const void* scales, int rows, int cols, float g, void* y,
-                        int64_t y_stride, llama_stream_t stream) {
+int llama_dequantize_mx(const LlamaMxMatrix* m, void* y, int64_t y_stride, llama_stream_t stream) {
   MxRowsArgs a{};
-  const int st = mx_rows_args(format, y, y_stride, rows, cols, g, codes, scales, &a);
-  if (st || rows == 0) return st;
+  const int st = mx_rows_args(m, y, y_stride, &a);
+  if (st || m->rows == 0) return st;
   a.y = y;
-  a.codes = const_cast<void*>(codes);
-  a.scales = const_cast<void*>(scales);
-  return cuda_status(dequantize_mx_launch(format, a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(dequantize_mx_launch(m->format, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int llama_fused_add_rmsnorm_mx(int format, const void* x, const void* residual_in, void* residual_out, void* codes,
-                               void* scales, float g, const void* gamma, int rows, int H, float eps,
-                               llama_stream_t stream) {
-  const int st = check_mx(format, rows, H);
+int llama_fused_add_rmsnorm_mx(const void* x, const void* residual_in, void* residual_out, const LlamaMxMatrix* out,
+                               const void* gamma, float eps, llama_stream_t stream) {
+  int st = check_mx(out);
   if (st) return st;
-  if (!(eps >= 0.f) || !mx_factor_ok(format, g)) return LLAMA_ERR_ARG;
-  if (H > 16384) return LLAMA_ERR_UNSUPPORTED;
-  if (rows == 0) return LLAMA_OK;
-  if (!x || !codes || !scales || !gamma) return LLAMA_ERR_ARG;
-  if (!a16(x) || !a16(codes) || !a16(scales) || !a16(gamma) || (residual_in && !a16(residual_in)) ||
-      (residual_out && !a16(residual_out)))
+  if (!(eps >= 0.f)) return LLAMA_ERR_ARG;
+  if (out->cols > 16384) return LLAMA_ERR_UNSUPPORTED;
+  if (out->rows == 0) return LLAMA_OK;
+  if (!x || !gamma) return LLAMA_ERR_ARG;
+  if ((st = mx_arrays(out))) return st;
+  if (!a16(x) || !a16(gamma) || (residual_in && !a16(residual_in)) || (residual_out && !a16(residual_out)))
     return LLAMA_ERR_UNSUPPORTED;
   MxNormArgs a{};
   a.x = x;
   a.res_in = residual_in;
   a.gamma = gamma;
   a.res_out = residual_out;
-  a.codes = codes;
-  a.scales = scales;
-  a.rows = rows;
-  a.cols = H;
-  a.ktiles = mx_ktiles(format, H);
+  a.codes = out->codes;
+  a.scales = out->scales;
+  a.rows = out->rows;
+  a.cols = out->cols;
+  a.ktiles = mx_ktiles(out->format, out->cols);
   a.eps = eps;
-  a.inv_g = 1.f / g;
+  a.inv_g = 1.f / out->g;
   a.sixth = a.inv_g * (1.f / 6.f);
-  return cuda_status(add_rmsnorm_mx_launch(format, a, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(add_rmsnorm_mx_launch(out->format, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t llama_linear_mx_workspace_size(void) { return gemm_mx_partials_bytes(num_sms()) + 256; }
 
-// The checks that the two products share (of w, `n_w` matrices).
-static int check_mx_product(int format, int M, int N, int K, const MxOperand& x, const MxOperand* w, int n_w,
-                            const float* alpha) {
-  int st = check_mx(format, M, K);
-  if (!st) st = check_mx(format, N, K);
+// The checks that the two products share, of x and the matrices w[0 .. n) that it is multiplied with, each product times
+// alpha[i]; fills the arguments.
+static int mx_product_args(const LlamaMxMatrix* x, const LlamaMxMatrix* const* w, int n, const float* alpha,
+                           MxGemmArgs* g) {
+  int st = check_mx(x);
+  for (int i = 0; !st && i < n; ++i) st = check_mx(w[i]);
   if (st) return st;
-  if (N < 1) return LLAMA_ERR_ARG;
-  for (int i = 0; i < n_w; ++i)
-    if (!(fabsf(alpha[i]) < INFINITY)) return LLAMA_ERR_ARG;
-  if (M == 0) return LLAMA_OK;
-  if (!x.codes || !x.scales) return LLAMA_ERR_ARG;
-  for (int i = 0; i < n_w; ++i)
-    if (!w[i].codes || !w[i].scales) return LLAMA_ERR_ARG;
-  if (!a16(x.codes) || !a16(x.scales)) return LLAMA_ERR_UNSUPPORTED;
-  for (int i = 0; i < n_w; ++i)
-    if (!a16(w[i].codes) || !a16(w[i].scales)) return LLAMA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n; ++i) {
+    if (w[i]->format != x->format || w[i]->cols != x->cols || w[i]->rows != w[0]->rows || w[i]->rows < 1)
+      return LLAMA_ERR_ARG;
+    g->alpha[i] = static_cast<float>(static_cast<double>(alpha[i]) * x->g * w[i]->g);
+    if (!(fabsf(g->alpha[i]) < INFINITY)) return LLAMA_ERR_ARG;
+  }
+  if (w[0]->rows % 8) return LLAMA_ERR_UNSUPPORTED;
   // output tiles are counted in 32 bits
-  if (static_cast<long long>((M + 127LL) / 128) * ((N + 127LL) / 128) > 0x3fffffffLL) return LLAMA_ERR_UNSUPPORTED;
+  if (((x->rows + 127LL) / 128) * ((w[0]->rows + 127LL) / 128) > 0x3fffffffLL) return LLAMA_ERR_UNSUPPORTED;
+  if (x->rows == 0) return LLAMA_OK;
+  if ((st = mx_arrays(x))) return st;
+  for (int i = 0; i < n; ++i)
+    if ((st = mx_arrays(w[i]))) return st;
+  g->fmt = x->format;
+  g->x = {x->codes, x->scales};
+  for (int i = 0; i < n; ++i) g->w[i] = {w[i]->codes, w[i]->scales};
+  g->M = x->rows;
+  g->N = w[0]->rows;
+  g->K = x->cols;
   return LLAMA_OK;
 }
 
-static int mx_product(MxGemmArgs& g, void* workspace, llama_stream_t stream) {
+static int mx_product(MxGemmArgs& g, void* workspace, size_t workspace_bytes, llama_stream_t stream) {
+  if (workspace == nullptr || workspace_bytes < llama_linear_mx_workspace_size()) return LLAMA_ERR_WORKSPACE;
   g.partials = reinterpret_cast<float*>(ws_base(workspace));
   g.partials_bytes = gemm_mx_partials_bytes(num_sms());
   g.err = device_error_word();
   return cuda_status(gemm_mx_launch(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int llama_linear_mx(int format, const void* x_codes, const void* x_scales, const void* w_codes, const void* w_scales,
-                    int M, int N, int K, float alpha, void* y, int out_fp32, void* workspace, size_t workspace_bytes,
-                    llama_stream_t stream) {
+int llama_linear_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* w, float alpha, void* y, int out_fp32,
+                    void* workspace, size_t workspace_bytes, llama_stream_t stream) {
   MxGemmArgs g{};
-  g.fmt = format;
-  g.x = {x_codes, x_scales};
-  g.w[0] = {w_codes, w_scales};
-  g.alpha[0] = alpha;
-  const int st = check_mx_product(format, M, N, K, g.x, g.w, 1, g.alpha);
-  if (st || M == 0) return st;
+  const int st = mx_product_args(x, &w, 1, &alpha, &g);
+  if (st || x->rows == 0) return st;
   if (!y) return LLAMA_ERR_ARG;
-  if (N % 8 || !a16(y)) return LLAMA_ERR_UNSUPPORTED;
-  if (workspace == nullptr || workspace_bytes < llama_linear_mx_workspace_size()) return LLAMA_ERR_WORKSPACE;
-  g.M = M;
-  g.N = N;
-  g.K = K;
+  if (!a16(y)) return LLAMA_ERR_UNSUPPORTED;
   g.out = y;
   g.out_f32 = out_fp32 != 0;
-  return mx_product(g, workspace, stream);
+  return mx_product(g, workspace, workspace_bytes, stream);
 }
 
-int llama_gate_up_silu_mx(int format, const void* x_codes, const void* x_scales, const void* gate_codes,
-                          const void* gate_scales, const void* up_codes, const void* up_scales, int M, int I, int K,
-                          float alpha_gate, float alpha_up, int out_format, float out_g, void* a, void* out_scales,
-                          void* workspace, size_t workspace_bytes, llama_stream_t stream) {
+int llama_gate_up_silu_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* gate, const LlamaMxMatrix* up, float alpha_gate,
+                          float alpha_up, void* y, const LlamaMxMatrix* out, void* workspace, size_t workspace_bytes,
+                          llama_stream_t stream) {
   MxGemmArgs g{};
-  g.fmt = format;
-  g.x = {x_codes, x_scales};
-  g.w[0] = {gate_codes, gate_scales};
-  g.w[1] = {up_codes, up_scales};
-  g.alpha[0] = alpha_gate;
-  g.alpha[1] = alpha_up;
-  if (out_format < LLAMA_MX_BF16 || out_format > LLAMA_MX_FP8) return LLAMA_ERR_ARG;
-  const int st = check_mx_product(format, M, I, K, g.x, g.w, 2, g.alpha);
+  const LlamaMxMatrix* w[2] = {gate, up};
+  const float alpha[2] = {alpha_gate, alpha_up};
+  int st = mx_product_args(x, w, 2, alpha, &g);
   if (st) return st;
-  if (out_format == LLAMA_MX_BF16 ? out_scales != nullptr : !mx_factor_ok(out_format, out_g)) return LLAMA_ERR_ARG;
-  if (I % 8 || (out_format != LLAMA_MX_BF16 && check_mx(out_format, M, I))) return LLAMA_ERR_UNSUPPORTED;
-  if (M == 0) return LLAMA_OK;
-  if (!a || (out_format != LLAMA_MX_BF16 && !out_scales)) return LLAMA_ERR_ARG;
-  if (!a16(a) || (out_scales && !a16(out_scales))) return LLAMA_ERR_UNSUPPORTED;
-  if (workspace == nullptr || workspace_bytes < llama_linear_mx_workspace_size()) return LLAMA_ERR_WORKSPACE;
-  g.M = M;
-  g.N = I;
-  g.K = K;
-  g.silu = true;
-  g.out_fmt = out_format;
-  g.out = a;
-  g.out_scales = out_scales;
-  if (out_format != LLAMA_MX_BF16) {
-    g.out_inv_g = 1.f / out_g;
-    g.out_sixth = g.out_inv_g * (1.f / 6.f);
+  if (out != nullptr) {
+    if ((st = check_mx(out))) return st;
+    if (y != nullptr || out->rows != x->rows || out->cols != gate->rows) return LLAMA_ERR_ARG;
   }
-  return mx_product(g, workspace, stream);
+  if (x->rows == 0) return LLAMA_OK;
+  if (out != nullptr) {
+    if ((st = mx_arrays(out))) return st;
+    g.out_fmt = out->format;
+    g.out = out->codes;
+    g.out_scales = out->scales;
+    g.out_inv_g = 1.f / out->g;
+    g.out_sixth = g.out_inv_g * (1.f / 6.f);
+  } else {
+    if (!y) return LLAMA_ERR_ARG;
+    if (!a16(y)) return LLAMA_ERR_UNSUPPORTED;
+    g.out = y;
+  }
+  g.silu = true;
+  return mx_product(g, workspace, workspace_bytes, stream);
 }
 
 int llama_sample(const float* logits, int rows, int vocab, const float* temperature, const int32_t* top_k,

@@ -167,7 +167,7 @@ __device__ __forceinline__ void epilogue_unit(const MxGemmParams& p, int row, in
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
       const float g = v[e] * p.alpha[0];
-      v[e] = g / (1.0f + __expf(-g)) * (up[e] * p.alpha[1]);
+      v[e] = g / (1.0f + expf(-g)) * (up[e] * p.alpha[1]);
     }
   } else {
 #pragma unroll

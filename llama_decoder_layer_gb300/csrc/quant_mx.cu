@@ -1,6 +1,8 @@
 // Microscaled matrices (the formats are in mx.cuh): quantising bf16 rows,
 // reading them back, and the fused residual add + RMSNorm whose output is
 // quantised, for a product of microscaled matrices to read.
+#include <math.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -171,7 +173,11 @@ __global__ void __launch_bounds__(kThreads) k_add_rmsnorm_mx(const MxNormArgs a)
   ss = 0.f;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) ss += red[w];
-  const float inv = rsqrtf(ss / static_cast<float>(a.cols) + a.eps);
+  // 1 / sqrt(y) = inv + low: the residual 1 - y inv^2, with the product's rounding, halved, so that the results below
+  // are off by little more than their own rounding (codes near a border then fall where they should)
+  const float y = ss / static_cast<float>(a.cols) + a.eps;
+  const float inv = rsqrtf(y), yi = y * inv;
+  const float low = yi < INFINITY ? 0.5f * inv * (fmaf(-yi, inv, 1.f) - fmaf(y, inv, -yi) * inv) : 0.f;
   uint4* res_out = static_cast<uint4*>(a.res_out) + base;
   uint8_t* codes = static_cast<uint8_t*>(a.codes) + base * mx_bits(FMT);
 #pragma unroll
@@ -189,7 +195,8 @@ __global__ void __launch_bounds__(kThreads) k_add_rmsnorm_mx(const MxNormArgs a)
       unpack8(static_cast<const uint4*>(a.gamma)[i], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[e] = v[c][e] * inv * g[e];
+        const float vg = v[c][e] * g[e];  // exact: 8 and 8 bits
+        h[e] = fmaf(vg, inv, vg * low);
         top = max(top, abs_bits(h[e]));
       }
     } else {

@@ -1,6 +1,7 @@
 """Microscaled matrices without a GPU: the layout, the 64-bit reference on
 hand-worked rows, and every refusal on the host."""
 
+import ctypes
 import math
 
 import numpy as np
@@ -72,72 +73,72 @@ def test_sizes(lib):
     assert lb.linear_mx_workspace_size() > 0
 
 
-def _rows_call(lib, write, **kw):
-    a = dict(fmt=R.NVFP4, x=FAKE, stride=64, rows=4, cols=64, g=1.0, codes=FAKE, scales=FAKE)
-    a.update(kw)
-    if write:
-        return lib.llama_quantize_mx(a["fmt"], a["x"], a["stride"], a["rows"], a["cols"], a["g"], a["codes"],
-                                     a["scales"], None)
-    return lib.llama_dequantize_mx(a["fmt"], a["codes"], a["scales"], a["rows"], a["cols"], a["g"], a["x"],
-                                   a["stride"], None)
+def matrix(fmt=R.NVFP4, rows=4, cols=64, g=1.0, codes=FAKE, scales=FAKE):
+    return ctypes.byref(lb.LlamaMxMatrix(fmt, rows, cols, g, codes, scales))
+
+
+BAD_MATRICES = (dict(fmt=0), dict(fmt=4), dict(rows=-1), dict(cols=0), dict(codes=None), dict(scales=None),
+                dict(g=0.0), dict(g=-1.0), dict(g=3.0), dict(g=math.inf), dict(g=math.nan), dict(g=2.0 ** 33),
+                dict(g=2.0 ** -33), dict(fmt=R.FP4, g=2.0), dict(fmt=R.FP8, g=0.5))
+UNSUPPORTED_MATRICES = (dict(cols=48), dict(cols=8), dict(codes=FAKE + 4), dict(scales=FAKE + 8), dict(rows=1 << 30))
 
 
 @pytest.mark.parametrize("write", [True, False])
 def test_quantise_and_read_back_are_refused_on_the_host(lib, write):
-    for kw in (dict(fmt=0), dict(fmt=4), dict(x=None), dict(codes=None), dict(scales=None), dict(rows=-1), dict(cols=0),
-               dict(stride=56), dict(stride=-64), dict(g=0.0), dict(g=-1.0), dict(g=3.0), dict(g=math.inf),
-               dict(g=math.nan), dict(g=2.0 ** 33), dict(g=2.0 ** -33), dict(fmt=R.FP4, g=2.0), dict(fmt=R.FP8, g=0.5)):
-        assert _rows_call(lib, write, **kw) == ARG, kw
-    for kw in (dict(cols=48), dict(cols=8), dict(stride=68), dict(x=FAKE + 8), dict(codes=FAKE + 4),
-               dict(scales=FAKE + 8), dict(rows=1 << 30)):
-        assert _rows_call(lib, write, **kw) == UNSUP, kw
-    assert _rows_call(lib, write, rows=0, x=None, codes=None, scales=None) == lb.LLAMA_OK
+    def call(x=FAKE, stride=64, m=None, **kw):
+        m = matrix(**kw) if m is None else m
+        return lib.llama_quantize_mx(x, stride, m, None) if write else lib.llama_dequantize_mx(m, x, stride, None)
+    for kw in BAD_MATRICES + (dict(x=None), dict(stride=56), dict(stride=-64)):
+        assert call(**kw) == ARG, kw
+    for kw in UNSUPPORTED_MATRICES[2:4] + (dict(cols=48), dict(stride=68), dict(x=FAKE + 8)):
+        assert call(**kw) == UNSUP, kw
+    null = ctypes.POINTER(lb.LlamaMxMatrix)()
+    assert call(m=null) == ARG
+    assert call(rows=0, x=None, codes=None, scales=None) == lb.LLAMA_OK
 
 
 def test_norm_is_refused_on_the_host(lib):
-    def call(**kw):
-        a = dict(fmt=R.FP8, x=FAKE, res=FAKE, out=FAKE, codes=FAKE, scales=FAKE, g=1.0, gamma=FAKE, rows=4, H=64, eps=1e-5)
-        a.update(kw)
-        return lib.llama_fused_add_rmsnorm_mx(a["fmt"], a["x"], a["res"], a["out"], a["codes"], a["scales"], a["g"],
-                                              a["gamma"], a["rows"], a["H"], a["eps"], None)
-    for kw in (dict(fmt=0), dict(fmt=7), dict(x=None), dict(codes=None), dict(scales=None), dict(gamma=None),
-               dict(rows=-1), dict(H=0), dict(eps=-1.0), dict(eps=math.nan), dict(g=2.0), dict(fmt=R.NVFP4, g=5.0)):
+    def call(x=FAKE, res=FAKE, out=FAKE, gamma=FAKE, eps=1e-5, **kw):
+        return lib.llama_fused_add_rmsnorm_mx(x, res, out, matrix(**kw), gamma, eps, None)
+    for kw in BAD_MATRICES + (dict(x=None), dict(gamma=None), dict(eps=-1.0), dict(eps=math.nan)):
         assert call(**kw) == ARG, kw
-    for kw in (dict(H=48), dict(H=16416), dict(x=FAKE + 2), dict(res=FAKE + 8), dict(out=FAKE + 8),
-               dict(codes=FAKE + 8), dict(scales=FAKE + 4), dict(gamma=FAKE + 8)):
+    for kw in UNSUPPORTED_MATRICES + (dict(cols=16416), dict(x=FAKE + 2), dict(res=FAKE + 8), dict(out=FAKE + 8),
+                                      dict(gamma=FAKE + 8)):
         assert call(**kw) == UNSUP, kw
     assert call(rows=0, x=None, codes=None, scales=None, gamma=None) == lb.LLAMA_OK
 
 
 def test_products_are_refused_on_the_host(lib):
-    def linear(**kw):
-        a = dict(fmt=R.NVFP4, xc=FAKE, xs=FAKE, wc=FAKE, ws=FAKE, M=4, N=64, K=64, alpha=1.0, y=FAKE, f32=0, work=FAKE,
-                 n=1 << 40)
-        a.update(kw)
-        return lib.llama_linear_mx(a["fmt"], a["xc"], a["xs"], a["wc"], a["ws"], a["M"], a["N"], a["K"], a["alpha"],
-                                   a["y"], a["f32"], a["work"], a["n"], None)
+    def linear(x={}, w={}, alpha=1.0, y=FAKE, work=FAKE, n=1 << 40):
+        return lib.llama_linear_mx(matrix(**x), matrix(**{"rows": 8, **w}), alpha, y, 0, work, n, None)
 
-    def silu(**kw):
-        a = dict(fmt=R.NVFP4, xc=FAKE, xs=FAKE, wc=FAKE, ws=FAKE, uc=FAKE, us=FAKE, M=4, N=64, K=64, alpha=1.0, beta=1.0,
-                 of=0, og=1.0, y=FAKE, os=None, work=FAKE, n=1 << 40)
-        a.update(kw)
-        return lib.llama_gate_up_silu_mx(a["fmt"], a["xc"], a["xs"], a["wc"], a["ws"], a["uc"], a["us"], a["M"], a["N"],
-                                         a["K"], a["alpha"], a["beta"], a["of"], a["og"], a["y"], a["os"], a["work"],
-                                         a["n"], None)
+    def silu(x={}, w={}, alpha=1.0, y=FAKE, work=FAKE, n=1 << 40, up={}, beta=1.0, out=None):
+        size = {"rows": 8, "cols": w.get("cols", 64), **{k: w[k] for k in ("rows", "fmt") if k in w}}
+        out = None if out is None else matrix(**{"fmt": R.FP8, "rows": 4, "cols": 8, **out})
+        return lib.llama_gate_up_silu_mx(matrix(**x), matrix(**{"rows": 8, **w}), matrix(**{**size, **up}), alpha, beta, y,
+                                         out, work, n, None)
     for call in (linear, silu):
-        for kw in (dict(fmt=0), dict(fmt=4), dict(xc=None), dict(xs=None), dict(wc=None), dict(ws=None), dict(M=-1),
-                   dict(N=0), dict(K=0), dict(alpha=math.nan), dict(alpha=math.inf), dict(y=None)):
+        for kw in BAD_MATRICES:
+            assert call(x=kw) == ARG and call(w=kw) == ARG, kw
+        for kw in (dict(x=dict(cols=96)), dict(w=dict(fmt=R.FP4)), dict(w=dict(rows=0)), dict(alpha=math.nan),
+                   dict(alpha=math.inf), dict(alpha=3e38, x=dict(g=4.0)), dict(y=None)):
             assert call(**kw) == ARG, kw
-        for kw in (dict(K=48), dict(N=60), dict(xc=FAKE + 8), dict(xs=FAKE + 8), dict(wc=FAKE + 8), dict(ws=FAKE + 4),
-                   dict(y=FAKE + 8)):
+        for kw in UNSUPPORTED_MATRICES:
+            assert call(x=kw) == UNSUP and call(w=kw) == UNSUP, kw
+        for kw in (dict(w=dict(rows=12)), dict(y=FAKE + 8)):
             assert call(**kw) == UNSUP, kw
         assert call(work=None) == WS and call(n=16) == WS
-        assert call(M=0, xc=None, xs=None, wc=None, ws=None, y=None, work=None) == lb.LLAMA_OK
-    for kw in (dict(uc=None), dict(us=None), dict(beta=math.nan), dict(of=-1), dict(of=4), dict(os=FAKE),
-               dict(of=R.FP8), dict(of=R.FP8, os=FAKE, og=2.0), dict(of=R.NVFP4, os=FAKE, og=3.0)):
-        assert silu(**kw) == ARG, kw
-    for kw in (dict(uc=FAKE + 8), dict(us=FAKE + 8), dict(of=R.FP8, os=FAKE, N=72), dict(of=R.FP8, os=FAKE + 8)):
-        assert silu(**kw) == UNSUP, kw
+        assert call(x=dict(rows=0, codes=None, scales=None), y=None, work=None) == lb.LLAMA_OK
+    for kw in BAD_MATRICES + (dict(fmt=R.FP8), dict(rows=16), dict(cols=96)):
+        assert silu(up=kw) == ARG, kw
+    assert silu(beta=math.nan) == ARG
+    w32 = dict(rows=32)
+    for kw in (dict(fmt=0), dict(rows=5), dict(cols=64), dict(g=2.0), dict(codes=None)):
+        assert silu(w=w32, y=None, out={"cols": 32, **kw}) == ARG, kw
+    assert silu(w=w32, out=dict(cols=32)) == ARG  # y and out
+    for kw in (dict(codes=FAKE + 8), dict(scales=FAKE + 8)):
+        assert silu(w=w32, y=None, out={"cols": 32, **kw}) == UNSUP, kw
+    assert silu(w=dict(rows=40), y=None, out=dict(cols=40)) == UNSUP
 
 
 def test_binding_refuses_what_is_not_a_matrix():
