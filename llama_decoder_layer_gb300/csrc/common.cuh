@@ -229,6 +229,21 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// one lane of a converged warp (always the same one)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// lane 0's value, known to be the same in every lane (operands computed from such values can stay in uniform registers,
+// where the tensor-core instructions take them from)
+__device__ __forceinline__ bool warp_same(bool v) { return __shfl_sync(0xffffffffu, v ? 1 : 0, 0) != 0; }
+
 // ---------------------------------------------------------------------------
 // TMA
 // ---------------------------------------------------------------------------

@@ -57,13 +57,28 @@ struct Stage {
   static constexpr bool kE8m0 = FMT != kMxNvfp4;
 };
 
+// Tensor maps: codes in boxes of 128 rows x 128 bytes, swizzled; scales in boxes of a stage's tiles of 128 rows, as
+// 8-byte elements.  What lies outside reads as zero.
+struct MxMaps {
+  CUtensorMap x, x_scales, w[2], w_scales[2];
+};
+constexpr int kScaleElems = kMxTileBytes / 8;  // of a scale tile
+
+template <int EPI>
+__device__ __forceinline__ void prefetch_maps(const MxMaps& m) {
+  tma_prefetch_desc(&m.x);
+  tma_prefetch_desc(&m.x_scales);
+#pragma unroll
+  for (int i = 0; i < (is_silu(EPI) ? 2 : 1); ++i) {
+    tma_prefetch_desc(&m.w[i]);
+    tma_prefetch_desc(&m.w_scales[i]);
+  }
+}
+
 struct MxGemmParams {
-  int M, N, kb;             // kb: stages along K
-  int last_steps;           // MMAs of the last one
-  int ktiles, w_tiles;      // scale tiles along K, and row tiles of w
+  int M, N, kb;    // kb: stages along K
+  int last_steps;  // MMAs of the last one
   int tiles_m, tiles_n, tiles, group_m;
-  int stages;
-  const uint8_t *x_scales, *w_scales[2];
   float alpha[2];
   void* out;
   uint8_t* out_scales;
@@ -152,28 +167,22 @@ __device__ __forceinline__ void store_codes32(const MxGemmParams& p, int row, in
     reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
 }
 
-// Columns [32 u, 32 u + 32) of the tile's outputs (silu: NB / 2 of them).  ld(column, v) returns 32 accumulator columns of
-// the thread's row; it is called by whole warps.
-template <int EPI, int NB, class Loader>
-__device__ __forceinline__ void epilogue_unit(const MxGemmParams& p, int row, int tn, int u, const Loader& ld,
-                                              uint32_t (&words)[2]) {
-  const int n = tn * (is_silu(EPI) ? NB / 2 : NB) + 32 * u;
-  if (n >= p.N) return;
-  float v[32];
-  ld(32 * u, v);
+// 32 results of a row at output column n, from the accumulators v (silu: gate) and up.
+template <int EPI>
+__device__ __forceinline__ void finish32(const MxGemmParams& p, int row, int n, float (&v)[32], const float* up,
+                                         uint32_t (&words)[2]) {
+  if (row >= p.M || n >= p.N) return;
   if constexpr (is_silu(EPI)) {
-    float up[32];
-    ld(NB / 2 + 32 * u, up);
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
       const float g = v[e] * p.alpha[0];
-      v[e] = g / (1.0f + expf(-g)) * (up[e] * p.alpha[1]);
+      // (the quotient by an instruction's reciprocal: 2 units in the last place; 0 where exp is beyond 2^126)
+      v[e] = __fdividef(g, 1.0f + __expf(-g)) * (up[e] * p.alpha[1]);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] *= p.alpha[0];
   }
-  if (row >= p.M) return;
   if constexpr (out_fmt(EPI) != 0) {
     store_codes32<out_fmt(EPI)>(p, row, n, v, words);
   } else if constexpr (EPI == kMxF32) {
@@ -203,22 +212,68 @@ __device__ __forceinline__ void store_words(const MxGemmParams& p, int row, int 
       *reinterpret_cast<uint32_t*>(p.out_scales + mx_scale_at(row, tn * kWords + i, p.out_ktiles)) = words[i];
 }
 
-struct TmemLoader {
-  uint32_t taddr;
-  __device__ __forceinline__ void operator()(int col, float (&v)[32]) const { tmem_ld32(taddr + col, v); }
-};
+// The whole 256-column tile of one row (a thread), from its accumulator at taddr.  release() is called once the 64 columns
+// shared with the other accumulator (this one's last if it is the first, its first if the second) are in registers.
+template <int EPI, class Release>
+__device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, int row, int tn, uint32_t taddr, int acc,
+                                              const Release& release) {
+  const bool any = row - (threadIdx.x & 31) < p.M;  // a warp whose rows are all past M has nothing to do
+  uint32_t words[2] = {0, 0};
+  float keep[2][32];
+  const int shared = acc == 0 ? 192 : 0;
+  if (any) {
+    tmem_ld32(taddr + shared, keep[0]);
+    tmem_ld32(taddr + shared + 32, keep[1]);
+  }
+  release();
+  if (!any) return;
+  if constexpr (is_silu(EPI)) {
+    // outputs 32 u: gate columns 32 u, up columns 128 + 32 u; kept: up of u = 2, 3 or gate of u = 0, 1
+    const int n0 = tn * 128;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int u = acc == 0 ? 2 + i : i;
+      float other[32];
+      tmem_ld32(taddr + 32 * u + (acc == 0 ? 0 : 128), other);
+      if (acc == 0) {
+        finish32<EPI>(p, row, n0 + 32 * u, other, keep[i], words);
+      } else {
+        finish32<EPI>(p, row, n0 + 32 * u, keep[i], other, words);
+      }
+    }
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const int u = acc == 0 ? i : 2 + i;
+      if (n0 + 32 * u >= p.N) break;
+      tmem_ld32(taddr + 32 * u, keep[0]);
+      tmem_ld32(taddr + 128 + 32 * u, keep[1]);
+      finish32<EPI>(p, row, n0 + 32 * u, keep[0], keep[1], words);
+    }
+    if constexpr (out_fmt(EPI) != 0) store_words<EPI>(p, row, tn, words);
+  } else {
+    const int n0 = tn * 256;
+    finish32<EPI>(p, row, n0 + shared, keep[0], nullptr, words);
+    finish32<EPI>(p, row, n0 + shared + 32, keep[1], nullptr, words);
+#pragma unroll 1
+    for (int i = 0; i < 6; ++i) {
+      const int c = acc == 0 ? 32 * i : 64 + 32 * i;
+      if (n0 + c >= p.N) break;
+      tmem_ld32(taddr + c, keep[0]);
+      finish32<EPI>(p, row, n0 + c, keep[0], nullptr, words);
+    }
+  }
+}
 
 // ---------------------------------------------------------------------------
 // Persistent, one CTA an SM, whole tiles in a grouped raster.
 // ---------------------------------------------------------------------------
 template <int FMT, int EPI, int NB>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_gemm_mx(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-              const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ MxGemmParams p) {
+    k_gemm_mx(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
   using S = Stage<FMT>;
   using R = Ring<FMT, NB>;
   using T = Tmem<FMT, NB>;
-  static_assert(!is_silu(EPI) || NB == 256, "SiLU tiles hold 128 gate and 128 up columns");
+  static_assert(NB == 256, "the epilogue takes 256 columns");
   constexpr int nst = R::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -235,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * nst + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (2 * nst + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < nst; ++s) {
       mbar_init(full_bar(s), 1);
@@ -248,9 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB0);
-    if (is_silu(EPI)) tma_prefetch_desc(&tmB1);
+    prefetch_maps<EPI>(maps);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -259,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();
 
   if (warp == 0) {
@@ -280,22 +333,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
           const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
-          const int kt = kb * S::kTiles;
-          const uint32_t bytes = min(S::kTiles, p.ktiles - kt) * kMxTileBytes;  // of the scales of 128 rows
-          int pieces = 1;  // 128-row pieces of w that are there
-          if (NB == 256 && (is_silu(EPI) || 2 * tn + 1 < p.w_tiles)) pieces = 2;
-          mbar_arrive_expect_tx(full_bar(stage), R::kA + R::kB + bytes * (1 + pieces));
-          tma_load_2d(sa, &tmA, full_bar(stage), kb * kRowBytes, tm * BM, pol_a);
-          bulk_load(ssa, p.x_scales + (static_cast<size_t>(tm) * p.ktiles + kt) * kMxTileBytes, bytes, full_bar(stage), pol_a);
+          const int kx = kb * S::kTiles * kScaleElems;
+          mbar_arrive_expect_tx(full_bar(stage), R::kBytes);
+          tma_load_2d(sa, &maps.x, full_bar(stage), kb * kRowBytes, tm * BM, pol_a);
+          tma_load_2d(ssa, &maps.x_scales, full_bar(stage), kx, tm, pol_a);
 #pragma unroll
           for (int i = 0; i < NB / 128; ++i) {
             const int rt = is_silu(EPI) ? tn : tn * (NB / 128) + i;  // 128 rows of w
-            tma_load_2d(sb + i * 128 * kRowBytes, is_silu(EPI) && i ? &tmB1 : &tmB0, full_bar(stage), kb * kRowBytes, rt * 128,
-                        pol_b);
-            if (i < pieces)
-              bulk_load(ssb + i * R::kSa,
-                        p.w_scales[is_silu(EPI) ? i : 0] + (static_cast<size_t>(rt) * p.ktiles + kt) * kMxTileBytes, bytes,
-                        full_bar(stage), pol_b);
+            const int w = is_silu(EPI) ? i : 0;
+            tma_load_2d(sb + i * 128 * kRowBytes, &maps.w[w], full_bar(stage), kb * kRowBytes, rt * 128, pol_b);
+            tma_load_2d(ssb + i * R::kSa, &maps.w_scales[w], full_bar(stage), kx, rt, pol_b);
           }
         }
         __syncwarp();
@@ -327,19 +374,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // NB 256: the other accumulator's shared columns have been read; else: all of this one
       const int wait_acc = NB == 256 ? acc ^ 1 : acc;
       const uint32_t wait_phase = NB == 256 ? (acc ? acc_phase : acc_phase ^ 1u) : acc_phase ^ 1u;
-      if (!mbar_wait(tempty_bar(wait_acc), wait_phase, abort_flag)) {
+      if (!warp_same(mbar_wait(tempty_bar(wait_acc), wait_phase, abort_flag))) {
         ok = false;
         break;
       }
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc * T::kAcc;
       for (int kb = 0; kb < p.kb; ++kb) {
-        if (!mbar_wait(full_bar(stage), phase, abort_flag)) {
+        if (!warp_same(mbar_wait(full_bar(stage), phase, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
           const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
 #pragma unroll
@@ -361,16 +408,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_base + T::kSb + (NB / 128) * 4 * i, kb > 0 || k > 0 ? 1u : 0u);
           }
           tc_commit(empty_bar(stage));
-          issued = true;
         }
         __syncwarp();
+        issued = true;
         if (++stage == nst) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) break;
-      if (lane == 0) tc_commit(tfull_bar(acc));
+      if (elect_one()) tc_commit(tfull_bar(acc));
       __syncwarp();
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
@@ -380,14 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       *abort_flag = 1;
     }
     // all MMAs and copies this thread issued must finish before tensor memory is freed
-    if (lane == 0 && issued) tc_commit(drain_bar);
+    if (issued && elect_one()) tc_commit(drain_bar);
     __syncwarp();
-    if (__shfl_sync(0xffffffffu, issued ? 1 : 0, 0)) mbar_wait(drain_bar, 0, nullptr);
+    if (issued) mbar_wait(drain_bar, 0, nullptr);
   } else {
     // ---------------- epilogue ----------------
     const int quad = warp & 3;  // tensor-memory lane quarter this warp may access
-    constexpr int kUnits = (is_silu(EPI) ? NB / 2 : NB) / 32;
-    constexpr int kShared = NB == 256 ? kUnits / (is_silu(EPI) ? 2 : 4) : kUnits;  // units that touch shared columns
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -399,21 +444,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const int row = tm * BM + quad * 32 + lane;
-      const TmemLoader ld{tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc};
-      uint32_t words[2] = {0, 0};
-      // the first accumulator's shared columns are its last, the second's its first
-      const int first = NB == 256 && acc == 0 ? kUnits - kShared : 0;
-#pragma unroll 1
-      for (int i = 0; i < kUnits; ++i) {
-        epilogue_unit<EPI, NB>(p, row, tn, (first + i) % kUnits, ld, words);
-        if (i == kShared - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tempty_bar(acc));
-        }
-      }
-      if constexpr (out_fmt(EPI) != 0) store_words<EPI>(p, row, tn, words);
+      epilogue_tile<EPI>(p, tm * BM + quad * 32 + lane, tn,
+                         tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc, acc, [&]() {
+                           tc_fence_before();
+                           __syncwarp();
+                           if (lane == 0) mbar_arrive(tempty_bar(acc));
+                         });
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -427,6 +463,228 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+}
+
+// ---------------------------------------------------------------------------
+// Persistent on SM pairs (2-CTA clusters): tiles of 256 x 256, MMAs with M = 256.  CTA r has rows 128 r .. of the tile's x
+// and half of its columns of w (silu: gate on rank 0, up on rank 1) in its shared memory, the scales of its x rows and of
+// all columns, and the accumulator of its rows, so that an SM loads 32 KB of codes where one alone loads 48.
+// Both CTAs' copies complete on rank 0's full barriers; one thread of rank 0 issues copies of scales and MMAs for both, and
+// commits to both CTAs' barriers.
+// ---------------------------------------------------------------------------
+template <int FMT>
+struct PairRing {
+  static constexpr int kA = BM * kRowBytes, kB = 128 * kRowBytes;
+  static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = 2 * kSa;
+  static constexpr int kBytes = kA + kB + kSa + kSb;  // of a stage, a CTA
+  static constexpr int kStages = kRingBudget / kBytes < kMaxStages ? kRingBudget / kBytes : kMaxStages;
+  static constexpr int kSmem = kStages * kBytes + 2048;
+};
+
+template <int FMT, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gemm_mx_pair(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
+  using S = Stage<FMT>;
+  using R = PairRing<FMT>;
+  using T = Tmem<FMT, 256>;
+  constexpr int nst = R::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  const uint32_t sbase = raw_addr + pad;
+  const uint32_t scales = sbase + nst * (R::kA + R::kB);
+  uint8_t* meta = smem_raw + pad + nst * R::kBytes;
+  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull[2], tempty[2], drain
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * nst + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * nst + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * nst + 4);
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1);
+  // this CTA and its peer stop waiting once either of them gives up
+  auto give_up = [&]() {
+    *abort_flag = 1;
+    st_cluster_u32(peer_abort, 1u);
+  };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 8);  // the four epilogue warps of each CTA
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_maps<EPI>(maps);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  pdl_wait();
+  const int npairs = static_cast<int>(gridDim.x) >> 1, first = static_cast<int>(blockIdx.x) >> 1;
+
+  if (warp == 0) {
+    // ---------------- copies (both CTAs) ----------------
+    const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_first();
+    int stage = 0;
+    uint32_t phase = 0;
+    long long used = 0;
+    bool ok = true;
+    for (int t = first; ok && t < p.tiles; t += npairs) {
+      int tm, tn;
+      tile_coords(p, t, tm, tn);
+      const int xt = 2 * tm + rank;                          // this CTA's 128 rows of x
+      const int w = is_silu(EPI) ? rank : 0;
+      const int wt = is_silu(EPI) ? tn : 2 * tn + rank;      // and of w
+      for (int kb = 0; kb < p.kb; ++kb) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
+          const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
+          const uint32_t fb = mapa_shared(full_bar(stage), 0);
+          const int kx = kb * S::kTiles * kScaleElems;
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * R::kBytes);
+          tma_load_2d_pair(sa, &maps.x, fb, kb * kRowBytes, xt * 128, pol_a);
+          tma_load_2d_pair(sb, &maps.w[w], fb, kb * kRowBytes, wt * 128, pol_b);
+          tma_load_2d_pair(ssa, &maps.x_scales, fb, kx, xt, pol_a);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            tma_load_2d_pair(ssb + i * R::kSa, &maps.w_scales[is_silu(EPI) ? i : 0], fb, kx, is_silu(EPI) ? tn : 2 * tn + i,
+                             pol_b);
+        }
+        __syncwarp();
+        ++used;
+        if (++stage == nst) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0) pdl_trigger();
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmProducer);
+      give_up();
+    }
+    // rank 0's full barriers count both CTAs' bytes: after their last phases every copy has landed
+    if (rank == 0)
+      for (int s = 0; s < nst; ++s) {
+        const long long uses = (used - s + nst - 1) / nst;
+        if (uses > 0) mbar_wait(full_bar(s), static_cast<uint32_t>(uses - 1) & 1u, nullptr);
+      }
+  } else if (warp == 1) {
+    // ---------------- MMAs (rank 0) ----------------
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_mx(2 * BM, 256, S::kBits, S::kE8m0);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = first; ok && t < p.tiles; t += npairs) {
+        if (!warp_same(mbar_wait(tempty_bar(acc ^ 1), acc ? acc_phase : acc_phase ^ 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * T::kAcc;
+        for (int kb = 0; kb < p.kb; ++kb) {
+          if (!warp_same(mbar_wait(full_bar(stage), phase, abort_flag))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
+            const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
+#pragma unroll
+            for (int i = 0; i < S::kTiles; ++i) {
+              tc_copy_scales<true>(tmem_base + T::kSa + 4 * i, smem_desc_scales(ssa + i * kMxTileBytes));
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                tc_copy_scales<true>(tmem_base + T::kSb + 8 * i + 4 * j, smem_desc_scales(ssb + j * R::kSa + i * kMxTileBytes));
+            }
+            const int steps = kb + 1 < p.kb ? S::kSteps : p.last_steps;
+#pragma unroll
+            for (int k = 0; k < S::kSteps; ++k) {
+              if (k >= steps) break;
+              const int i = k / S::kPerTile;
+              tc_mma_mx<S::kBits, S::kStepScales, true>(d_tmem, smem_desc_sw128(sa + 32 * k), smem_desc_sw128(sb + 32 * k),
+                                                        idesc_mx_scale(idesc, k % S::kPerTile * S::kStepScales),
+                                                        tmem_base + T::kSa + 4 * i, tmem_base + T::kSb + 8 * i,
+                                                        kb > 0 || k > 0 ? 1u : 0u);
+            }
+            tc_commit_pair(empty_bar(stage), 3);
+          }
+          __syncwarp();
+          if (++stage == nst) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) tc_commit_pair(tfull_bar(acc), 3);
+        __syncwarp();
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!ok) {
+        if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmMma);
+        give_up();
+      }
+      // completes in both CTAs once everything issued above has
+      if (elect_one()) tc_commit_pair(drain_bar, 3);
+      __syncwarp();
+    }
+    // no CTA frees tensor memory that the pair's MMAs may still write
+    mbar_wait(drain_bar, 0, nullptr);
+  } else {
+    // ---------------- epilogue (both CTAs, their own rows) ----------------
+    const int quad = warp & 3;
+    const uint32_t tempty_lead = mapa_shared(tempty_bar(0), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int t = first; t < p.tiles; t += npairs) {
+      int tm, tn;
+      tile_coords(p, t, tm, tn);
+      if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      epilogue_tile<EPI>(p, (2 * tm + rank) * BM + quad * 32 + lane, tn,
+                         tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc, acc, [&]() {
+                           tc_fence_before();
+                           __syncwarp();
+                           if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * acc);
+                         });
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
+      give_up();
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync();  // no CTA leaves while its peer may still signal its barriers
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, kTmemCols);
 }
 
 // ---------------------------------------------------------------------------
@@ -449,26 +707,83 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [rows, row_bytes] bytes in boxes of box_rows x 128 bytes, 128-byte swizzle; bytes out of range read as zero
-bool make_tmap(CUtensorMap* m, const void* base, int rows, long long row_bytes, int box_rows) {
+bool encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, long long cols, long long rows,
+               long long row_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  cuuint32_t box[2] = {kRowBytes, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int EPI, int NB>
-int launch_typed(const CUtensorMap& ta, const CUtensorMap& tb0, const CUtensorMap& tb1, const MxGemmParams& p, int grid,
-                 cudaStream_t s) {
+// the maps of one operand of `rows` rows
+bool operand_maps(CUtensorMap* codes, CUtensorMap* scales, const MxOperand& o, int rows, long long row_bytes, int ktiles,
+                  int stage_tiles) {
+  return encode_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, row_bytes, rows, row_bytes, kRowBytes, 128,
+                   CU_TENSOR_MAP_SWIZZLE_128B) &&
+         encode_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, o.scales, static_cast<long long>(ktiles) * kScaleElems,
+                   (rows + kMxTileRows - 1) / kMxTileRows, static_cast<long long>(ktiles) * kMxTileBytes,
+                   stage_tiles * kScaleElems, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <int FMT, int EPI>
+cudaError_t raise_limits() {
   static SmemLimits limits;
-  const cudaError_t e = limits.raise({smem_need(k_gemm_mx<FMT, EPI, NB>, Ring<FMT, NB>::kSmem)});
+  return limits.raise({smem_need(k_gemm_mx<FMT, EPI, 256>, Ring<FMT, 256>::kSmem),
+                       smem_need(k_gemm_mx_pair<FMT, EPI>, PairRing<FMT>::kSmem)});
+}
+
+// SM pairs that can work at once (2-CTA clusters resident); cached per device.
+template <int FMT, int EPI>
+int max_active_pairs() {
+  constexpr int kDevs = 64;
+  static std::atomic<int> cache[kDevs];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 0;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * 128);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = PairRing<FMT>::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_gemm_mx_pair<FMT, EPI>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;
+    }
+    cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n > 0 ? n : 0;
+}
+
+template <int FMT, int EPI>
+int launch_typed(const MxMaps& maps, MxGemmParams& p, cudaStream_t s) {
+  const cudaError_t e = raise_limits<FMT, EPI>();
   if (e != cudaSuccess) return e;
-  return launch_kernel(k_gemm_mx<FMT, EPI, NB>, dim3(grid), dim3(kThreads), Ring<FMT, NB>::kSmem, s, true, ta, tb0, tb1, p);
+  const int sms = num_sms();
+  p.tiles_n = is_silu(EPI) ? (p.N + 127) / 128 : (p.N + 255) / 256;
+  p.tiles_m = (p.M + BM - 1) / BM;
+  const int pairs = static_cast<long long>(p.tiles_m) * p.tiles_n > sms ? max_active_pairs<FMT, EPI>() : 0;
+  if (pairs > 0) {
+    p.tiles_m = (p.M + 2 * BM - 1) / (2 * BM);
+    p.tiles = p.tiles_m * p.tiles_n;
+    p.group_m = p.tiles_m < 12 ? p.tiles_m : 12;
+    return launch_kernel_cluster(k_gemm_mx_pair<FMT, EPI>, dim3(2 * (p.tiles < pairs ? p.tiles : pairs)), dim3(kThreads),
+                                 PairRing<FMT>::kSmem, s, true, 2, maps, p);
+  }
+  p.tiles = p.tiles_m * p.tiles_n;
+  p.group_m = p.tiles_m < 24 ? p.tiles_m : 24;
+  return launch_kernel(k_gemm_mx<FMT, EPI, 256>, dim3(p.tiles < sms ? p.tiles : sms), dim3(kThreads),
+                       Ring<FMT, 256>::kSmem, s, true, maps, p);
 }
 
 template <int FMT>
@@ -476,46 +791,33 @@ int launch_fmt(const MxGemmArgs& a, cudaStream_t s) {
   using S = Stage<FMT>;
   MxGemmParams p{};
   const long long row_bytes = static_cast<long long>(a.K) * S::kBits / 8;
+  const int ktiles = (a.K / mx_group(FMT) + kMxTileGroups - 1) / kMxTileGroups;
   p.M = a.M;
   p.N = a.N;
   p.kb = static_cast<int>((row_bytes + kRowBytes - 1) / kRowBytes);
   p.last_steps = (a.K - (p.kb - 1) * S::kElems + S::kStepElems - 1) / S::kStepElems;
-  p.ktiles = (a.K / mx_group(FMT) + kMxTileGroups - 1) / kMxTileGroups;
-  p.w_tiles = (a.N + kMxTileRows - 1) / kMxTileRows;
-  p.x_scales = static_cast<const uint8_t*>(a.x.scales);
-  for (int i = 0; i < 2; ++i) {
-    p.w_scales[i] = static_cast<const uint8_t*>(a.w[i].scales);
-    p.alpha[i] = a.alpha[i];
-  }
+  for (int i = 0; i < 2; ++i) p.alpha[i] = a.alpha[i];
   p.out = a.out;
   p.out_scales = static_cast<uint8_t*>(a.out_scales);
   if (a.out_fmt) p.out_ktiles = (a.N / mx_group(a.out_fmt) + kMxTileGroups - 1) / kMxTileGroups;
   p.out_inv_g = a.out_inv_g;
   p.out_sixth = a.out_sixth;
   p.err = a.err;
-  constexpr int NB = 256;
-  p.tiles_m = (a.M + BM - 1) / BM;
-  p.tiles_n = a.silu ? (a.N + NB / 2 - 1) / (NB / 2) : (a.N + NB - 1) / NB;
-  p.tiles = p.tiles_m * p.tiles_n;
-  p.group_m = p.tiles_m < 24 ? p.tiles_m : 24;
-  const int sms = num_sms(), grid = p.tiles < sms ? p.tiles : sms;
-  CUtensorMap ta, tb0, tb1;
-  if (!make_tmap(&ta, a.x.codes, a.M, row_bytes, BM) || !make_tmap(&tb0, a.w[0].codes, a.N, row_bytes, 128))
-    return cudaErrorInvalidValue;
-  tb1 = tb0;
-  if (a.silu && !make_tmap(&tb1, a.w[1].codes, a.N, row_bytes, 128)) return cudaErrorInvalidValue;
-  if (!a.silu)
-    return a.out_f32 ? launch_typed<FMT, kMxF32, NB>(ta, tb0, tb1, p, grid, s)
-                     : launch_typed<FMT, kMxBf16, NB>(ta, tb0, tb1, p, grid, s);
+  MxMaps maps{};
+  bool ok = operand_maps(&maps.x, &maps.x_scales, a.x, a.M, row_bytes, ktiles, S::kTiles);
+  for (int i = 0; i < (a.silu ? 2 : 1); ++i)
+    ok = ok && operand_maps(&maps.w[i], &maps.w_scales[i], a.w[i], a.N, row_bytes, ktiles, S::kTiles);
+  if (!ok) return cudaErrorInvalidValue;
+  if (!a.silu) return a.out_f32 ? launch_typed<FMT, kMxF32>(maps, p, s) : launch_typed<FMT, kMxBf16>(maps, p, s);
   switch (a.out_fmt) {
     case 0:
-      return launch_typed<FMT, kMxSilu, NB>(ta, tb0, tb1, p, grid, s);
+      return launch_typed<FMT, kMxSilu>(maps, p, s);
     case kMxNvfp4:
-      return launch_typed<FMT, kMxSiluNvfp4, NB>(ta, tb0, tb1, p, grid, s);
+      return launch_typed<FMT, kMxSiluNvfp4>(maps, p, s);
     case kMxFp4:
-      return launch_typed<FMT, kMxSiluFp4, NB>(ta, tb0, tb1, p, grid, s);
+      return launch_typed<FMT, kMxSiluFp4>(maps, p, s);
     default:
-      return launch_typed<FMT, kMxSiluFp8, NB>(ta, tb0, tb1, p, grid, s);
+      return launch_typed<FMT, kMxSiluFp8>(maps, p, s);
   }
 }
 

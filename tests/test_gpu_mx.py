@@ -241,7 +241,8 @@ def sum_slack(size, K):
 
 
 SIZES = [(1, 8, 32), (1, 256, 64), (3, 264, 96), (17, 520, 160), (128, 256, 256), (129, 392, 288), (130, 128, 512),
-         (64, 4096, 4096), (300, 1384, 2080), (513, 768, 1024), (5, 8, 14336), (1021, 520, 1376)]
+         (64, 4096, 4096), (300, 1384, 2080), (513, 768, 1024), (5, 8, 14336), (1021, 520, 1376),
+         (2500, 2056, 288), (4000, 1288, 1056)]  # more tiles than SMs: SM pairs
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -263,7 +264,8 @@ def test_linear(fmt, M, N, K, dtype):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,I,K,out_fmt", [(1, 32, 32, 0), (1, 128, 64, 3), (3, 136, 96, 0), (64, 1376, 512, 3),
                                            (130, 160, 288, 1), (77, 416, 2080, 2), (300, 1376, 512, 0),
-                                           (129, 352, 1024, 3), (64, 14336, 256, 1)])
+                                           (129, 352, 1024, 3), (64, 14336, 256, 1), (2500, 1096, 160, 0),
+                                           (2500, 1120, 544, 3), (4000, 800, 96, 1)])
 def test_gate_up_silu(fmt, M, I, K, out_fmt):
     gx, gg, gu = (2.0 ** -3, 2.0 ** -9, 2.0 ** -8) if fmt == R.NVFP4 else (1.0, 1.0, 1.0)
     (x, xv), (gate, gv), (up, uv) = (random_matrix(M, K, fmt, gx, 1), random_matrix(I, K, fmt, gg, 2),
