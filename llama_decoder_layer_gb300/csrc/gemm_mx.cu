@@ -6,13 +6,13 @@
 // each result is rounded once: to bf16, or with its row's neighbours to the
 // codes and scales of a microscaled matrix that the next product reads.
 //
-// Tiles are 128 rows of x by NB columns (rows of w).  A stage of the operand ring holds 128 bytes of every row (256 e2m1 or
-// 128 e4m3 elements, one swizzle row) and the scale tiles that belong to them; the issuing thread copies these into tensor
-// memory and then issues the stage's four MMAs, in order.
-//
-// With 256 columns two accumulators do not fit beside the scales (512 columns of tensor memory), so the second starts at
-// column 192: the MMAs of the next tile may begin once the epilogue has read the 64 columns that the two share, which it
-// reads first.
+// Two kernels: whole tiles of 256 x 256 on SM pairs (k_gemm_mx_pair), and for few tiles ones of 128 x 128 with K split over a
+// cluster (k_gemm_mx_split).  In both a stage of the operand ring holds 128 bytes of every row (256 e2m1 or 128 e4m3
+// elements, one swizzle row) and the scale tiles that belong to them; the issuing thread copies these into tensor memory and
+// then issues the stage's four MMAs, in order.  Up to sixteen instructions a stage come from that thread, so everything
+// they take is computed under control flow that is the warp's (warp_same, elect_one): their operands stay in uniform
+// registers, where moving them there from lane registers cost some 50 cycles for each (70B gate_up, 4128 rows, nvfp4: 1.18 ms
+// and then 0.59).
 #include <cuda.h>
 #include <math.h>
 
@@ -79,8 +79,10 @@ struct MxGemmParams {
   int M, N, kb;    // kb: stages along K
   int last_steps;  // MMAs of the last one
   int tiles_m, tiles_n, tiles, group_m;
+  int stages, a_rows, recv_rows;  // few tiles: the ring, its rows of x (64 if M <= 64), accumulator rows that are exchanged
   float alpha[2];
   void* out;
+  bool sectors;  // rows of out begin on 32 bytes
   uint8_t* out_scales;
   int out_ktiles;
   float out_inv_g, out_sixth;
@@ -97,37 +99,37 @@ __device__ __forceinline__ void tile_coords(const MxGemmParams& p, int tile, int
   tn = r / gm;
 }
 
-template <int FMT, int NB>
-struct Ring {
-  static constexpr int kA = BM * kRowBytes, kB = NB * kRowBytes;
-  static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = kSa * (NB / kMxTileRows);
-  static constexpr int kBytes = kA + kB + kSa + kSb;  // of a stage
-  static constexpr int kStages = kRingBudget / kBytes < kMaxStages ? kRingBudget / kBytes : kMaxStages;
-  static constexpr int kSmem = kStages * kBytes + 2048;
-};
-
-// Tensor memory: two accumulators, then the scales of a stage.
-template <int FMT, int NB>
-struct Tmem {
-  static constexpr int kAcc = NB == 256 ? 192 : NB;  // from the first accumulator to the second
-  static constexpr int kSa = kAcc + NB, kSb = kSa + 4 * Stage<FMT>::kTiles;
-  static_assert(kSb + 4 * (NB / 128) * Stage<FMT>::kTiles <= kTmemCols, "tensor memory");
+// Tensor memory of an SM pair's CTA: two accumulators of 256 columns that share 64, then the scales of a stage.
+template <int FMT>
+struct PairTmem {
+  static constexpr int kAcc = 192;  // from the first accumulator to the second
+  static constexpr int kSa = kAcc + 256, kSb = kSa + 4 * Stage<FMT>::kTiles;
+  static_assert(kSb + 8 * Stage<FMT>::kTiles <= kTmemCols, "tensor memory");
 };
 
 // ---------------------------------------------------------------------------
 // Epilogue: 32 output columns of a thread's row at a time.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* o, const float (&v)[32], int n) {
-  if (n >= 32) {
-    uint4* d = reinterpret_cast<uint4*>(o);
+// 32 bytes of a thread: a whole sector of L2, which results leave first (they are not read again here).  Half sectors, 16
+// bytes each, made a 256 x 256 tile of bf16 results wait 2.5 us longer.
+__device__ __forceinline__ void store32(void* dst, const uint32_t* w) {
+  asm volatile("st.global.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "l"(policy_evict_first())
+               : "memory");
+}
+
+// W words (a multiple of 8), 16-byte aligned; sectors: 32-byte aligned
+template <int W>
+__device__ __forceinline__ void store_words32(void* dst, const uint32_t (&w)[W], bool sectors) {
+  uint4* d = static_cast<uint4*>(dst);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      d[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                        pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (e < n) o[e] = __float2bfloat16_rn(v[e]);
+  for (int i = 0; i < W / 8; ++i) {
+    if (sectors) {
+      store32(d + 2 * i, w + 8 * i);
+    } else {
+      d[2 * i] = make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]);
+      d[2 * i + 1] = make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
+    }
   }
 }
 
@@ -162,9 +164,8 @@ __device__ __forceinline__ void store_codes32(const MxGemmParams& p, int row, in
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < mx_bits(OF) / 4; ++i)
-    reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  if constexpr (OF == kMxFp8) store_words32(dst, w, p.sectors);
+  else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // 32 results of a row at output column n, from the accumulators v (silu: gate) and up.
@@ -185,19 +186,20 @@ __device__ __forceinline__ void finish32(const MxGemmParams& p, int row, int n, 
   }
   if constexpr (out_fmt(EPI) != 0) {
     store_codes32<out_fmt(EPI)>(p, row, n, v, words);
-  } else if constexpr (EPI == kMxF32) {
-    float* o = static_cast<float*>(p.out) + static_cast<size_t>(row) * p.N + n;
-    if (n + 32 <= p.N) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        reinterpret_cast<float4*>(o)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (n + e < p.N) o[e] = v[e];
-    }
   } else {
-    store_bf16x32(static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(row) * p.N + n, v, p.N - n);
+    constexpr bool kF32 = EPI == kMxF32;
+    uint8_t* o = static_cast<uint8_t*>(p.out) + (static_cast<size_t>(row) * p.N + n) * (kF32 ? 4 : 2);
+    uint32_t w[kF32 ? 32 : 16];
+#pragma unroll
+    for (int e = 0; e < (kF32 ? 32 : 16); ++e) w[e] = kF32 ? __float_as_uint(v[e]) : pack_bf16x2(v[2 * e % 32], v[(2 * e + 1) % 32]);
+    if (n + 32 <= p.N) {
+      store_words32(o, w, p.sectors);
+    } else {  // 8, 16 or 24 columns are left
+#pragma unroll
+      for (int q = 0; q < (kF32 ? 8 : 4); ++q)
+        if (n + q * (kF32 ? 4 : 8) < p.N)
+          reinterpret_cast<uint4*>(o)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
   }
 }
 
@@ -265,207 +267,6 @@ __device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, int row, in
 }
 
 // ---------------------------------------------------------------------------
-// Persistent, one CTA an SM, whole tiles in a grouped raster.
-// ---------------------------------------------------------------------------
-template <int FMT, int EPI, int NB>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_gemm_mx(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
-  using S = Stage<FMT>;
-  using R = Ring<FMT, NB>;
-  using T = Tmem<FMT, NB>;
-  static_assert(NB == 256, "the epilogue takes 256 columns");
-  constexpr int nst = R::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_addr = smem_u32(smem_raw);
-  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
-  const uint32_t sbase = raw_addr + pad;
-  const uint32_t scales = sbase + nst * (R::kA + R::kB);  // behind the swizzled tiles
-  uint8_t* meta = smem_raw + pad + nst * R::kBytes;
-  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull[2], tempty[2], drain
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 5));
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * nst + a); };
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * nst + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * nst + 4);
-
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < nst; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 4);
-    }
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-    prefetch_maps<EPI>(maps);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  pdl_wait();
-
-  if (warp == 0) {
-    // ---------------- copies ----------------
-    const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_first();
-    int stage = 0;
-    uint32_t phase = 0;
-    long long used = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
-      int tm, tn;
-      tile_coords(p, t, tm, tn);
-      for (int kb = 0; kb < p.kb; ++kb) {
-        if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
-          const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
-          const int kx = kb * S::kTiles * kScaleElems;
-          mbar_arrive_expect_tx(full_bar(stage), R::kBytes);
-          tma_load_2d(sa, &maps.x, full_bar(stage), kb * kRowBytes, tm * BM, pol_a);
-          tma_load_2d(ssa, &maps.x_scales, full_bar(stage), kx, tm, pol_a);
-#pragma unroll
-          for (int i = 0; i < NB / 128; ++i) {
-            const int rt = is_silu(EPI) ? tn : tn * (NB / 128) + i;  // 128 rows of w
-            const int w = is_silu(EPI) ? i : 0;
-            tma_load_2d(sb + i * 128 * kRowBytes, &maps.w[w], full_bar(stage), kb * kRowBytes, rt * 128, pol_b);
-            tma_load_2d(ssb + i * R::kSa, &maps.w_scales[w], full_bar(stage), kx, rt, pol_b);
-          }
-        }
-        __syncwarp();
-        ++used;
-        if (++stage == nst) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (lane == 0) pdl_trigger();
-    if (!ok) {
-      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmProducer);
-      *abort_flag = 1;
-    }
-    // every copy has landed before the CTA can exit: use u of stage s completes its phase u
-    for (int s = 0; s < nst; ++s) {
-      const long long uses = (used - s + nst - 1) / nst;
-      if (uses > 0) mbar_wait(full_bar(s), static_cast<uint32_t>(uses - 1) & 1u, nullptr);
-    }
-  } else if (warp == 1) {
-    // ---------------- MMAs ----------------
-    constexpr uint32_t idesc = idesc_mx(BM, NB, S::kBits, S::kE8m0);
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    bool ok = true, issued = false;
-    int n_tiles = 0;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++n_tiles) {
-      // NB 256: the other accumulator's shared columns have been read; else: all of this one
-      const int wait_acc = NB == 256 ? acc ^ 1 : acc;
-      const uint32_t wait_phase = NB == 256 ? (acc ? acc_phase : acc_phase ^ 1u) : acc_phase ^ 1u;
-      if (!warp_same(mbar_wait(tempty_bar(wait_acc), wait_phase, abort_flag))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * T::kAcc;
-      for (int kb = 0; kb < p.kb; ++kb) {
-        if (!warp_same(mbar_wait(full_bar(stage), phase, abort_flag))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t sa = sbase + stage * (R::kA + R::kB), sb = sa + R::kA;
-          const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
-#pragma unroll
-          for (int i = 0; i < S::kTiles; ++i) {
-            tc_copy_scales<false>(tmem_base + T::kSa + 4 * i, smem_desc_scales(ssa + i * kMxTileBytes));
-#pragma unroll
-            for (int j = 0; j < NB / 128; ++j)
-              tc_copy_scales<false>(tmem_base + T::kSb + (NB / 128) * 4 * i + 4 * j,
-                                    smem_desc_scales(ssb + j * R::kSa + i * kMxTileBytes));
-          }
-          const int steps = kb + 1 < p.kb ? S::kSteps : p.last_steps;
-#pragma unroll
-          for (int k = 0; k < S::kSteps; ++k) {
-            if (k >= steps) break;
-            const int i = k / S::kPerTile;
-            tc_mma_mx<S::kBits, S::kStepScales, false>(
-                d_tmem, smem_desc_sw128(sa + 32 * k), smem_desc_sw128(sb + 32 * k),
-                idesc_mx_scale(idesc, k % S::kPerTile * S::kStepScales), tmem_base + T::kSa + 4 * i,
-                tmem_base + T::kSb + (NB / 128) * 4 * i, kb > 0 || k > 0 ? 1u : 0u);
-          }
-          tc_commit(empty_bar(stage));
-        }
-        __syncwarp();
-        issued = true;
-        if (++stage == nst) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      if (!ok) break;
-      if (elect_one()) tc_commit(tfull_bar(acc));
-      __syncwarp();
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
-    }
-    if (!ok) {
-      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmMma);
-      *abort_flag = 1;
-    }
-    // all MMAs and copies this thread issued must finish before tensor memory is freed
-    if (issued && elect_one()) tc_commit(drain_bar);
-    __syncwarp();
-    if (issued) mbar_wait(drain_bar, 0, nullptr);
-  } else {
-    // ---------------- epilogue ----------------
-    const int quad = warp & 3;  // tensor-memory lane quarter this warp may access
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x) {
-      int tm, tn;
-      tile_coords(p, t, tm, tn);
-      if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      epilogue_tile<EPI>(p, tm * BM + quad * 32 + lane, tn,
-                         tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc, acc, [&]() {
-                           tc_fence_before();
-                           __syncwarp();
-                           if (lane == 0) mbar_arrive(tempty_bar(acc));
-                         });
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
-    }
-    if (!ok) {
-      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
-      *abort_flag = 1;
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
-}
-
-// ---------------------------------------------------------------------------
 // Persistent on SM pairs (2-CTA clusters): tiles of 256 x 256, MMAs with M = 256.  CTA r has rows 128 r .. of the tile's x
 // and half of its columns of w (silu: gate on rank 0, up on rank 1) in its shared memory, the scales of its x rows and of
 // all columns, and the accumulator of its rows, so that an SM loads 32 KB of codes where one alone loads 48.
@@ -486,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_gemm_mx_pair(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
   using S = Stage<FMT>;
   using R = PairRing<FMT>;
-  using T = Tmem<FMT, 256>;
+  using T = PairTmem<FMT>;
   constexpr int nst = R::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -688,6 +489,285 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
+// Few tiles (decode batches): tiles of 128 x 128 (silu: 64 gate and 64 up columns), K split over the CTAs of a cluster, CTA
+// rank r over stages [r kb / S, (r + 1) kb / S).  Two CTAs an SM where there are more CTAs than SMs: they stream weights at
+// the rate of HBM whatever their number on an SM, so a wave need not be whole.  Every 32-column chunk of the CTAs'
+// accumulators goes into the shared memory of the CTA that finishes its unit (stores to another CTA need no round trip), and
+// is summed there in rank order.
+// ---------------------------------------------------------------------------
+constexpr int kSplitCols = 128;
+constexpr int kSplitTmemCols = 256;
+constexpr int kSplitMaxCluster = 8;
+
+template <int FMT, int EPI>
+struct SplitStage {
+  static constexpr int kB = kSplitCols * kRowBytes;
+  static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = kSa * (is_silu(EPI) ? 2 : 1);
+  static constexpr int kUnits = is_silu(EPI) ? 2 : 4;          // 32 outputs each
+  static constexpr int kChunks = is_silu(EPI) ? 2 : 1;         // accumulator chunks of a unit: gate, up
+  static constexpr int kTsa = kSplitCols, kTsb = kTsa + 4 * Stage<FMT>::kTiles;  // tensor memory of the scales
+  static_assert(kTsb + 8 * Stage<FMT>::kTiles <= kSplitTmemCols, "tensor memory");
+  __host__ __device__ static constexpr int bytes(int a_rows) { return a_rows * kRowBytes + kB + kSa + kSb; }
+  // chunks that a CTA of S receives from each, and the bytes of them all, `rows` accumulator rows each
+  __host__ __device__ static constexpr int local_chunks(int S) { return (kUnits + S - 1) / S * kChunks; }
+  __host__ __device__ static constexpr int recv_bytes(int S, int rows) { return S * local_chunks(S) * rows * 128; }
+};
+
+// The scale bytes of a unit (32 outputs from column n on), and zeros for the groups that fill up the row's last word.
+template <int OF>
+__device__ __forceinline__ void store_unit_scales(const MxGemmParams& p, int row, int n, const uint32_t (&words)[2]) {
+  constexpr int G = mx_group(OF), kGroups = 32 / G;
+  const int g0 = n / G, at = n % 128 / G;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const uint32_t w = at + g < 4 ? words[0] : words[1];
+    p.out_scales[mx_scale_at(row, (g0 + g) >> 2, p.out_ktiles) + ((g0 + g) & 3)] = static_cast<uint8_t>(w >> ((at + g & 3) * 8));
+  }
+  if (n + 32 >= p.N)
+    for (int g = g0 + kGroups; g < 4 * p.out_ktiles; ++g) p.out_scales[mx_scale_at(row, g >> 2, p.out_ktiles) + (g & 3)] = 0;
+}
+
+struct TmemLoader {
+  uint32_t taddr;
+  __device__ __forceinline__ void operator()(int col, float (&v)[32]) const { tmem_ld32(taddr + col, v); }
+};
+
+// Receive buffer of a CTA: [source rank][local chunk][8 float4 columns][rows], so that a warp's rows are contiguous.
+__device__ __forceinline__ uint32_t recv_at(int s, int nloc, int li, int q, int row, int rows) {
+  return static_cast<uint32_t>((((s * nloc + li) * 8 + q) * rows + row) * 16);
+}
+
+template <class R>
+struct RecvLoader {
+  const uint8_t* recv;
+  int ctas, nloc, row, rows;
+  __device__ __forceinline__ void operator()(int col, float (&v)[32]) const {
+    const int c = col / 32, u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+    for (int s = 0; s < ctas; ++s) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float4 t = *reinterpret_cast<const float4*>(recv + recv_at(s, nloc, li, q, row, rows));
+        v[4 * q] += t.x;
+        v[4 * q + 1] += t.y;
+        v[4 * q + 2] += t.z;
+        v[4 * q + 3] += t.w;
+      }
+    }
+  }
+};
+
+// unit u of tile column tn for one row; ld(column, v) gives 32 accumulator columns
+template <int EPI, class Loader>
+__device__ __forceinline__ void split_unit(const MxGemmParams& p, int row, int tn, int u, const Loader& ld) {
+  const int n = tn * (is_silu(EPI) ? kSplitCols / 2 : kSplitCols) + 32 * u;
+  if (n >= p.N) return;
+  float v[32], up[32];
+  uint32_t words[2] = {0, 0};
+  ld(32 * u, v);
+  if constexpr (is_silu(EPI)) ld(kSplitCols / 2 + 32 * u, up);
+  finish32<EPI>(p, row, n, v, up, words);
+  if constexpr (out_fmt(EPI) != 0) {
+    if (row < p.M) store_unit_scales<out_fmt(EPI)>(p, row, n, words);
+  }
+}
+
+template <int FMT, int EPI>
+__global__ void __launch_bounds__(kThreads, 2)
+    k_gemm_mx_split(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
+  using S = Stage<FMT>;
+  using R = SplitStage<FMT, EPI>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  const uint32_t sbase = raw_addr + pad;
+  const int nst = p.stages, a_bytes = p.a_rows * kRowBytes, tile_bytes = a_bytes + R::kB;
+  const uint32_t scales = sbase + nst * tile_bytes;
+  uint8_t* meta = smem_raw + pad + nst * R::bytes(p.a_rows);
+  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 1));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * nst);
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+  const int kb0 = rank * p.kb / ctas, kb1 = (rank + 1) * p.kb / ctas;
+  int tm, tn;
+  tile_coords(p, static_cast<int>(blockIdx.x) / ctas, tm, tn);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_maps<EPI>(maps);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kSplitTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  pdl_wait();
+
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_first();
+    int stage = 0, used = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        const uint32_t sa = sbase + stage * tile_bytes, sb = sa + a_bytes;
+        const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
+        const int kx = kb * S::kTiles * kScaleElems;
+        mbar_arrive_expect_tx(full_bar(stage), R::bytes(p.a_rows));
+        if constexpr (is_silu(EPI)) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            tma_load_2d(sb + i * R::kB / 2, &maps.w[i], full_bar(stage), kb * kRowBytes, tn * 64, pol_b);
+            tma_load_2d(ssb + i * R::kSa, &maps.w_scales[i], full_bar(stage), kx, tn >> 1, pol_b);
+          }
+        } else {
+          tma_load_2d(sb, &maps.w[0], full_bar(stage), kb * kRowBytes, tn * 128, pol_b);
+          tma_load_2d(ssb, &maps.w_scales[0], full_bar(stage), kx, tn, pol_b);
+        }
+        tma_load_2d(sa, &maps.x, full_bar(stage), kb * kRowBytes, tm * BM, pol_a);
+        tma_load_2d(ssa, &maps.x_scales, full_bar(stage), kx, tm, pol_a);
+      }
+      __syncwarp();
+      ++used;
+      if (++stage == nst) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (lane == 0) pdl_trigger();
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmProducer);
+      *abort_flag = 1;
+    }
+    // every copy has landed before shared memory is used again or left: of the stages in use, the last phase of each
+    for (int s = 0; s < nst && s < used; ++s) mbar_wait(full_bar(s), static_cast<uint32_t>((used - 1 - s) / nst) & 1u, nullptr);
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    constexpr uint32_t idesc = idesc_mx(BM, is_silu(EPI) ? 64 : 128, S::kBits, S::kE8m0);
+    const uint32_t gate_cols = is_silu(EPI) ? (tn & 1) * 2 : 0;  // a tile's 64 rows of w in their 128-row scale tile
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!warp_same(mbar_wait(full_bar(stage), phase, abort_flag))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t sa = sbase + stage * tile_bytes, sb = sa + a_bytes;
+        const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
+#pragma unroll
+        for (int i = 0; i < S::kTiles; ++i) {
+          tc_copy_scales<false>(tmem_base + R::kTsa + 4 * i, smem_desc_scales(ssa + i * kMxTileBytes));
+#pragma unroll
+          for (int j = 0; j < R::kChunks; ++j)
+            tc_copy_scales<false>(tmem_base + R::kTsb + 4 * (R::kChunks * i + j),
+                                  smem_desc_scales(ssb + j * R::kSa + i * kMxTileBytes));
+        }
+        const int steps = kb + 1 < p.kb ? S::kSteps : p.last_steps;
+#pragma unroll
+        for (int k = 0; k < S::kSteps; ++k) {
+          if (k >= steps) break;
+          const int i = k / S::kPerTile;
+#pragma unroll
+          for (int j = 0; j < R::kChunks; ++j)
+            tc_mma_mx<S::kBits, S::kStepScales, false>(
+                tmem_base + 64 * j, smem_desc_sw128(sa + 32 * k), smem_desc_sw128(sb + j * (R::kB / 2) + 32 * k),
+                idesc_mx_scale(idesc, k % S::kPerTile * S::kStepScales), tmem_base + R::kTsa + 4 * i,
+                tmem_base + R::kTsb + 4 * (R::kChunks * i + j) + gate_cols, kb > kb0 || k > 0 ? 1u : 0u);
+        }
+        tc_commit(empty_bar(stage));
+      }
+      __syncwarp();
+      if (++stage == nst) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmMma);
+      *abort_flag = 1;
+    }
+    // completes once everything issued above has: the accumulator is whole (or, given up, no longer written)
+    if (elect_one()) tc_commit(tfull_bar);
+    __syncwarp();
+  }
+  if (!mbar_wait(tfull_bar, 0, nullptr)) {
+    if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
+    *abort_flag = 1;
+  }
+  tc_fence_after();
+
+  const int quad = warp & 3;  // tensor-memory lane quarter this warp may access
+  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+  if (ctas == 1) {
+    __syncthreads();
+    if (warp >= 2 && !*abort_flag && tm * BM + quad * 32 < p.M) {
+      const TmemLoader ld{taddr};
+#pragma unroll 1
+      for (int u = 0; u < R::kUnits; ++u) split_unit<EPI>(p, tm * BM + quad * 32 + lane, tn, u, ld);
+    }
+  } else {
+    const int nloc = R::local_chunks(ctas);
+    __syncwarp();
+    cluster_sync();  // every CTA's MMAs and copies are done: the rings may be written
+    if (warp >= 2 && !*abort_flag && tm * BM + quad * 32 < p.M) {
+#pragma unroll 1
+      for (int c = 0; c < kSplitCols / 32; ++c) {
+        const int u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits;
+        uint32_t r[32];
+        tmem_ld32_async(taddr + 32 * c, r);
+        tmem_ld_wait(r);
+        const uint32_t dst = mapa_shared(sbase + recv_at(rank, nloc, li, 0, quad * 32 + lane, p.recv_rows),
+                                         static_cast<uint32_t>(u % ctas));
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          st_cluster_f4(dst + q * p.recv_rows * 16,
+                        make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
+                                    __uint_as_float(r[4 * q + 3])));
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // every chunk has arrived; no CTA touches another's shared memory after this
+    if (!*abort_flag) {
+      // this CTA's units, row group by row group, spread over its warps
+      int item = 0;
+      for (int u = rank; u < R::kUnits; u += ctas)
+        for (int g = 0; g < 4 && tm * BM + g * 32 < p.M; ++g)
+          if (item++ % (kThreads / 32) == warp) {
+            const RecvLoader<R> ld{smem_raw + pad, ctas, nloc, g * 32 + lane, p.recv_rows};
+            split_unit<EPI>(p, tm * BM + g * 32 + lane, tn, u, ld);
+          }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, kSplitTmemCols);
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -721,8 +801,8 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, long 
 
 // the maps of one operand of `rows` rows
 bool operand_maps(CUtensorMap* codes, CUtensorMap* scales, const MxOperand& o, int rows, long long row_bytes, int ktiles,
-                  int stage_tiles) {
-  return encode_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, row_bytes, rows, row_bytes, kRowBytes, 128,
+                  int stage_tiles, int box_rows) {
+  return encode_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, row_bytes, rows, row_bytes, kRowBytes, box_rows,
                    CU_TENSOR_MAP_SWIZZLE_128B) &&
          encode_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, o.scales, static_cast<long long>(ktiles) * kScaleElems,
                    (rows + kMxTileRows - 1) / kMxTileRows, static_cast<long long>(ktiles) * kMxTileBytes,
@@ -732,7 +812,7 @@ bool operand_maps(CUtensorMap* codes, CUtensorMap* scales, const MxOperand& o, i
 template <int FMT, int EPI>
 cudaError_t raise_limits() {
   static SmemLimits limits;
-  return limits.raise({smem_need(k_gemm_mx<FMT, EPI, 256>, Ring<FMT, 256>::kSmem),
+  return limits.raise({smem_need(k_gemm_mx_split<FMT, EPI>, kMaxSmemBytes),
                        smem_need(k_gemm_mx_pair<FMT, EPI>, PairRing<FMT>::kSmem)});
 }
 
@@ -765,59 +845,95 @@ int max_active_pairs() {
   return n > 0 ? n : 0;
 }
 
+// Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S
+// CTAs; of 256 x 256 for SM pairs.  Measured: a stage of a pair's tile takes 0.28, and a tile 2 more; a stage of a CTA of the
+// split kernel 0.26, or 0.46 with two on an SM; 4 and 3.5 pass besides; both read weights at 6.2 TB/s at most.  (8192 x 8192,
+// nvfp4: 256 rows 15.5 on pairs and 12.0 split, 384 rows 15.5 and 17.2; 4096 x 14336, fp8, 256 rows: 35.3 and 18.8; 57344 x
+// 8192, nvfp4, 16 rows: 56.1 and 46.6.)  With more tiles of more than 64 rows than the SMs hold at once the split kernel
+// does not keep that up (gate_up 2 x 28672 x 8192, nvfp4, 128 rows: 47.5 and 54).
+bool use_pairs(int M, long long tiles, int S, long long pair_tiles, int kb, double weight_bytes, int sms) {
+  if (M > 64 && tiles > 2 * sms) return true;
+  const double hbm = weight_bytes / 6.2e6;
+  const long long pairs = sms / 2, waves = (pair_tiles + pairs - 1) / pairs, ctas = tiles * S;
+  const double pair = waves * (kb * 0.28 + 2), stages = static_cast<double>(kb) / S;
+  const double split = ctas <= sms ? stages * 0.26 : (ctas + 2 * sms - 1) / (2 * sms) * (stages * 0.46);
+  return (pair > hbm ? pair : hbm) + 4 < (split > hbm ? split : hbm) + 3.5;
+}
+
 template <int FMT, int EPI>
-int launch_typed(const MxMaps& maps, MxGemmParams& p, cudaStream_t s) {
+int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
+  using T = Stage<FMT>;
+  using R = SplitStage<FMT, EPI>;
   const cudaError_t e = raise_limits<FMT, EPI>();
   if (e != cudaSuccess) return e;
   const int sms = num_sms();
-  p.tiles_n = is_silu(EPI) ? (p.N + 127) / 128 : (p.N + 255) / 256;
+  const long long row_bytes = static_cast<long long>(a.K) * T::kBits / 8;
+  const int ktiles = (a.K / mx_group(FMT) + kMxTileGroups - 1) / kMxTileGroups;
+  const int pair_m = (p.M + 2 * BM - 1) / (2 * BM), pair_n = is_silu(EPI) ? (p.N + 127) / 128 : (p.N + 255) / 256;
   p.tiles_m = (p.M + BM - 1) / BM;
-  const int pairs = static_cast<long long>(p.tiles_m) * p.tiles_n > sms ? max_active_pairs<FMT, EPI>() : 0;
-  if (pairs > 0) {
-    p.tiles_m = (p.M + 2 * BM - 1) / (2 * BM);
-    p.tiles = p.tiles_m * p.tiles_n;
-    p.group_m = p.tiles_m < 12 ? p.tiles_m : 12;
+  p.tiles_n = is_silu(EPI) ? (p.N + 63) / 64 : (p.N + 127) / 128;
+  p.tiles = p.tiles_m * p.tiles_n;
+  p.a_rows = p.M <= 64 ? 64 : 128;
+  p.recv_rows = p.M >= 128 ? 128 : (p.M + 31) / 32 * 32;
+  const int stage_bytes = R::bytes(p.a_rows);
+  // As many CTAs a tile as the SMs have room for, four stages or more each; without a split two CTAs an SM if they are more
+  // than the SMs.
+  int S = 1;
+  for (int n = kSplitMaxCluster; n > 1 && S == 1; --n)
+    if (static_cast<long long>(p.tiles) * n <= sms && p.kb >= 4 * n && R::recv_bytes(n, p.recv_rows) <= kRingBudget / stage_bytes * stage_bytes)
+      S = n;
+  const bool pair = use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
+                              (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
+  MxMaps maps{};
+  const int w_box = !pair && is_silu(EPI) ? 64 : 128;
+  bool ok = operand_maps(&maps.x, &maps.x_scales, a.x, a.M, row_bytes, ktiles, T::kTiles, pair ? 128 : p.a_rows);
+  for (int i = 0; i < (is_silu(EPI) ? 2 : 1); ++i)
+    ok = ok && operand_maps(&maps.w[i], &maps.w_scales[i], a.w[i], a.N, row_bytes, ktiles, T::kTiles, w_box);
+  if (!ok) return cudaErrorInvalidValue;
+  if (pair) {
+    const int pairs = max_active_pairs<FMT, EPI>();
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    p.tiles_m = pair_m;
+    p.tiles_n = pair_n;
+    p.tiles = pair_m * pair_n;
+    p.group_m = pair_m < 12 ? pair_m : 12;
     return launch_kernel_cluster(k_gemm_mx_pair<FMT, EPI>, dim3(2 * (p.tiles < pairs ? p.tiles : pairs)), dim3(kThreads),
                                  PairRing<FMT>::kSmem, s, true, 2, maps, p);
   }
-  p.tiles = p.tiles_m * p.tiles_n;
-  p.group_m = p.tiles_m < 24 ? p.tiles_m : 24;
-  return launch_kernel(k_gemm_mx<FMT, EPI, 256>, dim3(p.tiles < sms ? p.tiles : sms), dim3(kThreads),
-                       Ring<FMT, 256>::kSmem, s, true, maps, p);
+  p.group_m = p.tiles_m;
+  const int ctas = p.tiles * S, budget = ctas > sms ? kMaxSmemBytes / 2 - 1024 - 2048 : kRingBudget;
+  p.stages = budget / stage_bytes < kMaxStages ? budget / stage_bytes : kMaxStages;
+  const size_t smem = static_cast<size_t>(p.stages) * stage_bytes + 2048;
+  return launch_kernel_cluster(k_gemm_mx_split<FMT, EPI>, dim3(ctas), dim3(kThreads), smem, s, true, S, maps, p);
 }
 
 template <int FMT>
 int launch_fmt(const MxGemmArgs& a, cudaStream_t s) {
   using S = Stage<FMT>;
   MxGemmParams p{};
-  const long long row_bytes = static_cast<long long>(a.K) * S::kBits / 8;
-  const int ktiles = (a.K / mx_group(FMT) + kMxTileGroups - 1) / kMxTileGroups;
   p.M = a.M;
   p.N = a.N;
-  p.kb = static_cast<int>((row_bytes + kRowBytes - 1) / kRowBytes);
+  p.kb = static_cast<int>((static_cast<long long>(a.K) * S::kBits / 8 + kRowBytes - 1) / kRowBytes);
   p.last_steps = (a.K - (p.kb - 1) * S::kElems + S::kStepElems - 1) / S::kStepElems;
   for (int i = 0; i < 2; ++i) p.alpha[i] = a.alpha[i];
   p.out = a.out;
+  const long long out_row = a.out_fmt ? static_cast<long long>(a.N) * mx_bits(a.out_fmt) / 8 : a.N * (a.out_f32 ? 4LL : 2LL);
+  p.sectors = (out_row | static_cast<long long>(reinterpret_cast<uintptr_t>(a.out))) % 32 == 0;
   p.out_scales = static_cast<uint8_t*>(a.out_scales);
   if (a.out_fmt) p.out_ktiles = (a.N / mx_group(a.out_fmt) + kMxTileGroups - 1) / kMxTileGroups;
   p.out_inv_g = a.out_inv_g;
   p.out_sixth = a.out_sixth;
   p.err = a.err;
-  MxMaps maps{};
-  bool ok = operand_maps(&maps.x, &maps.x_scales, a.x, a.M, row_bytes, ktiles, S::kTiles);
-  for (int i = 0; i < (a.silu ? 2 : 1); ++i)
-    ok = ok && operand_maps(&maps.w[i], &maps.w_scales[i], a.w[i], a.N, row_bytes, ktiles, S::kTiles);
-  if (!ok) return cudaErrorInvalidValue;
-  if (!a.silu) return a.out_f32 ? launch_typed<FMT, kMxF32>(maps, p, s) : launch_typed<FMT, kMxBf16>(maps, p, s);
+  if (!a.silu) return a.out_f32 ? launch_typed<FMT, kMxF32>(a, p, s) : launch_typed<FMT, kMxBf16>(a, p, s);
   switch (a.out_fmt) {
     case 0:
-      return launch_typed<FMT, kMxSilu>(maps, p, s);
+      return launch_typed<FMT, kMxSilu>(a, p, s);
     case kMxNvfp4:
-      return launch_typed<FMT, kMxSiluNvfp4>(maps, p, s);
+      return launch_typed<FMT, kMxSiluNvfp4>(a, p, s);
     case kMxFp4:
-      return launch_typed<FMT, kMxSiluFp4>(maps, p, s);
+      return launch_typed<FMT, kMxSiluFp4>(a, p, s);
     default:
-      return launch_typed<FMT, kMxSiluFp8>(maps, p, s);
+      return launch_typed<FMT, kMxSiluFp8>(a, p, s);
   }
 }
 
