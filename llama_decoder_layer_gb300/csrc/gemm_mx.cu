@@ -79,7 +79,9 @@ struct MxGemmParams {
   int M, N, kb;    // kb: stages along K
   int last_steps;  // MMAs of the last one
   int tiles_m, tiles_n, tiles, group_m;
-  int stages, a_rows, recv_rows;  // few tiles: the ring, its rows of x (64 if M <= 64), accumulator rows that are exchanged
+  // few tiles: the ring, and its rows of x, a multiple of 32 (the MMA reads bytes of w as the rows to 128, whose results are
+  // never looked at)
+  int stages, a_rows;
   float alpha[2];
   void* out;
   bool sectors;  // rows of out begin on 32 bytes
@@ -617,6 +619,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   pdl_wait();
+  // every CTA is resident (or soon will be): the next kernel may set up beside them where there is room
+  if (threadIdx.x == 0) pdl_trigger();
 
   if (warp == 0) {
     // ---------------- copies ----------------
@@ -654,7 +658,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         phase ^= 1u;
       }
     }
-    if (lane == 0) pdl_trigger();
     if (!ok) {
       if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmProducer);
       *abort_flag = 1;
@@ -739,11 +742,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t r[32];
         tmem_ld32_async(taddr + 32 * c, r);
         tmem_ld_wait(r);
-        const uint32_t dst = mapa_shared(sbase + recv_at(rank, nloc, li, 0, quad * 32 + lane, p.recv_rows),
+        const uint32_t dst = mapa_shared(sbase + recv_at(rank, nloc, li, 0, quad * 32 + lane, p.a_rows),
                                          static_cast<uint32_t>(u % ctas));
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          st_cluster_f4(dst + q * p.recv_rows * 16,
+          st_cluster_f4(dst + q * p.a_rows * 16,
                         make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
                                     __uint_as_float(r[4 * q + 3])));
       }
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int u = rank; u < R::kUnits; u += ctas)
         for (int g = 0; g < 4 && tm * BM + g * 32 < p.M; ++g)
           if (item++ % (kThreads / 32) == warp) {
-            const RecvLoader<R> ld{smem_raw + pad, ctas, nloc, g * 32 + lane, p.recv_rows};
+            const RecvLoader<R> ld{smem_raw + pad, ctas, nloc, g * 32 + lane, p.a_rows};
             split_unit<EPI>(p, tm * BM + g * 32 + lane, tn, u, ld);
           }
     }
@@ -873,14 +876,13 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   p.tiles_m = (p.M + BM - 1) / BM;
   p.tiles_n = is_silu(EPI) ? (p.N + 63) / 64 : (p.N + 127) / 128;
   p.tiles = p.tiles_m * p.tiles_n;
-  p.a_rows = p.M <= 64 ? 64 : 128;
-  p.recv_rows = p.M >= 128 ? 128 : (p.M + 31) / 32 * 32;
+  p.a_rows = p.M >= 128 ? 128 : (p.M + 31) / 32 * 32;
   const int stage_bytes = R::bytes(p.a_rows);
   // As many CTAs a tile as the SMs have room for, four stages or more each; without a split two CTAs an SM if they are more
   // than the SMs.
   int S = 1;
   for (int n = kSplitMaxCluster; n > 1 && S == 1; --n)
-    if (static_cast<long long>(p.tiles) * n <= sms && p.kb >= 4 * n && R::recv_bytes(n, p.recv_rows) <= kRingBudget / stage_bytes * stage_bytes)
+    if (static_cast<long long>(p.tiles) * n <= sms && p.kb >= 4 * n && R::recv_bytes(n, p.a_rows) <= kRingBudget / stage_bytes * stage_bytes)
       S = n;
   const bool pair = use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
                               (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
@@ -903,6 +905,9 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   p.group_m = p.tiles_m;
   const int ctas = p.tiles * S, budget = ctas > sms ? kMaxSmemBytes / 2 - 1024 - 2048 : kRingBudget;
   p.stages = budget / stage_bytes < kMaxStages ? budget / stage_bytes : kMaxStages;
+  // no more than a CTA fills, or the exchange needs
+  const int fill = (p.kb + S - 1) / S, need = S > 1 ? (R::recv_bytes(S, p.a_rows) + stage_bytes - 1) / stage_bytes : 1;
+  if (p.stages > fill) p.stages = fill > need ? fill : need;
   const size_t smem = static_cast<size_t>(p.stages) * stage_bytes + 2048;
   return launch_kernel_cluster(k_gemm_mx_split<FMT, EPI>, dim3(ctas), dim3(kThreads), smem, s, true, S, maps, p);
 }

@@ -52,25 +52,41 @@ __device__ __forceinline__ void unpack8(const uint4& u, float* v) {
   v[7] = bf16_hi(u.w);
 }
 
-// One thread a group.
-template <int FMT>
+// Grids of up to this many CTAs let the next kernel start at once and set up beside them (a larger grid's last CTAs would
+// share their SMs with it).
+constexpr unsigned kEarlyTriggerCtas = 256;
+
+// One thread a group.  SECTORS: rows begin on 32 bytes, which a thread then reads at once.
+template <int FMT, bool SECTORS>
 __global__ void __launch_bounds__(kThreads) k_quantize_mx(const MxRowsArgs a) {
   constexpr int G = mx_group(FMT), C = G / 8;
   pdl_wait();
+  if (gridDim.x <= kEarlyTriggerCtas) pdl_trigger();
   const MxPlace p = mx_place(a);
-  uint4 u[C];
+  uint32_t u[C * 4];
 #pragma unroll
-  for (int c = 0; c < C; ++c) u[c] = make_uint4(0, 0, 0, 0);
+  for (int c = 0; c < C * 4; ++c) u[c] = 0;
   if (p.there) {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + p.row * a.x_stride) + p.grp * C;
+    if constexpr (SECTORS) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) u[c] = src[c];
+      for (int c = 0; c < C; c += 2) ld_global_v8(src + c, u + 4 * c);
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint4 q = src[c];
+        u[4 * c] = q.x;
+        u[4 * c + 1] = q.y;
+        u[4 * c + 2] = q.z;
+        u[4 * c + 3] = q.w;
+      }
+    }
   }
   float x[C][8];
   uint32_t top = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    unpack8(u[c], x[c]);
+    unpack8(make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]), x[c]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, abs_bits(x[c][e]));
   }
@@ -86,8 +102,13 @@ __global__ void __launch_bounds__(kThreads) k_quantize_mx(const MxRowsArgs a) {
     } else if constexpr (FMT == kMxFp4) {
       *reinterpret_cast<uint4*>(dst) = make_uint4(w[0].x, w[1].x, w[2].x, w[3].x);
     } else {
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+      if constexpr (SECTORS) {  // (codes begin on 32 bytes too)
+        const uint32_t q[8] = {w[0].x, w[0].y, w[1].x, w[1].y, w[2].x, w[2].y, w[3].x, w[3].y};
+        st_global_v8(dst, q);
+      } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[2].x, w[2].y, w[3].x, w[3].y);
+      }
     }
   }
   const uint32_t word = scale_word(p.there ? s.byte : 0u);
@@ -96,17 +117,20 @@ __global__ void __launch_bounds__(kThreads) k_quantize_mx(const MxRowsArgs a) {
 }
 
 // bf16(code * scale * g), one thread a group.
-template <int FMT>
+template <int FMT, bool SECTORS>
 __global__ void __launch_bounds__(kThreads) k_dequantize_mx(const MxRowsArgs a) {
   constexpr int G = mx_group(FMT), C = G / 8;
   pdl_wait();
+  if (gridDim.x <= kEarlyTriggerCtas) pdl_trigger();
   const MxPlace p = mx_place(a);
   if (!p.there) return;
   const uint8_t* src = static_cast<const uint8_t*>(a.codes) +
                        static_cast<size_t>(p.row) * (a.groups * (G * mx_bits(FMT) / 8)) + p.grp * (G * mx_bits(FMT) / 8);
   const uint8_t byte = static_cast<const uint8_t*>(a.scales)[mx_scale_at(p.row, p.grp >> 2, a.ktiles) + (p.grp & 3)];
   uint32_t w[G * mx_bits(FMT) / 32];
-  if constexpr (FMT == kMxNvfp4) {
+  if constexpr (FMT == kMxFp8 && SECTORS) {
+    ld_global_v8(src, w);
+  } else if constexpr (FMT == kMxNvfp4) {
     const uint2 v = *reinterpret_cast<const uint2*>(src);
     w[0] = v.x;
     w[1] = v.y;
@@ -122,12 +146,22 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_mx(const MxRowsArgs a) 
   }
   const float s = FMT == kMxNvfp4 ? e4m3_value(byte) * a.g : e8m0_value(byte);
   uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + p.row * a.x_stride) + p.grp * C;
+  uint32_t o[C * 4];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     float v[8];
     mx_values8<FMT>(FMT == kMxFp8 ? make_uint2(w[2 * c], w[2 * c + 1]) : make_uint2(w[c], 0), v);
-    dst[c] = make_uint4(pack_bf16x2(v[0] * s, v[1] * s), pack_bf16x2(v[2] * s, v[3] * s),
-                        pack_bf16x2(v[4] * s, v[5] * s), pack_bf16x2(v[6] * s, v[7] * s));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[4 * c + e] = pack_bf16x2(v[2 * e] * s, v[2 * e + 1] * s);
+  }
+#pragma unroll
+  for (int c = 0; c < C; c += 2) {
+    if constexpr (SECTORS) {
+      st_global_v8(dst + c, o + 4 * c);
+    } else {
+      dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+      dst[c + 1] = make_uint4(o[4 * c + 4], o[4 * c + 5], o[4 * c + 6], o[4 * c + 7]);
+    }
   }
 }
 
@@ -139,6 +173,7 @@ __global__ void __launch_bounds__(kThreads) k_add_rmsnorm_mx(const MxNormArgs a)
   constexpr int L = mx_group(FMT) / 8;  // lanes a group
   __shared__ float red[kThreads / 32];
   pdl_wait();
+  if (gridDim.x <= kEarlyTriggerCtas) pdl_trigger();
   const int row = blockIdx.x, nch = a.cols >> 3;
   const size_t base = static_cast<size_t>(row) * nch;
   const uint4* x = static_cast<const uint4*>(a.x) + base;
@@ -236,18 +271,27 @@ unsigned group_ctas(const MxRowsArgs& a) {
   return static_cast<unsigned>((n + kThreads - 1) / kThreads);
 }
 
+// bf16 rows and codes on 32 bytes (rows of codes are multiples of 16 or 32 bytes)
+bool whole_sectors(const void* rows, const MxRowsArgs& a) {
+  return a.x_stride % 16 == 0 && ((reinterpret_cast<uintptr_t>(rows) | reinterpret_cast<uintptr_t>(a.codes)) & 31) == 0;
+}
+
 }  // namespace
 
 int quantize_mx_launch(int fmt, const MxRowsArgs& a, cudaStream_t s) {
   auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(group_ctas(a)), dim3(kThreads), 0, s, true, a); };
-  return fmt == kMxNvfp4 ? go(k_quantize_mx<kMxNvfp4>) : fmt == kMxFp4 ? go(k_quantize_mx<kMxFp4>) : go(k_quantize_mx<kMxFp8>);
+  const bool whole = whole_sectors(a.x, a);
+  if (fmt == kMxNvfp4) return whole ? go(k_quantize_mx<kMxNvfp4, true>) : go(k_quantize_mx<kMxNvfp4, false>);
+  if (fmt == kMxFp4) return whole ? go(k_quantize_mx<kMxFp4, true>) : go(k_quantize_mx<kMxFp4, false>);
+  return whole ? go(k_quantize_mx<kMxFp8, true>) : go(k_quantize_mx<kMxFp8, false>);
 }
 
 int dequantize_mx_launch(int fmt, const MxRowsArgs& a, cudaStream_t s) {
   auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(group_ctas(a)), dim3(kThreads), 0, s, true, a); };
-  return fmt == kMxNvfp4 ? go(k_dequantize_mx<kMxNvfp4>)
-         : fmt == kMxFp4 ? go(k_dequantize_mx<kMxFp4>)
-                         : go(k_dequantize_mx<kMxFp8>);
+  const bool whole = whole_sectors(a.y, a);
+  if (fmt == kMxNvfp4) return whole ? go(k_dequantize_mx<kMxNvfp4, true>) : go(k_dequantize_mx<kMxNvfp4, false>);
+  if (fmt == kMxFp4) return whole ? go(k_dequantize_mx<kMxFp4, true>) : go(k_dequantize_mx<kMxFp4, false>);
+  return whole ? go(k_dequantize_mx<kMxFp8, true>) : go(k_dequantize_mx<kMxFp8, false>);
 }
 
 int add_rmsnorm_mx_launch(int fmt, const MxNormArgs& a, cudaStream_t s) {
