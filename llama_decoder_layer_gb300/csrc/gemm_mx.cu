@@ -170,6 +170,15 @@ __device__ __forceinline__ void store_codes32(const MxGemmParams& p, int row, in
   else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// g / (1 + exp(-g)).  Below -87 exp(87) stands for exp(-g), so that the sum stays where the hardware's reciprocal is a normal
+// number; one Newton step brings that to the last place.  (A NaN comes back through the product.)
+__device__ __forceinline__ float silu(float g) {
+  const float d = 1.0f + expf(fminf(-g, 87.f));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return g * fmaf(r, fmaf(-d, r, 1.0f), r);
+}
+
 // 32 results of a row at output column n, from the accumulators v (silu: gate) and up.
 template <int EPI>
 __device__ __forceinline__ void finish32(const MxGemmParams& p, int row, int n, float (&v)[32], const float* up,
@@ -177,11 +186,7 @@ __device__ __forceinline__ void finish32(const MxGemmParams& p, int row, int n, 
   if (row >= p.M || n >= p.N) return;
   if constexpr (is_silu(EPI)) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float g = v[e] * p.alpha[0];
-      // (the quotient by an instruction's reciprocal: 2 units in the last place; 0 where exp is beyond 2^126)
-      v[e] = __fdividef(g, 1.0f + __expf(-g)) * (up[e] * p.alpha[1]);
-    }
+    for (int e = 0; e < 32; ++e) v[e] = silu(v[e] * p.alpha[0]) * (up[e] * p.alpha[1]);
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] *= p.alpha[0];
