@@ -471,11 +471,9 @@ int llama_fused_add_rmsnorm_mx(const void* x, const void* residual_in, void* res
  * bf16 (out_fp32 = 0) or fp32, rounded once from fp32 sums.  N is a multiple of
  * 8.  No row of y depends on another row of x, but M decides how K is split over
  * SMs (few tiles), and so the order of the sums; that order is fixed, so a call
- * repeats bit for bit.  The workspace (llama_linear_mx_workspace_size) is the
- * call's while it runs. */
+ * repeats bit for bit.  No workspace is needed. */
 int llama_linear_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* w, float alpha, void* y, int out_fp32,
-                    void* workspace, size_t workspace_bytes, llama_stream_t stream);
-size_t llama_linear_mx_workspace_size(void);
+                    llama_stream_t stream);
 
 /* a[M, I] = silu(x gate^T) * (x up^T), the gate_up projection with SiluAndMul in
  * its epilogue, for x [M, K] and gate, up [I, K] of one format (two matrices, so
@@ -485,8 +483,7 @@ size_t llama_linear_mx_workspace_size(void);
  * 32), is given and the other NULL.  The fp32 results are rounded once, at the
  * end. */
 int llama_gate_up_silu_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* gate, const LlamaMxMatrix* up, float alpha_gate,
-                          float alpha_up, void* y, const LlamaMxMatrix* out, void* workspace, size_t workspace_bytes,
-                          llama_stream_t stream);
+                          float alpha_up, void* y, const LlamaMxMatrix* out, llama_stream_t stream);
 
 /* Sampling beyond greedy ([LLAMA-70B] Sampler, sample(): temperature scaling,
  * the top-k / top-p sampler, greedy rows below a temperature threshold, the

@@ -112,9 +112,8 @@ SIGNATURES = {
     "llama_quantize_mx": (_I, [_VP, _I64, _P_MX, _VP]),
     "llama_dequantize_mx": (_I, [_P_MX, _VP, _I64, _VP]),
     "llama_fused_add_rmsnorm_mx": (_I, [_VP, _VP, _VP, _P_MX, _VP, _F, _VP]),
-    "llama_linear_mx": (_I, [_P_MX, _P_MX, _F, _VP, _I, _VP, _SZ, _VP]),
-    "llama_linear_mx_workspace_size": (_SZ, []),
-    "llama_gate_up_silu_mx": (_I, [_P_MX, _P_MX, _P_MX, _F, _F, _VP, _P_MX, _VP, _SZ, _VP]),
+    "llama_linear_mx": (_I, [_P_MX, _P_MX, _F, _VP, _I, _VP]),
+    "llama_gate_up_silu_mx": (_I, [_P_MX, _P_MX, _P_MX, _F, _F, _VP, _P_MX, _VP]),
     "llama_get_device_error": (_I, [_VP, ctypes.POINTER(ctypes.c_int)]),
     "llama_status_string": (ctypes.c_char_p, [_I]),
     "llama_num_sms": (_I, []),
@@ -618,27 +617,26 @@ def fused_add_rmsnorm_mx(x: torch.Tensor, residual_in: Optional[torch.Tensor], r
 
 def linear_mx_workspace_size() -> int:
     """Bytes of workspace of linear_mx and gate_up_silu_mx."""
-    return int(lib().llama_linear_mx_workspace_size())
+    return 0
 
 
-def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, workspace: torch.Tensor, alpha: float = 1.0,
-              stream=None) -> None:
+def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+              alpha: float = 1.0, stream=None) -> None:
     """out [M, N] (bf16 or fp32) = alpha x w^T for x [M, K] and w [N, K] of one
     format; see llama_linear_mx in the header."""
     where = "llama_linear_mx"
     dtype = out.dtype
-    if (out.shape != (x.rows, w.rows) or not out.is_contiguous() or workspace.dtype is not torch.uint8 or
-            not workspace.is_contiguous() or (dtype is not torch.bfloat16 and dtype is not torch.float32)):
+    if (out.shape != (x.rows, w.rows) or not out.is_contiguous() or
+            (dtype is not torch.bfloat16 and dtype is not torch.float32)):
         raise LlamaError(LLAMA_ERR_ARG, where)
-    s = _mx_stream(where, stream, x, w, out, workspace)
-    st = lib().llama_linear_mx(x.ref, w.ref, alpha, out.data_ptr(), 1 if dtype is torch.float32 else 0,
-                               workspace.data_ptr(), workspace.numel(), s)
+    s = _mx_stream(where, stream, x, w, out)
+    st = lib().llama_linear_mx(x.ref, w.ref, alpha, out.data_ptr(), 1 if dtype is torch.float32 else 0, s)
     if st:
         raise LlamaError(st, where)
 
 
-def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, workspace: torch.Tensor, alpha_gate: float = 1.0,
-                    alpha_up: float = 1.0, stream=None) -> None:
+def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, workspace: Optional[torch.Tensor] = None,
+                    alpha_gate: float = 1.0, alpha_up: float = 1.0, stream=None) -> None:
     """out = silu(alpha_gate x gate^T) * (alpha_up x up^T) for x [M, K] and gate,
     up [I, K] of one format; out a bf16 tensor [M, I] or an MxMatrix; see
     llama_gate_up_silu_mx in the header."""
@@ -650,11 +648,10 @@ def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, workspace: t
         y = out.data_ptr()
     else:
         raise LlamaError(LLAMA_ERR_ARG, where)
-    if out.shape != (x.rows, gate.rows) or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+    if out.shape != (x.rows, gate.rows):
         raise LlamaError(LLAMA_ERR_ARG, where)
-    s = _mx_stream(where, stream, x, gate, up, out, workspace)
-    st = lib().llama_gate_up_silu_mx(x.ref, gate.ref, up.ref, alpha_gate, alpha_up, y, to, workspace.data_ptr(),
-                                     workspace.numel(), s)
+    s = _mx_stream(where, stream, x, gate, up, out)
+    st = lib().llama_gate_up_silu_mx(x.ref, gate.ref, up.ref, alpha_gate, alpha_up, y, to, s)
     if st:
         raise LlamaError(st, where)
 

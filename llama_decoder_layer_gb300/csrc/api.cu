@@ -814,8 +814,6 @@ int llama_fused_add_rmsnorm_mx(const void* x, const void* residual_in, void* res
   return cuda_status(add_rmsnorm_mx_launch(out->format, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-size_t llama_linear_mx_workspace_size(void) { return gemm_mx_partials_bytes(num_sms()) + 256; }
-
 // The checks that the two products share, of x and the matrices w[0 .. n) that it is multiplied with, each product times
 // alpha[i]; fills the arguments.
 static int mx_product_args(const LlamaMxMatrix* x, const LlamaMxMatrix* const* w, int n, const float* alpha,
@@ -845,16 +843,13 @@ static int mx_product_args(const LlamaMxMatrix* x, const LlamaMxMatrix* const* w
   return LLAMA_OK;
 }
 
-static int mx_product(MxGemmArgs& g, void* workspace, size_t workspace_bytes, llama_stream_t stream) {
-  if (workspace == nullptr || workspace_bytes < llama_linear_mx_workspace_size()) return LLAMA_ERR_WORKSPACE;
-  g.partials = reinterpret_cast<float*>(ws_base(workspace));
-  g.partials_bytes = gemm_mx_partials_bytes(num_sms());
+static int mx_product(MxGemmArgs& g, llama_stream_t stream) {
   g.err = device_error_word();
   return cuda_status(gemm_mx_launch(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int llama_linear_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* w, float alpha, void* y, int out_fp32,
-                    void* workspace, size_t workspace_bytes, llama_stream_t stream) {
+                    llama_stream_t stream) {
   MxGemmArgs g{};
   const int st = mx_product_args(x, &w, 1, &alpha, &g);
   if (st || x->rows == 0) return st;
@@ -862,12 +857,11 @@ int llama_linear_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* w, float alpha,
   if (!a16(y)) return LLAMA_ERR_UNSUPPORTED;
   g.out = y;
   g.out_f32 = out_fp32 != 0;
-  return mx_product(g, workspace, workspace_bytes, stream);
+  return mx_product(g, stream);
 }
 
 int llama_gate_up_silu_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* gate, const LlamaMxMatrix* up, float alpha_gate,
-                          float alpha_up, void* y, const LlamaMxMatrix* out, void* workspace, size_t workspace_bytes,
-                          llama_stream_t stream) {
+                          float alpha_up, void* y, const LlamaMxMatrix* out, llama_stream_t stream) {
   MxGemmArgs g{};
   const LlamaMxMatrix* w[2] = {gate, up};
   const float alpha[2] = {alpha_gate, alpha_up};
@@ -891,7 +885,7 @@ int llama_gate_up_silu_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* gate, con
     g.out = y;
   }
   g.silu = true;
-  return mx_product(g, workspace, workspace_bytes, stream);
+  return mx_product(g, stream);
 }
 
 int llama_sample(const float* logits, int rows, int vocab, const float* temperature, const int32_t* top_k,

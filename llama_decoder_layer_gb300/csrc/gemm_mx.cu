@@ -949,8 +949,6 @@ int launch_fmt(const MxGemmArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t gemm_mx_partials_bytes(int) { return 256; }
-
 int gemm_mx_launch(const MxGemmArgs& a, cudaStream_t s) {
   if (a.M <= 0) return 0;
   switch (a.fmt) {

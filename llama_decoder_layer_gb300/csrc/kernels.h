@@ -203,11 +203,8 @@ struct MxGemmArgs {
   bool out_f32;        // fp32 instead of bf16 (no silu)
   void *out, *out_scales;  // [M, N], or codes and scales
   float out_inv_g, out_sixth;
-  float* partials;
-  size_t partials_bytes;
   int* err;
 };
-size_t gemm_mx_partials_bytes(int num_sms);
 int gemm_mx_launch(const MxGemmArgs& a, cudaStream_t s);
 
 // A side stream of the current device, forked off s (work queued on s before is complete before what is queued on it) and

@@ -43,10 +43,6 @@ def f64(t):
     return t.detach().double().cpu().numpy()
 
 
-def workspace():
-    return lb.alloc_workspace(lb.linear_mx_workspace_size())
-
-
 def empty(fmt, rows, cols, g=1.0, fill=0xAB):
     m = lb.MxMatrix.empty(fmt, rows, cols, g)
     m.codes.fill_(fill)
@@ -253,7 +249,7 @@ def test_linear(fmt, M, N, K, dtype):
     x, xv = random_matrix(M, K, fmt, gx, M)
     w, wv = random_matrix(N, K, fmt, gw, N + 1)
     out = torch.full((M, N), 7.0, dtype=dtype, device=DEV)
-    lb.linear_mx(x, w, out, workspace(), alpha=1.5)
+    lb.linear_mx(x, w, out, alpha=1.5)
     ok()
     y, size = dot(xv, wv)
     bar = 1.5 * sum_slack(size, K) + np.abs(1.5 * y) * ((BF16 if dtype is torch.bfloat16 else FP32) + FP32)
@@ -275,7 +271,7 @@ def test_gate_up_silu(fmt, M, I, K, out_fmt):
     ag, au = float(np.float32(ag)), float(np.float32(au))
     og = 2.0 ** -7 if out_fmt == R.NVFP4 else 1.0
     out = empty(out_fmt, M, I, og) if out_fmt else torch.full((M, I), 7.0, dtype=torch.bfloat16, device=DEV)
-    lb.gate_up_silu_mx(x, gate, up, out, workspace(), alpha_gate=ag, alpha_up=au)
+    lb.gate_up_silu_mx(x, gate, up, out, alpha_gate=ag, alpha_up=au)
     ok()
     g, u, dg, du = g * ag, u * au, ag * sum_slack(gs, K) + np.abs(g * ag) * FP32, au * sum_slack(us, K) + np.abs(u * au) * FP32
     silu = g / (1 + np.exp(-g))

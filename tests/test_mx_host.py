@@ -13,7 +13,7 @@ from llama_decoder_layer_gb300 import binding as lb
 from llama_decoder_layer_gb300 import build as lbuild
 
 FAKE = 256  # an aligned address nothing reads: every call here is refused before a launch
-ARG, UNSUP, WS = lb.LLAMA_ERR_ARG, lb.LLAMA_ERR_UNSUPPORTED, lb.LLAMA_ERR_WORKSPACE
+ARG, UNSUP = lb.LLAMA_ERR_ARG, lb.LLAMA_ERR_UNSUPPORTED
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -70,7 +70,6 @@ def test_sizes(lib):
     assert lib.llama_mx_scale_bytes(R.FP8, 0, 160) == 0
     for fmt, rows, cols in ((0, 4, 64), (4, 4, 64), (1, -1, 64), (1, 4, 0), (1, 4, 48), (3, 4, 100), (1, 1 << 30, 64)):
         assert lib.llama_mx_code_bytes(fmt, rows, cols) == 0 and lib.llama_mx_scale_bytes(fmt, rows, cols) == 0
-    assert lb.linear_mx_workspace_size() > 0
 
 
 def matrix(fmt=R.NVFP4, rows=4, cols=64, g=1.0, codes=FAKE, scales=FAKE):
@@ -109,14 +108,14 @@ def test_norm_is_refused_on_the_host(lib):
 
 
 def test_products_are_refused_on_the_host(lib):
-    def linear(x={}, w={}, alpha=1.0, y=FAKE, work=FAKE, n=1 << 40):
-        return lib.llama_linear_mx(matrix(**x), matrix(**{"rows": 8, **w}), alpha, y, 0, work, n, None)
+    def linear(x={}, w={}, alpha=1.0, y=FAKE):
+        return lib.llama_linear_mx(matrix(**x), matrix(**{"rows": 8, **w}), alpha, y, 0, None)
 
-    def silu(x={}, w={}, alpha=1.0, y=FAKE, work=FAKE, n=1 << 40, up={}, beta=1.0, out=None):
+    def silu(x={}, w={}, alpha=1.0, y=FAKE, up={}, beta=1.0, out=None):
         size = {"rows": 8, "cols": w.get("cols", 64), **{k: w[k] for k in ("rows", "fmt") if k in w}}
         out = None if out is None else matrix(**{"fmt": R.FP8, "rows": 4, "cols": 8, **out})
         return lib.llama_gate_up_silu_mx(matrix(**x), matrix(**{"rows": 8, **w}), matrix(**{**size, **up}), alpha, beta, y,
-                                         out, work, n, None)
+                                         out, None)
     for call in (linear, silu):
         for kw in BAD_MATRICES:
             assert call(x=kw) == ARG and call(w=kw) == ARG, kw
@@ -127,8 +126,7 @@ def test_products_are_refused_on_the_host(lib):
             assert call(x=kw) == UNSUP and call(w=kw) == UNSUP, kw
         for kw in (dict(w=dict(rows=12)), dict(y=FAKE + 8)):
             assert call(**kw) == UNSUP, kw
-        assert call(work=None) == WS and call(n=16) == WS
-        assert call(x=dict(rows=0, codes=None, scales=None), y=None, work=None) == lb.LLAMA_OK
+        assert call(x=dict(rows=0, codes=None, scales=None), y=None) == lb.LLAMA_OK
     for kw in BAD_MATRICES + (dict(fmt=R.FP8), dict(rows=16), dict(cols=96)):
         assert silu(up=kw) == ARG, kw
     assert silu(beta=math.nan) == ARG
@@ -158,7 +156,7 @@ def test_binding_refuses_what_is_not_a_matrix():
 def test_binding_refuses_tensors_of_another_kind():
     m = lb.MxMatrix.empty(R.FP8, 4, 64, device="cpu")
     other = lb.MxMatrix.empty(R.FP4, 4, 64, device="cpu")
-    x, ws = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.uint8)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
     y = torch.zeros(4, 4, dtype=torch.bfloat16)
     gamma = torch.ones(64, dtype=torch.bfloat16)
     for call in (
@@ -169,18 +167,17 @@ def test_binding_refuses_tensors_of_another_kind():
             lambda: lb.fused_add_rmsnorm_mx(x, x[:3], None, m, gamma, 1e-5, stream=0),
             lambda: lb.fused_add_rmsnorm_mx(x, None, x.float(), m, gamma, 1e-5, stream=0),
             lambda: lb.fused_add_rmsnorm_mx(x, None, None, m, gamma[:32], 1e-5, stream=0),
-            lambda: lb.linear_mx(m, other, y, ws, stream=0), lambda: lb.linear_mx(m, m, y.half(), ws, stream=0),
-            lambda: lb.linear_mx(m, m, y[:3], ws, stream=0), lambda: lb.linear_mx(m, m, y.T[:, :3].T, ws, stream=0),
-            lambda: lb.linear_mx(m, m, y, ws.float(), stream=0),
-            lambda: lb.gate_up_silu_mx(m, m, other, y, ws, stream=0),
-            lambda: lb.gate_up_silu_mx(m, m, lb.MxMatrix.empty(R.FP8, 5, 64, device="cpu"), y, ws, stream=0),
-            lambda: lb.gate_up_silu_mx(m, m, m, y.float(), ws, stream=0),
-            lambda: lb.gate_up_silu_mx(m, m, m, m, ws, stream=0)):
+            lambda: lb.linear_mx(m, other, y, stream=0), lambda: lb.linear_mx(m, m, y.half(), stream=0),
+            lambda: lb.linear_mx(m, m, y[:3], stream=0), lambda: lb.linear_mx(m, m, y.T[:, :3].T, stream=0),
+            lambda: lb.gate_up_silu_mx(m, m, other, y, stream=0),
+            lambda: lb.gate_up_silu_mx(m, m, lb.MxMatrix.empty(R.FP8, 5, 64, device="cpu"), y, stream=0),
+            lambda: lb.gate_up_silu_mx(m, m, m, y.float(), stream=0),
+            lambda: lb.gate_up_silu_mx(m, m, m, m, stream=0)):
         with pytest.raises(lb.LlamaError):
             call()
     # of the right kind, but not where the call runs
     for call in (lambda: lb.quantize_mx(x, m, stream=0), lambda: lb.dequantize_mx(m, x, stream=0),
                  lambda: lb.fused_add_rmsnorm_mx(x, None, None, m, gamma, 1e-5, stream=0),
-                 lambda: lb.linear_mx(m, m, y, ws, stream=0), lambda: lb.gate_up_silu_mx(m, m, m, y, ws, stream=0)):
+                 lambda: lb.linear_mx(m, m, y, stream=0), lambda: lb.gate_up_silu_mx(m, m, m, y, stream=0)):
         with pytest.raises(lb.LlamaError):
             call()
