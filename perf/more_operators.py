@@ -235,7 +235,6 @@ def prepare(c, seed):
         st["to_h"] = handle(st["to"]) if "to" in st else None
         if "xq" in st:
             st["x_h"], st["w_h"] = handle(st["xq"]), [handle(w) for w in st["w"]]
-            st["ws"] = lb.alloc_workspace(lb.linear_mx_workspace_size())
     return st
 
 
@@ -271,11 +270,11 @@ def _run_own(st):
     from llama_decoder_layer_gb300 import binding as lb
     op = st["op"]
     if op == "lin":
-        lb.linear_mx(st["x_h"], st["w_h"][0], st["out"], st["ws"])
+        lb.linear_mx(st["x_h"], st["w_h"][0], st["out"])
         return st["out"]
     if op == "mlp":
         to = st["out"] if st["to_h"] is None else st["to_h"]
-        lb.gate_up_silu_mx(st["x_h"], st["w_h"][0], st["w_h"][1], to, st["ws"])
+        lb.gate_up_silu_mx(st["x_h"], st["w_h"][0], st["w_h"][1], to)
         if st["to_h"] is not None:
             lb.dequantize_mx(st["to_h"], st["out"])
         return st["out"]
