@@ -615,13 +615,7 @@ def fused_add_rmsnorm_mx(x: torch.Tensor, residual_in: Optional[torch.Tensor], r
         raise LlamaError(st, where)
 
 
-def linear_mx_workspace_size() -> int:
-    """Bytes of workspace of linear_mx and gate_up_silu_mx."""
-    return 0
-
-
-def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
-              alpha: float = 1.0, stream=None) -> None:
+def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, alpha: float = 1.0, stream=None) -> None:
     """out [M, N] (bf16 or fp32) = alpha x w^T for x [M, K] and w [N, K] of one
     format; see llama_linear_mx in the header."""
     where = "llama_linear_mx"
@@ -635,8 +629,7 @@ def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, workspace: Optional[t
         raise LlamaError(st, where)
 
 
-def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, workspace: Optional[torch.Tensor] = None,
-                    alpha_gate: float = 1.0, alpha_up: float = 1.0, stream=None) -> None:
+def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, alpha_gate: float = 1.0, alpha_up: float = 1.0, stream=None) -> None:
     """out = silu(alpha_gate x gate^T) * (alpha_up x up^T) for x [M, K] and gate,
     up [I, K] of one format; out a bf16 tensor [M, I] or an MxMatrix; see
     llama_gate_up_silu_mx in the header."""
