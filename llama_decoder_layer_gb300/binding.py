@@ -629,7 +629,8 @@ def linear_mx(x: MxMatrix, w: MxMatrix, out: torch.Tensor, alpha: float = 1.0, s
         raise LlamaError(st, where)
 
 
-def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, alpha_gate: float = 1.0, alpha_up: float = 1.0, stream=None) -> None:
+def gate_up_silu_mx(x: MxMatrix, gate: MxMatrix, up: MxMatrix, out, alpha_gate: float = 1.0, alpha_up: float = 1.0,
+                    stream=None) -> None:
     """out = silu(alpha_gate x gate^T) * (alpha_up x up^T) for x [M, K] and gate,
     up [I, K] of one format; out a bf16 tensor [M, I] or an MxMatrix; see
     llama_gate_up_silu_mx in the header."""

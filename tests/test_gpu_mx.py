@@ -287,3 +287,165 @@ def test_gate_up_silu(fmt, M, I, K, out_fmt):
     else:
         err = np.abs(f64(out) - want)
         assert (err <= slack + np.abs(want) * BF16).all(), err.max()
+
+
+def to_matrix(x, fmt, g=1.0):
+    m = empty(fmt, *x.shape, g if fmt == R.NVFP4 else 1.0)
+    lb.quantize_mx(x, m)
+    return m
+
+
+def values(m):
+    """What a matrix on the GPU stands for, in 64 bits."""
+    b = m.scales.cpu().numpy()[R.scale_places(m.rows, m.cols // R.GROUP[m.format])]
+    return R.values(R.code_values(m.codes.cpu().numpy(), m.format), b, m.format, m.scale)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(5, 136, 96), (64, 4096, 4096), (2600, 2056, 160)])
+def test_a_bad_row_stays_by_itself(fmt, M, N, K):
+    gen = torch.Generator(device=DEV).manual_seed(M)
+    x, w = (torch.randn(r, K, generator=gen, device=DEV).bfloat16() for r in (M, N))
+    good, bad = torch.empty(M, N, dtype=torch.bfloat16, device=DEV), torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    lb.linear_mx(to_matrix(x, fmt, 2.0 ** -6), to_matrix(w, fmt, 2.0 ** -6), good)
+    x[2, 40], x[3, K - 1], w[7, 0] = float("nan"), float("inf"), float("-inf")
+    lb.linear_mx(to_matrix(x, fmt, 2.0 ** -6), to_matrix(w, fmt, 2.0 ** -6), bad)
+    ok()
+    assert bool(bad[2:4].isnan().all()) and bool(bad[:, 7].isnan().all())
+    keep_m, keep_n = (torch.ones(n, dtype=torch.bool, device=DEV) for n in (M, N))
+    keep_m[2:4], keep_n[7] = False, False
+    assert torch.equal(bad[keep_m][:, keep_n], good[keep_m][:, keep_n])
+
+
+def test_a_matrix_with_itself():
+    m, v = random_matrix(200, 512, R.FP8, 1.0, 5)
+    out = torch.empty(200, 200, device=DEV)
+    lb.linear_mx(m, m, out)
+    ok()
+    y, size = dot(v, v)
+    assert (np.abs(f64(out) - y) <= sum_slack(size, 512) + np.abs(y) * 2 * FP32).all()
+    assert torch.equal(out, out.T)
+
+
+def test_no_rows():
+    for fmt in FORMATS:
+        x, w = lb.MxMatrix.empty(fmt, 0, 64), to_matrix(torch.randn(32, 64, device=DEV).bfloat16(), fmt)
+        rows = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
+        lb.quantize_mx(rows, x)
+        lb.dequantize_mx(x, rows)
+        lb.fused_add_rmsnorm_mx(rows, None, rows, x, torch.ones(64, dtype=torch.bfloat16, device=DEV), 1e-5)
+        lb.linear_mx(x, w, torch.empty(0, 32, device=DEV))
+        lb.gate_up_silu_mx(x, w, w, lb.MxMatrix.empty(fmt, 0, 32))
+    ok()
+
+
+class Mlp:
+    """A norm, gate_up and down in one format, as a layer's second half calls them."""
+
+    def __init__(self, fmt, M, H, I, seed):
+        gen = torch.Generator(device=DEV).manual_seed(seed)
+        rand = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+        self.x, self.res = rand(M, H).bfloat16(), rand(M, H).bfloat16()
+        self.gamma = (1 + 0.2 * rand(H)).bfloat16()
+        self.gate, self.up = (to_matrix((rand(I, H) * H ** -0.5).bfloat16(), fmt, 2.0 ** -12) for _ in range(2))
+        self.down = to_matrix((rand(H, I) * I ** -0.5).bfloat16(), fmt, 2.0 ** -12)
+        self.h, self.a = empty(fmt, M, H, 2.0 ** -6 if fmt == R.NVFP4 else 1.0), empty(fmt, M, I, 2.0 ** -8 if fmt == R.NVFP4 else 1.0)
+        self.res_out, self.out = torch.empty_like(self.x), torch.empty_like(self.x)
+
+    def run(self, stream=None):
+        lb.fused_add_rmsnorm_mx(self.x, self.res, self.res_out, self.h, self.gamma, 1e-5, stream=stream)
+        lb.gate_up_silu_mx(self.h, self.gate, self.up, self.a, stream=stream)
+        lb.linear_mx(self.a, self.down, self.out, stream=stream)
+
+    def results(self):
+        return [t.clone() for t in (self.res_out, self.h.codes, self.h.scales, self.a.codes, self.a.scales, self.out)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,H,I", [(3, 512, 1376), (130, 1024, 2048), (1500, 2080, 4128)])
+def test_mlp_of_a_layer(fmt, M, H, I):
+    m = Mlp(fmt, M, H, I, 1)
+    m.run()
+    ok()
+    s = f64((m.x.float() + m.res.float()).bfloat16())
+    h = s / np.sqrt((s * s).mean(-1, keepdims=True) + np.float64(np.float32(1e-5))) * f64(m.gamma)
+    R.check_quantised(m.h.codes.cpu().numpy(), m.h.scales.cpu().numpy(), h, np.abs(h) * 2.0 ** -18, fmt, m.h.scale)
+    hv = values(m.h)
+    (g, gs), (u, us) = dot(hv, values(m.gate)), dot(hv, values(m.up))
+    dg, du = sum_slack(gs, H) + np.abs(g) * FP32, sum_slack(us, H) + np.abs(u) * FP32
+    silu = g / (1 + np.exp(-g))
+    slack = 1.1 * dg * np.abs(u) + (np.abs(silu) + 1.1 * dg) * du + np.abs(silu * u) * 2.0 ** -18
+    R.check_quantised(m.a.codes.cpu().numpy(), m.a.scales.cpu().numpy(), silu * u, slack, fmt, m.a.scale)
+    y, size = dot(values(m.a), values(m.down))
+    assert (np.abs(f64(m.out) - y) <= sum_slack(size, I) + np.abs(y) * (BF16 + FP32)).all()
+
+
+@pytest.mark.parametrize("fmt,M,H,I", [(R.NVFP4, 1, 512, 1376), (R.FP8, 64, 2048, 8192), (R.FP4, 1500, 2080, 4128)])
+def test_graph_replays_and_streams_give_the_same(fmt, M, H, I):
+    m, other = Mlp(fmt, M, H, I, 2), Mlp(fmt, M, H, I, 3)
+    m.run()
+    other.run()
+    ok()
+    want, want_other = m.results(), other.results()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        m.run()
+        m.run()
+    for t in (m.res_out, m.h.codes, m.a.codes, m.out):
+        t.zero_()
+    graph.replay()
+    other.out.zero_()
+    graph.replay()
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(m.results(), want))
+    # two streams at once, one given as the stream of the call, one the current stream
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        m.run(stream=s1)
+        with torch.cuda.stream(s2):
+            other.run()
+    torch.cuda.synchronize()
+    ok()
+    assert all(torch.equal(a, b) for a, b in zip(m.results(), want))
+    assert all(torch.equal(a, b) for a, b in zip(other.results(), want_other))
+
+
+def test_offsets_beyond_32_bits():
+    """Codes, rows and results of more than 2^32 bytes: the last rows are those of a small call."""
+    rows, cols, last = 300_000, 16384, 300
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[:1000].normal_()
+    x[1000:-last] = 0.5
+    x[-last:].normal_()
+    m = lb.MxMatrix.empty(R.FP8, rows, cols)
+    lb.quantize_mx(x, m)
+    tail = to_matrix(x[-last:].contiguous(), R.FP8)
+    assert torch.equal(m.codes[-last:], tail.codes)
+    back = torch.empty_like(x)
+    lb.dequantize_mx(m, back)
+    small = torch.empty(last, cols, dtype=torch.bfloat16, device=DEV)
+    lb.dequantize_mx(tail, small)
+    assert torch.equal(back[-last:], small)
+    lb.fused_add_rmsnorm_mx(x, None, back, m, torch.ones(cols, dtype=torch.bfloat16, device=DEV), 1e-5)
+    lb.fused_add_rmsnorm_mx(x[-last:], None, small, tail, torch.ones(cols, dtype=torch.bfloat16, device=DEV), 1e-5)
+    assert torch.equal(m.codes[-last:], tail.codes) and torch.equal(back[-last:], small)
+    del x, back
+    w = to_matrix(torch.randn(64, cols, device=DEV).bfloat16(), R.FP8)
+    # the weight is the large matrix: its last rows are the last results
+    out = torch.empty(64, rows, device=DEV)
+    lb.linear_mx(w, m, out)
+    ok()
+    y, size = dot(values(w), values(tail))
+    assert (np.abs(f64(out[:, -last:]) - y) <= sum_slack(size, cols) + np.abs(y) * 2 * FP32).all()
+    del m, out
+    # more than 2^32 bytes of results
+    a, b = to_matrix(torch.randn(9000, 64, device=DEV).bfloat16(), R.FP8), to_matrix(
+        torch.randn(262_144, 64, device=DEV).bfloat16(), R.FP8)
+    out = torch.empty(9000, 262_144, dtype=torch.bfloat16, device=DEV)
+    lb.linear_mx(a, b, out)
+    ok()
+    y = (torch.from_numpy(values(a)[-200:]).to(DEV) @ torch.from_numpy(values(b)).to(DEV).T)
+    assert float((out[-200:].double() - y).abs().max()) <= float(y.abs().max()) * 2 * BF16
