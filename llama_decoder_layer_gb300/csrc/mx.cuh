@@ -104,22 +104,20 @@ __device__ __forceinline__ MxScale mx_scale(uint32_t top, float sixth, float inv
   return s;
 }
 
-// Elements times their group's factor, before rounding.  nvfp4 of bf16 elements: x / (s g) is on a border of
-// e2m1 or 2^-10 away from it and the product is off by less than 2^-19 below 8, so that rounded to a
-// multiple of 2^-13 it falls where the quotient does.  The other formats' factors are powers of two: exact.
-template <int FMT, bool BF16>
-__device__ __forceinline__ float mx_scaled(float x, float factor) {
-  constexpr float kSnap = 1536.f;  // 1.5 * 2^10: its last bit is 2^-13
-  if constexpr (FMT == kMxNvfp4 && BF16) return fmaf(x, factor, kSnap) - kSnap;
-  return x * factor;
-}
-
-// eight codes: 4 bytes (e2m1, in .x) or 8 bytes (e4m3)
+// Eight codes, 4 bytes (e2m1, in .x) or 8 bytes (e4m3), of elements times their group's factor.  nvfp4 of bf16 elements:
+// x / (s g) is on a border of e2m1 or 2^-10 away from it and the product is off by less than 2^-19 below 8, so that rounded
+// to a multiple of 2^-13 (the last bit of a sum with 1.5 * 2^10) it falls where the quotient does.  The other formats'
+// factors are powers of two: exact.
 template <int FMT, bool BF16>
 __device__ __forceinline__ uint2 mx_codes8(const float (&x)[8], float factor) {
+  constexpr float kSnap = 1536.f;
+  const uint64_t f2 = f2_pack(factor, factor), up = f2_pack(kSnap, kSnap), down = f2_pack(-kSnap, -kSnap);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = mx_scaled<FMT, BF16>(x[i], factor);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t v = f2_pack(x[2 * i], x[2 * i + 1]);
+    f2_unpack(FMT == kMxNvfp4 && BF16 ? f2_add(f2_fma(v, f2, up), down) : f2_mul(v, f2), y[2 * i], y[2 * i + 1]);
+  }
   if constexpr (FMT == kMxFp8) {
     return make_uint2(f32x2_to_e4m3(y[0], y[1]) | f32x2_to_e4m3(y[2], y[3]) << 16,
                       f32x2_to_e4m3(y[4], y[5]) | f32x2_to_e4m3(y[6], y[7]) << 16);

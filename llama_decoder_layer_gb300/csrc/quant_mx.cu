@@ -83,13 +83,12 @@ __global__ void __launch_bounds__(kThreads) k_quantize_mx(const MxRowsArgs a) {
     }
   }
   float x[C][8];
-  uint32_t top = 0;
+  uint32_t top = 0;  // of two bf16 magnitudes at a time
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    unpack8(make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]), x[c]);
+  for (int c = 0; c < C; ++c) unpack8(make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]), x[c]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, abs_bits(x[c][e]));
-  }
+  for (int i = 0; i < 4 * C; ++i) top = __vmaxu2(top, u[i] & 0x7fff7fffu);
+  top = max(top & 0xffff0000u, top << 16);
   const MxScale s = mx_scale<FMT, true>(top, a.sixth, a.inv_g);
   if (p.there) {
     uint8_t* dst = static_cast<uint8_t*>(a.codes) + static_cast<size_t>(p.row) * (a.groups * (G * mx_bits(FMT) / 8)) +
