@@ -82,6 +82,10 @@ struct MxGemmParams {
   // few tiles: the ring, and its rows of x, a multiple of 32 (the MMA reads bytes of w as the rows to 128, whose results are
   // never looked at)
   int stages, a_rows;
+  int meta_at;  // the barriers' place, from the ring's begin
+  int recv_at;  // the receive buffer's place from the ring's begin: 0, over the ring, or behind it
+  int ktiles;   // scale tiles along K
+  const uint8_t *x_scales, *w_scales[2];
   float alpha[2];
   void* out;
   bool sectors;  // rows of out begin on 32 bytes
@@ -500,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // rank r over stages [r kb / S, (r + 1) kb / S).  Two CTAs an SM where there are more CTAs than SMs: they stream weights at
 // the rate of HBM whatever their number on an SM, so a wave need not be whole.  Every 32-column chunk of the CTAs'
 // accumulators goes into the shared memory of the CTA that finishes its unit (stores to another CTA need no round trip), and
-// is summed there in rank order.
+// is summed there in rank order.  Where the ring leaves room the chunks have a place of their own, so that a CTA need not
+// wait for the others' MMAs before it stores.
 // ---------------------------------------------------------------------------
 constexpr int kSplitCols = 128;
 constexpr int kSplitTmemCols = 256;
@@ -591,13 +596,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t sbase = raw_addr + pad;
   const int nst = p.stages, a_bytes = p.a_rows * kRowBytes, tile_bytes = a_bytes + R::kB;
   const uint32_t scales = sbase + nst * tile_bytes;
-  uint8_t* meta = smem_raw + pad + nst * R::bytes(p.a_rows);
-  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 1));
+  uint8_t* meta = smem_raw + pad + p.meta_at;
+  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull, recv
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 2));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
-  const uint32_t tfull_bar = bar0 + 8u * (2 * nst);
+  const uint32_t tfull_bar = bar0 + 8u * (2 * nst), recv_bar = bar0 + 8u * (2 * nst + 1);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
@@ -611,9 +616,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull_bar, 1);
+    mbar_init(recv_bar, ctas * min((p.M - tm * BM + 31) / 32, 4));  // an arrival of every warp that has rows, in every CTA
     *abort_flag = 0;
     fence_mbar_init();
-    prefetch_maps<EPI>(maps);
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.w[0]);
+    if (is_silu(EPI)) tma_prefetch_desc(&maps.w[1]);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kSplitTmemCols);
@@ -623,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  if (ctas > 1 && p.recv_at > 0) cluster_arrive();  // this CTA's receive buffer may be written
   pdl_wait();
   // every CTA is resident (or soon will be): the next kernel may set up beside them where there is room
   if (threadIdx.x == 0) pdl_trigger();
@@ -641,20 +650,24 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) {
         const uint32_t sa = sbase + stage * tile_bytes, sb = sa + a_bytes;
         const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
-        const int kx = kb * S::kTiles * kScaleElems;
-        mbar_arrive_expect_tx(full_bar(stage), R::bytes(p.a_rows));
+        const int kt = kb * S::kTiles;
+        const uint32_t sbytes = min(S::kTiles, p.ktiles - kt) * kMxTileBytes;  // of the scales of 128 rows
+        auto scales_of = [&](const uint8_t* all, int rt) {
+          return all + (static_cast<size_t>(rt) * p.ktiles + kt) * kMxTileBytes;
+        };
+        mbar_arrive_expect_tx(full_bar(stage), a_bytes + R::kB + sbytes * (1 + R::kChunks));
         if constexpr (is_silu(EPI)) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             tma_load_2d(sb + i * R::kB / 2, &maps.w[i], full_bar(stage), kb * kRowBytes, tn * 64, pol_b);
-            tma_load_2d(ssb + i * R::kSa, &maps.w_scales[i], full_bar(stage), kx, tn >> 1, pol_b);
+            bulk_load(ssb + i * R::kSa, scales_of(p.w_scales[i], tn >> 1), sbytes, full_bar(stage), pol_b);
           }
         } else {
           tma_load_2d(sb, &maps.w[0], full_bar(stage), kb * kRowBytes, tn * 128, pol_b);
-          tma_load_2d(ssb, &maps.w_scales[0], full_bar(stage), kx, tn, pol_b);
+          bulk_load(ssb, scales_of(p.w_scales[0], tn), sbytes, full_bar(stage), pol_b);
         }
         tma_load_2d(sa, &maps.x, full_bar(stage), kb * kRowBytes, tm * BM, pol_a);
-        tma_load_2d(ssa, &maps.x_scales, full_bar(stage), kx, tm, pol_a);
+        bulk_load(ssa, scales_of(p.x_scales, tm), sbytes, full_bar(stage), pol_a);
       }
       __syncwarp();
       ++used;
@@ -738,16 +751,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else {
     const int nloc = R::local_chunks(ctas);
+    const uint32_t recv = sbase + p.recv_at;
     __syncwarp();
-    cluster_sync();  // every CTA's MMAs and copies are done: the rings may be written
-    if (warp >= 2 && !*abort_flag && tm * BM + quad * 32 < p.M) {
+    if (p.recv_at == 0) cluster_arrive();  // this CTA's MMAs and copies are done: its ring may be written
+    cluster_wait();
+    const bool has_rows = tm * BM + quad * 32 < p.M;
+    if (warp >= 2 && has_rows) {
 #pragma unroll 1
       for (int c = 0; c < kSplitCols / 32; ++c) {
         const int u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits;
         uint32_t r[32];
         tmem_ld32_async(taddr + 32 * c, r);
         tmem_ld_wait(r);
-        const uint32_t dst = mapa_shared(sbase + recv_at(rank, nloc, li, 0, quad * 32 + lane, p.a_rows),
+        const uint32_t dst = mapa_shared(recv + recv_at(rank, nloc, li, 0, quad * 32 + lane, p.a_rows),
                                          static_cast<uint32_t>(u % ctas));
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -755,19 +771,30 @@ __global__ void __launch_bounds__(kThreads, 2)
                         make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
                                     __uint_as_float(r[4 * q + 3])));
       }
+      __syncwarp();
+      if (lane < min(R::kUnits, ctas)) mbar_arrive_cluster(mapa_shared(recv_bar, lane));
     }
     __syncwarp();
-    cluster_sync();  // every chunk has arrived; no CTA touches another's shared memory after this
-    if (!*abort_flag) {
-      // this CTA's units, row group by row group, spread over its warps
-      int item = 0;
-      for (int u = rank; u < R::kUnits; u += ctas)
-        for (int g = 0; g < 4 && tm * BM + g * 32 < p.M; ++g)
-          if (item++ % (kThreads / 32) == warp) {
-            const RecvLoader<R> ld{smem_raw + pad, ctas, nloc, g * 32 + lane, p.a_rows};
-            split_unit<EPI>(p, tm * BM + g * 32 + lane, tn, u, ld);
-          }
+    cluster_arrive();  // this CTA writes to no other any more
+    if (rank < R::kUnits && !*abort_flag) {
+      if (!mbar_wait_cluster(recv_bar, 0)) {
+        if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
+        *abort_flag = 1;
+      } else {
+        // this CTA's units, row group by row group, spread over its warps
+        int item = 0;
+#pragma unroll 1
+        for (int u = rank; u < R::kUnits; u += ctas)
+#pragma unroll 1
+          for (int g = 0; g < 4 && tm * BM + g * 32 < p.M; ++g)
+            if (item++ % (kThreads / 32) == warp) {
+              const RecvLoader<R> ld{smem_raw + pad + p.recv_at, ctas, nloc, g * 32 + lane, p.a_rows};
+              split_unit<EPI>(p, tm * BM + g * 32 + lane, tn, u, ld);
+            }
+      }
     }
+    __syncwarp();
+    cluster_wait();  // no CTA leaves while another may write to it
   }
   tc_fence_before();
   __syncthreads();
@@ -808,13 +835,15 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, long 
 }
 
 // the maps of one operand of `rows` rows
+// (scales null: they are copied untiled)
 bool operand_maps(CUtensorMap* codes, CUtensorMap* scales, const MxOperand& o, int rows, long long row_bytes, int ktiles,
                   int stage_tiles, int box_rows) {
   return encode_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, row_bytes, rows, row_bytes, kRowBytes, box_rows,
                    CU_TENSOR_MAP_SWIZZLE_128B) &&
-         encode_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, o.scales, static_cast<long long>(ktiles) * kScaleElems,
+         (scales == nullptr ||
+          encode_2d(scales, CU_TENSOR_MAP_DATA_TYPE_UINT64, o.scales, static_cast<long long>(ktiles) * kScaleElems,
                    (rows + kMxTileRows - 1) / kMxTileRows, static_cast<long long>(ktiles) * kMxTileBytes,
-                   stage_tiles * kScaleElems, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+                   stage_tiles * kScaleElems, 1, CU_TENSOR_MAP_SWIZZLE_NONE));
 }
 
 template <int FMT, int EPI>
@@ -893,9 +922,10 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
                               (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
   MxMaps maps{};
   const int w_box = !pair && is_silu(EPI) ? 64 : 128;
-  bool ok = operand_maps(&maps.x, &maps.x_scales, a.x, a.M, row_bytes, ktiles, T::kTiles, pair ? 128 : p.a_rows);
+  bool ok = operand_maps(&maps.x, pair ? &maps.x_scales : nullptr, a.x, a.M, row_bytes, ktiles, T::kTiles,
+                         pair ? 128 : p.a_rows);
   for (int i = 0; i < (is_silu(EPI) ? 2 : 1); ++i)
-    ok = ok && operand_maps(&maps.w[i], &maps.w_scales[i], a.w[i], a.N, row_bytes, ktiles, T::kTiles, w_box);
+    ok = ok && operand_maps(&maps.w[i], pair ? &maps.w_scales[i] : nullptr, a.w[i], a.N, row_bytes, ktiles, T::kTiles, w_box);
   if (!ok) return cudaErrorInvalidValue;
   if (pair) {
     const int pairs = max_active_pairs<FMT, EPI>();
@@ -908,13 +938,25 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
                                  PairRing<FMT>::kSmem, s, true, 2, maps, p);
   }
   p.group_m = p.tiles_m;
+  p.ktiles = ktiles;
+  p.x_scales = static_cast<const uint8_t*>(a.x.scales);
+  for (int i = 0; i < 2; ++i) p.w_scales[i] = static_cast<const uint8_t*>(a.w[i].scales);
   const int ctas = p.tiles * S, budget = ctas > sms ? kMaxSmemBytes / 2 - 1024 - 2048 : kRingBudget;
+  const int fill = (p.kb + S - 1) / S;  // stages that a CTA fills
   p.stages = budget / stage_bytes < kMaxStages ? budget / stage_bytes : kMaxStages;
-  // no more than a CTA fills, or the exchange needs
-  const int fill = (p.kb + S - 1) / S, need = S > 1 ? (R::recv_bytes(S, p.a_rows) + stage_bytes - 1) / stage_bytes : 1;
-  if (p.stages > fill) p.stages = fill > need ? fill : need;
-  const size_t smem = static_cast<size_t>(p.stages) * stage_bytes + 2048;
-  return launch_kernel_cluster(k_gemm_mx_split<FMT, EPI>, dim3(ctas), dim3(kThreads), smem, s, true, S, maps, p);
+  if (p.stages > fill) p.stages = fill;
+  p.meta_at = p.stages * stage_bytes;
+  if (S > 1) {
+    const int recv = R::recv_bytes(S, p.a_rows);
+    if (p.meta_at + recv <= budget) {
+      p.recv_at = p.meta_at;
+      p.meta_at += recv;
+    } else if (p.meta_at < recv) {
+      p.meta_at = recv;
+    }
+  }
+  return launch_kernel_cluster(k_gemm_mx_split<FMT, EPI>, dim3(ctas), dim3(kThreads), static_cast<size_t>(p.meta_at) + 2048, s,
+                               true, S, maps, p);
 }
 
 template <int FMT>
