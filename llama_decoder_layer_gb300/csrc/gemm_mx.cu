@@ -557,14 +557,17 @@ struct RecvLoader {
     const int c = col / 32, u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits;
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = 0.f;
+#pragma unroll 2
     for (int s = 0; s < ctas; ++s) {
+      float4 t[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t[q] = *reinterpret_cast<const float4*>(recv + recv_at(s, nloc, li, q, row, rows));
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const float4 t = *reinterpret_cast<const float4*>(recv + recv_at(s, nloc, li, q, row, rows));
-        v[4 * q] += t.x;
-        v[4 * q + 1] += t.y;
-        v[4 * q + 2] += t.z;
-        v[4 * q + 3] += t.w;
+        v[4 * q] += t[q].x;
+        v[4 * q + 1] += t[q].y;
+        v[4 * q + 2] += t[q].z;
+        v[4 * q + 3] += t[q].w;
       }
     }
   }
@@ -765,11 +768,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_ld_wait(r);
         const uint32_t dst = mapa_shared(recv + recv_at(rank, nloc, li, 0, quad * 32 + lane, p.a_rows),
                                          static_cast<uint32_t>(u % ctas));
+        if (tm * BM + quad * 32 + lane < p.M) {  // (other rows' sums are never looked at)
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          st_cluster_f4(dst + q * p.a_rows * 16,
-                        make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
-                                    __uint_as_float(r[4 * q + 3])));
+          for (int q = 0; q < 8; ++q)
+            st_cluster_f4(dst + q * p.a_rows * 16,
+                          make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
+                                      __uint_as_float(r[4 * q + 3])));
+        }
       }
       __syncwarp();
       if (lane < min(R::kUnits, ctas)) mbar_arrive_cluster(mapa_shared(recv_bar, lane));
