@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc, acc, [&]() {
                            tc_fence_before();
                            __syncwarp();
-                           if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * acc);
+                           if (lane == 0) mbar_arrive_cluster_relaxed(tempty_lead + 8u * acc);
                          });
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
