@@ -58,9 +58,10 @@ struct Stage {
 };
 
 // Tensor maps: codes in boxes of 128 rows x 128 bytes, swizzled; scales in boxes of a stage's tiles of 128 rows, as
-// 8-byte elements.  What lies outside reads as zero.
+// 8-byte elements; the results in boxes of 32 rows x 128 bytes (4-bit codes: 64), swizzled.  What lies outside reads as zero
+// and is not written.
 struct MxMaps {
-  CUtensorMap x, x_scales, w[2], w_scales[2];
+  CUtensorMap x, x_scales, w[2], w_scales[2], out;
 };
 constexpr int kScaleElems = kMxTileBytes / 8;  // of a scale tile
 
@@ -139,20 +140,18 @@ __device__ __forceinline__ void store_words32(void* dst, const uint32_t (&w)[W],
   }
 }
 
-// 32 results to codes, at columns n .. n + 31 of the row; `words` collects the tile's scale words (128 columns).
+// 32 results, columns n .. n + 31 of a row, to codes; `words` collects the scale words of its 128 columns.
 template <int OF>
-__device__ __forceinline__ void store_codes32(const MxGemmParams& p, int row, int n, const float (&v)[32],
-                                              uint32_t (&words)[2]) {
+__device__ __forceinline__ void codes32(const MxGemmParams& p, int n, const float (&v)[32], uint32_t (&w)[mx_bits(OF)],
+                                        uint32_t (&words)[2]) {
   constexpr int G = mx_group(OF), kGroups = 32 / G;
-  uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * (p.N / 8 * mx_bits(OF)) + n / 8 * mx_bits(OF);
-  uint32_t w[mx_bits(OF)];
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < G; ++e) top = max(top, abs_bits(v[g * G + e]));
     const MxScale s = mx_scale<OF, false>(top, p.out_sixth, p.out_inv_g);
-    const int at = n % 128 / G + g;  // among the tile's groups
+    const int at = n % 128 / G + g;  // among the groups of 128 columns
     words[0] |= at < 4 ? s.byte << (at * 8) : 0u;
     words[1] |= at < 4 ? 0u : s.byte << (at * 8 - 32);
 #pragma unroll
@@ -170,8 +169,6 @@ __device__ __forceinline__ void store_codes32(const MxGemmParams& p, int row, in
       }
     }
   }
-  if constexpr (OF == kMxFp8) store_words32(dst, w, p.sectors);
-  else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // g / (1 + exp(-g)).  Below -87 exp(87) stands for exp(-g), so that the sum stays where the hardware's reciprocal is a normal
@@ -183,20 +180,26 @@ __device__ __forceinline__ float silu(float g) {
   return g * fmaf(r, fmaf(-d, r, 1.0f), r);
 }
 
-// 32 results of a row at output column n, from the accumulators v (silu: gate) and up.
+// 32 results from the accumulators v (silu: gate) and up, into v
+template <int EPI>
+__device__ __forceinline__ void results32(const MxGemmParams& p, float (&v)[32], const float* up) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = is_silu(EPI) ? silu(v[e] * p.alpha[0]) * (up[e] * p.alpha[1]) : v[e] * p.alpha[0];
+}
+
+// 32 results of a row at output column n, from the accumulators v (silu: gate) and up, stored by their thread
 template <int EPI>
 __device__ __forceinline__ void finish32(const MxGemmParams& p, int row, int n, float (&v)[32], const float* up,
                                          uint32_t (&words)[2]) {
   if (row >= p.M || n >= p.N) return;
-  if constexpr (is_silu(EPI)) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = silu(v[e] * p.alpha[0]) * (up[e] * p.alpha[1]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] *= p.alpha[0];
-  }
-  if constexpr (out_fmt(EPI) != 0) {
-    store_codes32<out_fmt(EPI)>(p, row, n, v, words);
+  results32<EPI>(p, v, up);
+  constexpr int OF = out_fmt(EPI);
+  if constexpr (OF != 0) {
+    uint32_t w[mx_bits(OF)];
+    codes32<OF>(p, n, v, w, words);
+    uint8_t* dst = static_cast<uint8_t*>(p.out) + static_cast<size_t>(row) * (p.N / 8 * mx_bits(OF)) + n / 8 * mx_bits(OF);
+    if constexpr (OF == kMxFp8) store_words32(dst, w, p.sectors);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     constexpr bool kF32 = EPI == kMxF32;
     uint8_t* o = static_cast<uint8_t*>(p.out) + (static_cast<size_t>(row) * p.N + n) * (kF32 ? 4 : 2);
@@ -225,13 +228,49 @@ __device__ __forceinline__ void store_words(const MxGemmParams& p, int row, int 
       *reinterpret_cast<uint32_t*>(p.out_scales + mx_scale_at(row, tn * kWords + i, p.out_ktiles)) = words[i];
 }
 
-// The whole 256-column tile of one row (a thread), from its accumulator at taddr.  release() is called once the 64 columns
+// A warp's results on their way to memory: 32 rows of up to 128 bytes in shared memory, swizzled as the tensor map of the
+// output says, and from there by a tiled store, which writes whole lines and leaves out what lies past the last row or
+// column (threads storing their own rows, 32 lines an instruction, held a 256 x 256 tile's epilogue for twice as long).  Two
+// buffers: one is filled while the other is read.
+struct OutBoxes {
+  const CUtensorMap* map;
+  uint32_t buf;  // this warp's two buffers
+  int row0;      // of the warp
+  int next;
+  // nanoseconds between a tile's boxes where another tile's MMAs run meanwhile: the results of a tile at once crowd out the
+  // copies of operands (8192 x 8192, nvfp4, 32768 rows: 19.3 thousand cycles of MMAs a tile instead of 18.4)
+  int pace;
+  static constexpr int kBytes = 32 * 128;
+
+  __device__ __forceinline__ uint32_t begin() {
+    if ((threadIdx.x & 31) == 0) bulk_wait_read<1>();
+    __syncwarp();
+    return buf + (next & 1) * kBytes;
+  }
+  // 16 bytes of the lane's row; rows of 128 bytes, or of 64
+  template <int ROW>
+  __device__ __forceinline__ static void put(uint32_t box, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const int lane = threadIdx.x & 31;
+    st_shared_v4(box + lane * ROW + ((ROW == 128 ? chunk ^ (lane & 7) : chunk ^ ((lane >> 1) & 3)) << 4), a, b, c, d);
+  }
+  // x: the box's first element in the output's rows
+  __device__ __forceinline__ void end(uint32_t box, int x) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      tma_store_2d(map, box, x, row0, policy_evict_first());
+      bulk_commit();
+    }
+    ++next;
+  }
+};
+
+// The whole 256-column tile of a warp's 32 rows, from the accumulator at taddr.  release() is called once the 64 columns
 // shared with the other accumulator (this one's last if it is the first, its first if the second) are in registers.
 template <int EPI, class Release>
-__device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, int row, int tn, uint32_t taddr, int acc,
+__device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, OutBoxes& boxes, int tn, uint32_t taddr, int acc,
                                               const Release& release) {
-  const bool any = row - (threadIdx.x & 31) < p.M;  // a warp whose rows are all past M has nothing to do
-  uint32_t words[2] = {0, 0};
+  const bool any = boxes.row0 < p.M;  // a warp whose rows are all past M has nothing to do
   float keep[2][32];
   const int shared = acc == 0 ? 192 : 0;
   if (any) {
@@ -240,39 +279,100 @@ __device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, int row, in
   }
   release();
   if (!any) return;
-  if constexpr (is_silu(EPI)) {
+  if constexpr (out_fmt(EPI) != 0) {
     // outputs 32 u: gate columns 32 u, up columns 128 + 32 u; kept: up of u = 2, 3 or gate of u = 0, 1
+    constexpr int OF = out_fmt(EPI), kRow = 16 * mx_bits(OF);  // bytes of 128 outputs
     const int n0 = tn * 128;
+    uint32_t words[2] = {0, 0};
+    const uint32_t box = boxes.begin();
+    auto unit = [&](int u, float (&gate)[32], const float (&up)[32]) {
+      if (n0 + 32 * u >= p.N) return;
+      results32<EPI>(p, gate, up);
+      uint32_t w[mx_bits(OF)];
+      codes32<OF>(p, n0 + 32 * u, gate, w, words);
+#pragma unroll
+      for (int i = 0; i < mx_bits(OF) / 4; ++i)
+        OutBoxes::put<kRow>(box, u * (mx_bits(OF) / 4) + i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int u = acc == 0 ? 2 + i : i;
       float other[32];
-      tmem_ld32(taddr + 32 * u + (acc == 0 ? 0 : 128), other);
-      if (acc == 0) {
-        finish32<EPI>(p, row, n0 + 32 * u, other, keep[i], words);
-      } else {
-        finish32<EPI>(p, row, n0 + 32 * u, keep[i], other, words);
-      }
+      tmem_ld32(taddr + (acc == 0 ? 64 + 32 * i : 128 + 32 * i), other);
+      if (acc == 0) unit(2 + i, other, keep[i]);
+      else unit(i, keep[i], other);
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       const int u = acc == 0 ? i : 2 + i;
-      if (n0 + 32 * u >= p.N) break;
       tmem_ld32(taddr + 32 * u, keep[0]);
       tmem_ld32(taddr + 128 + 32 * u, keep[1]);
-      finish32<EPI>(p, row, n0 + 32 * u, keep[0], keep[1], words);
+      unit(u, keep[0], keep[1]);
     }
-    if constexpr (out_fmt(EPI) != 0) store_words<EPI>(p, row, tn, words);
+    boxes.end(box, n0 / 8 * mx_bits(OF));
+    store_words<EPI>(p, boxes.row0 + (threadIdx.x & 31), tn, words);
   } else {
-    const int n0 = tn * 256;
-    finish32<EPI>(p, row, n0 + shared, keep[0], nullptr, words);
-    finish32<EPI>(p, row, n0 + shared + 32, keep[1], nullptr, words);
+    // 64 results of a row (fp32: 32) are a box
+    auto store = [&](int n, const float (&a)[32], const float (&b)[32]) {
+      if constexpr (EPI == kMxF32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (n + 32 * i >= p.N) break;
+          const float(&v)[32] = i ? b : a;
+          const uint32_t box = boxes.begin();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            OutBoxes::put<128>(box, q, __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                               __float_as_uint(v[4 * q + 3]));
+          boxes.end(box, n + 32 * i);
+        }
+      } else {
+        const uint32_t box = boxes.begin();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          OutBoxes::put<128>(box, q, pack_bf16x2(a[8 * q], a[8 * q + 1]), pack_bf16x2(a[8 * q + 2], a[8 * q + 3]),
+                             pack_bf16x2(a[8 * q + 4], a[8 * q + 5]), pack_bf16x2(a[8 * q + 6], a[8 * q + 7]));
+          OutBoxes::put<128>(box, 4 + q, pack_bf16x2(b[8 * q], b[8 * q + 1]), pack_bf16x2(b[8 * q + 2], b[8 * q + 3]),
+                             pack_bf16x2(b[8 * q + 4], b[8 * q + 5]), pack_bf16x2(b[8 * q + 6], b[8 * q + 7]));
+        }
+        boxes.end(box, n);
+      }
+    };
+    if constexpr (is_silu(EPI)) {
+      const int n0 = tn * 128, first = acc == 0 ? 64 : 0;  // the half whose up (gate) columns are kept
+      float other[2][32];
 #pragma unroll 1
-    for (int i = 0; i < 6; ++i) {
-      const int c = acc == 0 ? 32 * i : 64 + 32 * i;
-      if (n0 + c >= p.N) break;
-      tmem_ld32(taddr + c, keep[0]);
-      finish32<EPI>(p, row, n0 + c, keep[0], nullptr, words);
+      for (int h = 0; h < 2; ++h) {
+        const int c = h == 0 ? first : 64 - first;
+        if (n0 + c >= p.N) continue;
+        if (h == 1 && boxes.pace > 0) __nanosleep(boxes.pace);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (h == 1) tmem_ld32(taddr + c + 32 * i + (acc == 0 ? 128 : 0), keep[i]);
+          tmem_ld32(taddr + c + 32 * i + (acc == 0 ? 0 : 128), other[i]);
+          // (gate, up) = (other, keep) or (keep, other)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float g = acc == 0 ? other[i][e] : keep[i][e], u = acc == 0 ? keep[i][e] : other[i][e];
+            other[i][e] = silu(g * p.alpha[0]) * (u * p.alpha[1]);
+          }
+        }
+        store(n0 + c, other[0], other[1]);
+      }
+    } else {
+      const int n0 = tn * 256;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int c = i == 0 ? shared : acc == 0 ? 64 * (i - 1) : 64 * i;
+        if (n0 + c >= p.N) continue;
+        if (i > 0) {
+          if (boxes.pace > 0) __nanosleep(boxes.pace);
+          tmem_ld32(taddr + c, keep[0]);
+          tmem_ld32(taddr + c + 32, keep[1]);
+        }
+        results32<EPI>(p, keep[0], nullptr);
+        results32<EPI>(p, keep[1], nullptr);
+        store(n0 + c, keep[0], keep[1]);
+      }
     }
   }
 }
@@ -289,8 +389,9 @@ struct PairRing {
   static constexpr int kA = BM * kRowBytes, kB = 128 * kRowBytes;
   static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = 2 * kSa;
   static constexpr int kBytes = kA + kB + kSa + kSb;  // of a stage, a CTA
-  static constexpr int kStages = kRingBudget / kBytes < kMaxStages ? kRingBudget / kBytes : kMaxStages;
-  static constexpr int kSmem = kStages * kBytes + 2048;
+  static constexpr int kOut = 4 * 2 * OutBoxes::kBytes;  // the epilogue warps' buffers
+  static constexpr int kStages = (kRingBudget - kOut) / kBytes < kMaxStages ? (kRingBudget - kOut) / kBytes : kMaxStages;
+  static constexpr int kSmem = kStages * kBytes + kOut + 2048;
 };
 
 template <int FMT, int EPI>
@@ -304,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   const uint32_t sbase = raw_addr + pad;
-  const uint32_t scales = sbase + nst * (R::kA + R::kB);
-  uint8_t* meta = smem_raw + pad + nst * R::kBytes;
+  const uint32_t out_buf = sbase + nst * (R::kA + R::kB), scales = out_buf + R::kOut;
+  uint8_t* meta = smem_raw + pad + nst * R::kBytes + R::kOut;
   const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull[2], tempty[2], drain
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 5));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -336,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_maps<EPI>(maps);
+    tma_prefetch_desc(&maps.out);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
@@ -467,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- epilogue (both CTAs, their own rows) ----------------
     const int quad = warp & 3;
     const uint32_t tempty_lead = mapa_shared(tempty_bar(0), 0);
+    OutBoxes boxes{&maps.out, out_buf + quad * 2 * OutBoxes::kBytes, 0, 0, 0};
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
@@ -478,12 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      epilogue_tile<EPI>(p, (2 * tm + rank) * BM + quad * 32 + lane, tn,
-                         tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc, acc, [&]() {
-                           tc_fence_before();
-                           __syncwarp();
-                           if (lane == 0) mbar_arrive_cluster_relaxed(tempty_lead + 8u * acc);
-                         });
+      boxes.row0 = (2 * tm + rank) * BM + quad * 32;
+      boxes.pace = t + npairs < p.tiles ? 16 * p.kb : 0;  // (a stage's MMAs take some 300)
+      epilogue_tile<EPI>(p, boxes, tn, tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc, acc, [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty_lead + 8u * acc);
+      });
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1u;
     }
@@ -491,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
       give_up();
     }
+    if (lane == 0) bulk_wait_all();  // no store reads shared memory of a CTA that has left
   }
 
   tc_fence_before();
@@ -931,6 +1036,17 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
                          pair ? 128 : p.a_rows);
   for (int i = 0; i < (is_silu(EPI) ? 2 : 1); ++i)
     ok = ok && operand_maps(&maps.w[i], pair ? &maps.w_scales[i] : nullptr, a.w[i], a.N, row_bytes, ktiles, T::kTiles, w_box);
+  if (pair) {
+    constexpr bool kCodes = out_fmt(EPI) != 0, kF32 = EPI == kMxF32;
+    const long long cols = kCodes ? static_cast<long long>(p.N) / 8 * mx_bits(out_fmt(EPI)) : p.N;
+    const int elem = kCodes ? 1 : kF32 ? 4 : 2, box = kCodes ? 16 * mx_bits(out_fmt(EPI)) : 128;  // bytes
+    ok = ok && encode_2d(&maps.out,
+                         kCodes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                         : kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         p.out, cols, p.M, cols * elem, box / elem, 32,
+                         box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   if (!ok) return cudaErrorInvalidValue;
   if (pair) {
     const int pairs = max_active_pairs<FMT, EPI>();
