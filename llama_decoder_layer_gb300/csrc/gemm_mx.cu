@@ -33,6 +33,7 @@ constexpr int kRowBytes = 128;    // of every row of a stage
 constexpr int kThreads = 192;     // warp 0 copies, warp 1 MMAs, warps 2-5 epilogue
 constexpr int kTmemCols = 512;
 constexpr int kMaxStages = 8;
+constexpr int kDevs = 64;  // devices that values are cached for
 constexpr int kMaxSmemBytes = 232448;              // the opt-in limit per CTA (227 KB)
 constexpr int kRingBudget = kMaxSmemBytes - 2048;  // the rest: barriers, alignment slack
 
@@ -963,33 +964,45 @@ cudaError_t raise_limits() {
                        smem_need(k_gemm_mx_pair<FMT, EPI>, PairRing<FMT>::kSmem)});
 }
 
-// SM pairs that can work at once (2-CTA clusters resident); cached per device.
-template <int FMT, int EPI>
-int max_active_pairs() {
-  constexpr int kDevs = 64;
-  static std::atomic<int> cache[kDevs];
+// Clusters of S CTAs of a kernel that are resident at once, of those that take an SM each; cached per device.  (A cluster's
+// SMs are of one GPC, so that the SMs hold fewer clusters than their number says.)
+template <typename... KArgs>
+int max_clusters(void (*kernel)(KArgs...), int S, size_t smem, std::atomic<int>* cache) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 0;
   int n = cache[dev].load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * 128);
+    cfg.gridDim = dim3(S * 256);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = PairRing<FMT>::kSmem;
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.x = static_cast<unsigned>(S);
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_gemm_mx_pair<FMT, EPI>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = -1;
     }
     cache[dev].store(n, std::memory_order_relaxed);
   }
   return n > 0 ? n : 0;
+}
+
+template <int FMT, int EPI>
+int max_active_pairs() {
+  static std::atomic<int> cache[kDevs];
+  return max_clusters(k_gemm_mx_pair<FMT, EPI>, 2, PairRing<FMT>::kSmem, cache);
+}
+
+// (the same for every kernel that takes an SM: asked of one)
+int max_active_splits(int S) {
+  static std::atomic<int> cache[kSplitMaxCluster + 1][kDevs];
+  const cudaError_t e = raise_limits<kMxFp8, kMxBf16>();
+  return e != cudaSuccess ? 0 : max_clusters(k_gemm_mx_split<kMxFp8, kMxBf16>, S, kMaxSmemBytes, cache[S]);
 }
 
 // Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S
@@ -1026,7 +1039,8 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   // than the SMs.
   int S = 1;
   for (int n = kSplitMaxCluster; n > 1 && S == 1; --n)
-    if (static_cast<long long>(p.tiles) * n <= sms && p.kb >= 4 * n && R::recv_bytes(n, p.a_rows) <= kRingBudget / stage_bytes * stage_bytes)
+    if (static_cast<long long>(p.tiles) * n <= sms && p.kb >= 4 * n &&
+        R::recv_bytes(n, p.a_rows) <= kRingBudget / stage_bytes * stage_bytes && max_active_splits(n) >= p.tiles)
       S = n;
   const bool pair = use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
                               (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
