@@ -16,6 +16,7 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -1006,18 +1007,22 @@ int max_active_splits(int S) {
 }
 
 // Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S
-// CTAs; of 256 x 256 for SM pairs.  Measured: a stage of a pair's tile takes 0.28, and a tile 2 more; a stage of a CTA of the
-// split kernel 0.26, or 0.46 with two on an SM; 4 and 3.5 pass besides; both read weights at 6.2 TB/s at most.  (8192 x 8192,
-// nvfp4: 256 rows 15.5 on pairs and 12.0 split, 384 rows 15.5 and 17.2; 4096 x 14336, fp8, 256 rows: 35.3 and 18.8; 57344 x
-// 8192, nvfp4, 16 rows: 56.1 and 46.6.)  With more tiles of more than 64 rows than the SMs hold at once the split kernel
-// does not keep that up (gate_up 2 x 28672 x 8192, nvfp4, 128 rows: 47.5 and 54).
+// CTAs; of 256 x 256 for SM pairs.  Fitted to 600 random sizes, of which the chosen kernel takes 0.4% more than the better
+// one in the mean: a stage of a pair's tile takes 0.28 and a tile 0.4 more, 0.8 at least; a stage of a CTA of the split
+// kernel 0.26, with two on an SM 0.44 to 0.46 and 1.3 a wave, of up to 64 rows 0.5; 5.2 (3.2 of them besides the reads of
+// weights) and 3.5 pass besides.  Weights are read at 5.4 TB/s by pairs and at 6.2 by the split kernel, 5.4 where more than
+// 64 rows of x have more tiles than the SMs hold.  (Split and pairs: 8192 x 8192, nvfp4, 256 rows 12.0 and 15.5, 384 rows
+// 17.2 and 15.5; 4096 x 14336, fp8, 256 rows 18.8 and 35.3; 57344 x 8192, nvfp4, 16 rows 46.6 and 56.1; gate and up of 28672
+// x 8192, nvfp4, 128 rows 54 and 47.5.)
 bool use_pairs(int M, long long tiles, int S, long long pair_tiles, int kb, double weight_bytes, int sms) {
-  if (M > 64 && tiles > 2 * sms) return true;
-  const double hbm = weight_bytes / 6.2e6;
   const long long pairs = sms / 2, waves = (pair_tiles + pairs - 1) / pairs, ctas = tiles * S;
-  const double pair = waves * (kb * 0.28 + 2), stages = static_cast<double>(kb) / S;
-  const double split = ctas <= sms ? stages * 0.26 : (ctas + 2 * sms - 1) / (2 * sms) * (stages * 0.46);
-  return (pair > hbm ? pair : hbm) + 4 < (split > hbm ? split : hbm) + 3.5;
+  const double pair = std::max(2 + waves * std::max(kb * 0.28 + 0.4, 0.8), weight_bytes / 5.4e6);
+  const double stages = static_cast<double>(kb) / S, wave = M > 64 ? 1.3 : 0.5;
+  double split = stages * 0.26;
+  if (ctas > 2 * sms) split = (ctas + 2 * sms - 1) / (2 * sms) * (stages * 0.46 + wave);
+  else if (ctas > sms) split = stages * 0.44 + 1;
+  split = std::max(split, weight_bytes / (M > 64 && ctas > 2 * sms ? 5.4e6 : 6.2e6));
+  return pair + 3.2 < split + 3.5;
 }
 
 template <int FMT, int EPI>
