@@ -164,49 +164,56 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_mx(const MxRowsArgs a) 
   }
 }
 
-// The residual add and RMSNorm of rowops.cu (one CTA a row, the row in registers), its output quantised: a thread has
-// chunks of 8 elements, 2 or 4 lanes a group.  The norm's fp32 result is quantised as it is, without a rounding to bf16
-// before.
-template <int FMT, int MAXC>
-__global__ void __launch_bounds__(kThreads) k_add_rmsnorm_mx(const MxNormArgs a) {
+// The residual add and RMSNorm of rowops.cu, its output quantised: T threads a row (32: a CTA has eight rows, a warp each),
+// the row in registers in chunks of 8 elements, 2 or 4 lanes a group.  The norm's fp32 result is quantised as it is, without
+// a rounding to bf16 before.
+template <int FMT, int T, int MAXC>
+__global__ void __launch_bounds__(T == 32 ? kThreads : T) k_add_rmsnorm_mx(const MxNormArgs a) {
   constexpr int L = mx_group(FMT) / 8;  // lanes a group
-  __shared__ float red[kThreads / 32];
+  constexpr int kRows = T == 32 ? kThreads / 32 : 1;
+  __shared__ float red[32];
   pdl_wait();
   if (gridDim.x <= kEarlyTriggerCtas) pdl_trigger();
-  const int row = blockIdx.x, nch = a.cols >> 3;
+  const int warp = threadIdx.x >> 5;
+  const int row = blockIdx.x * kRows + (kRows > 1 ? warp : 0), nch = a.cols >> 3;
+  if (kRows > 1 && row >= a.rows) return;
+  const int tid = T == 32 ? threadIdx.x & 31 : threadIdx.x;
   const size_t base = static_cast<size_t>(row) * nch;
   const uint4* x = static_cast<const uint4*>(a.x) + base;
   const uint4* res = static_cast<const uint4*>(a.res_in) + base;
-  float v[MAXC][8];
+  uint4 u[MAXC];  // the new residual: a bf16 tensor, and the norm is taken of that tensor
   float ss = 0.f;
 #pragma unroll
-  for (int c = 0; c < MAXC; ++c) {
-    const int i = threadIdx.x + c * kThreads;
+  for (int c = 0; c < MAXC; ++c) u[c] = tid + c * T < nch ? x[tid + c * T] : make_uint4(0, 0, 0, 0);
+  if (a.res_in != nullptr) {
+    uint4 r[MAXC];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
-    if (i < nch) {
-      unpack8(x[i], v[c]);
-      if (a.res_in != nullptr) {
-        float r[8];
-        unpack8(res[i], r);
+    for (int c = 0; c < MAXC; ++c) r[c] = tid + c * T < nch ? res[tid + c * T] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[c][e] += r[e];
-      }
-      // the new residual is a bf16 tensor; the norm is taken of that tensor
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[c][e] = round_bf16(v[c][e]);
-        ss += v[c][e] * v[c][e];
-      }
+    for (int c = 0; c < MAXC; ++c) {
+      float p[8], q[8];
+      unpack8(u[c], p);
+      unpack8(r[c], q);
+      u[c] = make_uint4(pack_bf16x2(p[0] + q[0], p[1] + q[1]), pack_bf16x2(p[2] + q[2], p[3] + q[3]),
+                        pack_bf16x2(p[4] + q[4], p[5] + q[5]), pack_bf16x2(p[6] + q[6], p[7] + q[7]));
     }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
-  __syncthreads();
-  ss = 0.f;
+  for (int c = 0; c < MAXC; ++c) {
+    float v[8];
+    unpack8(u[c], v);
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) ss += red[w];
+    for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if constexpr (T > 32) {
+    if ((threadIdx.x & 31) == 0) red[warp] = ss;
+    __syncthreads();
+    ss = 0.f;
+#pragma unroll
+    for (int w = 0; w < T / 32; ++w) ss += red[w];
+  }
   // 1 / sqrt(y) = inv + low: the residual 1 - y inv^2, with the product's rounding, halved, so that the results below
   // are off by little more than their own rounding (codes near a border then fall where they should)
   const float y = ss / static_cast<float>(a.cols) + a.eps;
@@ -216,20 +223,19 @@ __global__ void __launch_bounds__(kThreads) k_add_rmsnorm_mx(const MxNormArgs a)
   uint8_t* codes = static_cast<uint8_t*>(a.codes) + base * mx_bits(FMT);
 #pragma unroll
   for (int c = 0; c < MAXC; ++c) {
-    const int i = threadIdx.x + c * kThreads;
-    if (c * kThreads >= nch) break;  // the same for the whole CTA
+    const int i = tid + c * T;
+    if (c * T >= nch) break;  // the same for the whole row
     const bool there = i < nch;
     float h[8];
     uint32_t top = 0;
     if (there) {
-      if (a.res_out != nullptr)
-        res_out[i] = make_uint4(pack_bf16x2(v[c][0], v[c][1]), pack_bf16x2(v[c][2], v[c][3]),
-                                pack_bf16x2(v[c][4], v[c][5]), pack_bf16x2(v[c][6], v[c][7]));
-      float g[8];
+      if (a.res_out != nullptr) res_out[i] = u[c];
+      float v[8], g[8];
+      unpack8(u[c], v);
       unpack8(static_cast<const uint4*>(a.gamma)[i], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float vg = v[c][e] * g[e];  // exact: 8 and 8 bits
+        const float vg = v[e] * g[e];  // exact: 8 and 8 bits
         h[e] = fmaf(vg, inv, vg * low);
         top = max(top, abs_bits(h[e]));
       }
@@ -254,15 +260,29 @@ __global__ void __launch_bounds__(kThreads) k_add_rmsnorm_mx(const MxNormArgs a)
   }
 }
 
+// Many rows: a warp each up to 1024 elements (10099 x 192: 4.0 us; a CTA of 256 threads each 11.6), then four chunks a
+// thread at most (5906 x 15840: 99 us, eight 149).  The row is kept as the bf16 numbers it is made of, four registers a
+// chunk, so that an SM holds 1024 threads or more with all their loads in flight (32768 x 8192: 267 us, 7.0 TB/s; as
+// floats 311).  Few rows: as many threads as chunks, for the latency (128 x 8192: 3.1 us, 256 threads 4.4).
 template <int FMT>
 int norm_typed(const MxNormArgs& a, cudaStream_t s) {
-  const int per = (a.cols / 8 + kThreads - 1) / kThreads;
-  auto go = [&](auto kernel) { return launch_kernel(kernel, dim3(a.rows), dim3(kThreads), 0, s, true, a); };
-  if (per <= 1) return go(k_add_rmsnorm_mx<FMT, 1>);
-  if (per <= 2) return go(k_add_rmsnorm_mx<FMT, 2>);
-  if (per <= 4) return go(k_add_rmsnorm_mx<FMT, 4>);
-  if (per <= 8) return go(k_add_rmsnorm_mx<FMT, 8>);
-  return cudaErrorInvalidValue;
+  const int nch = a.cols / 8;
+  auto go = [&](auto kernel, int rows, int threads) {
+    return launch_kernel(kernel, dim3((a.rows + rows - 1) / rows), dim3(threads), 0, s, true, a);
+  };
+  if (nch <= 32) return go(k_add_rmsnorm_mx<FMT, 32, 1>, 8, kThreads);
+  if (a.rows <= 2 * num_sms()) {
+    if (nch <= 256) return go(k_add_rmsnorm_mx<FMT, 256, 1>, 1, 256);
+    if (nch <= 512) return go(k_add_rmsnorm_mx<FMT, 512, 1>, 1, 512);
+    if (nch <= 1024) return go(k_add_rmsnorm_mx<FMT, 1024, 1>, 1, 1024);
+    return go(k_add_rmsnorm_mx<FMT, 1024, 2>, 1, 1024);
+  }
+  if (nch <= 64) return go(k_add_rmsnorm_mx<FMT, 32, 2>, 8, kThreads);
+  if (nch <= 128) return go(k_add_rmsnorm_mx<FMT, 32, 4>, 8, kThreads);
+  if (nch <= 256) return go(k_add_rmsnorm_mx<FMT, 256, 1>, 1, 256);
+  if (nch <= 512) return go(k_add_rmsnorm_mx<FMT, 256, 2>, 1, 256);
+  if (nch <= 1024) return go(k_add_rmsnorm_mx<FMT, 256, 4>, 1, 256);
+  return go(k_add_rmsnorm_mx<FMT, 512, 4>, 1, 512);
 }
 
 unsigned group_ctas(const MxRowsArgs& a) {

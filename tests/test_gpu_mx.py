@@ -147,7 +147,9 @@ def test_every_code_and_scale_reads_back(fmt):
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("rows,H,res", [(1, 32, True), (3, 96, False), (130, 1376, True), (7, 2048, True),
-                                        (64, 4096, True), (300, 8192, False), (2, 16384, True), (5, 12320, True)])
+                                        (64, 4096, True), (300, 8192, False), (2, 16384, True), (5, 12320, True),
+                                        (403, 224, True), (331, 480, False), (345, 992, True), (309, 1056, True),
+                                        (310, 4064, True), (307, 8160, True), (306, 16352, True)])
 def test_norm(fmt, rows, H, res):
     gen = torch.Generator().manual_seed(rows + H)
     x = (torch.randn(rows, H, generator=gen) * 3).bfloat16()
