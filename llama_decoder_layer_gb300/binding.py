@@ -553,17 +553,16 @@ class MxMatrix:
         return self.index
 
 
-def _mx_stream(where: str, stream, *things) -> Optional[int]:
+def _mx_stream(where: str, stream, first, *others) -> Optional[int]:
     """The stream's handle, once every tensor and matrix is known to be on the
     current CUDA device, where the call runs."""
-    for t in things:
-        if t.get_device() < 0:
+    device = first.get_device()
+    for t in others:
+        if t.get_device() != device:
             raise LlamaError(LLAMA_ERR_ARG, where)
-    here = torch._C._cuda_getDevice()
-    for t in things:
-        if t.get_device() != here:
-            raise LlamaError(LLAMA_ERR_ARG, where)
-    return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
+    if device < 0 or device != torch._C._cuda_getDevice():
+        raise LlamaError(LLAMA_ERR_ARG, where)
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def _row_stride(t: torch.Tensor, shape, where: str) -> int:
@@ -572,6 +571,13 @@ def _row_stride(t: torch.Tensor, shape, where: str) -> int:
         row, col = t.stride()
         if col == 1:
             return row if shape[0] > 1 else shape[1]
+    raise LlamaError(LLAMA_ERR_ARG, where)
+
+
+def _dense_rows(t: torch.Tensor, m: MxMatrix, where: str) -> int:
+    """The address of t, dense bf16 rows of m's shape, where m is."""
+    if t.dtype is torch.bfloat16 and t.shape == m.shape and t.get_device() == m.index and t.is_contiguous():
+        return t.data_ptr()
     raise LlamaError(LLAMA_ERR_ARG, where)
 
 
@@ -602,15 +608,13 @@ def fused_add_rmsnorm_mx(x: torch.Tensor, residual_in: Optional[torch.Tensor], r
     """fused_add_rmsnorm with the normed rows quantised into out; see
     llama_fused_add_rmsnorm_mx in the header."""
     where = "llama_fused_add_rmsnorm_mx"
-    rows = [t for t in (x, residual_in, residual_out) if t is not None]
-    for t in rows:
-        if t.dtype is not torch.bfloat16 or t.shape != out.shape or not t.is_contiguous():
-            raise LlamaError(LLAMA_ERR_ARG, where)
+    px = _dense_rows(x, out, where)
+    r_in = None if residual_in is None else _dense_rows(residual_in, out, where)
+    r_out = None if residual_out is None else _dense_rows(residual_out, out, where)
     if gamma.dtype is not torch.bfloat16 or gamma.numel() != out.cols or not gamma.is_contiguous():
         raise LlamaError(LLAMA_ERR_ARG, where)
-    s = _mx_stream(where, stream, out, gamma, *rows)
-    st = lib().llama_fused_add_rmsnorm_mx(x.data_ptr(), _ptr(residual_in), _ptr(residual_out), out.ref,
-                                          gamma.data_ptr(), eps, s)
+    s = _mx_stream(where, stream, out, gamma)
+    st = lib().llama_fused_add_rmsnorm_mx(px, r_in, r_out, out.ref, gamma.data_ptr(), eps, s)
     if st:
         raise LlamaError(st, where)
 
