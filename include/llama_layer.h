@@ -428,7 +428,8 @@ int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, c
  * so llama_mx_scale_bytes() counts whole tiles.  Rows past the last one of a
  * scale array may hold any bytes and are left as they are; bytes of groups
  * past a row's last, up to a multiple of four, are zero (the calls below write
- * them so).  cols is a multiple of 32, both arrays are 16-byte aligned.
+ * them so).  cols is a multiple of 32 up to 2^26, both arrays are 16-byte
+ * aligned.  A call's results overlap none of its inputs but where it says so.
  * Quantising: s = e4m3(max |x| / (6 g)) for nvfp4, else the smallest power of two
  * with which no element of the group is beyond the largest code;
  * code = round(x / (s g)); both to nearest, ties to even, saturating (what rounds

@@ -521,7 +521,7 @@ class MxMatrix:
     _FP8), its codes [rows, bytes of a row] and scales, both uint8, and its factor
     g (``scale``, a power of two; 1 but for LLAMA_MX_NVFP4); see the header.  It
     holds the caller's tensors, which keep their memory (no resize_ or set_) while
-    it lives."""
+    it lives, and cannot be changed."""
 
     __slots__ = ("format", "rows", "cols", "codes", "scales", "scale", "shape", "index", "c", "ref")
 
@@ -534,10 +534,14 @@ class MxMatrix:
                 (n == 0 and rows > 0) or codes.numel() != lib().llama_mx_code_bytes(format, rows, cols) or
                 scales.numel() < n):
             raise LlamaError(LLAMA_ERR_ARG, where)
-        self.format, self.rows, self.cols, self.shape = format, rows, cols, (rows, cols)
-        self.codes, self.scales, self.scale, self.index = codes, scales, float(scale), codes.get_device()
-        self.c = LlamaMxMatrix(format, rows, cols, self.scale, codes.data_ptr(), scales.data_ptr())
-        self.ref = ctypes.byref(self.c)
+        c = LlamaMxMatrix(format, rows, cols, float(scale), codes.data_ptr(), scales.data_ptr())
+        for name, value in (("format", format), ("rows", rows), ("cols", cols), ("shape", (rows, cols)),
+                            ("codes", codes), ("scales", scales), ("scale", float(scale)),
+                            ("index", codes.get_device()), ("c", c), ("ref", ctypes.byref(c))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("an MxMatrix cannot be changed")
 
     @staticmethod
     def empty(format: int, rows: int, cols: int, scale: float = 1.0, device="cuda") -> "MxMatrix":

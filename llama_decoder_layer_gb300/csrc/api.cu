@@ -722,8 +722,8 @@ int llama_qk_norm_rope(const LlamaQkNormRopeConfig* cfg, const void* q_norm_w, c
 // Whether there is a matrix of this format and size.
 static int check_mx_size(int format, int rows, int cols) {
   if (format < LLAMA_MX_NVFP4 || format > LLAMA_MX_FP8 || rows < 0 || cols < 1) return LLAMA_ERR_ARG;
-  if (cols % 32) return LLAMA_ERR_UNSUPPORTED;
-  // groups are counted in 32 bits on the device
+  // (stages and groups are counted in 32 bits on the device)
+  if (cols % 32 || cols > (1 << 26)) return LLAMA_ERR_UNSUPPORTED;
   if (static_cast<long long>(rows) * ((cols / mx_group(format) + 3) / 4 * 4) > 0x7fffff00LL) return LLAMA_ERR_UNSUPPORTED;
   return LLAMA_OK;
 }

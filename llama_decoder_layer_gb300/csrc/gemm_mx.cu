@@ -173,10 +173,11 @@ __device__ __forceinline__ void codes32(const MxGemmParams& p, int n, const floa
   }
 }
 
-// g / (1 + exp(-g)).  Below -87 exp(87) stands for exp(-g), so that the sum stays where the hardware's reciprocal is a normal
-// number; one Newton step brings that to the last place.  (A NaN comes back through the product.)
+// g / (1 + exp(-g)), by the hardware's reciprocal and one Newton step to the last place.  Below -87 it is below 2^-118, and
+// -87 stands for g, so that the reciprocal is a normal number.  (A NaN stays one.)
 __device__ __forceinline__ float silu(float g) {
-  const float d = 1.0f + expf(fminf(-g, 87.f));
+  g = g < -87.f ? -87.f : g;
+  const float d = 1.0f + expf(-g);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return g * fmaf(r, fmaf(-d, r, 1.0f), r);
@@ -613,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // accumulators goes into the shared memory of the CTA that finishes its unit (stores to another CTA need no round trip), and
 // is summed there in rank order.  Where the ring leaves room the chunks have a place of their own, so that a CTA need not
 // wait for the others' MMAs before it stores.
+// (Tensor memory: the CTAs of a cluster, which wait for one another, have four stages or more, 80 KB, so that none shares an
+// SM with a CTA of a pair, which holds all of its tensor memory and waits for its peer.)
 // ---------------------------------------------------------------------------
 constexpr int kSplitCols = 128;
 constexpr int kSplitTmemCols = 256;
@@ -1047,8 +1050,9 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
     if (static_cast<long long>(p.tiles) * n <= sms && p.kb >= 4 * n &&
         R::recv_bytes(n, p.a_rows) <= kRingBudget / stage_bytes * stage_bytes && max_active_splits(n) >= p.tiles)
       S = n;
-  const bool pair = use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
-                              (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
+  const int pairs = max_active_pairs<FMT, EPI>();
+  const bool pair = pairs > 0 && use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
+                                           (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
   MxMaps maps{};
   const int w_box = !pair && is_silu(EPI) ? 64 : 128;
   bool ok = operand_maps(&maps.x, pair ? &maps.x_scales : nullptr, a.x, a.M, row_bytes, ktiles, T::kTiles,
@@ -1068,8 +1072,6 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   }
   if (!ok) return cudaErrorInvalidValue;
   if (pair) {
-    const int pairs = max_active_pairs<FMT, EPI>();
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
     p.tiles_m = pair_m;
     p.tiles_n = pair_n;
     p.tiles = pair_m * pair_n;

@@ -20,6 +20,10 @@ Tolerances.
   silu(g) matters).
 """
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -339,6 +343,65 @@ def test_no_rows():
         lb.linear_mx(x, w, torch.empty(0, 32, device=DEV))
         lb.gate_up_silu_mx(x, w, w, lb.MxMatrix.empty(fmt, 0, 32))
     ok()
+
+
+@pytest.mark.parametrize("M,I", [(3, 64), (2600, 2080)])
+@pytest.mark.parametrize("out_fmt", [0, R.FP8])
+def test_silu_far_out(M, I, out_fmt):
+    """Gate sums from -3e38 to 3e38, and zero: silu is g or 0 there, and never a NaN; a sum beyond fp32 is an infinity."""
+    K = 32
+    xv, gv, uv = np.zeros((M, K)), np.zeros((I, K)), np.zeros((I, K))
+    xv[:, 0], uv[:, 0] = 1.0, 0.5
+    powers = np.array([-384.0, -3.0, -0.875, 0.0, 0.75, 3.0, 416.0, 0.25])
+    gv[:, 0] = powers[np.arange(I) % 8]
+    one = lambda v: lb.MxMatrix(R.FP8, K, *(torch.from_numpy(t).to(DEV) for t in R.pack(  # noqa: E731
+        v, np.full((len(v), 1), 127), R.FP8)))
+    for alpha in (1.0, 100.0, 1e20, 2.0 ** 119):  # 2^119: 384 gives 2.6e38, 416 2.8e38
+        out = empty(out_fmt, M, I) if out_fmt else torch.empty(M, I, dtype=torch.bfloat16, device=DEV)
+        lb.gate_up_silu_mx(one(xv), one(gv), one(uv), out, alpha_gate=alpha)
+        ok()
+        g = (xv @ gv.T) * np.float64(np.float32(alpha))
+        want = np.where(g < -700, 0.0, g / (1 + np.exp(np.minimum(-g, 700)))) * 0.5
+        slack = np.abs(want) * 2.0 ** -18 + 2.0 ** -110  # (silu(-87) is below 2^-118)
+        if out_fmt:
+            R.check_quantised(out.codes.cpu().numpy(), out.scales.cpu().numpy(), want, slack, out_fmt, 1.0)
+        else:
+            assert (np.abs(f64(out) - want) <= slack + np.abs(want) * BF16).all()
+    out = torch.empty(M, I, dtype=torch.bfloat16, device=DEV)
+    lb.gate_up_silu_mx(one(xv), one(gv), one(uv), out, alpha_gate=3e38)  # 416 * 3e38: infinite
+    ok()
+    o = f64(out)
+    assert (o[:, 6::8] == np.inf).all() and (np.abs(o[:, 0::8]) <= 2.0 ** -110).all() and (o[:, 3::8] == 0).all()
+
+
+FIRST_UNDER_CAPTURE = """
+import torch
+from llama_decoder_layer_gb300 import binding as lb
+F = lb.LLAMA_MX_NVFP4
+x, w = (torch.randn(n, 512, device="cuda").bfloat16() for n in (M, 2056))
+mx, mw = lb.MxMatrix.empty(F, M, 512, 2.0 ** -6), lb.MxMatrix.empty(F, 2056, 512, 2.0 ** -6)
+res, g = torch.empty_like(x), torch.ones(512, dtype=torch.bfloat16, device="cuda")
+out, eager = torch.empty(M, 2056, device="cuda"), torch.empty(M, 2056, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    lb.quantize_mx(w, mw)
+    lb.fused_add_rmsnorm_mx(x, None, res, mx, g, 1e-5)
+    lb.linear_mx(mx, mw, out)
+graph.replay()
+torch.cuda.synchronize()
+lb.linear_mx(mx, mw, eager)
+torch.cuda.synchronize()
+assert lb.get_device_error()[0] == 0 and torch.equal(out, eager) and bool(out.abs().sum() > 0)
+print("same")
+"""
+
+
+@pytest.mark.parametrize("M", [2, 3000])
+def test_the_first_calls_of_a_process_may_be_captured(M):
+    r = subprocess.run([sys.executable, "-c", f"M = {M}\n" + FIRST_UNDER_CAPTURE], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 class Mlp:

@@ -68,7 +68,8 @@ def test_sizes(lib):
     assert lib.llama_mx_scale_bytes(R.NVFP4, 129, 96) == 2 * 2 * 512
     assert lib.llama_mx_scale_bytes(R.FP4, 128, 96) == 512 and lib.llama_mx_scale_bytes(R.FP8, 1, 160) == 1024
     assert lib.llama_mx_scale_bytes(R.FP8, 0, 160) == 0
-    for fmt, rows, cols in ((0, 4, 64), (4, 4, 64), (1, -1, 64), (1, 4, 0), (1, 4, 48), (3, 4, 100), (1, 1 << 30, 64)):
+    for fmt, rows, cols in ((0, 4, 64), (4, 4, 64), (1, -1, 64), (1, 4, 0), (1, 4, 48), (3, 4, 100), (1, 1 << 30, 64),
+                            (2, 1, (1 << 26) + 32)):
         assert lib.llama_mx_code_bytes(fmt, rows, cols) == 0 and lib.llama_mx_scale_bytes(fmt, rows, cols) == 0
 
 
@@ -151,6 +152,14 @@ def test_binding_refuses_what_is_not_a_matrix():
     for fmt, rows, cols in ((0, 3, 64), (R.FP4, -1, 64), (R.FP4, 3, 40)):
         with pytest.raises(lb.LlamaError):
             lb.MxMatrix.empty(fmt, rows, cols, device="cpu")
+
+
+def test_a_matrix_cannot_be_changed():
+    m = lb.MxMatrix.empty(R.NVFP4, 3, 64, 0.5, device="cpu")
+    assert (m.c.format, m.c.rows, m.c.cols, m.c.g, m.c.codes) == (R.NVFP4, 3, 64, 0.5, m.codes.data_ptr())
+    for name in ("scale", "codes", "rows"):
+        with pytest.raises(AttributeError):
+            setattr(m, name, getattr(m, name))
 
 
 def test_binding_refuses_tensors_of_another_kind():
