@@ -557,6 +557,9 @@ class MxMatrix:
         return self.index
 
 
+_BF16, _CUDA = torch.bfloat16, torch._C  # (looked up once: a call has some ten such steps of 50 ns)
+
+
 def _mx_stream(where: str, stream, first, *others) -> Optional[int]:
     """The stream's handle, once every tensor and matrix is known to be on the
     current CUDA device, where the call runs."""
@@ -564,23 +567,26 @@ def _mx_stream(where: str, stream, first, *others) -> Optional[int]:
     for t in others:
         if t.get_device() != device:
             raise LlamaError(LLAMA_ERR_ARG, where)
-    if device < 0 or device != torch._C._cuda_getDevice():
+    if device < 0 or device != _CUDA._cuda_getDevice():
         raise LlamaError(LLAMA_ERR_ARG, where)
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    return _CUDA._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
-def _row_stride(t: torch.Tensor, shape, where: str) -> int:
-    """Elements from one row to the next of t [rows, cols] bf16, whose rows are dense."""
-    if t.dtype is torch.bfloat16 and t.shape == shape:
+def _rows_of(t: torch.Tensor, m: MxMatrix, where: str, stream):
+    """(elements from one row to the next of t, bf16 rows of m's shape where m is; the stream's handle)."""
+    if t.dtype is _BF16 and t.shape == m.shape:
         row, col = t.stride()
         if col == 1:
-            return row if shape[0] > 1 else shape[1]
+            device = t.get_device()
+            if device == m.index and device >= 0 and device == _CUDA._cuda_getDevice():
+                return (row if m.rows > 1 else m.cols,
+                        _CUDA._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     raise LlamaError(LLAMA_ERR_ARG, where)
 
 
 def _dense_rows(t: torch.Tensor, m: MxMatrix, where: str) -> int:
     """The address of t, dense bf16 rows of m's shape, where m is."""
-    if t.dtype is torch.bfloat16 and t.shape == m.shape and t.get_device() == m.index and t.is_contiguous():
+    if t.dtype is _BF16 and t.shape == m.shape and t.get_device() == m.index and t.is_contiguous():
         return t.data_ptr()
     raise LlamaError(LLAMA_ERR_ARG, where)
 
@@ -589,8 +595,7 @@ def quantize_mx(x: torch.Tensor, out: MxMatrix, stream=None) -> None:
     """x [rows, cols] bf16 (any stride between rows) quantised into out; see
     llama_quantize_mx in the header."""
     where = "llama_quantize_mx"
-    stride = _row_stride(x, out.shape, where)
-    s = _mx_stream(where, stream, x, out)
+    stride, s = _rows_of(x, out, where, stream)
     st = lib().llama_quantize_mx(x.data_ptr(), stride, out.ref, s)
     if st:
         raise LlamaError(st, where)
@@ -600,8 +605,7 @@ def dequantize_mx(m: MxMatrix, out: torch.Tensor, stream=None) -> None:
     """The values of m as bf16, into out [rows, cols] (any stride between
     rows); see llama_dequantize_mx in the header."""
     where = "llama_dequantize_mx"
-    stride = _row_stride(out, m.shape, where)
-    s = _mx_stream(where, stream, m, out)
+    stride, s = _rows_of(out, m, where, stream)
     st = lib().llama_dequantize_mx(m.ref, out.data_ptr(), stride, s)
     if st:
         raise LlamaError(st, where)
@@ -615,7 +619,7 @@ def fused_add_rmsnorm_mx(x: torch.Tensor, residual_in: Optional[torch.Tensor], r
     px = _dense_rows(x, out, where)
     r_in = None if residual_in is None else _dense_rows(residual_in, out, where)
     r_out = None if residual_out is None else _dense_rows(residual_out, out, where)
-    if gamma.dtype is not torch.bfloat16 or gamma.numel() != out.cols or not gamma.is_contiguous():
+    if gamma.dtype is not _BF16 or gamma.numel() != out.cols or not gamma.is_contiguous():
         raise LlamaError(LLAMA_ERR_ARG, where)
     s = _mx_stream(where, stream, out, gamma)
     st = lib().llama_fused_add_rmsnorm_mx(px, r_in, r_out, out.ref, gamma.data_ptr(), eps, s)

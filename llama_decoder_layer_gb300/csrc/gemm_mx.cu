@@ -59,9 +59,9 @@ struct Stage {
   static constexpr bool kE8m0 = FMT != kMxNvfp4;
 };
 
-// Tensor maps: codes in boxes of 128 rows x 128 bytes, swizzled; scales in boxes of a stage's tiles of 128 rows, as
-// 8-byte elements; the results in boxes of 32 rows x 128 bytes (4-bit codes: 64), swizzled.  What lies outside reads as zero
-// and is not written.
+// Tensor maps: codes in boxes of up to 128 rows x 128 bytes, swizzled; for pairs also the scales, in boxes of a stage's tiles
+// of 128 rows, as 8-byte elements, and the results in boxes of 32 rows x 128 bytes (4-bit codes: 64), swizzled.  What lies
+// outside reads as zero and is not written.
 struct MxMaps {
   CUtensorMap x, x_scales, w[2], w_scales[2], out;
 };
@@ -612,12 +612,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Few tiles (decode batches), bound by the weights' bytes (70B down projection, nvfp4: 24.2 us for one row, 6.4 TB/s but for
-// 3.5 us of set-up and exchange, 26.4 for 128 rows): tiles of 128 x 128 (silu: 64 gate and 64 up columns), K split over the CTAs of a cluster, CTA
-// rank r over stages [r kb / S, (r + 1) kb / S).  Two CTAs an SM where there are more CTAs than SMs: they stream weights at
-// the rate of HBM whatever their number on an SM, so a wave need not be whole.  Every 32-column chunk of the CTAs'
-// accumulators goes into the shared memory of the CTA that finishes its unit (stores to another CTA need no round trip), and
-// is summed there in rank order.  Where the ring leaves room the chunks have a place of their own, so that a CTA need not
-// wait for the others' MMAs before it stores.
+// 3.5 us of set-up and exchange, 26.4 for 128 rows): tiles of 128 x 128 (silu: 64 gate and 64 up columns), K split over the
+// CTAs of a cluster, CTA rank r over stages [r kb / S, (r + 1) kb / S).  Two CTAs an SM where there are more CTAs than SMs:
+// they stream weights at the rate of HBM whatever their number on an SM, so a wave need not be whole.  Every 32-column chunk
+// of the CTAs' accumulators goes into the shared memory of the CTA that finishes its unit (stores to another CTA need no
+// round trip), and is summed there in rank order.  Where the ring leaves room the chunks have a place of their own, so that
+// a CTA need not wait for the others' MMAs before it stores.
 // (Tensor memory: the CTAs of a cluster, which wait for one another, have four stages or more, 80 KB, so that none shares an
 // SM with a CTA of a pair, which holds all of its tensor memory and waits for its peer.)
 // ---------------------------------------------------------------------------
@@ -953,8 +953,7 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, long 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// the maps of one operand of `rows` rows
-// (scales null: they are copied untiled)
+// the maps of one operand of `rows` rows (scales null: they are copied untiled)
 bool operand_maps(CUtensorMap* codes, CUtensorMap* scales, const MxOperand& o, int rows, long long row_bytes, int ktiles,
                   int stage_tiles, int box_rows) {
   return encode_2d(codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, row_bytes, rows, row_bytes, kRowBytes, box_rows,
