@@ -612,14 +612,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------
 // Few tiles (decode batches), bound by the weights' bytes (70B down projection, nvfp4: 24.2 us for one row, 6.4 TB/s but for
-// 3.5 us of set-up and exchange, 26.4 for 128 rows): tiles of 128 x 128 (silu: 64 gate and 64 up columns), K split over the
+// 3.5 us of set-up and exchange, 25.8 for 128 rows): tiles of 128 x 128 (silu: 64 gate and 64 up columns), K split over the
 // CTAs of a cluster, CTA rank r over stages [r kb / S, (r + 1) kb / S).  Two CTAs an SM where there are more CTAs than SMs:
 // they stream weights at the rate of HBM whatever their number on an SM, so a wave need not be whole.  Every 32-column chunk
 // of the CTAs' accumulators goes into the shared memory of the CTA that finishes its unit (stores to another CTA need no
-// round trip), and is summed there in rank order.  Where the ring leaves room the chunks have a place of their own, so that
-// a CTA need not wait for the others' MMAs before it stores.
-// (Tensor memory: the CTAs of a cluster, which wait for one another, have four stages or more, 80 KB, so that none shares an
-// SM with a CTA of a pair, which holds all of its tensor memory and waits for its peer.)
+// round trip) and is summed there in rank order; that CTA's own part stays in its tensor memory.  Where two stages less of
+// the ring leave room the chunks have a place of their own, so that a CTA need not wait for the others' MMAs before it
+// stores (operands read from HBM, without either and with both: 421 x 1384 x 2080, fp8, 7.9 and 7.2 us; 128 x 4096 x 14336,
+// nvfp4, 11.8 and 11.2; 128 x 8192 x 28672 28.2 and 27.5; one row of 4096 x 4096 5.5 and 5.6).
+// (Tensor memory: the CTAs of a cluster, which wait for one another, hold four stages, 80 KB, or more, or else two or three
+// and received chunks up to the whole budget, so that none shares an SM with a CTA of a pair, which holds all of its tensor
+// memory and waits for its peer.)
 // ---------------------------------------------------------------------------
 constexpr int kSplitCols = 128;
 constexpr int kSplitTmemCols = 256;
@@ -634,9 +637,9 @@ struct SplitStage {
   static constexpr int kTsa = kSplitCols, kTsb = kTsa + 4 * Stage<FMT>::kTiles;  // tensor memory of the scales
   static_assert(kTsb + 8 * Stage<FMT>::kTiles <= kSplitTmemCols, "tensor memory");
   __host__ __device__ static constexpr int bytes(int a_rows) { return a_rows * kRowBytes + kB + kSa + kSb; }
-  // chunks that a CTA of S receives from each, and the bytes of them all, `rows` accumulator rows each
+  // chunks that a CTA of S receives from each of the others, and the bytes of them all, `rows` accumulator rows each
   __host__ __device__ static constexpr int local_chunks(int S) { return (kUnits + S - 1) / S * kChunks; }
-  __host__ __device__ static constexpr int recv_bytes(int S, int rows) { return S * local_chunks(S) * rows * 128; }
+  __host__ __device__ static constexpr int recv_bytes(int S, int rows) { return (S - 1) * local_chunks(S) * rows * 128; }
 };
 
 // The scale bytes of a unit (32 outputs from column n on), and zeros for the groups that fill up the row's last word.
@@ -658,24 +661,34 @@ struct TmemLoader {
   __device__ __forceinline__ void operator()(int col, float (&v)[32]) const { tmem_ld32(taddr + col, v); }
 };
 
-// Receive buffer of a CTA: [source rank][local chunk][8 float4 columns][rows], so that a warp's rows are contiguous.
-__device__ __forceinline__ uint32_t recv_at(int s, int nloc, int li, int q, int row, int rows) {
-  return static_cast<uint32_t>((((s * nloc + li) * 8 + q) * rows + row) * 16);
+// Receive buffer of CTA `to`: [source rank, without its own][local chunk][8 float4 columns][rows], so that a warp's rows are
+// contiguous.
+__device__ __forceinline__ uint32_t recv_at(int from, int to, int nloc, int li, int q, int row, int rows) {
+  return static_cast<uint32_t>(((((from < to ? from : from - 1) * nloc + li) * 8 + q) * rows + row) * 16);
 }
 
+// The sum over the CTAs in rank order: this CTA's part from tensor memory, the others' from where they stored them.
 template <class R>
-struct RecvLoader {
+struct SumLoader {
+  uint32_t taddr;
   const uint8_t* recv;
-  int ctas, nloc, row, rows;
+  int ctas, rank, nloc, row, rows;
   __device__ __forceinline__ void operator()(int col, float (&v)[32]) const {
     const int c = col / 32, u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits;
+    float own[32];
+    tmem_ld32(taddr + col, own);
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = 0.f;
 #pragma unroll 2
     for (int s = 0; s < ctas; ++s) {
+      if (s == rank) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] += own[e];
+        continue;
+      }
       float4 t[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) t[q] = *reinterpret_cast<const float4*>(recv + recv_at(s, nloc, li, q, row, rows));
+      for (int q = 0; q < 8; ++q) t[q] = *reinterpret_cast<const float4*>(recv + recv_at(s, rank, nloc, li, q, row, rows));
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         v[4 * q] += t[q].x;
@@ -733,7 +746,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull_bar, 1);
-    mbar_init(recv_bar, ctas * min((p.M - tm * BM + 31) / 32, 4));  // an arrival of every warp that has rows, in every CTA
+    // an arrival of every warp that has rows, in every other CTA
+    mbar_init(recv_bar, max(ctas - 1, 1) * min((p.M - tm * BM + 31) / 32, 4));
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.x);
@@ -872,17 +886,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     if (p.recv_at == 0) cluster_arrive();  // this CTA's MMAs and copies are done: its ring may be written
     cluster_wait();
-    const bool has_rows = tm * BM + quad * 32 < p.M;
-    if (warp >= 2 && has_rows) {
+    const bool has_rows = warp >= 2 && tm * BM + quad * 32 < p.M;
+    const int row_in_tile = quad * 32 + lane;
+    if (has_rows) {
 #pragma unroll 1
       for (int c = 0; c < kSplitCols / 32; ++c) {
-        const int u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits;
+        const int u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits, to = u % ctas;
+        if (to == rank) continue;
         uint32_t r[32];
         tmem_ld32_async(taddr + 32 * c, r);
         tmem_ld_wait(r);
-        const uint32_t dst = mapa_shared(recv + recv_at(rank, nloc, li, 0, quad * 32 + lane, p.a_rows),
-                                         static_cast<uint32_t>(u % ctas));
-        if (tm * BM + quad * 32 + lane < p.M) {  // (other rows' sums are never looked at)
+        const uint32_t dst = mapa_shared(recv + recv_at(rank, to, nloc, li, 0, row_in_tile, p.a_rows), static_cast<uint32_t>(to));
+        if (tm * BM + row_in_tile < p.M) {  // (other rows' sums are never looked at)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             st_cluster_f4(dst + q * p.a_rows * 16,
@@ -891,25 +906,18 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       __syncwarp();
-      if (lane < min(R::kUnits, ctas)) mbar_arrive_cluster(mapa_shared(recv_bar, lane));
+      if (lane < min(R::kUnits, ctas) && lane != rank) mbar_arrive_cluster(mapa_shared(recv_bar, lane));
     }
     __syncwarp();
     cluster_arrive();  // this CTA writes to no other any more
-    if (rank < R::kUnits && !*abort_flag) {
-      if (!mbar_wait_cluster(recv_bar, 0)) {
+    if (has_rows && rank < R::kUnits) {
+      if (!warp_same(mbar_wait_cluster(recv_bar, 0))) {
         if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
         *abort_flag = 1;
       } else {
-        // this CTA's units, row group by row group, spread over its warps
-        int item = 0;
+        const SumLoader<R> ld{taddr, smem_raw + pad + p.recv_at, ctas, rank, nloc, row_in_tile, p.a_rows};
 #pragma unroll 1
-        for (int u = rank; u < R::kUnits; u += ctas)
-#pragma unroll 1
-          for (int g = 0; g < 4 && tm * BM + g * 32 < p.M; ++g)
-            if (item++ % (kThreads / 32) == warp) {
-              const RecvLoader<R> ld{smem_raw + pad + p.recv_at, ctas, nloc, g * 32 + lane, p.a_rows};
-              split_unit<EPI>(p, tm * BM + g * 32 + lane, tn, u, ld);
-            }
+        for (int u = rank; u < R::kUnits; u += ctas) split_unit<EPI>(p, tm * BM + row_in_tile, tn, u, ld);
       }
     }
     __syncwarp();
@@ -1094,17 +1102,15 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   for (int i = 0; i < 2; ++i) p.w_scales[i] = static_cast<const uint8_t*>(a.w[i].scales);
   const int ctas = p.tiles * S, budget = ctas > sms ? kMaxSmemBytes / 2 - 1024 - 2048 : kRingBudget;
   const int fill = (p.kb + S - 1) / S;  // stages that a CTA fills
-  p.stages = budget / stage_bytes < kMaxStages ? budget / stage_bytes : kMaxStages;
-  if (p.stages > fill) p.stages = fill;
-  p.meta_at = p.stages * stage_bytes;
-  if (S > 1) {
-    const int recv = R::recv_bytes(S, p.a_rows);
-    if (p.meta_at + recv <= budget) {
-      p.recv_at = p.meta_at;
-      p.meta_at += recv;
-    } else if (p.meta_at < recv) {
-      p.meta_at = recv;
-    }
+  const int recv = S > 1 ? R::recv_bytes(S, p.a_rows) : 0;
+  auto stages = [&](int bytes) { return std::min({bytes / stage_bytes, kMaxStages, fill}); };
+  p.stages = stages(budget);
+  p.meta_at = std::max(p.stages * stage_bytes, recv);
+  // (a split has four stages to fill or more, so that two at least are left)
+  if (S > 1 && stages(budget - recv) >= p.stages - 2) {
+    p.stages = stages(budget - recv);
+    p.recv_at = p.stages * stage_bytes;
+    p.meta_at = p.recv_at + recv;
   }
   return launch_kernel_cluster(k_gemm_mx_split<FMT, EPI>, dim3(ctas), dim3(kThreads), static_cast<size_t>(p.meta_at) + 2048, s,
                                true, S, maps, p);
