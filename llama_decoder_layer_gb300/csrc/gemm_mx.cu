@@ -620,6 +620,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the ring leave room the chunks have a place of their own, so that a CTA need not wait for the others' MMAs before it
 // stores (operands read from HBM, without either and with both: 421 x 1384 x 2080, fp8, 7.9 and 7.2 us; 128 x 4096 x 14336,
 // nvfp4, 11.8 and 11.2; 128 x 8192 x 28672 28.2 and 27.5; one row of 4096 x 4096 5.5 and 5.6).
+// fp8: the tensor cores cut a sum's low bits at every step, so that the error grows with the steps (against 64 bits, rms over
+// the mean size: 4096 elements in one chain 2.6e-7, fp32 itself 1.0e-7).  A CTA of kHalvedStages or more begins a second
+// accumulator half way, and the halves are added in fp32: 1.4e-7, and 1.1 to 5.9e-7 for 16384 elements where one chain has
+// 1.5 to 14e-7.  The MMAs wait meanwhile until the columns that the second half's scales take are read (64 x 4096 x 14336
+// 13.5 us without it and 13.8 with; 128 x 8192 x 8192 16.9 and 17.25).  Sums of 4-bit products are exact or nearly so.
 // (Tensor memory: the CTAs of a cluster, which wait for one another, hold four stages, 80 KB, or more, or else two or three
 // and received chunks up to the whole budget, so that none shares an SM with a CTA of a pair, which holds all of its tensor
 // memory and waits for its peer.)
@@ -627,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kSplitCols = 128;
 constexpr int kSplitTmemCols = 256;
 constexpr int kSplitMaxCluster = 8;
+constexpr int kHalvedStages = 16;  // a chain of 11 stages is as near as fp32: 1.0e-7, both
 
 template <int FMT, int EPI>
 struct SplitStage {
@@ -634,8 +640,10 @@ struct SplitStage {
   static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = kSa * (is_silu(EPI) ? 2 : 1);
   static constexpr int kUnits = is_silu(EPI) ? 2 : 4;          // 32 outputs each
   static constexpr int kChunks = is_silu(EPI) ? 2 : 1;         // accumulator chunks of a unit: gate, up
-  static constexpr int kTsa = kSplitCols, kTsb = kTsa + 4 * Stage<FMT>::kTiles;  // tensor memory of the scales
-  static_assert(kTsb + 8 * Stage<FMT>::kTiles <= kSplitTmemCols, "tensor memory");
+  // columns of the scales, and of them all
+  static constexpr int kTsa = 0, kTsb = 4 * Stage<FMT>::kTiles, kTsCols = kTsb + 8 * Stage<FMT>::kTiles;
+  static constexpr bool kHalves = Stage<FMT>::kBits == 8;
+  static_assert(kSplitCols + kTsCols <= kSplitTmemCols && (!kHalves || kTsCols <= 32), "tensor memory");
   __host__ __device__ static constexpr int bytes(int a_rows) { return a_rows * kRowBytes + kB + kSa + kSb; }
   // chunks that a CTA of S receives from each of the others, and the bytes of them all, `rows` accumulator rows each
   __host__ __device__ static constexpr int local_chunks(int S) { return (kUnits + S - 1) / S * kChunks; }
@@ -656,9 +664,26 @@ __device__ __forceinline__ void store_unit_scales(const MxGemmParams& p, int row
     for (int g = g0 + kGroups; g < 4 * p.out_ktiles; ++g) p.out_scales[mx_scale_at(row, g >> 2, p.out_ktiles) + (g & 3)] = 0;
 }
 
-struct TmemLoader {
+// This CTA's sums; if `halves`, of two accumulators, the first's columns 0 to 31 in registers.
+template <int FMT>
+struct OwnLoader {
   uint32_t taddr;
-  __device__ __forceinline__ void operator()(int col, float (&v)[32]) const { tmem_ld32(taddr + col, v); }
+  bool halves;
+  const uint32_t (&first)[32];
+  __device__ __forceinline__ void operator()(int col, float (&v)[32]) const {
+    tmem_ld32(taddr + col, v);
+    if constexpr (Stage<FMT>::kBits == 8) {
+      if (!halves) return;
+      if (col == 0) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(first[e]);
+      }
+      float second[32];
+      tmem_ld32(taddr + kSplitCols + col, second);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e] += second[e];
+    }
+  }
 };
 
 // Receive buffer of CTA `to`: [source rank, without its own][local chunk][8 float4 columns][rows], so that a warp's rows are
@@ -668,15 +693,15 @@ __device__ __forceinline__ uint32_t recv_at(int from, int to, int nloc, int li, 
 }
 
 // The sum over the CTAs in rank order: this CTA's part from tensor memory, the others' from where they stored them.
-template <class R>
+template <class R, class Own>
 struct SumLoader {
-  uint32_t taddr;
+  const Own& mine;
   const uint8_t* recv;
   int ctas, rank, nloc, row, rows;
   __device__ __forceinline__ void operator()(int col, float (&v)[32]) const {
     const int c = col / 32, u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits;
     float own[32];
-    tmem_ld32(taddr + col, own);
+    mine(col, own);
 #pragma unroll
     for (int e = 0; e < 32; ++e) v[e] = 0.f;
 #pragma unroll 2
@@ -727,16 +752,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int nst = p.stages, a_bytes = p.a_rows * kRowBytes, tile_bytes = a_bytes + R::kB;
   const uint32_t scales = sbase + nst * tile_bytes;
   uint8_t* meta = smem_raw + pad + p.meta_at;
-  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull, recv
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 2));
+  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull, recv, half, saved
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 4));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
-  const uint32_t tfull_bar = bar0 + 8u * (2 * nst), recv_bar = bar0 + 8u * (2 * nst + 1);
+  const uint32_t tfull_bar = bar0 + 8u * (2 * nst), recv_bar = tfull_bar + 8, half_bar = tfull_bar + 16, saved_bar = tfull_bar + 24;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int kb0 = rank * p.kb / ctas, kb1 = (rank + 1) * p.kb / ctas;
+  const bool halves = R::kHalves && kb1 - kb0 >= kHalvedStages;
+  const int kb_half = halves ? (kb0 + kb1) / 2 : kb1;
   int tm, tn;
   tile_coords(p, static_cast<int>(blockIdx.x) / ctas, tm, tn);
 
@@ -746,6 +773,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull_bar, 1);
+    mbar_init(half_bar, 1);
+    mbar_init(saved_bar, 4);  // an arrival of every warp that finishes rows
     // an arrival of every warp that has rows, in every other CTA
     mbar_init(recv_bar, max(ctas - 1, 1) * min((p.M - tm * BM + 31) / 32, 4));
     *abort_flag = 0;
@@ -817,10 +846,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---------------- MMAs ----------------
     constexpr uint32_t idesc = idesc_mx(BM, is_silu(EPI) ? 64 : 128, S::kBits, S::kE8m0);
     const uint32_t gate_cols = is_silu(EPI) ? (tn & 1) * 2 : 0;  // a tile's 64 rows of w in their 128-row scale tile
-    int stage = 0;
-    uint32_t phase = 0;
+    int stage = 0, first = kb0;
+    uint32_t phase = 0, acc = tmem_base, ts = tmem_base + kSplitCols;  // the accumulator, the scales
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
+      if (R::kHalves && kb == kb_half) {
+        if (elect_one()) tc_commit(half_bar);
+        __syncwarp();
+        if (!warp_same(mbar_wait(saved_bar, 0, abort_flag))) {
+          ok = false;
+          break;
+        }
+        first = kb;
+        acc = tmem_base + kSplitCols;
+        ts = tmem_base;
+      }
       if (!warp_same(mbar_wait(full_bar(stage), phase, abort_flag))) {
         ok = false;
         break;
@@ -831,10 +871,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t ssa = scales + stage * (R::kSa + R::kSb), ssb = ssa + R::kSa;
 #pragma unroll
         for (int i = 0; i < S::kTiles; ++i) {
-          tc_copy_scales<false>(tmem_base + R::kTsa + 4 * i, smem_desc_scales(ssa + i * kMxTileBytes));
+          tc_copy_scales<false>(ts + R::kTsa + 4 * i, smem_desc_scales(ssa + i * kMxTileBytes));
 #pragma unroll
           for (int j = 0; j < R::kChunks; ++j)
-            tc_copy_scales<false>(tmem_base + R::kTsb + 4 * (R::kChunks * i + j),
+            tc_copy_scales<false>(ts + R::kTsb + 4 * (R::kChunks * i + j),
                                   smem_desc_scales(ssb + j * R::kSa + i * kMxTileBytes));
         }
         const int steps = kb + 1 < p.kb ? S::kSteps : p.last_steps;
@@ -845,9 +885,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int j = 0; j < R::kChunks; ++j)
             tc_mma_mx<S::kBits, S::kStepScales, false>(
-                tmem_base + 64 * j, smem_desc_sw128(sa + 32 * k), smem_desc_sw128(sb + j * (R::kB / 2) + 32 * k),
-                idesc_mx_scale(idesc, k % S::kPerTile * S::kStepScales), tmem_base + R::kTsa + 4 * i,
-                tmem_base + R::kTsb + 4 * (R::kChunks * i + j) + gate_cols, kb > kb0 || k > 0 ? 1u : 0u);
+                acc + 64 * j, smem_desc_sw128(sa + 32 * k), smem_desc_sw128(sb + j * (R::kB / 2) + 32 * k),
+                idesc_mx_scale(idesc, k % S::kPerTile * S::kStepScales), ts + R::kTsa + 4 * i,
+                ts + R::kTsb + 4 * (R::kChunks * i + j) + gate_cols, kb > first || k > 0 ? 1u : 0u);
         }
         tc_commit(empty_bar(stage));
       }
@@ -865,20 +905,34 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (elect_one()) tc_commit(tfull_bar);
     __syncwarp();
   }
+  const int quad = warp & 3;  // tensor-memory lane quarter this warp may access
+  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+  uint32_t first[32];  // the first half's sums of columns 0 to 31, where the second half's scales go
+  if (halves && warp >= 2) {
+    if (warp_same(mbar_wait(half_bar, 0, abort_flag))) {
+      tc_fence_after();
+      tmem_ld32_async(taddr, first);
+      tmem_ld_wait(first);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(saved_bar);
+    } else {
+      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
+      *abort_flag = 1;
+    }
+  }
   if (!mbar_wait(tfull_bar, 0, nullptr)) {
     if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
     *abort_flag = 1;
   }
   tc_fence_after();
 
-  const int quad = warp & 3;  // tensor-memory lane quarter this warp may access
-  const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+  const OwnLoader<FMT> mine{taddr, halves, first};
   if (ctas == 1) {
     __syncthreads();
     if (warp >= 2 && !*abort_flag && tm * BM + quad * 32 < p.M) {
-      const TmemLoader ld{taddr};
 #pragma unroll 1
-      for (int u = 0; u < R::kUnits; ++u) split_unit<EPI>(p, tm * BM + quad * 32 + lane, tn, u, ld);
+      for (int u = 0; u < R::kUnits; ++u) split_unit<EPI>(p, tm * BM + quad * 32 + lane, tn, u, mine);
     }
   } else {
     const int nloc = R::local_chunks(ctas);
@@ -893,16 +947,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int c = 0; c < kSplitCols / 32; ++c) {
         const int u = c % R::kUnits, li = u / ctas * R::kChunks + c / R::kUnits, to = u % ctas;
         if (to == rank) continue;
-        uint32_t r[32];
-        tmem_ld32_async(taddr + 32 * c, r);
-        tmem_ld_wait(r);
+        float v[32];
+        mine(32 * c, v);
         const uint32_t dst = mapa_shared(recv + recv_at(rank, to, nloc, li, 0, row_in_tile, p.a_rows), static_cast<uint32_t>(to));
         if (tm * BM + row_in_tile < p.M) {  // (other rows' sums are never looked at)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            st_cluster_f4(dst + q * p.a_rows * 16,
-                          make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), __uint_as_float(r[4 * q + 2]),
-                                      __uint_as_float(r[4 * q + 3])));
+            st_cluster_f4(dst + q * p.a_rows * 16, make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]));
         }
       }
       __syncwarp();
@@ -915,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
         *abort_flag = 1;
       } else {
-        const SumLoader<R> ld{taddr, smem_raw + pad + p.recv_at, ctas, rank, nloc, row_in_tile, p.a_rows};
+        const SumLoader<R, OwnLoader<FMT>> ld{mine, smem_raw + pad + p.recv_at, ctas, rank, nloc, row_in_tile, p.a_rows};
 #pragma unroll 1
         for (int u = rank; u < R::kUnits; u += ctas) split_unit<EPI>(p, tm * BM + row_in_tile, tn, u, ld);
       }

@@ -263,6 +263,14 @@ def test_linear(fmt, M, N, K, dtype):
     assert (err <= bar).all(), (err.max(), bar[err > bar][:5], np.argwhere(err > bar)[:5])
 
 
+# K of a block from 15 to 17 stages of 128 elements on, where fp8 sums are of two
+# accumulators: not split with one block an SM and with two, split in two, in eight
+@pytest.mark.parametrize("M,N,K", [(40, 9864, 1920), (40, 9864, 2048), (33, 9864, 2112), (64, 19464, 2080), (130, 4864, 4160),
+                                   (1, 424, 16544), (65, 424, 16416), (128, 1032, 16384), (128, 136, 32800)])
+def test_linear_long_sums(M, N, K):
+    test_linear(R.FP8, M, N, K, torch.float32)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,I,K,out_fmt", [(1, 32, 32, 0), (1, 128, 64, 3), (3, 136, 96, 0), (64, 1376, 512, 3),
                                            (130, 160, 288, 1), (77, 416, 2080, 2), (300, 1376, 512, 0),
@@ -293,6 +301,12 @@ def test_gate_up_silu(fmt, M, I, K, out_fmt):
     else:
         err = np.abs(f64(out) - want)
         assert (err <= slack + np.abs(want) * BF16).all(), err.max()
+
+
+@pytest.mark.parametrize("M,I,K,out_fmt", [(33, 5152, 2080, 3), (70, 5136, 2112, 0), (64, 9792, 2080, 1), (96, 1376, 12416, 2),
+                                           (17, 72, 16544, 0)])
+def test_gate_up_silu_long_sums(M, I, K, out_fmt):
+    test_gate_up_silu(R.FP8, M, I, K, out_fmt)
 
 
 def to_matrix(x, fmt, g=1.0):
