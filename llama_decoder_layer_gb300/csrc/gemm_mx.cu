@@ -46,6 +46,18 @@ __host__ __device__ constexpr int out_fmt(int epi) {
   return epi == kMxSiluNvfp4 ? kMxNvfp4 : epi == kMxSiluFp4 ? kMxFp4 : epi == kMxSiluFp8 ? kMxFp8 : 0;
 }
 
+// The tensor cores cut a sum's low bits at every step, always towards zero, so that the error grows with the steps and
+// faster than that of sums rounded to nearest (against 64 bits, rms over that of the results, fp8 on SM pairs in one chain and
+// then fp32: K = 2048 1.1e-7 and 0.6e-7, 8192 4.8e-7 and 1.2e-7, 28672 24e-7 and 2.7e-7; terms of one sign 190e-7 at 28672).
+// Results in fp32, and those that are quantised from it, are therefore sums of chains of no more than so many stages, which
+// are added in fp32: 1.3e-7 at K = 28672, one sign 5e-7.  Few sums of 4-bit products are cut at all: exact for rows whose scales
+// are near one another, and in chains twice as long 5e-7 to 8e-7 where they spread over ten binades (one chain 40e-7).
+template <int FMT>
+constexpr int kChainStages = FMT == kMxFp8 ? 16 : 32;
+
+// Results in bf16 round to 2^-9 of themselves, next to which a chain of all K is nothing.
+__host__ __device__ constexpr bool is_bf16(int epi) { return epi == kMxBf16 || epi == kMxSilu; }
+
 // What a format makes of a stage.
 template <int FMT>
 struct Stage {
@@ -81,6 +93,8 @@ __device__ __forceinline__ void prefetch_maps(const MxMaps& m) {
 struct MxGemmParams {
   int M, N, kb;    // kb: stages along K
   int last_steps;  // MMAs of the last one
+  // SM pairs: a tile's sums are of `chains` chains of chain_len stages, the first chain_more of them one longer
+  int chains, chain_len, chain_more;
   int tiles_m, tiles_n, tiles, group_m;
   // few tiles: the ring, and its rows of x, a multiple of 32 (the MMA reads bytes of w as the rows to 128, whose results are
   // never looked at)
@@ -220,24 +234,14 @@ __device__ __forceinline__ void finish32(const MxGemmParams& p, int row, int n, 
   }
 }
 
-// the scale words of a tile's 128 outputs of the row
-template <int EPI>
-__device__ __forceinline__ void store_words(const MxGemmParams& p, int row, int tn, const uint32_t (&words)[2]) {
-  constexpr int kWords = out_fmt(EPI) == kMxNvfp4 ? 2 : 1;
-  if (row >= p.M) return;
-#pragma unroll
-  for (int i = 0; i < kWords; ++i)
-    if (tn * kWords + i < p.out_ktiles)
-      *reinterpret_cast<uint32_t*>(p.out_scales + mx_scale_at(row, tn * kWords + i, p.out_ktiles)) = words[i];
-}
-
 // A warp's results on their way to memory: 32 rows of up to 128 bytes in shared memory, swizzled as the tensor map of the
 // output says, and from there by a tiled store, which writes whole lines and leaves out what lies past the last row or
-// column (threads storing their own rows, 32 lines an instruction, held a 256 x 256 tile's epilogue for twice as long).  Two
-// buffers: one is filled while the other is read.
+// column (threads storing their own rows, 32 lines an instruction, held a 256 x 256 tile's epilogue for twice as long).  With
+// two buffers one is filled while the other is read.
+template <int BUFS>
 struct OutBoxes {
   const CUtensorMap* map;
-  uint32_t buf;  // this warp's two buffers
+  uint32_t buf;  // this warp's buffers
   int row0;      // of the warp
   int next;
   // nanoseconds between a tile's boxes where another tile's MMAs run meanwhile: the results of a tile at once crowd out the
@@ -246,15 +250,15 @@ struct OutBoxes {
   static constexpr int kBytes = 32 * 128;
 
   __device__ __forceinline__ uint32_t begin() {
-    if ((threadIdx.x & 31) == 0) bulk_wait_read<1>();
+    if ((threadIdx.x & 31) == 0) bulk_wait_read<BUFS - 1>();
     __syncwarp();
-    return buf + (next & 1) * kBytes;
+    return buf + (next & (BUFS - 1)) * kBytes;
   }
-  // 16 bytes of the lane's row; rows of 128 bytes, or of 64
+  // 16 bytes of the lane's row; rows of 128, 64 or 32 bytes
   template <int ROW>
   __device__ __forceinline__ static void put(uint32_t box, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const int lane = threadIdx.x & 31;
-    st_shared_v4(box + lane * ROW + ((ROW == 128 ? chunk ^ (lane & 7) : chunk ^ ((lane >> 1) & 3)) << 4), a, b, c, d);
+    const int lane = threadIdx.x & 31, at = ROW == 128 ? lane & 7 : ROW == 64 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+    st_shared_v4(box + lane * ROW + ((chunk ^ at) << 4), a, b, c, d);
   }
   // x: the box's first element in the output's rows
   __device__ __forceinline__ void end(uint32_t box, int x) {
@@ -268,10 +272,11 @@ struct OutBoxes {
   }
 };
 
-// The whole 256-column tile of a warp's 32 rows, from the accumulator at taddr.  release() is called once the 64 columns
-// shared with the other accumulator (this one's last if it is the first, its first if the second) are in registers.
+// bf16 results: the whole 256-column tile of a warp's 32 rows, from the accumulator at taddr, 64 results of a row at a time.
+// release() is called once the 64 columns shared with the other accumulator (this one's last if it is the first, its first
+// if the second) are in registers.
 template <int EPI, class Release>
-__device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, OutBoxes& boxes, int tn, uint32_t taddr, int acc,
+__device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, OutBoxes<2>& boxes, int tn, uint32_t taddr, int acc,
                                               const Release& release) {
   const bool any = boxes.row0 < p.M;  // a warp whose rows are all past M has nothing to do
   float keep[2][32];
@@ -282,100 +287,142 @@ __device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, OutBoxes& b
   }
   release();
   if (!any) return;
-  if constexpr (out_fmt(EPI) != 0) {
-    // outputs 32 u: gate columns 32 u, up columns 128 + 32 u; kept: up of u = 2, 3 or gate of u = 0, 1
-    constexpr int OF = out_fmt(EPI), kRow = 16 * mx_bits(OF);  // bytes of 128 outputs
-    const int n0 = tn * 128;
-    uint32_t words[2] = {0, 0};
+  auto store = [&](int n, const float (&a)[32], const float (&b)[32]) {
     const uint32_t box = boxes.begin();
-    auto unit = [&](int u, float (&gate)[32], const float (&up)[32]) {
-      if (n0 + 32 * u >= p.N) return;
-      results32<EPI>(p, gate, up);
-      uint32_t w[mx_bits(OF)];
-      codes32<OF>(p, n0 + 32 * u, gate, w, words);
 #pragma unroll
-      for (int i = 0; i < mx_bits(OF) / 4; ++i)
-        OutBoxes::put<kRow>(box, u * (mx_bits(OF) / 4) + i, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float other[32];
-      tmem_ld32(taddr + (acc == 0 ? 64 + 32 * i : 128 + 32 * i), other);
-      if (acc == 0) unit(2 + i, other, keep[i]);
-      else unit(i, keep[i], other);
+    for (int q = 0; q < 4; ++q) {
+      boxes.put<128>(box, q, pack_bf16x2(a[8 * q], a[8 * q + 1]), pack_bf16x2(a[8 * q + 2], a[8 * q + 3]),
+                     pack_bf16x2(a[8 * q + 4], a[8 * q + 5]), pack_bf16x2(a[8 * q + 6], a[8 * q + 7]));
+      boxes.put<128>(box, 4 + q, pack_bf16x2(b[8 * q], b[8 * q + 1]), pack_bf16x2(b[8 * q + 2], b[8 * q + 3]),
+                     pack_bf16x2(b[8 * q + 4], b[8 * q + 5]), pack_bf16x2(b[8 * q + 6], b[8 * q + 7]));
     }
+    boxes.end(box, n);
+  };
+  if constexpr (is_silu(EPI)) {
+    const int n0 = tn * 128, first = acc == 0 ? 64 : 0;  // the half whose up (gate) columns are kept
+    float other[2][32];
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      const int u = acc == 0 ? i : 2 + i;
-      tmem_ld32(taddr + 32 * u, keep[0]);
-      tmem_ld32(taddr + 128 + 32 * u, keep[1]);
-      unit(u, keep[0], keep[1]);
+    for (int h = 0; h < 2; ++h) {
+      const int c = h == 0 ? first : 64 - first;
+      if (n0 + c >= p.N) continue;
+      if (h == 1 && boxes.pace > 0) __nanosleep(boxes.pace);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (h == 1) tmem_ld32(taddr + c + 32 * i + (acc == 0 ? 128 : 0), keep[i]);
+        tmem_ld32(taddr + c + 32 * i + (acc == 0 ? 0 : 128), other[i]);
+        // (gate, up) = (other, keep) or (keep, other)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float g = acc == 0 ? other[i][e] : keep[i][e], u = acc == 0 ? keep[i][e] : other[i][e];
+          other[i][e] = silu(g * p.alpha[0]) * (u * p.alpha[1]);
+        }
+      }
+      store(n0 + c, other[0], other[1]);
     }
-    boxes.end(box, n0 / 8 * mx_bits(OF));
-    store_words<EPI>(p, boxes.row0 + (threadIdx.x & 31), tn, words);
   } else {
-    // 64 results of a row (fp32: 32) are a box
-    auto store = [&](int n, const float (&a)[32], const float (&b)[32]) {
-      if constexpr (EPI == kMxF32) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (n + 32 * i >= p.N) break;
-          const float(&v)[32] = i ? b : a;
-          const uint32_t box = boxes.begin();
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            OutBoxes::put<128>(box, q, __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                               __float_as_uint(v[4 * q + 3]));
-          boxes.end(box, n + 32 * i);
-        }
-      } else {
-        const uint32_t box = boxes.begin();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          OutBoxes::put<128>(box, q, pack_bf16x2(a[8 * q], a[8 * q + 1]), pack_bf16x2(a[8 * q + 2], a[8 * q + 3]),
-                             pack_bf16x2(a[8 * q + 4], a[8 * q + 5]), pack_bf16x2(a[8 * q + 6], a[8 * q + 7]));
-          OutBoxes::put<128>(box, 4 + q, pack_bf16x2(b[8 * q], b[8 * q + 1]), pack_bf16x2(b[8 * q + 2], b[8 * q + 3]),
-                             pack_bf16x2(b[8 * q + 4], b[8 * q + 5]), pack_bf16x2(b[8 * q + 6], b[8 * q + 7]));
-        }
-        boxes.end(box, n);
-      }
-    };
-    if constexpr (is_silu(EPI)) {
-      const int n0 = tn * 128, first = acc == 0 ? 64 : 0;  // the half whose up (gate) columns are kept
-      float other[2][32];
+    const int n0 = tn * 256;
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const int c = h == 0 ? first : 64 - first;
-        if (n0 + c >= p.N) continue;
-        if (h == 1 && boxes.pace > 0) __nanosleep(boxes.pace);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (h == 1) tmem_ld32(taddr + c + 32 * i + (acc == 0 ? 128 : 0), keep[i]);
-          tmem_ld32(taddr + c + 32 * i + (acc == 0 ? 0 : 128), other[i]);
-          // (gate, up) = (other, keep) or (keep, other)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float g = acc == 0 ? other[i][e] : keep[i][e], u = acc == 0 ? keep[i][e] : other[i][e];
-            other[i][e] = silu(g * p.alpha[0]) * (u * p.alpha[1]);
-          }
-        }
-        store(n0 + c, other[0], other[1]);
+    for (int i = 0; i < 4; ++i) {
+      const int c = i == 0 ? shared : acc == 0 ? 64 * (i - 1) : 64 * i;
+      if (n0 + c >= p.N) continue;
+      if (i > 0) {
+        if (boxes.pace > 0) __nanosleep(boxes.pace);
+        tmem_ld32(taddr + c, keep[0]);
+        tmem_ld32(taddr + c + 32, keep[1]);
       }
+      results32<EPI>(p, keep[0], nullptr);
+      results32<EPI>(p, keep[1], nullptr);
+      store(n0 + c, keep[0], keep[1]);
+    }
+  }
+}
+
+// A warp's part of a 256 x 256 tile: 32 rows and half of the columns in registers, a row a thread, 64 neighbours twice: of
+// gate and the same of up, or (no silu) all neighbours.
+template <int EPI>
+__device__ __forceinline__ int part_col(int half, int j) {
+  return is_silu(EPI) ? 64 * half + 128 * j : 128 * half + 64 * j;
+}
+
+// v = the accumulator at taddr, or (not the first chain of the tile) v += it.  release() is called once the columns shared
+// with the other accumulator are in registers: the last 64 of the first one, which only the second half has, as j = 1; the
+// first 64 of the second, which the first half has, as j = 0.
+template <int EPI, class Release>
+__device__ __forceinline__ void add_chain(float (&v)[2][64], uint32_t taddr, int acc, int half, bool first, const Release& release) {
+  auto add = [&](float (&c)[64], int j) {
+    const uint32_t at = taddr + part_col<EPI>(half, j);
+    if (first) {
+      tmem_ld64(at, c);
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < 64; h += 16) {
+      float t[16];
+      tmem_ld16(at + h, t);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) c[h + e] += t[e];
+    }
+  };
+  if (half == acc) release();
+  if (acc == 0) {
+    add(v[1], 1);
+    if (half != acc) release();
+    add(v[0], 0);
+  } else {
+    add(v[0], 0);
+    if (half != acc) release();
+    add(v[1], 1);
+  }
+}
+
+__device__ __forceinline__ float (&half_of(float (&v)[64], int i))[32] { return reinterpret_cast<float(&)[32]>(v[32 * i]); }
+
+// fp32 or quantised results from a warp's sums, stored as boxes of 32 rows and 32 outputs, or 64.
+template <int EPI>
+__device__ __forceinline__ void finish_tile(const MxGemmParams& p, OutBoxes<1>& boxes, int tn, int half, float (&v)[2][64]) {
+  constexpr int OF = out_fmt(EPI);
+  if constexpr (EPI == kMxF32) {
+    const int n0 = tn * 256 + 128 * half;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n0 + 32 * i >= p.N) break;
+      if (i > 0 && boxes.pace > 0) __nanosleep(boxes.pace);
+      float(&r)[32] = half_of(v[i / 2], i % 2);
+      results32<EPI>(p, r, nullptr);
+      const uint32_t box = boxes.begin();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        boxes.put<128>(box, q, __float_as_uint(r[4 * q]), __float_as_uint(r[4 * q + 1]), __float_as_uint(r[4 * q + 2]),
+                       __float_as_uint(r[4 * q + 3]));
+      boxes.end(box, n0 + 32 * i);
+    }
+  } else {
+    constexpr int kChunks = mx_bits(OF) / 4;  // 16 bytes of 32 outputs' codes
+    const int n0 = tn * 128 + 64 * half, row = boxes.row0 + (threadIdx.x & 31);
+    uint32_t words[2] = {0, 0};
+    if (n0 < p.N) {
+      const uint32_t box = boxes.begin();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (n0 + 32 * i >= p.N) break;
+        float(&r)[32] = half_of(v[0], i);
+        results32<EPI>(p, r, half_of(v[1], i));
+        uint32_t w[mx_bits(OF)];
+        codes32<OF>(p, n0 + 32 * i, r, w, words);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j)
+          boxes.put<32 * kChunks>(box, i * kChunks + j, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      }
+      boxes.end(box, n0 / 8 * mx_bits(OF));
+    }
+    if (row >= p.M) return;
+    // the scales of the row's 64 outputs, a word or half of one, zeros past the last group
+    if constexpr (OF == kMxNvfp4) {
+      if (2 * tn + half < p.out_ktiles)
+        *reinterpret_cast<uint32_t*>(p.out_scales + mx_scale_at(row, 2 * tn + half, p.out_ktiles)) = half ? words[1] : words[0];
     } else {
-      const int n0 = tn * 256;
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int c = i == 0 ? shared : acc == 0 ? 64 * (i - 1) : 64 * i;
-        if (n0 + c >= p.N) continue;
-        if (i > 0) {
-          if (boxes.pace > 0) __nanosleep(boxes.pace);
-          tmem_ld32(taddr + c, keep[0]);
-          tmem_ld32(taddr + c + 32, keep[1]);
-        }
-        results32<EPI>(p, keep[0], nullptr);
-        results32<EPI>(p, keep[1], nullptr);
-        store(n0 + c, keep[0], keep[1]);
-      }
+      *reinterpret_cast<uint16_t*>(p.out_scales + mx_scale_at(row, tn, p.out_ktiles) + 2 * half) =
+          static_cast<uint16_t>(words[0] >> (16 * half));
     }
   }
 }
@@ -387,6 +434,11 @@ __device__ __forceinline__ void epilogue_tile(const MxGemmParams& p, OutBoxes& b
 // The tensor cores are what is busy (8192 cubed, nvfp4: 150 us, 7.3 PFLOP/s; 4096 x 8192 x 8192 under the profiler: 79% of the
 // tensor pipe in nvfp4, 87% in fp8, seven waves of tiles of which the last is not full); in long runs the part is at its
 // power limit (70B o_proj, 32768 rows, fp8: 1.20 ms at first, 1.35 over a second).
+// Results in bf16 are taken from the accumulator 64 columns at a time by four warps.  For the others eight warps keep a tile's
+// sums in registers, 128 columns of a row each, and add a chain's accumulator to them while the other one is filled, so that
+// a chain more costs its hand-over, 0.35 us (4096 x 8192 x 8192, fp8 to fp32, four chains for one: 148 us and then 156; gate_up
+// 4096 x 14336 x 4096, fp8 to fp8, two for one: 261 and 262), and a tile of few stages is done sooner than four warps finish
+// it (gate_up 2004 x 16896 x 1280, nvfp4 to fp8: 61 us and then 43).
 // Both CTAs' copies complete on rank 0's full barriers; one thread of rank 0 issues copies of scales and MMAs for both, and
 // commits to both CTAs' barriers.
 // ---------------------------------------------------------------------------
@@ -395,13 +447,16 @@ struct PairRing {
   static constexpr int kA = BM * kRowBytes, kB = 128 * kRowBytes;
   static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = 2 * kSa;
   static constexpr int kBytes = kA + kB + kSa + kSb;  // of a stage, a CTA
-  static constexpr int kOut = 4 * 2 * OutBoxes::kBytes;  // the epilogue warps' buffers
+  static constexpr int kOut = 8 * OutBoxes<1>::kBytes;  // the epilogue warps' buffers: four of two, or eight of one
   static constexpr int kStages = (kRingBudget - kOut) / kBytes < kMaxStages ? (kRingBudget - kOut) / kBytes : kMaxStages;
   static constexpr int kSmem = kStages * kBytes + kOut + 2048;
 };
 
+constexpr int epilogue_warps(int epi) { return is_bf16(epi) ? 4 : 8; }
+constexpr int pair_threads(int epi) { return 64 + 32 * epilogue_warps(epi); }
+
 template <int FMT, int EPI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(pair_threads(EPI), 1)
     k_gemm_mx_pair(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
   using S = Stage<FMT>;
   using R = PairRing<FMT>;
@@ -437,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 8);  // the four epilogue warps of each CTA
+      mbar_init(tempty_bar(a), 2 * epilogue_warps(EPI));  // of both CTAs
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -514,17 +569,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int t = first; ok && t < p.tiles; t += npairs) {
+      // the stages from kb to end, a tile's or (chains) a part of them, into an accumulator
+      auto chain = [&](int kb, const int end) {
         if (!warp_same(mbar_wait(tempty_bar(acc ^ 1), acc ? acc_phase : acc_phase ^ 1u, abort_flag))) {
           ok = false;
-          break;
+          return;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * T::kAcc;
-        for (int kb = 0; kb < p.kb; ++kb) {
+        for (const int begin = kb; kb < end; ++kb) {
           if (!warp_same(mbar_wait(full_bar(stage), phase, abort_flag))) {
             ok = false;
-            break;
+            return;
           }
           tc_fence_after();
           if (elect_one()) {
@@ -545,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_mma_mx<S::kBits, S::kStepScales, true>(d_tmem, smem_desc_sw128(sa + 32 * k), smem_desc_sw128(sb + 32 * k),
                                                         idesc_mx_scale(idesc, k % S::kPerTile * S::kStepScales),
                                                         tmem_base + T::kSa + 4 * i, tmem_base + T::kSb + 8 * i,
-                                                        kb > 0 || k > 0 ? 1u : 0u);
+                                                        kb > begin || k > 0 ? 1u : 0u);
             }
             tc_commit_pair(empty_bar(stage), 3);
           }
@@ -555,11 +611,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             phase ^= 1u;
           }
         }
-        if (!ok) break;
         if (elect_one()) tc_commit_pair(tfull_bar(acc), 3);
         __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+      };
+      for (int t = first; ok && t < p.tiles; t += npairs) {
+        if constexpr (is_bf16(EPI)) {
+          chain(0, p.kb);
+        } else {
+          for (int c = 0, kb = 0; ok && c < p.chains; ++c) {
+            const int end = kb + p.chain_len + (c < p.chain_more ? 1 : 0);
+            chain(kb, end);
+            kb = end;
+          }
+        }
       }
       if (!ok) {
         if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmMma);
@@ -573,29 +639,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(drain_bar, 0, nullptr);
   } else {
     // ---------------- epilogue (both CTAs, their own rows) ----------------
-    const int quad = warp & 3;
+    constexpr int kBufs = is_bf16(EPI) ? 2 : 1;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t tempty_lead = mapa_shared(tempty_bar(0), 0);
-    OutBoxes boxes{&maps.out, out_buf + quad * 2 * OutBoxes::kBytes, 0, 0, 0};
+    OutBoxes<kBufs> boxes{&maps.out, out_buf + (warp - 2) * kBufs * OutBoxes<kBufs>::kBytes, 0, 0, 0};
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int t = first; t < p.tiles; t += npairs) {
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(tempty_lead + 8u * acc);
+    };
+    for (int t = first; ok && t < p.tiles; t += npairs) {
       int tm, tn;
       tile_coords(p, t, tm, tn);
-      if (!mbar_wait(tfull_bar(acc), acc_phase, abort_flag)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
       boxes.row0 = (2 * tm + rank) * BM + quad * 32;
-      boxes.pace = t + npairs < p.tiles ? 16 * p.kb : 0;  // (a stage's MMAs take some 300)
-      epilogue_tile<EPI>(p, boxes, tn, tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc, acc, [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(tempty_lead + 8u * acc);
-      });
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      // (a stage's MMAs take some 300; fp32 results of 4096 x 8192 x 2048, fp8: 54.4 us at 16 a stage, 51.6 at 40)
+      boxes.pace = t + npairs < p.tiles ? (EPI == kMxF32 ? 40 : 16) * p.chain_len : 0;
+      // the next accumulator's sums, once they are there
+      auto sums = [&](auto use) {
+        ok = mbar_wait(tfull_bar(acc), acc_phase, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        use(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * T::kAcc);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      };
+      if constexpr (is_bf16(EPI)) {
+        sums([&](uint32_t taddr) { epilogue_tile<EPI>(p, boxes, tn, taddr, acc, release); });
+      } else {
+        const bool any = boxes.row0 < p.M;  // a warp whose rows are all past M has nothing to do
+        float v[2][64];
+#pragma unroll 1
+        for (int c = 0; ok && c < p.chains; ++c)
+          sums([&](uint32_t taddr) {
+            if (any) add_chain<EPI>(v, taddr, acc, half, c == 0, release);
+            else release();
+          });
+        if (ok && any) finish_tile<EPI>(p, boxes, tn, half, v);
+      }
     }
     if (!ok) {
       if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
@@ -1033,14 +1116,14 @@ cudaError_t raise_limits() {
 // Clusters of S CTAs of a kernel that are resident at once, of those that take an SM each; cached per device.  (A cluster's
 // SMs are of one GPC, so that the SMs hold fewer clusters than their number says.)
 template <typename... KArgs>
-int max_clusters(void (*kernel)(KArgs...), int S, size_t smem, std::atomic<int>* cache) {
+int max_clusters(void (*kernel)(KArgs...), int S, int threads, size_t smem, std::atomic<int>* cache) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 0;
   int n = cache[dev].load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(S * 256);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -1061,14 +1144,14 @@ int max_clusters(void (*kernel)(KArgs...), int S, size_t smem, std::atomic<int>*
 template <int FMT, int EPI>
 int max_active_pairs() {
   static std::atomic<int> cache[kDevs];
-  return max_clusters(k_gemm_mx_pair<FMT, EPI>, 2, PairRing<FMT>::kSmem, cache);
+  return max_clusters(k_gemm_mx_pair<FMT, EPI>, 2, pair_threads(EPI), PairRing<FMT>::kSmem, cache);
 }
 
 // (the same for every kernel that takes an SM: asked of one)
 int max_active_splits(int S) {
   static std::atomic<int> cache[kSplitMaxCluster + 1][kDevs];
   const cudaError_t e = raise_limits<kMxFp8, kMxBf16>();
-  return e != cudaSuccess ? 0 : max_clusters(k_gemm_mx_split<kMxFp8, kMxBf16>, S, kMaxSmemBytes, cache[S]);
+  return e != cudaSuccess ? 0 : max_clusters(k_gemm_mx_split<kMxFp8, kMxBf16>, S, kThreads, kMaxSmemBytes, cache[S]);
 }
 
 // Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S
@@ -1124,13 +1207,15 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   if (pair) {
     constexpr bool kCodes = out_fmt(EPI) != 0, kF32 = EPI == kMxF32;
     const long long cols = kCodes ? static_cast<long long>(p.N) / 8 * mx_bits(out_fmt(EPI)) : p.N;
-    const int elem = kCodes ? 1 : kF32 ? 4 : 2, box = kCodes ? 16 * mx_bits(out_fmt(EPI)) : 128;  // bytes
+    const int elem = kCodes ? 1 : kF32 ? 4 : 2, box = kCodes ? 8 * mx_bits(out_fmt(EPI)) : 128;  // bytes
     ok = ok && encode_2d(&maps.out,
                          kCodes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                          : kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                          p.out, cols, p.M, cols * elem, box / elem, 32,
-                         box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                         box == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                         : box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_32B);
   }
   if (!ok) return cudaErrorInvalidValue;
   if (pair) {
@@ -1144,7 +1229,10 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
     const long long group = (32LL << 20) / (2 * BM * row_bytes);
     p.group_m = group < 4 ? 4 : group < pair_m ? static_cast<int>(group) : pair_m;
     if (p.group_m > pair_m) p.group_m = pair_m;
-    return launch_kernel_cluster(k_gemm_mx_pair<FMT, EPI>, dim3(2 * (p.tiles < pairs ? p.tiles : pairs)), dim3(kThreads),
+    p.chains = is_bf16(EPI) ? 1 : (p.kb + kChainStages<FMT> - 1) / kChainStages<FMT>;
+    p.chain_len = p.kb / p.chains;
+    p.chain_more = p.kb % p.chains;
+    return launch_kernel_cluster(k_gemm_mx_pair<FMT, EPI>, dim3(2 * (p.tiles < pairs ? p.tiles : pairs)), dim3(pair_threads(EPI)),
                                  PairRing<FMT>::kSmem, s, true, 2, maps, p);
   }
   p.group_m = p.tiles_m;
