@@ -51,11 +51,14 @@ __host__ __device__ constexpr int out_fmt(int epi) {
 // then fp32: K = 2048 1.1e-7 and 0.6e-7, 8192 4.8e-7 and 1.2e-7, 28672 24e-7 and 2.7e-7; terms of one sign 190e-7 at 28672).
 // Results in fp32, and those that are quantised from it, are therefore sums of chains of no more than so many stages, which
 // are added in fp32: 1.3e-7 at K = 28672, one sign 5e-7.  Few sums of 4-bit products are cut at all: exact for rows whose scales
-// are near one another, and in chains twice as long 5e-7 to 8e-7 where they spread over ten binades (one chain 40e-7).
+// are near one another; where those of x spread over some ten binades, K = 28672, in one chain 39e-7 to 45e-7, in chains
+// twice as long as fp8's 7e-7 to 11e-7, fp32 10e-7 to 12e-7.
 template <int FMT>
 constexpr int kChainStages = FMT == kMxFp8 ? 16 : 32;
 
-// Results in bf16 round to 2^-9 of themselves, next to which a chain of all K is nothing.
+// Results in bf16 round to 2^-8 of themselves: a chain of 256 stages is off by 2^-15 at the worst (fp8, terms of one sign).
+// Longer sums are not left to SM pairs, which take one chain for bf16.
+constexpr int kBf16Stages = 256;
 __host__ __device__ constexpr bool is_bf16(int epi) { return epi == kMxBf16 || epi == kMxSilu; }
 
 // What a format makes of a stage.
@@ -703,11 +706,10 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
 // the ring leave room the chunks have a place of their own, so that a CTA need not wait for the others' MMAs before it
 // stores (operands read from HBM, without either and with both: 421 x 1384 x 2080, fp8, 7.9 and 7.2 us; 128 x 4096 x 14336,
 // nvfp4, 11.8 and 11.2; 128 x 8192 x 28672 28.2 and 27.5; one row of 4096 x 4096 5.5 and 5.6).
-// fp8: the tensor cores cut a sum's low bits at every step, so that the error grows with the steps (against 64 bits, rms over
-// the mean size: 4096 elements in one chain 2.6e-7, fp32 itself 1.0e-7).  A CTA of kHalvedStages or more begins a second
-// accumulator half way, and the halves are added in fp32: 1.4e-7, and 1.1 to 5.9e-7 for 16384 elements where one chain has
-// 1.5 to 14e-7.  The MMAs wait meanwhile until the columns that the second half's scales take are read (64 x 4096 x 14336
-// 13.5 us without it and 13.8 with; 128 x 8192 x 8192 16.9 and 17.25).  Sums of 4-bit products are exact or nearly so.
+// A CTA's sums are of chains, too, where its stages are more than one's (kChain): the MMAs wait while the accumulator is added
+// to the sums of the chains before it.  Those lie in tensor memory but for what the scales leave no room for.  fp8 codes
+// behind gate_up that differ from 64 bits, 64 x 14336 x 4096: 33 of 3.7 million in chains of 16 stages, 21 of 11, 18 of 8
+// (fp32 20), at 23.45, 23.55 and 23.7 us.  64 x 4096 x 14336 to fp32 in one chain, two and three a CTA 14.3, 14.5 and 14.85 us.
 // (Tensor memory: the CTAs of a cluster, which wait for one another, hold four stages, 80 KB, or more, or else two or three
 // and received chunks up to the whole budget, so that none shares an SM with a CTA of a pair, which holds all of its tensor
 // memory and waits for its peer.)
@@ -715,7 +717,6 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
 constexpr int kSplitCols = 128;
 constexpr int kSplitTmemCols = 256;
 constexpr int kSplitMaxCluster = 8;
-constexpr int kHalvedStages = 16;  // a chain of 11 stages is as near as fp32: 1.0e-7, both
 
 template <int FMT, int EPI>
 struct SplitStage {
@@ -723,10 +724,13 @@ struct SplitStage {
   static constexpr int kSa = Stage<FMT>::kTiles * kMxTileBytes, kSb = kSa * (is_silu(EPI) ? 2 : 1);
   static constexpr int kUnits = is_silu(EPI) ? 2 : 4;          // 32 outputs each
   static constexpr int kChunks = is_silu(EPI) ? 2 : 1;         // accumulator chunks of a unit: gate, up
-  // columns of the scales, and of them all
-  static constexpr int kTsa = 0, kTsb = 4 * Stage<FMT>::kTiles, kTsCols = kTsb + 8 * Stage<FMT>::kTiles;
-  static constexpr bool kHalves = Stage<FMT>::kBits == 8;
-  static_assert(kSplitCols + kTsCols <= kSplitTmemCols && (!kHalves || kTsCols <= 32), "tensor memory");
+  // Tensor memory: the scales, then the sums of the chains that are done, in the place of the accumulator's columns but for
+  // the first kKept chunks of 32, which stay in registers; then the accumulator.
+  static constexpr int kTsa = 0, kTsb = 4 * Stage<FMT>::kTiles, kTsCols = kTsb + 4 * kChunks * Stage<FMT>::kTiles;
+  static constexpr int kKept = (kTsCols + 31) / 32, kAcc = kSplitCols;
+  static_assert(kAcc + kSplitCols <= kSplitTmemCols, "tensor memory");
+  // stages of a chain, of which one more costs less here than on SM pairs
+  static constexpr int kChain = is_bf16(EPI) ? FMT == kMxFp8 ? 32 : kBf16Stages : FMT == kMxFp8 ? 12 : kChainStages<FMT>;
   __host__ __device__ static constexpr int bytes(int a_rows) { return a_rows * kRowBytes + kB + kSa + kSb; }
   // chunks that a CTA of S receives from each of the others, and the bytes of them all, `rows` accumulator rows each
   __host__ __device__ static constexpr int local_chunks(int S) { return (kUnits + S - 1) / S * kChunks; }
@@ -747,27 +751,51 @@ __device__ __forceinline__ void store_unit_scales(const MxGemmParams& p, int row
     for (int g = g0 + kGroups; g < 4 * p.out_ktiles; ++g) p.out_scales[mx_scale_at(row, g >> 2, p.out_ktiles) + (g & 3)] = 0;
 }
 
-// This CTA's sums; if `halves`, of two accumulators, the first's columns 0 to 31 in registers.
-template <int FMT>
+// 32 columns of this CTA's sums: the accumulator's and, if there are chains before it, theirs.
+template <class R>
 struct OwnLoader {
   uint32_t taddr;
-  bool halves;
-  const uint32_t (&first)[32];
+  bool chains;
+  const float (&kept)[R::kKept][32];
   __device__ __forceinline__ void operator()(int col, float (&v)[32]) const {
-    tmem_ld32(taddr + col, v);
-    if constexpr (Stage<FMT>::kBits == 8) {
-      if (!halves) return;
-      if (col == 0) {
+    tmem_ld32(taddr + R::kAcc + col, v);
+    if (!chains) return;
+    if (col >= 32 * R::kKept) {
+      float t[32];
+      tmem_ld32(taddr + col, t);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(first[e]);
-      }
-      float second[32];
-      tmem_ld32(taddr + kSplitCols + col, second);
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] += second[e];
+      for (int e = 0; e < 32; ++e) v[e] += t[e];
     }
+#pragma unroll
+    for (int i = 0; i < R::kKept; ++i)
+      if (col == 32 * i) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] += kept[i][e];
+      }
   }
 };
+
+// Adds the accumulator of a chain that is done to the sums of those before it (first: there are none).
+template <class R>
+__device__ __forceinline__ void save_chain(uint32_t taddr, bool first, float (&kept)[R::kKept][32]) {
+#pragma unroll
+  for (int i = 0; i < kSplitCols / 32; ++i) {
+    float v[32];
+    tmem_ld32(taddr + R::kAcc + 32 * i, v);
+    if (i < R::kKept) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) kept[i % R::kKept][e] = first ? v[e] : kept[i % R::kKept][e] + v[e];
+    } else {
+      if (!first) {
+        float t[32];
+        tmem_ld32(taddr + 32 * i, t);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] += t[e];
+      }
+      tmem_st32(taddr + 32 * i, v);
+    }
+  }
+}
 
 // Receive buffer of CTA `to`: [source rank, without its own][local chunk][8 float4 columns][rows], so that a warp's rows are
 // contiguous.
@@ -823,7 +851,11 @@ __device__ __forceinline__ void split_unit(const MxGemmParams& p, int row, int t
   }
 }
 
-template <int FMT, int EPI>
+// Whether the kernel for sums of several chains also takes those of one.  (gate_up in nvfp4, whose scales leave the most of the
+// chains' sums to registers, takes 53.2 us then for 64 x 28672 x 8192, 50.8 in a kernel of its own.)
+constexpr bool one_split(int fmt, int epi) { return fmt != kMxNvfp4 || !is_silu(epi); }
+
+template <int FMT, int EPI, bool CHAINS>
 __global__ void __launch_bounds__(kThreads, 2)
     k_gemm_mx_split(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
   using S = Stage<FMT>;
@@ -835,18 +867,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int nst = p.stages, a_bytes = p.a_rows * kRowBytes, tile_bytes = a_bytes + R::kB;
   const uint32_t scales = sbase + nst * tile_bytes;
   uint8_t* meta = smem_raw + pad + p.meta_at;
-  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull, recv, half, saved
+  const uint32_t bar0 = smem_u32(meta);  // full[S], empty[S], tfull, recv, done, saved
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meta + 8 * (2 * nst + 4));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
-  const uint32_t tfull_bar = bar0 + 8u * (2 * nst), recv_bar = tfull_bar + 8, half_bar = tfull_bar + 16, saved_bar = tfull_bar + 24;
+  const uint32_t tfull_bar = bar0 + 8u * (2 * nst), recv_bar = tfull_bar + 8, done_bar = tfull_bar + 16, saved_bar = tfull_bar + 24;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int kb0 = rank * p.kb / ctas, kb1 = (rank + 1) * p.kb / ctas;
-  const bool halves = R::kHalves && kb1 - kb0 >= kHalvedStages;
-  const int kb_half = halves ? (kb0 + kb1) / 2 : kb1;
+  // chains of chain_len stages, the first chain_more of them one longer
+  const int chains = CHAINS ? (kb1 - kb0 + R::kChain - 1) / R::kChain : 1, chain_len = (kb1 - kb0) / chains, chain_more = (kb1 - kb0) % chains;
   int tm, tn;
   tile_coords(p, static_cast<int>(blockIdx.x) / ctas, tm, tn);
 
@@ -856,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull_bar, 1);
-    mbar_init(half_bar, 1);
+    mbar_init(done_bar, 1);
     mbar_init(saved_bar, 4);  // an arrival of every warp that finishes rows
     // an arrival of every warp that has rows, in every other CTA
     mbar_init(recv_bar, max(ctas - 1, 1) * min((p.M - tm * BM + 31) / 32, 4));
@@ -929,20 +961,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ---------------- MMAs ----------------
     constexpr uint32_t idesc = idesc_mx(BM, is_silu(EPI) ? 64 : 128, S::kBits, S::kE8m0);
     const uint32_t gate_cols = is_silu(EPI) ? (tn & 1) * 2 : 0;  // a tile's 64 rows of w in their 128-row scale tile
-    int stage = 0, first = kb0;
-    uint32_t phase = 0, acc = tmem_base, ts = tmem_base + kSplitCols;  // the accumulator, the scales
+    const uint32_t acc = tmem_base + R::kAcc, ts = tmem_base;  // the accumulator, the scales
+    int stage = 0, first = kb0, chain = 0, end = kb0 + chain_len + (chain_more > 0 ? 1 : 0);
+    uint32_t phase = 0;
     bool ok = true;
     for (int kb = kb0; kb < kb1; ++kb) {
-      if (R::kHalves && kb == kb_half) {
-        if (elect_one()) tc_commit(half_bar);
+      if (CHAINS && kb == end) {
+        if (elect_one()) tc_commit(done_bar);
         __syncwarp();
-        if (!warp_same(mbar_wait(saved_bar, 0, abort_flag))) {
+        if (!warp_same(mbar_wait(saved_bar, chain & 1, abort_flag))) {
           ok = false;
           break;
         }
+        ++chain;
         first = kb;
-        acc = tmem_base + kSplitCols;
-        ts = tmem_base;
+        end = kb + chain_len + (chain < chain_more ? 1 : 0);
       }
       if (!warp_same(mbar_wait(full_bar(stage), phase, abort_flag))) {
         ok = false;
@@ -990,18 +1023,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const int quad = warp & 3;  // tensor-memory lane quarter this warp may access
   const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-  uint32_t first[32];  // the first half's sums of columns 0 to 31, where the second half's scales go
-  if (halves && warp >= 2) {
-    if (warp_same(mbar_wait(half_bar, 0, abort_flag))) {
+  float kept[R::kKept][32];
+  if (CHAINS && warp >= 2) {
+#pragma unroll 1
+    for (int c = 0; c + 1 < chains; ++c) {
+      if (!warp_same(mbar_wait(done_bar, c & 1, abort_flag))) {
+        if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
+        *abort_flag = 1;
+        break;
+      }
       tc_fence_after();
-      tmem_ld32_async(taddr, first);
-      tmem_ld_wait(first);
+      save_chain<R>(taddr, c == 0, kept);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(saved_bar);
-    } else {
-      if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
-      *abort_flag = 1;
     }
   }
   if (!mbar_wait(tfull_bar, 0, nullptr)) {
@@ -1010,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   tc_fence_after();
 
-  const OwnLoader<FMT> mine{taddr, halves, first};
+  const OwnLoader<R> mine{taddr, chains > 1, kept};
   if (ctas == 1) {
     __syncthreads();
     if (warp >= 2 && !*abort_flag && tm * BM + quad * 32 < p.M) {
@@ -1049,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) report_error(p.err, kErrTimeout, kWhereGemmEpilogue);
         *abort_flag = 1;
       } else {
-        const SumLoader<R, OwnLoader<FMT>> ld{mine, smem_raw + pad + p.recv_at, ctas, rank, nloc, row_in_tile, p.a_rows};
+        const SumLoader<R, OwnLoader<R>> ld{mine, smem_raw + pad + p.recv_at, ctas, rank, nloc, row_in_tile, p.a_rows};
 #pragma unroll 1
         for (int u = rank; u < R::kUnits; u += ctas) split_unit<EPI>(p, tm * BM + row_in_tile, tn, u, ld);
       }
@@ -1109,7 +1144,8 @@ bool operand_maps(CUtensorMap* codes, CUtensorMap* scales, const MxOperand& o, i
 template <int FMT, int EPI>
 cudaError_t raise_limits() {
   static SmemLimits limits;
-  return limits.raise({smem_need(k_gemm_mx_split<FMT, EPI>, kMaxSmemBytes),
+  return limits.raise({smem_need(k_gemm_mx_split<FMT, EPI, true>, kMaxSmemBytes),
+                       smem_need(k_gemm_mx_split<FMT, EPI, one_split(FMT, EPI)>, kMaxSmemBytes),
                        smem_need(k_gemm_mx_pair<FMT, EPI>, PairRing<FMT>::kSmem)});
 }
 
@@ -1151,7 +1187,7 @@ int max_active_pairs() {
 int max_active_splits(int S) {
   static std::atomic<int> cache[kSplitMaxCluster + 1][kDevs];
   const cudaError_t e = raise_limits<kMxFp8, kMxBf16>();
-  return e != cudaSuccess ? 0 : max_clusters(k_gemm_mx_split<kMxFp8, kMxBf16>, S, kThreads, kMaxSmemBytes, cache[S]);
+  return e != cudaSuccess ? 0 : max_clusters(k_gemm_mx_split<kMxFp8, kMxBf16, true>, S, kThreads, kMaxSmemBytes, cache[S]);
 }
 
 // Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S
@@ -1196,8 +1232,9 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
         R::recv_bytes(n, p.a_rows) <= kRingBudget / stage_bytes * stage_bytes && max_active_splits(n) >= p.tiles)
       S = n;
   const int pairs = max_active_pairs<FMT, EPI>();
-  const bool pair = pairs > 0 && use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
-                                           (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
+  const bool pair = pairs > 0 && (!is_bf16(EPI) || p.kb <= kBf16Stages) &&
+                    use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
+                              (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
   MxMaps maps{};
   const int w_box = !pair && is_silu(EPI) ? 64 : 128;
   bool ok = operand_maps(&maps.x, pair ? &maps.x_scales : nullptr, a.x, a.M, row_bytes, ktiles, T::kTiles,
@@ -1251,8 +1288,8 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
     p.recv_at = p.stages * stage_bytes;
     p.meta_at = p.recv_at + recv;
   }
-  return launch_kernel_cluster(k_gemm_mx_split<FMT, EPI>, dim3(ctas), dim3(kThreads), static_cast<size_t>(p.meta_at) + 2048, s,
-                               true, S, maps, p);
+  return launch_kernel_cluster(fill > R::kChain ? k_gemm_mx_split<FMT, EPI, true> : k_gemm_mx_split<FMT, EPI, one_split(FMT, EPI)>,
+                               dim3(ctas), dim3(kThreads), static_cast<size_t>(p.meta_at) + 2048, s, true, S, maps, p);
 }
 
 template <int FMT>

@@ -28,8 +28,8 @@ pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
 CHAIN = {R.NVFP4: 128, R.FP4: 128, R.FP8: 64}  # steps
-# on SM pairs
-SIZES = [(2600, 2048)]
+# K split over a cluster, not split, and SM pairs
+SIZES = [(64, 512), (64, 9728), (100, 19456), (2600, 2048)]
 
 
 def matrix(fmt, rows, cols, seed, positive=False):
@@ -73,6 +73,18 @@ def test_sums_of_one_sign(fmt, M, N, K):
     bar = 2.0 ** -24 * ((chain + 1) / 2 + (steps / chain / 3) ** 0.5)
     got = off(fmt, M, N, K, True)
     assert got <= bar, (got, bar)
+
+
+@pytest.mark.parametrize("fmt,K", [(R.FP8, 70016), (R.FP4, 200064)])
+def test_bf16_results_of_very_long_sums(fmt, K):
+    """Against fp32 results of the same sums: a rounding to bf16, half a step of 2^-7, and a sixteenth of that for the cuts of
+    a chain of 256 stages (1024 steps, half a unit each in the mean, all on one side: 1025 / 2 2^-24 = 2^-15)."""
+    (a, _), (b, _) = matrix(fmt, 520, K, 1, True), matrix(fmt, 264, K, 2, True)
+    y, z = (torch.empty(520, 264, dtype=t, device=DEV) for t in (torch.float32, torch.bfloat16))
+    lb.linear_mx(a, b, y)
+    lb.linear_mx(a, b, z)
+    assert lb.get_device_error()[0] == lb.LLAMA_OK
+    assert float(((z.double() - y.double()).abs() / y.double()).max()) <= 2.0 ** -8 + 2.0 ** -12
 
 
 @pytest.mark.parametrize("M,I", [(64, 2048), (2600, 1024)])
