@@ -17,7 +17,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 
 #include "common.cuh"
@@ -34,7 +33,6 @@ constexpr int kRowBytes = 128;    // of every row of a stage
 constexpr int kThreads = 192;     // warp 0 copies, warp 1 MMAs, warps 2-5 epilogue
 constexpr int kTmemCols = 512;
 constexpr int kMaxStages = 8;
-constexpr int kDevs = 64;  // devices that values are cached for
 constexpr int kMaxSmemBytes = 232448;              // the opt-in limit per CTA (227 KB)
 constexpr int kRingBudget = kMaxSmemBytes - 2048;  // the rest: barriers, alignment slack
 
@@ -1149,45 +1147,20 @@ cudaError_t raise_limits() {
                        smem_need(k_gemm_mx_pair<FMT, EPI>, PairRing<FMT>::kSmem)});
 }
 
-// Clusters of S CTAs of a kernel that are resident at once, of those that take an SM each; cached per device.  (A cluster's
-// SMs are of one GPC, so that the SMs hold fewer clusters than their number says.)
-template <typename... KArgs>
-int max_clusters(void (*kernel)(KArgs...), int S, int threads, size_t smem, std::atomic<int>* cache) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return 0;
-  int n = cache[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(S * 256);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(S);
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = -1;
-    }
-    cache[dev].store(n, std::memory_order_relaxed);
-  }
-  return n > 0 ? n : 0;
-}
-
+// Clusters of S CTAs that are resident at once, of those that take an SM each.  (A cluster's SMs are of one GPC, so that the
+// SMs hold fewer clusters than their number says.)
 template <int FMT, int EPI>
-int max_active_pairs() {
-  static std::atomic<int> cache[kDevs];
-  return max_clusters(k_gemm_mx_pair<FMT, EPI>, 2, pair_threads(EPI), PairRing<FMT>::kSmem, cache);
+cudaError_t max_active_pairs(int* n) {
+  static ClusterLimit limit;
+  return limit.get(reinterpret_cast<const void*>(k_gemm_mx_pair<FMT, EPI>), 2, pair_threads(EPI), PairRing<FMT>::kSmem, n);
 }
 
 // (the same for every kernel that takes an SM: asked of one)
-int max_active_splits(int S) {
-  static std::atomic<int> cache[kSplitMaxCluster + 1][kDevs];
+cudaError_t max_active_splits(int S, int* n) {
+  static ClusterLimit limits[kSplitMaxCluster + 1];
   const cudaError_t e = raise_limits<kMxFp8, kMxBf16>();
-  return e != cudaSuccess ? 0 : max_clusters(k_gemm_mx_split<kMxFp8, kMxBf16, true>, S, kThreads, kMaxSmemBytes, cache[S]);
+  if (e != cudaSuccess) return e;
+  return limits[S].get(reinterpret_cast<const void*>(k_gemm_mx_split<kMxFp8, kMxBf16, true>), S, kThreads, kMaxSmemBytes, n);
 }
 
 // Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S
@@ -1213,7 +1186,7 @@ template <int FMT, int EPI>
 int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   using T = Stage<FMT>;
   using R = SplitStage<FMT, EPI>;
-  const cudaError_t e = raise_limits<FMT, EPI>();
+  cudaError_t e = raise_limits<FMT, EPI>();
   if (e != cudaSuccess) return e;
   const int sms = num_sms();
   const long long row_bytes = static_cast<long long>(a.K) * T::kBits / 8;
@@ -1229,9 +1202,13 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
   int S = 1;
   for (int n = kSplitMaxCluster; n > 1 && S == 1; --n)
     if (static_cast<long long>(p.tiles) * n <= sms && p.kb >= 4 * n &&
-        R::recv_bytes(n, p.a_rows) <= kRingBudget / stage_bytes * stage_bytes && max_active_splits(n) >= p.tiles)
-      S = n;
-  const int pairs = max_active_pairs<FMT, EPI>();
+        R::recv_bytes(n, p.a_rows) <= kRingBudget / stage_bytes * stage_bytes) {
+      int room = 0;
+      if ((e = max_active_splits(n, &room)) != cudaSuccess) return e;
+      if (room >= p.tiles) S = n;
+    }
+  int pairs = 0;
+  if ((e = max_active_pairs<FMT, EPI>(&pairs)) != cudaSuccess) return e;
   const bool pair = pairs > 0 && (!is_bf16(EPI) || p.kb <= kBf16Stages) &&
                     use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
                               (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);

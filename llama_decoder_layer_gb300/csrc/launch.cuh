@@ -59,6 +59,44 @@ class SmemLimits {
   std::atomic<bool> done_[kDevs] = {};
 };
 
+// How many clusters of a kernel a device holds at once, asked once on every
+// device.  An error is not kept: the next call asks again.
+class ClusterLimit {
+ public:
+  cudaError_t get(const void* kernel, int ctas, int threads, size_t smem, int* clusters) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kDevs;
+    const int kept = known ? n_[dev].load(std::memory_order_relaxed) : 0;
+    if (kept > 0) {
+      *clusters = kept - 1;
+      return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas * 256);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    *clusters = n > 0 ? n : 0;
+    if (known) n_[dev].store(*clusters + 1, std::memory_order_relaxed);
+    return cudaSuccess;
+  }
+
+ private:
+  static constexpr int kDevs = 64;
+  std::atomic<int> n_[kDevs] = {};  // one more than their number
+};
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool pdl,
                           Args&&... args) {
