@@ -585,7 +585,8 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
 
 // 32 lanes x 32 consecutive columns: thread i of the warp writes lane
 // (base lane + i), columns [col, col + 32)
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+// (async: written for this thread once tmem_st_wait() returns)
+__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const float (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -601,7 +602,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
       "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
       "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  tmem_st32_async(taddr, v);
+  tmem_st_wait();
 }
 
 // 32 lanes x 16 consecutive columns (thread i of the warp writes lane base + i)

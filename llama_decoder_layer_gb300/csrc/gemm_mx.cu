@@ -656,8 +656,9 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
       int tm, tn;
       tile_coords(p, t, tm, tn);
       boxes.row0 = (2 * tm + rank) * BM + quad * 32;
-      // (a stage's MMAs take some 300; fp32 results of 4096 x 8192 x 2048, fp8: 54.4 us at 16 a stage, 51.6 at 40)
-      boxes.pace = t + npairs < p.tiles ? (EPI == kMxF32 ? 40 : 16) * p.chain_len : 0;
+      // (a stage's MMAs take some 300; fp32 results of 4096 x 8192 x 2048, fp8, whose tiles have 16 stages: 54.9 us at 16 a
+      // stage, 52.6 at 40; x 8192, nvfp4, 32 stages: 83.0 and 85.5)
+      boxes.pace = t + npairs >= p.tiles ? 0 : EPI == kMxF32 ? min(40 * p.chain_len, 640) : 16 * p.chain_len;
       // the next accumulator's sums, once they are there
       auto sums = [&](auto use) {
         ok = mbar_wait(tfull_bar(acc), acc_phase, abort_flag);
@@ -773,26 +774,34 @@ struct OwnLoader {
   }
 };
 
-// Adds the accumulator of a chain that is done to the sums of those before it (first: there are none).
-template <class R>
-__device__ __forceinline__ void save_chain(uint32_t taddr, bool first, float (&kept)[R::kKept][32]) {
+// Adds the accumulator of a chain that is done to the sums of those before it (first: there are none).  release() is called
+// once the accumulator is in registers.
+template <class R, class Release>
+__device__ __forceinline__ void save_chain(uint32_t taddr, bool first, float (&kept)[R::kKept][32], const Release& release) {
 #pragma unroll
   for (int i = 0; i < kSplitCols / 32; ++i) {
+    uint32_t a[32], b[32];
+    tmem_ld32_async(taddr + R::kAcc + 32 * i, a);
+    if (i >= R::kKept && !first) {
+      tmem_ld32_async(taddr + 32 * i, b);
+      tmem_ld_wait(b);
+    }
+    tmem_ld_wait(a);
+    if (i + 1 == kSplitCols / 32) release();
     float v[32];
-    tmem_ld32(taddr + R::kAcc + 32 * i, v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float sum = i < R::kKept ? kept[i % R::kKept][e] : __uint_as_float(b[e]);
+      v[e] = first ? __uint_as_float(a[e]) : sum + __uint_as_float(a[e]);
+    }
     if (i < R::kKept) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) kept[i % R::kKept][e] = first ? v[e] : kept[i % R::kKept][e] + v[e];
+      for (int e = 0; e < 32; ++e) kept[i % R::kKept][e] = v[e];
     } else {
-      if (!first) {
-        float t[32];
-        tmem_ld32(taddr + 32 * i, t);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] += t[e];
-      }
-      tmem_st32(taddr + 32 * i, v);
+      tmem_st32_async(taddr + 32 * i, v);
     }
   }
+  tmem_st_wait();
 }
 
 // Receive buffer of CTA `to`: [source rank, without its own][local chunk][8 float4 columns][rows], so that a warp's rows are
@@ -849,10 +858,8 @@ __device__ __forceinline__ void split_unit(const MxGemmParams& p, int row, int t
   }
 }
 
-// Whether the kernel for sums of several chains also takes those of one.  (gate_up in nvfp4, whose scales leave the most of the
-// chains' sums to registers, takes 53.2 us then for 64 x 28672 x 8192, 50.8 in a kernel of its own.)
-constexpr bool one_split(int fmt, int epi) { return fmt != kMxNvfp4 || !is_silu(epi); }
-
+// CHAINS: a CTA's stages may be more than a chain's.  (A kernel of its own for those that are not: with the chains' code in it
+// 3 x 448 x 2048, nvfp4, takes 4.9 us and without 4.45; gate_up 64 x 28672 x 8192 53.2 and 50.8.)
 template <int FMT, int EPI, bool CHAINS>
 __global__ void __launch_bounds__(kThreads, 2)
     k_gemm_mx_split(const __grid_constant__ MxMaps maps, const __grid_constant__ MxGemmParams p) {
@@ -1031,10 +1038,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         break;
       }
       tc_fence_after();
-      save_chain<R>(taddr, c == 0, kept);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(saved_bar);
+      save_chain<R>(taddr, c == 0, kept, [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(saved_bar);
+      });
     }
   }
   if (!mbar_wait(tfull_bar, 0, nullptr)) {
@@ -1142,8 +1150,8 @@ bool operand_maps(CUtensorMap* codes, CUtensorMap* scales, const MxOperand& o, i
 template <int FMT, int EPI>
 cudaError_t raise_limits() {
   static SmemLimits limits;
-  return limits.raise({smem_need(k_gemm_mx_split<FMT, EPI, true>, kMaxSmemBytes),
-                       smem_need(k_gemm_mx_split<FMT, EPI, one_split(FMT, EPI)>, kMaxSmemBytes),
+  return limits.raise({smem_need(k_gemm_mx_split<FMT, EPI, false>, kMaxSmemBytes),
+                       smem_need(k_gemm_mx_split<FMT, EPI, true>, kMaxSmemBytes),
                        smem_need(k_gemm_mx_pair<FMT, EPI>, PairRing<FMT>::kSmem)});
 }
 
@@ -1265,8 +1273,8 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
     p.recv_at = p.stages * stage_bytes;
     p.meta_at = p.recv_at + recv;
   }
-  return launch_kernel_cluster(fill > R::kChain ? k_gemm_mx_split<FMT, EPI, true> : k_gemm_mx_split<FMT, EPI, one_split(FMT, EPI)>,
-                               dim3(ctas), dim3(kThreads), static_cast<size_t>(p.meta_at) + 2048, s, true, S, maps, p);
+  return launch_kernel_cluster(fill > R::kChain ? k_gemm_mx_split<FMT, EPI, true> : k_gemm_mx_split<FMT, EPI, false>, dim3(ctas),
+                               dim3(kThreads), static_cast<size_t>(p.meta_at) + 2048, s, true, S, maps, p);
 }
 
 template <int FMT>
