@@ -7,10 +7,10 @@
 // codes and scales of a microscaled matrix that the next product reads.
 //
 // Two kernels: whole tiles of 256 x 256 on SM pairs (k_gemm_mx_pair), and for few tiles ones of 128 x 128 with K split over a
-// cluster (k_gemm_mx_split).  In both a stage of the operand ring holds 128 bytes of every row (256 e2m1 or 128 e4m3
-// elements, one swizzle row) and the scale tiles that belong to them; the issuing thread copies these into tensor memory and
-// then issues the stage's four MMAs, in order.  Up to sixteen instructions a stage come from that thread, so everything
-// they take is computed under control flow that is the warp's (warp_same, elect_one): their operands stay in uniform
+// cluster (k_gemm_mx_split).  In both a stage of the operand ring holds 128 bytes of every row (256 e2m1 or 128 e4m3 elements,
+// one swizzle row) and the scale tiles that belong to them; the issuing thread copies these into tensor memory and then issues
+// the stage's four MMAs (gate_up of few tiles: eight), in order.  Up to twenty instructions a stage come from that thread, so
+// everything they take is computed under control flow that is the warp's (warp_same, elect_one): their operands stay in uniform
 // registers, where moving them there from lane registers cost some 50 cycles for each (70B gate_up, 4128 rows, nvfp4: 1.18 ms
 // and then 0.59).
 #include <cuda.h>
@@ -44,19 +44,20 @@ __host__ __device__ constexpr int out_fmt(int epi) {
   return epi == kMxSiluNvfp4 ? kMxNvfp4 : epi == kMxSiluFp4 ? kMxFp4 : epi == kMxSiluFp8 ? kMxFp8 : 0;
 }
 
-// The tensor cores cut a sum's low bits at every step, always towards zero, so that the error grows with the steps and
-// faster than that of sums rounded to nearest (against 64 bits, rms over that of the results, fp8 on SM pairs in one chain and
-// then fp32: K = 2048 1.1e-7 and 0.6e-7, 8192 4.8e-7 and 1.2e-7, 28672 24e-7 and 2.7e-7; terms of one sign 190e-7 at 28672).
-// Results in fp32, and those that are quantised from it, are therefore sums of chains of no more than so many stages, which
-// are added in fp32: 1.3e-7 at K = 28672, one sign 5e-7.  Few sums of 4-bit products are cut at all: exact for rows whose scales
-// are near one another; where those of x spread over some ten binades, K = 28672, in one chain 39e-7 to 45e-7, in chains
-// twice as long as fp8's 7e-7 to 11e-7, fp32 10e-7 to 12e-7.
+// The tensor cores cut a sum's low bits at every step, always towards zero, so that the error grows with the steps and faster
+// than that of sums rounded to nearest (against 64 bits, rms over that of the results, fp8 on SM pairs in one chain and then
+// fp32: K = 2048 1.1e-7 and 0.6e-7, 8192 4.8e-7 and 1.2e-7, 28672 24e-7 and 2.7e-7; terms of one sign 190e-7 at 28672).  Results
+// in fp32, and those that are quantised from it, are therefore sums of chains of no more than so many stages, which are added
+// in fp32: 1.3e-7 at K = 28672, one sign 5e-7.  Few sums of 4-bit products are cut at all: exact for rows whose scales are near
+// one another; where those of x spread over some ten binades, K = 28672, in one chain 39e-7 to 45e-7, in chains twice as long
+// as fp8's 7e-7 to 11e-7, fp32 10e-7 to 12e-7.
 template <int FMT>
 constexpr int kChainStages = FMT == kMxFp8 ? 16 : 32;
 
-// Results in bf16 round to 2^-8 of themselves: a chain of 256 stages is off by 2^-15 at the worst (fp8, terms of one sign).
-// Longer sums are not left to SM pairs, which take one chain for bf16.
-constexpr int kBf16Stages = 256;
+// Results in bf16 round to 2^-8 of themselves.  Terms of one sign put a chain of n stages, 4 n steps of half a last place each,
+// off by 2 n 2^-24: SM pairs take bf16 sums in one chain of up to 1024 stages (2^-13; longer ones are left to the other
+// kernel), which takes 4-bit ones in chains of 256.
+constexpr int kPairBf16Stages = 1024, kSplitBf16Stages = 256;
 __host__ __device__ constexpr bool is_bf16(int epi) { return epi == kMxBf16 || epi == kMxSilu; }
 
 // What a format makes of a stage.
@@ -349,7 +350,8 @@ __device__ __forceinline__ int part_col(int half, int j) {
 // with the other accumulator are in registers: the last 64 of the first one, which only the second half has, as j = 1; the
 // first 64 of the second, which the first half has, as j = 0.
 template <int EPI, class Release>
-__device__ __forceinline__ void add_chain(float (&v)[2][64], uint32_t taddr, int acc, int half, bool first, const Release& release) {
+__device__ __forceinline__ void add_chain(float (&v)[2][64], uint32_t taddr, int acc, int half, bool first,
+                                          const Release& release) {
   auto add = [&](float (&c)[64], int j) {
     const uint32_t at = taddr + part_col<EPI>(half, j);
     if (first) {
@@ -698,8 +700,10 @@ __global__ void __launch_bounds__(pair_threads(EPI), 1)
 // ---------------------------------------------------------------------------
 // Few tiles (decode batches), bound by the weights' bytes (70B down projection, nvfp4: 24.2 us for one row, 6.4 TB/s but for
 // 3.5 us of set-up and exchange, 25.8 for 128 rows): tiles of 128 x 128 (silu: 64 gate and 64 up columns), K split over the
-// CTAs of a cluster, CTA rank r over stages [r kb / S, (r + 1) kb / S).  Two CTAs an SM where there are more CTAs than SMs:
-// they stream weights at the rate of HBM whatever their number on an SM, so a wave need not be whole.  Every 32-column chunk
+// CTAs of a cluster, CTA rank r over stages [r kb / S, (r + 1) kb / S).  Two CTAs an SM where there are more CTAs than SMs,
+// which share what the SM can take in, so that SMs with two decide the time: 64 rows, K = 8192, fp8, 124 tiles 24.6 us (1.20
+// times the weights' bytes at the copy rate), 170 33.6 (1.20), 300 51.9 (1.05); fewer tiles than half the SMs are split, and
+// 80, which are not, leave 72 SMs without work: 19.5 (1.47).  Every 32-column chunk
 // of the CTAs' accumulators goes into the shared memory of the CTA that finishes its unit (stores to another CTA need no
 // round trip) and is summed there in rank order; that CTA's own part stays in its tensor memory.  Where two stages less of
 // the ring leave room the chunks have a place of their own, so that a CTA need not wait for the others' MMAs before it
@@ -729,7 +733,7 @@ struct SplitStage {
   static constexpr int kKept = (kTsCols + 31) / 32, kAcc = kSplitCols;
   static_assert(kAcc + kSplitCols <= kSplitTmemCols, "tensor memory");
   // stages of a chain, of which one more costs less here than on SM pairs
-  static constexpr int kChain = is_bf16(EPI) ? FMT == kMxFp8 ? 32 : kBf16Stages : FMT == kMxFp8 ? 12 : kChainStages<FMT>;
+  static constexpr int kChain = is_bf16(EPI) ? FMT == kMxFp8 ? 32 : kSplitBf16Stages : FMT == kMxFp8 ? 12 : kChainStages<FMT>;
   __host__ __device__ static constexpr int bytes(int a_rows) { return a_rows * kRowBytes + kB + kSa + kSb; }
   // chunks that a CTA of S receives from each of the others, and the bytes of them all, `rows` accumulator rows each
   __host__ __device__ static constexpr int local_chunks(int S) { return (kUnits + S - 1) / S * kChunks; }
@@ -877,13 +881,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (nst + s); };
-  const uint32_t tfull_bar = bar0 + 8u * (2 * nst), recv_bar = tfull_bar + 8, done_bar = tfull_bar + 16, saved_bar = tfull_bar + 24;
+  const uint32_t tfull_bar = bar0 + 8u * (2 * nst), recv_bar = tfull_bar + 8, done_bar = tfull_bar + 16,
+                 saved_bar = tfull_bar + 24;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int ctas = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
   const int kb0 = rank * p.kb / ctas, kb1 = (rank + 1) * p.kb / ctas;
   // chains of chain_len stages, the first chain_more of them one longer
-  const int chains = CHAINS ? (kb1 - kb0 + R::kChain - 1) / R::kChain : 1, chain_len = (kb1 - kb0) / chains, chain_more = (kb1 - kb0) % chains;
+  const int stages = kb1 - kb0, chains = CHAINS ? (stages + R::kChain - 1) / R::kChain : 1;
+  const int chain_len = stages / chains, chain_more = stages % chains;
   int tm, tn;
   tile_coords(p, static_cast<int>(blockIdx.x) / ctas, tm, tn);
 
@@ -1171,14 +1177,15 @@ cudaError_t max_active_splits(int S, int* n) {
   return limits[S].get(reinterpret_cast<const void*>(k_gemm_mx_split<kMxFp8, kMxBf16, true>), S, kThreads, kMaxSmemBytes, n);
 }
 
-// Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S
-// CTAs; of 256 x 256 for SM pairs.  Fitted to 600 random sizes, of which the chosen kernel takes 0.4% more than the better
-// one in the mean: a stage of a pair's tile takes 0.28 and a tile 0.4 more, 0.8 at least; a stage of a CTA of the split
-// kernel 0.26, with two on an SM 0.44 to 0.46 and 1.3 a wave, of up to 64 rows 0.5; 5.2 (3.2 of them besides the reads of
-// weights) and 3.5 pass besides.  Weights are read at 5.4 TB/s by pairs and at 6.2 by the split kernel, 5.4 where more than
-// 64 rows of x have more tiles than the SMs hold.  (Split and pairs: 8192 x 8192, nvfp4, 256 rows 12.0 and 15.5, 384 rows
-// 17.2 and 15.5; 4096 x 14336, fp8, 256 rows 18.8 and 35.3; 57344 x 8192, nvfp4, 16 rows 46.6 and 56.1; gate and up of 28672
-// x 8192, nvfp4, 128 rows 54 and 47.5.)
+// Which kernel, by estimates of both in microseconds.  tiles: of 128 x 128 for the split kernel, which splits K over S CTAs; of
+// 256 x 256 for SM pairs.  Fitted to 600 random sizes; of 1000 others, bf16, fp32 and quantised results, operands from HBM, the
+// chosen kernel takes 0.1% more than the better one in the mean.  It is a choice, not a prediction: a tile of gate_up takes 2.3
+// us at least, and both kernels take longer than estimated there.  A stage of a pair's tile takes 0.28 and a tile 0.4 more, 0.8
+// at least; a stage of a CTA of the split kernel 0.26, with two on an SM 0.44 to 0.46 and 1.3 a wave, of up to 64 rows 0.5; 5.2
+// (3.2 of them besides the reads of weights) and 3.5 pass besides.  Weights are read at 5.4 TB/s by pairs and at 6.2 by the
+// split kernel, 5.4 where more than 64 rows of x have more tiles than the SMs hold.  (Split and pairs: 8192 x 8192, nvfp4, 256
+// rows 12.0 and 15.5, 384 rows 17.2 and 15.5; 4096 x 14336, fp8, 256 rows 18.8 and 35.3; 57344 x 8192, nvfp4, 16 rows 46.6 and
+// 56.1; gate and up of 28672 x 8192, nvfp4, 128 rows 54 and 47.5.)
 bool use_pairs(int M, long long tiles, int S, long long pair_tiles, int kb, double weight_bytes, int sms) {
   const long long pairs = sms / 2, waves = (pair_tiles + pairs - 1) / pairs, ctas = tiles * S;
   const double pair = std::max(2 + waves * std::max(kb * 0.28 + 0.4, 0.8), weight_bytes / 5.4e6);
@@ -1217,7 +1224,7 @@ int launch_typed(const MxGemmArgs& a, MxGemmParams& p, cudaStream_t s) {
     }
   int pairs = 0;
   if ((e = max_active_pairs<FMT, EPI>(&pairs)) != cudaSuccess) return e;
-  const bool pair = pairs > 0 && (!is_bf16(EPI) || p.kb <= kBf16Stages) &&
+  const bool pair = pairs > 0 && (!is_bf16(EPI) || p.kb <= kPairBf16Stages) &&
                     use_pairs(p.M, p.tiles, S, static_cast<long long>(pair_m) * pair_n, p.kb,
                               (is_silu(EPI) ? 2. : 1.) * p.N * row_bytes * (1 + 1. / 16), sms);
   MxMaps maps{};

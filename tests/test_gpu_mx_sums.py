@@ -75,12 +75,13 @@ def test_sums_of_one_sign(fmt, M, N, K):
     assert got <= bar, (got, bar)
 
 
-@pytest.mark.parametrize("fmt,K", [(R.FP8, 70016), (R.FP4, 200064)])
-def test_bf16_results_of_very_long_sums(fmt, K):
+@pytest.mark.parametrize("fmt,M,N,K", [(R.FP8, 520, 264, 70016), (R.FP4, 520, 264, 200064), (R.FP8, 2600, 1032, 131072),
+                                       (R.FP8, 2600, 1032, 131104)])
+def test_bf16_results_of_very_long_sums(fmt, M, N, K):
     """Against fp32 results of the same sums: a rounding to bf16, half a step of 2^-7, and a sixteenth of that for the cuts of
-    a chain of 256 stages (1024 steps, half a unit each in the mean, all on one side: 1025 / 2 2^-24 = 2^-15)."""
-    (a, _), (b, _) = matrix(fmt, 520, K, 1, True), matrix(fmt, 264, K, 2, True)
-    y, z = (torch.empty(520, 264, dtype=t, device=DEV) for t in (torch.float32, torch.bfloat16))
+    a chain of up to 1024 stages (4096 steps, half a unit each in the mean, all on one side: 4097 / 2 2^-24 = 2^-13)."""
+    (a, _), (b, _) = matrix(fmt, M, K, 1, True), matrix(fmt, N, K, 2, True)
+    y, z = (torch.empty(M, N, dtype=t, device=DEV) for t in (torch.float32, torch.bfloat16))
     lb.linear_mx(a, b, y)
     lb.linear_mx(a, b, z)
     assert lb.get_device_error()[0] == lb.LLAMA_OK
