@@ -473,11 +473,12 @@ int llama_fused_add_rmsnorm_mx(const void* x, const void* residual_in, void* res
  * 8.  The tensor cores cut a sum to 24 bits at every step of 32 or 64 elements;
  * for fp32 results, and the quantised ones below, a chain of such steps ends after
  * 2048 elements in fp8 and 8192 in 4 bits, and the chains are added in fp32, so
- * that the error does not grow with K beyond that of fp32 sums.  (bf16 results
- * have chains whose error is a thirtieth of their own rounding at the worst.)  No
- * row of y depends on another row of x, but M decides how K is split over SMs and
- * chains, and so the order of the sums; that order is fixed, so a call
- * repeats bit for bit.  No workspace is needed. */
+ * that the error stays about that of one chain (fp8, random operands: 1.1e-7 to
+ * 1.3e-7 of the results' rms at any K up to 28672, sums in fp32 0.6e-7 to 2.7e-7).
+ * bf16 results have longer chains, off by a thirtieth of their own rounding at the
+ * worst.  No row of y depends on another row of x, but M decides how K is split
+ * over SMs and chains, and so the order of the sums; that order is fixed, so a
+ * call repeats bit for bit.  No workspace is needed. */
 int llama_linear_mx(const LlamaMxMatrix* x, const LlamaMxMatrix* w, float alpha, void* y, int out_fp32,
                     llama_stream_t stream);
 
