@@ -462,8 +462,8 @@ int llama_dequantize_mx(const LlamaMxMatrix* m, void* y, int64_t y_stride, llama
 /* llama_fused_add_rmsnorm with its output quantised: r = bf16(x (+ residual_in));
  * r / sqrt(mean(r^2) + eps) * gamma, for every row of x [out->rows, out->cols],
  * goes to out.  The norm's fp32 result is quantised without a rounding to bf16
- * before.  residual_out may be NULL or alias x / residual_in.  cols is a
- * multiple of 32 up to 16384. */
+ * before, and a row's result does not depend on the number of rows.  residual_out
+ * may be NULL or alias x / residual_in.  cols is a multiple of 32 up to 16384. */
 int llama_fused_add_rmsnorm_mx(const void* x, const void* residual_in, void* residual_out, const LlamaMxMatrix* out,
                                const void* gamma, float eps, llama_stream_t stream);
 

@@ -168,6 +168,42 @@ __global__ void __launch_bounds__(kThreads) k_dequantize_mx(const MxRowsArgs a) 
   }
 }
 
+// The sum over a row's chunks, ss[c] of this thread's, in an order that does not depend on T, so that a row's codes do not depend
+// on the number of rows: blocks of 32 neighbouring chunks over the lanes, pairs 16 apart first, then the blocks in the same
+// way, pairs 32 apart first.  A block is a warp's chunks of one c; with each exchange a lane goes on with half of its blocks
+// (6 exchanges for four).
+template <int T, int MAXC>
+__device__ __forceinline__ float row_sum(float (&ss)[MAXC], float* red) {
+  constexpr int kLanes = 32 / MAXC, kBlocks = MAXC * T / 32;  // lanes that hold a block's sum in the end, block c from c kLanes on
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = MAXC, o = 16; o > 0; o >>= 1, n = n > 1 ? n / 2 : 1) {
+    const bool high = (lane & o) != 0;
+    if (n > 1) {
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const float keep = high ? ss[i + n / 2] : ss[i], give = high ? ss[i] : ss[i + n / 2];
+        ss[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    } else {
+      ss[0] += __shfl_xor_sync(0xffffffffu, ss[0], o);
+    }
+  }
+  float sum = ss[0];
+  if constexpr (T == 32) {
+#pragma unroll
+    for (int o = 16; o >= kLanes; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  } else {
+    if (lane % kLanes == 0) red[lane / kLanes * (T / 32) + (threadIdx.x >> 5)] = sum;
+    __syncthreads();
+    sum = red[lane % (kBlocks < 32 ? kBlocks : 32)];
+    if constexpr (kBlocks > 32) sum += red[lane + 32];
+#pragma unroll
+    for (int o = (kBlocks < 32 ? kBlocks : 32) / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  return sum;
+}
+
 // The residual add and RMSNorm of rowops.cu, its output quantised: T threads a row (32: a CTA has eight rows, a warp each),
 // the row in registers in chunks of 8 elements, 2 or 4 lanes a group.  The norm's fp32 result is quantised as it is, without
 // a rounding to bf16 before.
@@ -175,7 +211,7 @@ template <int FMT, int T, int MAXC>
 __global__ void __launch_bounds__(T == 32 ? kThreads : T) k_add_rmsnorm_mx(const MxNormArgs a) {
   constexpr int L = mx_group(FMT) / 8;  // lanes a group
   constexpr int kRows = T == 32 ? kThreads / 32 : 1;
-  __shared__ float red[32];
+  __shared__ float red[MAXC * T / 32];
   pdl_wait();
   if (gridDim.x <= kEarlyTriggerCtas) pdl_trigger();
   const int warp = threadIdx.x >> 5;
@@ -186,7 +222,7 @@ __global__ void __launch_bounds__(T == 32 ? kThreads : T) k_add_rmsnorm_mx(const
   const uint4* x = static_cast<const uint4*>(a.x) + base;
   const uint4* res = static_cast<const uint4*>(a.res_in) + base;
   uint4 u[MAXC];  // the new residual: a bf16 tensor, and the norm is taken of that tensor
-  float ss = 0.f;
+  float ss[MAXC];
 #pragma unroll
   for (int c = 0; c < MAXC; ++c) u[c] = tid + c * T < nch ? x[tid + c * T] : make_uint4(0, 0, 0, 0);
   if (a.res_in != nullptr) {
@@ -207,20 +243,11 @@ __global__ void __launch_bounds__(T == 32 ? kThreads : T) k_add_rmsnorm_mx(const
     float v[8];
     unpack8(u[c], v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if constexpr (T > 32) {
-    if ((threadIdx.x & 31) == 0) red[warp] = ss;
-    __syncthreads();
-    ss = 0.f;
-#pragma unroll
-    for (int w = 0; w < T / 32; ++w) ss += red[w];
+    for (int e = 0; e < 8; ++e) ss[c] = e == 0 ? v[0] * v[0] : fmaf(v[e], v[e], ss[c]);
   }
   // 1 / sqrt(y) = inv + low: the residual 1 - y inv^2, with the product's rounding, halved, so that the results below
   // are off by little more than their own rounding (codes near a border then fall where they should)
-  const float y = ss / static_cast<float>(a.cols) + a.eps;
+  const float y = row_sum<T>(ss, red) / static_cast<float>(a.cols) + a.eps;
   const float inv = rsqrtf(y), yi = y * inv;
   const float low = yi < INFINITY ? 0.5f * inv * (fmaf(-yi, inv, 1.f) - fmaf(y, inv, -yi) * inv) : 0.f;
   uint4* res_out = static_cast<uint4*>(a.res_out) + base;
